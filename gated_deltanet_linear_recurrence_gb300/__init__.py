@@ -17,6 +17,8 @@ __all__ = ["gdn_prefill", "gdn_prefill_streamed", "gdn_prefill_streamed_workspac
            "gdn_prefill_noalloc", "gdn_decode_step", "gdn_decode_step_rmsnorm",
            "gdn_output_rmsnorm", "gdn_decode_multi", "gdn_attn_decode",
            "gdn_attn_decode_workspace_size", "gdn_attn_decode_block_keys",
+           "gdn_attn_prefill", "gdn_kv_append", "gdn_kv_gather", "gdn_attn_decode_paged",
+           "gdn_attn_decode_paged_workspace_size",
            "gdn_prefill_workspace_size",
            "gdn_stream_status", "gdn_status_string", "gdn_prefill_crossover_tokens",
            "gdn_prefill_form", "gdn_selftest_wait_timeout", "GdnError",
@@ -381,6 +383,177 @@ def gdn_attn_decode(q, k_cache, v_cache, cache_len, scale=None, o=None, layout="
                              h_q, h_kv, D, cap, dt, float(scale), lay, int(block_keys),
                              _ptr(workspace), ws_bytes, _stream(stream))
     _lib.check(st, "gdn_attn_decode")
+    return o
+
+
+_CACHE_DTYPES = {torch.bfloat16: _lib.GDN_CACHE_BF16, torch.float8_e4m3fn: _lib.GDN_CACHE_E4M3}
+
+
+def _token_stride(t, name):
+    """Elements between the tokens of t [T, heads, D]: the heads of a token lie side
+    by side, the tokens may be apart (a slice of a fused projection)."""
+    T, H, D = t.shape
+    if t.is_contiguous():
+        return H * D
+    s = t.stride()
+    _require(s[2] == 1 and (H == 1 or s[1] == D), f"{name}: a token's heads must be contiguous")
+    return s[0] if T > 1 else H * D
+
+
+def _int32_on_gpu(t, shape, name):
+    _require(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.shape == shape,
+             f"{name} must be {list(shape)} int32 on the GPU, contiguous")
+
+
+def _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp):
+    """(num_pages, h_kv, page_size, D, max_pages, dtype code) of a paged cache."""
+    shape = k_pages.shape
+    _require(len(shape) == 4 and v_pages.shape == shape and v_pages.dtype == k_pages.dtype,
+             "k_pages / v_pages must be [num_pages, h_kv, page_size, D] of one dtype")
+    _require(k_pages.is_contiguous() and v_pages.is_contiguous() and k_pages.is_cuda
+             and v_pages.is_cuda, "pages must be contiguous, on the GPU")
+    if k_pages.dtype not in _CACHE_DTYPES:
+        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
+    if k_pages.dtype == torch.float8_e4m3fn:
+        for e in (k_exp, v_exp):
+            _require(e is not None and e.shape == shape[:3] and e.dtype == torch.uint8
+                     and e.is_contiguous() and e.is_cuda,
+                     "k_exp / v_exp must be [num_pages, h_kv, page_size] uint8 on the GPU")
+    _require(page_table.dim() == 2, "page_table must be [num_seqs, max_pages]")
+    _int32_on_gpu(page_table, page_table.shape, "page_table")
+    return (*shape, page_table.shape[1], _CACHE_DTYPES[k_pages.dtype])
+
+
+def _keep_for(stream, *tensors):
+    """Tensors allocated here for a call on another stream than the current one must
+    not be given out again before that stream has passed the call."""
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def gdn_kv_append(k, v, k_pages, v_pages, page_table, cu_seqlens, start_pos, k_exp=None,
+                  v_exp=None, stream=None):
+    """Write packed new rows into a paged cache, in place (gdn_kv_append in include/gdn.h):
+    k, v [T, h_kv, D] bf16, tokens of sequence n = cu_seqlens[n] .. cu_seqlens[n+1]-1, to
+    its positions start_pos[n] ..; k_pages, v_pages [num_pages, h_kv, page_size, D] bf16,
+    or float8_e4m3fn with k_exp, v_exp [num_pages, h_kv, page_size] uint8 (each row's
+    power of two, bias 127); page_table [N, max_pages], cu_seqlens [N+1], start_pos [N]
+    int32 on the device.  k and v may be slices of a fused projection."""
+    lib = _lib.load()
+    P, h_kv, page, D, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
+    N, T = page_table.shape[0], k.shape[0]
+    _require(k.shape == (T, h_kv, D) and v.shape == k.shape, "k / v must be [T, h_kv, D]")
+    _require(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.is_cuda and v.is_cuda,
+             "k / v must be bfloat16 on the GPU")
+    _int32_on_gpu(cu_seqlens, (N + 1,), "cu_seqlens")
+    _int32_on_gpu(start_pos, (N,), "start_pos")
+    st = lib.gdn_kv_append(k.data_ptr(), v.data_ptr(), _token_stride(k, "k"),
+                           _token_stride(v, "v"), k_pages.data_ptr(), v_pages.data_ptr(),
+                           _ptr(k_exp), _ptr(v_exp), page_table.data_ptr(), cu_seqlens.data_ptr(),
+                           start_pos.data_ptr(), N, T, h_kv, D, page, P, max_pages, dt,
+                           _stream(stream))
+    _lib.check(st, "gdn_kv_append")
+
+
+def gdn_kv_gather(k_pages, v_pages, page_table, cu_seqlens, start_pos, total_tokens, k_exp=None,
+                  v_exp=None, k=None, v=None, stream=None):
+    """Read cached rows back as packed bf16 (gdn_kv_gather in include/gdn.h): rows
+    start_pos[n] .. of each sequence, cu_seqlens[n+1] - cu_seqlens[n] of them, total_tokens
+    in all.  Returns (k, v) [total_tokens, h_kv, D]; arguments as for gdn_kv_append."""
+    lib = _lib.load()
+    P, h_kv, page, D, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
+    N, T = page_table.shape[0], int(total_tokens)
+    _int32_on_gpu(cu_seqlens, (N + 1,), "cu_seqlens")
+    _int32_on_gpu(start_pos, (N,), "start_pos")
+    made = []
+    if k is None:
+        made.append(k := torch.empty((T, h_kv, D), dtype=torch.bfloat16, device=k_pages.device))
+    if v is None:
+        made.append(v := torch.empty((T, h_kv, D), dtype=torch.bfloat16, device=k_pages.device))
+    _require(k.shape == (T, h_kv, D) and v.shape == k.shape and k.dtype == torch.bfloat16
+             and v.dtype == torch.bfloat16 and k.is_cuda and v.is_cuda,
+             "k / v must be [total_tokens, h_kv, D] bfloat16 on the GPU")
+    st = lib.gdn_kv_gather(k.data_ptr(), v.data_ptr(), _token_stride(k, "k"),
+                           _token_stride(v, "v"), k_pages.data_ptr(), v_pages.data_ptr(),
+                           _ptr(k_exp), _ptr(v_exp), page_table.data_ptr(), cu_seqlens.data_ptr(),
+                           start_pos.data_ptr(), N, T, h_kv, D, page, P, max_pages, dt,
+                           _stream(stream))
+    _lib.check(st, "gdn_kv_gather")
+    _keep_for(stream, *made)
+    return k, v
+
+
+def gdn_attn_decode_paged_workspace_size(h_q, h_kv, head_dim):
+    return int(_lib.load().gdn_attn_decode_paged_workspace_size(h_q, h_kv, head_dim))
+
+
+def gdn_attn_decode_paged(q, k_pages, v_pages, page_table, cache_len, k_exp=None, v_exp=None,
+                          scale=None, o=None, workspace=None, stream=None):
+    """Decode attention over a paged cache (gdn_attn_decode_paged in include/gdn.h): q
+    [B, h_q, D] bf16, one new token of each sequence; pages, exponent bytes and page_table
+    as for gdn_kv_append; cache_len [B] int32 on the device.  ``scale`` defaults to
+    1/sqrt(D).  A workspace of gdn_attn_decode_paged_workspace_size() bytes is allocated
+    when none is given.  Returns o [B, h_q, D] bf16."""
+    lib = _lib.load()
+    P, h_kv, page, D, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
+    B, h_q, _ = q.shape
+    _require(q.shape[2] == D and q.dtype == torch.bfloat16 and q.is_cuda,
+             "q must be [B, h_q, D] bfloat16 on the GPU")
+    _require(page_table.shape[0] == B, "page_table must be [B, max_pages]")
+    _int32_on_gpu(cache_len, (B,), "cache_len")
+    made = []
+    if o is None:
+        made.append(o := torch.empty((B, h_q, D), dtype=torch.bfloat16, device=q.device))
+    _require(o.shape == (B, h_q, D) and o.dtype == torch.bfloat16 and o.is_contiguous()
+             and o.is_cuda, "o must be [B, h_q, D] bfloat16, contiguous, on the GPU")
+    if workspace is None:
+        need = lib.gdn_attn_decode_paged_workspace_size(h_q, h_kv, D)
+        made.append(workspace := torch.empty(need, dtype=torch.uint8, device=q.device))
+    st = lib.gdn_attn_decode_paged(q.data_ptr(), _token_stride(q, "q"), k_pages.data_ptr(),
+                                   v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp),
+                                   page_table.data_ptr(), cache_len.data_ptr(), o.data_ptr(), B,
+                                   h_q, h_kv, D, page, P, max_pages, dt,
+                                   float(D ** -0.5 if scale is None else scale),
+                                   workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    _lib.check(st, "gdn_attn_decode_paged")
+    _keep_for(stream, *made)
+    return o
+
+
+def gdn_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=None, stream=None):
+    """Causal grouped-query attention over packed prompts (gdn_attn_prefill in
+    include/gdn.h): q [Tq, h_q, D]; k, v [Tk, h_kv, D], bf16, D 128 or 256, h_q / h_kv <= 8;
+    the queries of sequence n (cu_seqlens_q) are the last of its positions (cu_seqlens_k,
+    by default the same offsets: whole prompts).  q, k and v may be slices of a fused
+    projection.  ``scale`` defaults to 1/sqrt(D).  Returns o [Tq, h_q, D]."""
+    lib = _lib.load()
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    Tq, h_q, D = q.shape
+    Tk, h_kv, _ = k.shape
+    N = cu_seqlens_q.numel() - 1
+    _require(k.shape[2] == D and v.shape == k.shape, "k / v must be [Tk, h_kv, D]")
+    _require(k.dtype == q.dtype and v.dtype == q.dtype, "q, k, v must share a dtype")
+    _require(q.is_cuda and k.is_cuda and v.is_cuda, "q, k, v must be on the GPU")
+    dt = _dtype_code(q)
+    _int32_on_gpu(cu_seqlens_q, (N + 1,), "cu_seqlens_q")
+    _int32_on_gpu(cu_seqlens_k, (N + 1,), "cu_seqlens_k")
+    made = []
+    if o is None:
+        made.append(o := torch.empty((Tq, h_q, D), dtype=q.dtype, device=q.device))
+    _require(o.shape == (Tq, h_q, D) and o.dtype == q.dtype and o.is_contiguous() and o.is_cuda,
+             "o must be [Tq, h_q, D], contiguous, of q's dtype, on the GPU")
+    st = lib.gdn_attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                              cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), N, Tq, Tk, h_q,
+                              h_kv, D, _token_stride(q, "q"), _token_stride(k, "k"),
+                              _token_stride(v, "v"), dt,
+                              float(D ** -0.5 if scale is None else scale), _stream(stream))
+    _lib.check(st, "gdn_attn_prefill")
+    _keep_for(stream, *made)
     return o
 
 

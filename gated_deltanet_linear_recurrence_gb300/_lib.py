@@ -14,9 +14,10 @@ STATUS_NAMES = {
     0: "GDN_OK", 1: "GDN_ERR_NULL_POINTER", 2: "GDN_ERR_INVALID_ARG",
     3: "GDN_ERR_UNSUPPORTED_SHAPE", 4: "GDN_ERR_UNSUPPORTED_DTYPE", 5: "GDN_ERR_MISALIGNED",
     6: "GDN_ERR_BAD_CU_SEQLENS", 7: "GDN_ERR_WORKSPACE_TOO_SMALL", 8: "GDN_ERR_DEVICE_TIMEOUT",
-    9: "GDN_ERR_CUDA", 10: "GDN_ERR_BAD_CACHE_LEN",
+    9: "GDN_ERR_CUDA", 10: "GDN_ERR_BAD_CACHE_LEN", 11: "GDN_ERR_BAD_PAGE",
 }
 GDN_F32, GDN_BF16 = 0, 1
+GDN_CACHE_BF16, GDN_CACHE_E4M3 = 1, 2
 GDN_OPT_QK_L2NORM = 1
 ALGOS = {"auto": 0, "scan": 1, "chunked": 2, "chunked_fused": 3, "chunked_split": 4,
          "chunked_coop": 5}
@@ -60,6 +61,18 @@ SIGNATURES = {
                                        ctypes.c_int, _f32, ctypes.c_int, _i32, _vp, _sz, _vp]),
     "gdn_attn_decode_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, ctypes.c_int, _i32]),
     "gdn_attn_decode_block_keys": (_i32, [_i32, _i32, _i32, _i32, _i32, ctypes.c_int, _i32]),
+    "gdn_kv_append": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _i32, _i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int,
+                                     _vp]),
+    "gdn_kv_gather": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _i32, _i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int,
+                                     _vp]),
+    "gdn_attn_decode_paged": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                             _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_int,
+                                             _f32, _vp, _sz, _vp]),
+    "gdn_attn_decode_paged_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "gdn_attn_prefill": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i32,
+                                        _i32, _i32, _i64, _i64, _i64, ctypes.c_int, _f32, _vp]),
     "gdn_stream_status": (ctypes.c_int, [_vp]),
     "gdn_selftest_wait_timeout": (ctypes.c_int, [_i32, _vp]),
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -1,0 +1,731 @@
+// attn_prefill.cu — causal grouped-query attention over packed prompts, on
+// tcgen05 with a pair of CTAs for each tile of queries.
+//
+// For query row r (token and query head) that sees the keys 0 .. lim_r - 1:
+//     s_rj = scale q_r.k_j,   o_r = sum_j 2^(t_rj - m_r) v_j / sum_j 2^(t_rj - m_r),
+//     t_rj = s_rj log2(e)
+// over 128-key tiles with a running reference m_r: as long as a tile's maximum
+// exceeds m_r by at most 8 (weights up to 2^8) m_r stays, so O is seldom rescaled.
+//
+// Tile.  A CTA pair takes 256 rows: 2 floor(128 / G) consecutive tokens of one
+// sequence with the G query heads of a KV head, rows (token, head) in that order,
+// which is the order in which q holds them (one TMA box fetches them).  Sharing
+// the rows of a KV head keeps the causal edge short (G tokens' rows end at the
+// same key) and fills tiles of short sequences.
+//
+// Bound by the tensor pipe: 4 D flops per row and key, 2 D/128 x 1024 cycles a
+// pair and 128 keys, against 64 exponentials a row and key-half.  With one CTA the
+// operands would not fit the shared-memory bandwidth: Q and K tiles read at 128
+// bytes a cycle and K and V written at 64.  cta_group::2 lets each CTA hold half
+// of K (keys) and of V (dimensions), and P stays in TMEM, which leaves
+//     Q 4 KB + K 2 KB a 64-cycle step; V 4 KB a 128-cycle step (D = 256)
+// to read and half of the writes.
+//
+// TMEM (512 columns): S of two key tiles (128 fp32 columns each, of which P's 64
+// columns of bf16 pairs then take the first half), O (D columns).  Shared memory:
+// Q (64 KB at D = 256), a ring of K and V tile halves in the order of their use,
+// K0 K1 V0 K2 V1 ..: the products of tile j + 1's scores run while the softmax
+// warps work on tile j.
+//
+// Roles (11 warps): 0-7 softmax (two threads a row, 64 columns each), 8 TMA, 9
+// products (the even CTA's issues them for the pair; the odd CTA's relays its own
+// copies' arrival), 10 the schedule.  The pairs are persistent.
+//
+// Rounding: P is rounded to bf16 for the second product (relative 2^-9 a weight,
+// the same as the output's rounding; the sums l stay fp32 over unrounded weights).
+//
+// What a query does not see must not reach it even as NaN: its scores are masked,
+// and in a tile that some row sees in part, V rows past every row's sight are
+// zeroed in shared memory and non-finite values in the rest replaced by zero; the
+// epilogue adds those back to the rows that do see them (from global memory, only
+// in tiles where any was found).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "attn_params.h"
+#include "attn_tc.cuh"
+#include "params.h"
+#include "per_device.h"
+#include "rows.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = 256;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kScheduleWarp = 10;
+constexpr int kThreads = 352;
+constexpr int kConsumerWarps = 10;  // of a scheduled tile: all but the schedule's own
+constexpr int kKeys = 128;          // keys a tile
+constexpr int kRows = 128;          // rows a CTA
+constexpr uint32_t kBarSoftmax = 1;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;  // log2 of the largest weight before m moves
+
+struct Tile {  // one unit of work of a pair; tiles < 0 ends the schedule
+  int32_t q0, k0;     // packed rows where the sequence's queries and keys start
+  int32_t a, off;     // queries of the sequence; keys before its first query (may be < 0)
+  int32_t tok0, kvh;  // first token of the pair's rows; KV head
+  int32_t tiles;      // key tiles to go through
+  int32_t sight;      // keys that the last row sees
+};
+
+template <int D>
+struct Cfg {
+  static constexpr uint32_t kQBytes = kRows * D * 2;
+  static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
+  static constexpr int kEntries = D == 256 ? 5 : 10;
+  static constexpr uint32_t kRing = kQBytes;
+  static constexpr uint32_t kShared = kRing + kEntries * kEntry;  // the barriers and the rest
+  static constexpr int kSteps = D / 16;
+  static constexpr uint32_t kTmemO = 256;
+  static constexpr uint32_t kTmemCols = 512;
+};
+
+struct Shared {  // beside the tiles
+  uint64_t full[10], pair_full[10], empty[10];
+  uint64_t q_full, q_pair_full, q_empty;
+  uint64_t s_ready[2], p_ready[2], o_ready[2], o_free;
+  uint64_t tile_full[2], tile_empty[2], flags_in, drained;
+  Tile tile[2];
+  uint32_t poison[2][2];  // [pass parity][half of the dimensions]: pass + 1 where V had a non-finite
+  uint32_t tmem;
+  float red[2][2][128];   // row maxima (and at the end sums) of the two column halves
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float poison_of(uint32_t bits16) {  // the value if it is not finite
+  return (bits16 & 0x7f80u) == 0x7f80u ? __uint_as_float(bits16 << 16) : 0.f;
+}
+
+// ------------------------------------------------------------------ schedule
+// One sequence's ranges (bad ones count no tiles; recorded once).
+struct Seq {
+  int q0, k0, a, b, tiles;
+};
+__device__ __forceinline__ Seq sequence(const AttnPrefillArgs& p, int n, int tokens, bool report) {
+  Seq s{0, 0, 0, 0, 0};
+  if (n >= p.num_seqs) return s;
+  const int q0 = __ldg(p.cu_q + n), q1 = __ldg(p.cu_q + n + 1);
+  const int k0 = __ldg(p.cu_k + n), k1 = __ldg(p.cu_k + n + 1);
+  const bool bad = q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k;
+  const bool open = (n == 0 && (q0 != 0 || k0 != 0)) ||
+                    (n == p.num_seqs - 1 && (q1 != p.total_q || k1 != p.total_k));
+  if (report && (bad || open)) raise_error(p.err, kErrBadCuSeqlens);
+  if (bad) return s;
+  s.q0 = q0;
+  s.k0 = k0;
+  s.a = q1 - q0;
+  s.b = k1 - k0;
+  s.tiles = (s.a + tokens - 1) / tokens;
+  return s;
+}
+// Tiles of s that see at least x >= 1 keys (its later tiles see more); all of them for x <= 0.
+__device__ __forceinline__ int tiles_from(const Seq& s, int x, int tokens) {
+  if (x <= 0) return s.tiles;
+  if (x > s.b || s.tiles == 0) return 0;
+  const int need = x - (s.b - s.a);  // tokens up to the first one that sees x keys
+  const int skip = need <= 0 ? 0 : (need - 1) / tokens;
+  return s.tiles - min(skip, s.tiles);
+}
+__device__ __forceinline__ Tile make_tile(const Seq& s, int i, int kvh, int tokens) {
+  Tile t;
+  t.q0 = s.q0;
+  t.k0 = s.k0;
+  t.a = s.a;
+  t.off = s.b - s.a;
+  t.tok0 = i * tokens;
+  t.kvh = kvh;
+  t.sight = max(0, t.off + min(s.a, t.tok0 + tokens));
+  t.tiles = (t.sight + kKeys - 1) / kKeys;
+  return t;
+}
+__device__ __forceinline__ Seq pick(const Seq& s, int lane) {
+  Seq r;
+  r.q0 = __shfl_sync(kFullMask, s.q0, lane);
+  r.k0 = __shfl_sync(kFullMask, s.k0, lane);
+  r.a = __shfl_sync(kFullMask, s.a, lane);
+  r.b = __shfl_sync(kFullMask, s.b, lane);
+  r.tiles = __shfl_sync(kFullMask, s.tiles, lane);
+  return r;
+}
+__device__ __forceinline__ int prefix(int x, int lane) {  // of the lanes before
+  int y = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int z = __shfl_up_sync(kFullMask, y, off);
+    if (lane >= off) y += z;
+  }
+  return y - x;
+}
+
+// Tiles in the order of the schedule, for one warp.  Up to 32 sequences: by how
+// many keys they see, most first.  More: sequence by sequence, last tile first
+// (their number evens the pairs' shares out).
+struct Schedule {
+  Seq s;       // this lane's sequence of the current 32
+  int base;    // first sequence of the current 32
+  int before;  // tiles of the sequences before them
+  int tokens, lane;
+  __device__ __forceinline__ void open(const AttnPrefillArgs& p, int toks, int ln, bool report) {
+    tokens = toks;
+    lane = ln;
+    base = before = 0;
+    s = sequence(p, lane, tokens, report);
+    if (report)  // the other sequences' checks
+      for (int n = 32 + lane; n < p.num_seqs; n += 32) sequence(p, n, tokens, true);
+  }
+  // tile number r (asked in increasing order) of KV head kvh; false past the end
+  __device__ __forceinline__ bool get(const AttnPrefillArgs& p, int r, int kvh, Tile* t) {
+    if (p.num_seqs <= 32) {
+      if (r >= __reduce_add_sync(kFullMask, s.tiles)) return false;
+      int lo = 0, hi = __reduce_max_sync(kFullMask, s.b) + 1;  // tiles_from(lo) > r >= tiles_from(hi)
+      while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (__reduce_add_sync(kFullMask, tiles_from(s, mid, tokens)) > r) lo = mid;
+        else hi = mid;
+      }
+      const int at = tiles_from(s, lo, tokens), above = tiles_from(s, lo + 1, tokens);
+      const int k = r - __reduce_add_sync(kFullMask, above);  // among the tiles that see lo keys
+      const int pre = prefix(at - above, lane);
+      const unsigned hit = __ballot_sync(kFullMask, k >= pre && k < pre + at - above);
+      const int src = __ffs(hit) - 1;
+      const Seq q = pick(s, src);
+      *t = make_tile(q, q.tiles - __shfl_sync(kFullMask, at, src) + k - __shfl_sync(kFullMask, pre, src),
+                     kvh, tokens);
+      return true;
+    }
+    for (;;) {
+      const int n = __reduce_add_sync(kFullMask, s.tiles);
+      if (r < before + n) break;
+      before += n;
+      base += 32;
+      if (base >= p.num_seqs) return false;
+      s = sequence(p, base + lane, tokens, false);
+    }
+    const int pre = before + prefix(s.tiles, lane);
+    const unsigned hit = __ballot_sync(kFullMask, r >= pre && r < pre + s.tiles);
+    const int src = __ffs(hit) - 1;
+    const Seq q = pick(s, src);
+    *t = make_tile(q, q.tiles - 1 - (r - __shfl_sync(kFullMask, pre, src)), kvh, tokens);
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const AttnPrefillArgs p) {
+  using C = Cfg<D>;
+  // the tiles fill shared memory but for the 2.5 KB of Shared: no room to align them here
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem + C::kShared);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int G = p.h_q / p.h_kv;
+  const int tok_cta = kRows / G, tokens = 2 * tok_cta;  // tokens a CTA, a pair
+  if (warp == 0) {
+    tc2::tmem_alloc(&sh.tmem, C::kTmemCols);
+    tc2::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::kEntries; ++i) {
+      tc::mbar_init(&sh.full[i], 1);
+      tc::mbar_init(&sh.pair_full[i], 1);
+      tc::mbar_init(&sh.empty[i], 1);
+    }
+    tc::mbar_init(&sh.q_full, 1);
+    tc::mbar_init(&sh.q_pair_full, 1);
+    tc::mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sh.s_ready[i], 1);
+      tc::mbar_init(&sh.p_ready[i], 2 * kSoftmaxWarps);
+      tc::mbar_init(&sh.o_ready[i], 1);
+      tc::mbar_init(&sh.tile_full[i], 1);
+      tc::mbar_init(&sh.tile_empty[i], kConsumerWarps);
+      sh.poison[i][0] = sh.poison[i][1] = 0;
+    }
+    tc::mbar_init(&sh.o_free, 2 * kSoftmaxWarps);
+    tc::mbar_init(&sh.flags_in, kSoftmaxWarps);
+    tc::mbar_init(&sh.drained, 1);
+    tc::fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t sbase = tc::smem_u32(smem);
+  bool ok = true;
+  tc::wait_prerequisites();  // q, k, v and the offsets come from earlier kernels
+  tc::allow_dependents();
+
+  // The warp's next tile (pass counts tiles); false at the end or when a wait expired.
+  auto next_tile = [&](int pass, Tile* t) {
+    const bool w = __all_sync(kFullMask, tc::mbar_wait(&sh.tile_full[pass & 1], (pass >> 1) & 1));
+    if (!w) {
+      ok = false;
+      return false;
+    }
+    *t = sh.tile[pass & 1];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sh.tile_empty[pass & 1]);
+    return t->tiles >= 0;
+  };
+
+  if (warp == kScheduleWarp) {
+    // ------------------------------------------------------------ schedule
+    const int pairs = gridDim.x / 2, me = blockIdx.x / 2;
+    Schedule sc;
+    sc.open(p, tokens, lane, blockIdx.x == 0);
+    for (int pass = 0;; ++pass) {
+      // pass by pass in alternating direction, so that the pairs' sums come out alike
+      const int64_t i = (int64_t)pass * pairs + ((pass & 1) ? pairs - 1 - me : me);
+      Tile t;
+      const bool more = sc.get(p, (int)(i / p.h_kv), (int)(i % p.h_kv), &t);
+      if (!more) t.tiles = -1;
+      if (pass >= 2 && !__all_sync(kFullMask, tc::mbar_wait(&sh.tile_empty[pass & 1], ((pass >> 1) - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        sh.tile[pass & 1] = t;
+        tc::mbar_arrive(&sh.tile_full[pass & 1]);
+      }
+      if (!more) break;
+    }
+  } else if (warp == kTmaWarp) {
+    // ------------------------------------------------------------ copies
+    Tile t;
+    int e = 0, used = 0;  // ring entries issued; tiles with Q
+    if (lane == 0) {
+      tc::prefetch_tmap(&tm_q);
+      tc::prefetch_tmap(&tm_k);
+      tc::prefetch_tmap(&tm_v);
+    }
+    for (int pass = 0; next_tile(pass, &t); ++pass) {
+      if (t.tiles == 0) continue;
+      if (lane == 0) {
+        if (used > 0) ok = tc::mbar_wait(&sh.q_empty, (used - 1) & 1);
+        if (ok) {
+          tc::mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tok_cta * G) * D * 2);
+          for (int kb = 0; kb < D / 64; ++kb)
+            tc::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G,
+                            t.q0 + t.tok0 + (int)rank * tok_cta, &sh.q_full);
+        }
+        auto slot = [&]() -> uint8_t* {  // the next ring entry, empty and armed
+          const int s = e % C::kEntries;
+          if (e >= C::kEntries) ok = ok && tc::mbar_wait(&sh.empty[s], ((e / C::kEntries) - 1) & 1);
+          if (!ok) return nullptr;
+          tc::mbar_arrive_expect_tx(&sh.full[s], C::kEntry);
+          return smem + C::kRing + s * C::kEntry;
+        };
+        for (int j = 0; j <= t.tiles && ok; ++j) {
+          if (j < t.tiles) {
+            if (uint8_t* dst = slot()) {
+              for (int kb = 0; kb < D / 64; ++kb)
+                tc::tma_load_3d(dst + kb * 8192, &tm_k, 64 * kb, t.kvh,
+                                t.k0 + j * kKeys + (int)rank * 64, &sh.full[e % C::kEntries]);
+              ++e;
+            }
+          }
+          if (j > 0) {
+            if (uint8_t* dst = slot()) {
+              for (int kb = 0; kb < D / 128; ++kb)
+                tc::tma_load_3d(dst + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
+                                t.k0 + (j - 1) * kKeys, &sh.full[e % C::kEntries]);
+              ++e;
+            }
+          }
+        }
+      }
+      ++used;
+      ok = __all_sync(kFullMask, ok);
+      if (!ok) break;
+    }
+    // copies still in flight land before the CTA ends (already so unless a wait expired)
+    if (lane == 0) {
+      for (int j = max(0, e - C::kEntries); j < e; ++j)
+        if (!tc::mbar_wait(&sh.full[j % C::kEntries], (j / C::kEntries) & 1)) ok = false;
+      if (used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    Tile t;
+    int e = 0, used = 0, g = 0;  // ring entries, tiles with Q, key tiles so far
+    const uint32_t idesc_s = tc::idesc_bf16_f32(256, kKeys, false, false);
+    const uint32_t idesc_o = tc::idesc_bf16_f32(256, D, false, true);
+    const uint64_t dq = tc::smem_desc(sbase, 16, 1024, tc::kLayoutSw128);
+    const uint64_t dk = tc::smem_desc(sbase + C::kRing, 16, 1024, tc::kLayoutSw128);
+    const uint64_t dv = tc::smem_desc(sbase + C::kRing, 16384, 1024, tc::kLayoutSw128);
+    const bool leader = tc::elect_one();
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool w = tc2::wait(bar, parity);
+      tc::fence_after_sync();
+      return __all_sync(kFullMask, w) != 0;
+    };
+    const uint32_t r_full = tc2::in_cta(sh.pair_full, 0), r_q = tc2::in_cta(&sh.q_pair_full, 0);
+    auto entry = [&]() {  // the next ring entry has landed in both CTAs (odd CTA: passes that on)
+      const int s = e % C::kEntries;
+      const uint32_t ph = (e / C::kEntries) & 1;
+      bool w = warp_wait(&sh.full[s], ph);
+      if (rank == 0) {
+        w = w && warp_wait(&sh.pair_full[s], ph);
+      } else if (w && leader) {
+        tc::fence_proxy_async();
+        tc2::arrive_remote(r_full + s * 8);
+      }
+      return w;
+    };
+    for (int pass = 0; next_tile(pass, &t); ++pass) {
+      if (t.tiles == 0) continue;
+      ok = warp_wait(&sh.q_full, used & 1);
+      if (rank == 0) {
+        ok = ok && warp_wait(&sh.q_pair_full, used & 1);
+      } else if (ok && leader) {
+        tc::fence_proxy_async();
+        tc2::arrive_remote(r_q);
+      }
+      for (int j = 0; j <= t.tiles && ok; ++j) {
+        if (j < t.tiles) {  // S = Q K^T of key tile j
+          if (!(ok = entry())) break;
+          const int s = e % C::kEntries;
+          if (rank == 0 && leader) {
+            const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
+#pragma unroll
+            for (int kk = 0; kk < C::kSteps; ++kk)
+              tc2::mma_ss(tmem + ((g + j) & 1) * 128, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                          dk + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+            tc2::commit(&sh.s_ready[(g + j) & 1]);
+            tc2::commit(&sh.empty[s]);
+            if (j == t.tiles - 1) tc2::commit(&sh.q_empty);
+          }
+          __syncwarp();
+          ++e;
+        }
+        if (j > 0) {  // O += P V of key tile j - 1
+          const int h = g + j - 1;
+          if (!(ok = entry())) break;
+          const int s = e % C::kEntries;
+          if (rank == 0) {
+            if (!(ok = warp_wait(&sh.p_ready[h & 1], (h >> 1) & 1))) break;
+            if (j == 1 && used > 0 && !(ok = warp_wait(&sh.o_free, (used - 1) & 1))) break;
+            if (leader) {
+              const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                tc2::mma_ts(tmem + C::kTmemO, tmem + (h & 1) * 128 + 8 * kk, dv + so + ((kk * 2048) >> 4),
+                            idesc_o, (j > 1) || (kk > 0));
+              tc2::commit(&sh.o_ready[h & 1]);
+              tc2::commit(&sh.empty[s]);
+            }
+          }
+          __syncwarp();
+          ++e;
+        }
+      }
+      if (!ok) break;
+      g += t.tiles;
+      ++used;
+    }
+    // every product issued has completed before TMEM is released
+    if (rank == 0) {
+      if (leader) tc2::commit(&sh.drained);
+      __syncwarp();
+    }
+    if (!warp_wait(&sh.drained, 0)) ok = false;
+  } else {
+    // ------------------------------------------------------------ softmax
+    Tile t;
+    int e = 0, used = 0, g = 0;
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const float c = p.scale * kLog2e;
+    const bool down = c < 0.f;  // the largest score is then the smallest product
+    const uint32_t r_p = tc2::in_cta(sh.p_ready, 0), r_free = tc2::in_cta(&sh.o_free, 0);
+    const uint32_t r_flags = tc2::in_cta(&sh.flags_in, rank ^ 1), r_poison = tc2::in_cta(sh.poison, rank ^ 1);
+    bool carried = true;  // no wait expired since the last barrier of these warps
+    for (int pass = 0;; ++pass) {
+      // all softmax warps go on or none: they meet at barriers without a limit
+      const bool more = next_tile(pass, &t);
+      if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, ok && carried)) || !more) break;
+      const int tok = t.tok0 + (int)rank * tok_cta + row / G;
+      const bool real = row < tok_cta * G && tok < t.a;
+      const int lim = real ? max(0, t.off + tok + 1) : 0;  // keys this row sees
+      const int whole = t.off + t.tok0 + 1;                // keys that every row of the pair sees
+      float m = -INFINITY, l = 0.f;
+      uint32_t* poison = sh.poison[used & 1];
+      for (int j = 0; j < t.tiles && ok; ++j) {
+        const int h = g + j, key0 = j * kKeys;
+        const bool edge = key0 + kKeys > whole;
+        bool w = carried && tc::mbar_wait(&sh.s_ready[h & 1], (h >> 1) & 1);
+        tc::fence_after_sync();
+        if (edge) {  // this CTA's half of V: see the note at the top
+          const int v = e + (j < t.tiles - 1 ? 2 * j + 2 : 2 * j + 1);
+          w = w && tc::mbar_wait(&sh.full[v % C::kEntries], (v / C::kEntries) & 1);
+          if (w) {
+            uint8_t* vt = smem + C::kRing + (v % C::kEntries) * C::kEntry;
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < (int)C::kEntry / 16 / kSoftmaxThreads; ++i) {
+              const int x = tid + i * kSoftmaxThreads, r = (x >> 3) & 127;
+              uint4* at = reinterpret_cast<uint4*>(vt + (x >> 10) * 16384 + r * 128 + (x & 7) * 16);
+              if (key0 + r >= t.sight) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else {
+                uint4 y = *at;
+                const uint32_t a0 = __vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u),
+                               a1 = __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u),
+                               a2 = __vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u),
+                               a3 = __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u);
+                if (a0 | a1 | a2 | a3) {
+                  found = true;
+                  *at = make_uint4(y.x & ~a0, y.y & ~a1, y.z & ~a2, y.w & ~a3);
+                }
+              }
+            }
+            if (found) {
+              poison[rank] = (uint32_t)used + 1;
+              tc2::store_remote(r_poison + ((used & 1) * 2 + rank) * 4, (uint32_t)used + 1);
+            }
+          }
+        }
+        w = __all_sync(kFullMask, w);
+        float s[64];
+        tc2::tmem_ld64(tmem + lanes + (h & 1) * 128 + 64 * half, s);
+        const int left = lim - key0 - 64 * half;  // columns of this thread that the row sees
+        if (edge) {
+          const float none = down ? INFINITY : -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) s[i] = i < left ? s[i] : none;
+        }
+        float x;
+        if (!down) {
+          x = s[0];
+#pragma unroll
+          for (int i = 1; i < 64; ++i) x = fmaxf(x, s[i]);
+        } else {
+          x = s[0];
+#pragma unroll
+          for (int i = 1; i < 64; ++i) x = fminf(x, s[i]);
+        }
+        sh.red[h & 1][half][row] = x;
+        tc::fence_before_sync();
+        if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, w))) break;
+        tc::fence_after_sync();
+        const float y = sh.red[h & 1][half ^ 1][row];
+        x = down ? fminf(x, y) : fmaxf(x, y);
+        const bool any = x != (down ? INFINITY : -INFINITY);
+        const float top = any ? x * c : -INFINITY;
+        const float next = top > m + kSlack || m == -INFINITY ? top : m;
+        const bool grow = next != m;
+        if (j > 0 && __any_sync(kFullMask, grow)) {  // O holds the tiles before: rescale it
+          const bool v = __all_sync(kFullMask, tc::mbar_wait(&sh.o_ready[(h - 1) & 1], ((h - 1) >> 1) & 1));
+          tc::fence_after_sync();
+          const float f = m == -INFINITY ? 0.f : ex2(m - next);
+          if (v) {
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+              float ov[32];
+              const uint32_t at = tmem + lanes + C::kTmemO + half * (D / 2) + 32 * i;
+              tc::tmem_ld32(at, ov);
+              if (grow) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) ov[k] *= f;
+              }
+              tc::tmem_st32(at, ov);
+            }
+          }
+          carried = v;
+          if (grow) l *= f;
+        }
+        m = next;
+        const float ref = m == -INFINITY ? 0.f : m;
+        uint32_t pk[32];
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          float p0 = ex2(fmaf(s[i], c, -ref)), p1 = ex2(fmaf(s[i + 1], c, -ref));
+          float p2 = ex2(fmaf(s[i + 2], c, -ref)), p3 = ex2(fmaf(s[i + 3], c, -ref));
+          if (edge) {
+            p0 = i < left ? p0 : 0.f;
+            p1 = i + 1 < left ? p1 : 0.f;
+            p2 = i + 2 < left ? p2 : 0.f;
+            p3 = i + 3 < left ? p3 : 0.f;
+          }
+          l0 += p0;
+          l1 += p1;
+          l2 += p2;
+          l3 += p3;
+          pk[i / 2] = pack_bf16(p0, p1);
+          pk[i / 2 + 1] = pack_bf16(p2, p3);
+        }
+        l += (l0 + l1) + (l2 + l3);
+        tc2::tmem_st32(tmem + lanes + (h & 1) * 128 + 32 * half, pk);
+        if (edge) tc::fence_proxy_async();  // the edited V rows -> the tensor core
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc2::arrive_remote(r_p + (h & 1) * 8);
+      }
+      // ---- the pair's rows are through their keys
+      float total = 0.f;
+      if (t.tiles > 0) {
+        if (!ok) break;
+        if (lane == 0) tc2::arrive_remote(r_flags);
+        bool w = carried && tc2::wait(&sh.flags_in, used & 1);
+        const int h = g + t.tiles - 1;
+        w = w && tc::mbar_wait(&sh.o_ready[h & 1], (h >> 1) & 1);
+        tc::fence_after_sync();
+        float* lsum = &sh.red[(h + 1) & 1][0][0];  // last read before the last tile's barrier
+        lsum[half * 128 + row] = l;
+        if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, w))) break;
+        total = lsum[row] + lsum[128 + row];
+      }
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const bool dirty = t.tiles > 0 && (poison[0] == (uint32_t)used + 1 || poison[1] == (uint32_t)used + 1);
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) +
+                         (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D + half * (D / 2);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        float ov[32];
+        if (t.tiles > 0) {
+          tc::tmem_ld32(tmem + lanes + C::kTmemO + half * (D / 2) + 32 * i, ov);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) ov[k] = 0.f;
+        }
+        if (t.tiles > 0 && i == D / 64 - 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc2::arrive_remote(r_free);  // O may be overwritten
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) ov[k] *= inv;
+        if (dirty && real) {
+          const int first = max(0, whole) / kKeys * kKeys;  // first key of the tiles that were edited
+          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)t.kvh * D + half * (D / 2) + 32 * i;
+          for (int key = first; key < lim; ++key) {
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(vr + ((int64_t)t.k0 + key) * p.v_stride);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const uint32_t two = __ldg(src + k);
+              ov[2 * k] += poison_of(two & 0xffffu);
+              ov[2 * k + 1] += poison_of(two >> 16);
+            }
+          }
+        }
+        if (real) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(o + 32 * i + k) =
+                make_uint4(pack_bf16(ov[k], ov[k + 1]), pack_bf16(ov[k + 2], ov[k + 3]),
+                           pack_bf16(ov[k + 4], ov[k + 5]), pack_bf16(ov[k + 6], ov[k + 7]));
+        }
+      }
+      if (t.tiles > 0) {
+        e += 2 * t.tiles;
+        g += t.tiles;
+        ++used;
+      }
+    }
+  }
+  if (!ok) raise_error(p.err, kErrDeviceTimeout);
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // neither CTA's memory is in use by the other any more
+  tc::fence_after_sync();
+  if (warp == 0) tc2::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// [rows][heads][D] bf16, `stride` elements between rows; boxes of 64 dimensions
+// x box_heads x box_rows with the 128-byte swizzle
+bool encode(CUtensorMap* map, const void* base, int D, int64_t heads, int64_t rows, int64_t stride,
+            int box_heads, int box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const AttnPrefillArgs& a, int sms, cudaStream_t stream) {
+  using C = Cfg<D>;
+  const int G = a.h_q / a.h_kv, tok_cta = kRows / G;
+  // with no keys no tile of K or V is ever copied; the maps then describe q
+  const bool keys = a.total_k > 0;
+  CUtensorMap mq, mk, mv;
+  if (!encode(&mq, a.q, D, a.h_q, a.total_q, a.q_stride, G, tok_cta) ||
+      !encode(&mk, keys ? a.k : a.q, D, keys ? a.h_kv : 1, keys ? a.total_k : 1, keys ? a.k_stride : a.q_stride,
+              1, 64) ||
+      !encode(&mv, keys ? a.v : a.q, D, keys ? a.h_kv : 1, keys ? a.total_k : 1, keys ? a.v_stride : a.q_stride,
+              1, kKeys))
+    return cudaErrorInvalidValue;
+  const int smem = (int)(C::kShared + sizeof(Shared));
+  static_assert(C::kShared + sizeof(Shared) <= 227 * 1024, "shared memory");
+  static PerDeviceOnce attrs;
+  cudaError_t e = attrs.run([&] {
+    return cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (e != cudaSuccess) return e;
+  int64_t pairs = (a.total_q / (2 * tok_cta) + a.num_seqs) * a.h_kv;  // at least as many as tiles
+  if (pairs > sms / 2) pairs = sms / 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, mq, mk, mv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefill(const AttnPrefillArgs& a, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  return a.head_dim == 256 ? launch<256>(a, sms, stream) : launch<128>(a, sms, stream);
+}
+
+}  // namespace gdn

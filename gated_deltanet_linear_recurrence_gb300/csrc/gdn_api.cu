@@ -7,6 +7,7 @@
 #include <cstdlib>
 #include <mutex>
 
+#include "attn_params.h"
 #include "gdn.h"
 #include "params.h"
 
@@ -275,6 +276,10 @@ Route route_prefill(gdn_algo algo, int32_t num_seqs, int64_t total_tokens, int32
 
 }  // namespace
 
+namespace gdn {
+bool device_error_word(int** out) { return error_word(out) == GDN_OK; }
+}  // namespace gdn
+
 extern "C" {
 
 const char* gdn_status_string(gdn_status s) {
@@ -290,6 +295,7 @@ const char* gdn_status_string(gdn_status s) {
     case GDN_ERR_DEVICE_TIMEOUT: return "GDN_ERR_DEVICE_TIMEOUT";
     case GDN_ERR_CUDA: return "GDN_ERR_CUDA";
     case GDN_ERR_BAD_CACHE_LEN: return "GDN_ERR_BAD_CACHE_LEN";
+    case GDN_ERR_BAD_PAGE: return "GDN_ERR_BAD_PAGE";
   }
   return "GDN_ERR_UNKNOWN";
 }

@@ -67,7 +67,8 @@ typedef enum {
   GDN_ERR_WORKSPACE_TOO_SMALL = 7,
   GDN_ERR_DEVICE_TIMEOUT = 8,    /* device-detected: a bounded wait expired */
   GDN_ERR_CUDA = 9,              /* a CUDA runtime call failed */
-  GDN_ERR_BAD_CACHE_LEN = 10     /* device-detected: a cache_len outside 0 .. capacity */
+  GDN_ERR_BAD_CACHE_LEN = 10,    /* device-detected: a cache_len outside 0 .. capacity */
+  GDN_ERR_BAD_PAGE = 11          /* device-detected: a cached position without a page of the pool */
 } gdn_status;
 
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype; /* dtype of q, k, v and o */
@@ -421,10 +422,125 @@ int32_t gdn_attn_decode_block_keys(int32_t batch, int32_t h_q, int32_t h_kv, int
                                    int32_t block_keys);
 
 /*
+ * The paged key-value cache of the full-attention layers, and the operators on
+ * it: gdn_kv_append, gdn_kv_gather and gdn_attn_decode_paged, beside
+ * gdn_attn_prefill, which runs those layers' prompts.  Page "Optimizing
+ * on-device inference for Apple Silicon", section "Read the attention cache
+ * efficiently", reads one sequence's dense cache; here sequences of different
+ * lengths share one pool of pages, whose rows may be 8-bit.
+ *
+ * Layout.  k_pages and v_pages [num_pages][h_kv][page_size][head_dim], bf16 or
+ * e4m3; page_table [num_seqs][max_pages] int32 (device): position p of sequence
+ * n is slot p % page_size of page page_table[n][p / page_size].  Entries for
+ * positions that a call does not touch are never used (they may hold anything).
+ * page_size is a power of two from 8 to 1024; head_dim 128 or 256; max_pages x
+ * page_size at most 2^31 - 2048 and num_pages x h_kv x page_size below 2^32 - 1
+ * (else GDN_ERR_UNSUPPORTED_SHAPE).  A position whose page is missing (past the
+ * table, or an entry outside 0 .. num_pages - 1) sets GDN_ERR_BAD_PAGE in the
+ * error word; its row is not written, reads back as zeros, and takes no part in
+ * attention.
+ *
+ * 8-bit rows (GDN_CACHE_E4M3).  k_exp and v_exp [num_pages][h_kv][page_size]
+ * hold an exponent byte for each (token, KV head) row: the value of a code c is
+ * c x 2^(byte - 127).  gdn_kv_append picks the smallest power of two that brings
+ * the row's largest finite magnitude to 448 or less (never below 2^-126; 1 for a
+ * row of zeros) and rounds each quotient, which is exact, to the nearest e4m3
+ * (ties to even); a value that is not finite is stored as NaN.  With
+ * GDN_CACHE_BF16 rows are copied and k_exp, v_exp are not used (may be NULL).
+ */
+typedef enum { GDN_CACHE_BF16 = 1, GDN_CACHE_E4M3 = 2 } gdn_cache_dtype;
+
+/*
+ * gdn_kv_append — write the rows of packed new tokens into the cache.  Sequence
+ * n owns tokens cu_seqlens[n] .. cu_seqlens[n+1]-1 (conditions as for
+ * gdn_prefill; none for an empty sequence) and they go to its positions
+ * start_pos[n], start_pos[n] + 1, ...  k and v: [total_tokens][h_kv][head_dim]
+ * bf16 with k_stride and v_stride elements from a token to the next (a multiple
+ * of 8, at least h_kv x head_dim: a slice of a fused projection needs no copy).
+ * Sequences must not share the pages that a call writes.  cu_seqlens
+ * [num_seqs + 1], start_pos [num_seqs] int32 on the device.  Tensors 16-byte
+ * aligned (int32 arrays 4-byte).  The rows of a token that cu_seqlens gives to no
+ * sequence are not written (GDN_ERR_BAD_CU_SEQLENS in the error word).
+ */
+gdn_status gdn_kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                         void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
+                         const int32_t* page_table, const int32_t* cu_seqlens,
+                         const int32_t* start_pos, int32_t num_seqs, int64_t total_tokens,
+                         int32_t h_kv, int32_t head_dim, int32_t page_size, int32_t num_pages,
+                         int32_t max_pages, gdn_cache_dtype cache_dtype, gdn_stream_t stream);
+
+/*
+ * gdn_kv_gather — the inverse: k and v receive the cached rows of positions
+ * start_pos[n] .. of each sequence as packed bf16 rows (with e4m3 each value
+ * code x 2^(byte - 127), which bf16 holds exactly), for example for
+ * gdn_attn_prefill of a prompt piece over the pieces cached before it.
+ * Arguments as for gdn_kv_append.
+ */
+gdn_status gdn_kv_gather(void* k, void* v, int64_t k_stride, int64_t v_stride,
+                         const void* k_pages, const void* v_pages, const uint8_t* k_exp,
+                         const uint8_t* v_exp, const int32_t* page_table,
+                         const int32_t* cu_seqlens, const int32_t* start_pos, int32_t num_seqs,
+                         int64_t total_tokens, int32_t h_kv, int32_t head_dim, int32_t page_size,
+                         int32_t num_pages, int32_t max_pages, gdn_cache_dtype cache_dtype,
+                         gdn_stream_t stream);
+
+/*
+ * gdn_attn_decode_paged — gdn_attn_decode over the paged cache: one query of
+ * each of `batch` sequences over its cache_len[b] cached rows, same formula,
+ * head mapping (1 to 8 query heads per KV head) and result for an empty cache
+ * (o = 0).  q [batch][h_q][head_dim] bf16 with q_stride elements between
+ * sequences (a multiple of 8), o dense; cache_len [batch] int32 on the device,
+ * 0 <= cache_len[b] <= max_pages x page_size (a value outside sets
+ * GDN_ERR_BAD_CACHE_LEN and gives o = 0).  Slots at or past cache_len[b] are
+ * never read.  The rows of the whole batch are dealt evenly to the CTAs whatever
+ * the lengths; sequences that several CTAs share are joined through `workspace`
+ * (at least gdn_attn_decode_paged_workspace_size(...) bytes, 16-byte aligned, any
+ * contents; else GDN_ERR_NULL_POINTER or GDN_ERR_WORKSPACE_TOO_SMALL) in a fixed
+ * order: the result does not vary from run to run.
+ */
+gdn_status gdn_attn_decode_paged(const void* q, int64_t q_stride, const void* k_pages,
+                                 const void* v_pages, const uint8_t* k_exp, const uint8_t* v_exp,
+                                 const int32_t* page_table, const int32_t* cache_len, void* o,
+                                 int32_t batch, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                                 int32_t page_size, int32_t num_pages, int32_t max_pages,
+                                 gdn_cache_dtype cache_dtype, float scale, void* workspace,
+                                 size_t workspace_bytes, gdn_stream_t stream);
+
+/* Workspace bytes for gdn_attn_decode_paged with these heads (it does not depend
+ * on the batch or the cache); 0 for invalid arguments. */
+size_t gdn_attn_decode_paged_workspace_size(int32_t h_q, int32_t h_kv, int32_t head_dim);
+
+/*
+ * gdn_attn_prefill — causal grouped-query attention over packed prompts (the
+ * prompt side of the layers gdn_attn_decode serves).  Sequence n has the a =
+ * cu_seqlens_q[n+1] - cu_seqlens_q[n] queries and b = cu_seqlens_k[n+1] -
+ * cu_seqlens_k[n] keys that the two offset arrays give it; its queries are the
+ * last a of its b positions (a = b for a whole prompt; b > a for a piece over
+ * earlier rows), so query i sees the keys 0 .. i + b - a:
+ *     s_ij = scale * (q_i . k_j),   o_i = sum_j softmax(s_i)_j v_j
+ * and o_i = 0 for a query that sees no key (b < a).  Keys and values that a
+ * query does not see have no effect on it, whatever they hold (NaN included).
+ *
+ * q [total_q][h_q][head_dim], k and v [total_k][h_kv][head_dim], all GDN_BF16
+ * (else GDN_ERR_UNSUPPORTED_DTYPE), with q_stride, k_stride, v_stride elements
+ * from a token to the next (multiples of 8; slices of a fused projection need no
+ * copy); o [total_q][h_q][head_dim] dense.  Query head h reads KV head
+ * h / (h_q / h_kv); 1 to 8 query heads per KV head; head_dim 128 or 256.
+ * cu_seqlens_q and cu_seqlens_k: int32 device arrays of num_seqs + 1 entries
+ * under gdn_prefill's conditions; a sequence whose range is bad is skipped and
+ * GDN_ERR_BAD_CU_SEQLENS recorded.  No workspace.
+ */
+gdn_status gdn_attn_prefill(const void* q, const void* k, const void* v, void* o,
+                            const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                            int32_t num_seqs, int64_t total_q, int64_t total_k, int32_t h_q,
+                            int32_t h_kv, int32_t head_dim, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, gdn_dtype dtype, float scale, gdn_stream_t stream);
+
+/*
  * gdn_stream_status — synchronise `stream`, then report (and clear) the
  * current device's error word: GDN_OK, GDN_ERR_BAD_CU_SEQLENS,
- * GDN_ERR_BAD_CACHE_LEN, GDN_ERR_DEVICE_TIMEOUT, or GDN_ERR_CUDA if the
- * stream reported a CUDA error.
+ * GDN_ERR_BAD_CACHE_LEN, GDN_ERR_BAD_PAGE, GDN_ERR_DEVICE_TIMEOUT, or
+ * GDN_ERR_CUDA if the stream reported a CUDA error.
  */
 gdn_status gdn_stream_status(gdn_stream_t stream);
 
