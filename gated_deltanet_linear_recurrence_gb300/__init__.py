@@ -34,8 +34,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: building a Stream object costs microseconds a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -393,35 +393,50 @@ def _token_stride(t, name):
     """Elements between the tokens of t [T, heads, D]: the heads of a token lie side
     by side, the tokens may be apart (a slice of a fused projection)."""
     T, H, D = t.shape
-    if t.is_contiguous():
+    if t.is_contiguous() or T <= 1 and H == 1 and t.stride(2) == 1:
         return H * D
-    s = t.stride()
-    _require(s[2] == 1 and (H == 1 or s[1] == D), f"{name}: a token's heads must be contiguous")
-    return s[0] if T > 1 else H * D
+    step, head, one = t.stride()
+    if one != 1 or (H > 1 and head != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return step if T > 1 else H * D
 
 
 def _int32_on_gpu(t, shape, name):
-    _require(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.shape == shape,
-             f"{name} must be {list(shape)} int32 on the GPU, contiguous")
+    if not (t.dtype is torch.int32 and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name} must be {list(shape)} int32 on the GPU, contiguous")
+
+
+def _bf16_on_gpu(t, shape, name, dense=False):
+    if not (t.dtype is torch.bfloat16 and t.is_cuda and t.shape == shape
+            and (not dense or t.is_contiguous())):
+        raise ValueError(f"{name} must be {list(shape)} bfloat16 on the GPU"
+                         + (", contiguous" if dense else ""))
 
 
 def _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp):
-    """(num_pages, h_kv, page_size, D, max_pages, dtype code) of a paged cache."""
-    shape = k_pages.shape
-    _require(len(shape) == 4 and v_pages.shape == shape and v_pages.dtype == k_pages.dtype,
-             "k_pages / v_pages must be [num_pages, h_kv, page_size, D] of one dtype")
-    _require(k_pages.is_contiguous() and v_pages.is_contiguous() and k_pages.is_cuda
-             and v_pages.is_cuda, "pages must be contiguous, on the GPU")
-    if k_pages.dtype not in _CACHE_DTYPES:
-        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
-    if k_pages.dtype == torch.float8_e4m3fn:
-        for e in (k_exp, v_exp):
-            _require(e is not None and e.shape == shape[:3] and e.dtype == torch.uint8
-                     and e.is_contiguous() and e.is_cuda,
-                     "k_exp / v_exp must be [num_pages, h_kv, page_size] uint8 on the GPU")
-    _require(page_table.dim() == 2, "page_table must be [num_seqs, max_pages]")
-    _int32_on_gpu(page_table, page_table.shape, "page_table")
-    return (*shape, page_table.shape[1], _CACHE_DTYPES[k_pages.dtype])
+    """(num_pages, h_kv, page_size, D, N, max_pages, dtype code) of a paged cache."""
+    shape, dtype = k_pages.shape, k_pages.dtype
+    code = _CACHE_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {dtype}")
+    if not (len(shape) == 4 and v_pages.shape == shape and v_pages.dtype is dtype
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and k_pages.is_cuda
+            and v_pages.is_cuda):
+        raise ValueError("k_pages / v_pages must be [num_pages, h_kv, page_size, D] of one dtype "
+                         "on the GPU, contiguous")
+    if code == _lib.GDN_CACHE_E4M3:
+        rows = shape[:3]
+        if (k_exp is None or v_exp is None
+                or not (k_exp.shape == rows and v_exp.shape == rows and k_exp.is_cuda
+                        and v_exp.is_cuda and k_exp.dtype is torch.uint8
+                        and v_exp.dtype is torch.uint8 and k_exp.is_contiguous()
+                        and v_exp.is_contiguous())):
+            raise ValueError("k_exp / v_exp must be [num_pages, h_kv, page_size] uint8 on the "
+                             "GPU, contiguous")
+    if not (page_table.dim() == 2 and page_table.dtype is torch.int32 and page_table.is_cuda
+            and page_table.is_contiguous()):
+        raise ValueError("page_table must be [num_seqs, max_pages] int32 on the GPU, contiguous")
+    return (*shape, *page_table.shape, code)
 
 
 def _keep_for(stream, *tensors):
@@ -443,11 +458,10 @@ def gdn_kv_append(k, v, k_pages, v_pages, page_table, cu_seqlens, start_pos, k_e
     power of two, bias 127); page_table [N, max_pages], cu_seqlens [N+1], start_pos [N]
     int32 on the device.  k and v may be slices of a fused projection."""
     lib = _lib.load()
-    P, h_kv, page, D, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
-    N, T = page_table.shape[0], k.shape[0]
-    _require(k.shape == (T, h_kv, D) and v.shape == k.shape, "k / v must be [T, h_kv, D]")
-    _require(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.is_cuda and v.is_cuda,
-             "k / v must be bfloat16 on the GPU")
+    P, h_kv, page, D, N, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
+    T = k.shape[0]
+    _bf16_on_gpu(k, (T, h_kv, D), "k")
+    _bf16_on_gpu(v, (T, h_kv, D), "v")
     _int32_on_gpu(cu_seqlens, (N + 1,), "cu_seqlens")
     _int32_on_gpu(start_pos, (N,), "start_pos")
     st = lib.gdn_kv_append(k.data_ptr(), v.data_ptr(), _token_stride(k, "k"),
@@ -464,8 +478,8 @@ def gdn_kv_gather(k_pages, v_pages, page_table, cu_seqlens, start_pos, total_tok
     start_pos[n] .. of each sequence, cu_seqlens[n+1] - cu_seqlens[n] of them, total_tokens
     in all.  Returns (k, v) [total_tokens, h_kv, D]; arguments as for gdn_kv_append."""
     lib = _lib.load()
-    P, h_kv, page, D, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
-    N, T = page_table.shape[0], int(total_tokens)
+    P, h_kv, page, D, N, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
+    T = int(total_tokens)
     _int32_on_gpu(cu_seqlens, (N + 1,), "cu_seqlens")
     _int32_on_gpu(start_pos, (N,), "start_pos")
     made = []
@@ -473,9 +487,8 @@ def gdn_kv_gather(k_pages, v_pages, page_table, cu_seqlens, start_pos, total_tok
         made.append(k := torch.empty((T, h_kv, D), dtype=torch.bfloat16, device=k_pages.device))
     if v is None:
         made.append(v := torch.empty((T, h_kv, D), dtype=torch.bfloat16, device=k_pages.device))
-    _require(k.shape == (T, h_kv, D) and v.shape == k.shape and k.dtype == torch.bfloat16
-             and v.dtype == torch.bfloat16 and k.is_cuda and v.is_cuda,
-             "k / v must be [total_tokens, h_kv, D] bfloat16 on the GPU")
+    _bf16_on_gpu(k, (T, h_kv, D), "k")
+    _bf16_on_gpu(v, (T, h_kv, D), "v")
     st = lib.gdn_kv_gather(k.data_ptr(), v.data_ptr(), _token_stride(k, "k"),
                            _token_stride(v, "v"), k_pages.data_ptr(), v_pages.data_ptr(),
                            _ptr(k_exp), _ptr(v_exp), page_table.data_ptr(), cu_seqlens.data_ptr(),
@@ -498,17 +511,14 @@ def gdn_attn_decode_paged(q, k_pages, v_pages, page_table, cache_len, k_exp=None
     1/sqrt(D).  A workspace of gdn_attn_decode_paged_workspace_size() bytes is allocated
     when none is given.  Returns o [B, h_q, D] bf16."""
     lib = _lib.load()
-    P, h_kv, page, D, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
-    B, h_q, _ = q.shape
-    _require(q.shape[2] == D and q.dtype == torch.bfloat16 and q.is_cuda,
-             "q must be [B, h_q, D] bfloat16 on the GPU")
-    _require(page_table.shape[0] == B, "page_table must be [B, max_pages]")
+    P, h_kv, page, D, B, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
+    h_q = q.shape[1]
+    _bf16_on_gpu(q, (B, h_q, D), "q")
     _int32_on_gpu(cache_len, (B,), "cache_len")
     made = []
     if o is None:
         made.append(o := torch.empty((B, h_q, D), dtype=torch.bfloat16, device=q.device))
-    _require(o.shape == (B, h_q, D) and o.dtype == torch.bfloat16 and o.is_contiguous()
-             and o.is_cuda, "o must be [B, h_q, D] bfloat16, contiguous, on the GPU")
+    _bf16_on_gpu(o, (B, h_q, D), "o", dense=True)
     if workspace is None:
         need = lib.gdn_attn_decode_paged_workspace_size(h_q, h_kv, D)
         made.append(workspace := torch.empty(need, dtype=torch.uint8, device=q.device))
@@ -536,21 +546,19 @@ def gdn_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=Non
     Tq, h_q, D = q.shape
     Tk, h_kv, _ = k.shape
     N = cu_seqlens_q.numel() - 1
-    _require(k.shape[2] == D and v.shape == k.shape, "k / v must be [Tk, h_kv, D]")
-    _require(k.dtype == q.dtype and v.dtype == q.dtype, "q, k, v must share a dtype")
-    _require(q.is_cuda and k.is_cuda and v.is_cuda, "q, k, v must be on the GPU")
-    dt = _dtype_code(q)
+    _bf16_on_gpu(q, (Tq, h_q, D), "q")
+    _bf16_on_gpu(k, (Tk, h_kv, D), "k")
+    _bf16_on_gpu(v, (Tk, h_kv, D), "v")
     _int32_on_gpu(cu_seqlens_q, (N + 1,), "cu_seqlens_q")
     _int32_on_gpu(cu_seqlens_k, (N + 1,), "cu_seqlens_k")
     made = []
     if o is None:
         made.append(o := torch.empty((Tq, h_q, D), dtype=q.dtype, device=q.device))
-    _require(o.shape == (Tq, h_q, D) and o.dtype == q.dtype and o.is_contiguous() and o.is_cuda,
-             "o must be [Tq, h_q, D], contiguous, of q's dtype, on the GPU")
+    _bf16_on_gpu(o, (Tq, h_q, D), "o", dense=True)
     st = lib.gdn_attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                               cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), N, Tq, Tk, h_q,
                               h_kv, D, _token_stride(q, "q"), _token_stride(k, "k"),
-                              _token_stride(v, "v"), dt,
+                              _token_stride(v, "v"), _lib.GDN_BF16,
                               float(D ** -0.5 if scale is None else scale), _stream(stream))
     _lib.check(st, "gdn_attn_prefill")
     _keep_for(stream, *made)

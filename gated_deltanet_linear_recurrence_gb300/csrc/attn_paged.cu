@@ -163,6 +163,21 @@ __device__ __forceinline__ void count_units(const PagedAttnArgs& p, int upto, in
   *total = all;
 }
 
+// The units of CTA c: the first `more` CTAs have size + 1 of them, the others size
+// (CTAs beyond the number of units none).
+struct Shares {
+  int64_t size, more, split;
+  __device__ __forceinline__ Shares(int64_t total, int ctas) {
+    size = total / ctas;
+    more = total - size * ctas;
+    split = more * (size + 1);
+  }
+  __device__ __forceinline__ int64_t start(int c) const { return c * size + min((int64_t)c, more); }
+  __device__ __forceinline__ int owner(int64_t u) const {
+    return u < split ? (int)(u / (size + 1)) : (int)(more + (u - split) / size);
+  }
+};
+
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttnArgs p) {
   constexpr int kRowBytes = kFp8 ? D : 2 * D;
@@ -209,11 +224,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttn
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  const int64_t C = min((int64_t)gridDim.x, total);  // every CTA below C has a unit
-  if (blockIdx.x >= C) return;
-  int64_t u = total * blockIdx.x / C;
-  const int64_t u_end = total * (blockIdx.x + 1) / C;
-  const int64_t u_start = u;
+  const Shares sh(total, gridDim.x);
+  const int64_t u_start = sh.start(blockIdx.x), u_end = sh.start(blockIdx.x + 1);
+  if (u_start == u_end) return;
+  int64_t u = u_start;
   if (before <= u && u < before + mine) {
     int b = b_lo;
     for (;; ++b) {
@@ -571,15 +585,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
     for (int d = tid; d < D; d += kJoinThreads) o[d] = __float2bfloat16_rn(0.f);
     return;
   }
-  // CTA c has units total c / C .. total (c + 1) / C - 1: the ones holding first and end - 1
-  const int64_t C = min((int64_t)p.ctas, total);
-  const int c_lo = (int)((C * (first + 1) - 1) / total), c_hi = (int)((C * end - 1) / total);
+  const Shares sh(total, p.ctas);
+  const int c_lo = sh.owner(first), c_hi = sh.owner(end - 1);
   if (c_lo == c_hi) return;  // written by its CTA
   const int n = c_hi - c_lo + 1;
+  // the CTA with the first unit wrote slot 1, those that start inside it slot 0
   auto part = [&](int s) {
-    const int c = c_lo + s;
-    const int slot = total * c / C > first ? 0 : 1;
-    return p.partial + (((int64_t)c * 2 + slot) * G + h) * (D + 2);
+    return p.partial + (((int64_t)(c_lo + s) * 2 + (s == 0)) * G + h) * (D + 2);
   };
   float mx = -INFINITY;
   for (int s = tid; s < n; s += kJoinThreads) {

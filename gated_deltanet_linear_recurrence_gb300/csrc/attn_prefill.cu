@@ -28,8 +28,8 @@
 // warps work on tile j.
 //
 // Roles (11 warps): 0-7 softmax (two threads a row, 64 columns each), 8 TMA, 9
-// products (the even CTA's issues them for the pair; the odd CTA's relays its own
-// copies' arrival), 10 the schedule.  The pairs are persistent.
+// products (the even CTA's issues them for the pair), 10 the schedule.  The pairs
+// are persistent.
 //
 // Rounding: P is rounded to bf16 for the second product (relative 2^-9 a weight,
 // the same as the output's rounding; the sums l stay fp32 over unrounded weights).
@@ -59,7 +59,8 @@ namespace {
 constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = 256;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kScheduleWarp = 10;
 constexpr int kThreads = 352;
-constexpr int kConsumerWarps = 10;  // of a scheduled tile: all but the schedule's own
+// Warps that read a scheduled tile: all but the schedule's own and, in the odd CTA, the products'.
+__device__ __forceinline__ uint32_t tile_readers(uint32_t rank) { return rank == 0 ? 10 : 9; }
 constexpr int kKeys = 128;          // keys a tile
 constexpr int kRows = 128;          // rows a CTA
 constexpr uint32_t kBarSoftmax = 1;
@@ -87,8 +88,8 @@ struct Cfg {
 };
 
 struct Shared {  // beside the tiles
-  uint64_t full[10], pair_full[10], empty[10];
-  uint64_t q_full, q_pair_full, q_empty;
+  uint64_t full[10], empty[10];
+  uint64_t q_full, q_empty;
   uint64_t s_ready[2], p_ready[2], o_ready[2], o_free;
   uint64_t tile_full[2], tile_empty[2], flags_in, drained;
   Tile tile[2];
@@ -108,6 +109,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float poison_of(uint32_t bits16) {  // the value if it is not finite
   return (bits16 & 0x7f80u) == 0x7f80u ? __uint_as_float(bits16 << 16) : 0.f;
+}
+
+__device__ __forceinline__ float largest64(const float (&s)[64]) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = tc2::max3(s[i], s[8 + i], s[16 + i]);
+#pragma unroll
+  for (int k = 24; k < 56; k += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = tc2::max3(x[i], s[k + i], s[k + 8 + i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaxf(x[i], s[56 + i]);
+  return tc2::max3(tc2::max3(x[0], x[1], x[2]), tc2::max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+}
+__device__ __forceinline__ float least64(const float (&s)[64]) {
+  float x = s[0];
+#pragma unroll
+  for (int i = 1; i < 64; ++i) x = fminf(x, s[i]);
+  return x;
 }
 
 // ------------------------------------------------------------------ schedule
@@ -243,18 +263,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kEntries; ++i) {
       tc::mbar_init(&sh.full[i], 1);
-      tc::mbar_init(&sh.pair_full[i], 1);
       tc::mbar_init(&sh.empty[i], 1);
     }
     tc::mbar_init(&sh.q_full, 1);
-    tc::mbar_init(&sh.q_pair_full, 1);
     tc::mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sh.s_ready[i], 1);
       tc::mbar_init(&sh.p_ready[i], 2 * kSoftmaxWarps);
       tc::mbar_init(&sh.o_ready[i], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
-      tc::mbar_init(&sh.tile_empty[i], kConsumerWarps);
+      tc::mbar_init(&sh.tile_empty[i], tile_readers(rank));
       sh.poison[i][0] = sh.poison[i][1] = 0;
     }
     tc::mbar_init(&sh.o_free, 2 * kSoftmaxWarps);
@@ -310,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ copies
     Tile t;
     int e = 0, used = 0;  // ring entries issued; tiles with Q
+    const uint32_t r_full = tc2::in_cta(sh.full, 0), r_q = tc2::in_cta(&sh.q_full, 0);
     if (lane == 0) {
       tc::prefetch_tmap(&tm_q);
       tc::prefetch_tmap(&tm_k);
@@ -318,34 +337,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int pass = 0; next_tile(pass, &t); ++pass) {
       if (t.tiles == 0) continue;
       if (lane == 0) {
+        const int whole = t.off + t.tok0 + 1;
         if (used > 0) ok = tc::mbar_wait(&sh.q_empty, (used - 1) & 1);
         if (ok) {
-          tc::mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tok_cta * G) * D * 2);
+          if (rank == 0) tc::mbar_arrive_expect_tx(&sh.q_full, 2u * (uint32_t)(tok_cta * G) * D * 2);
           for (int kb = 0; kb < D / 64; ++kb)
-            tc::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G,
-                            t.q0 + t.tok0 + (int)rank * tok_cta, &sh.q_full);
+            tc2::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G,
+                             t.q0 + t.tok0 + (int)rank * tok_cta, r_q);
         }
-        auto slot = [&]() -> uint8_t* {  // the next ring entry, empty and armed
+        // The next ring entry, when it is empty.  The bytes of both CTAs count on
+        // the even CTA's barrier; those of V in an edge tile on the CTA's own, for
+        // the softmax warps that edit them there (whose arrival on p_ready then
+        // stands for the odd CTA's V).  The odd CTA's barrier keeps step.
+        auto slot = [&](bool here) -> uint8_t* {
           const int s = e % C::kEntries;
           if (e >= C::kEntries) ok = ok && tc::mbar_wait(&sh.empty[s], ((e / C::kEntries) - 1) & 1);
           if (!ok) return nullptr;
-          tc::mbar_arrive_expect_tx(&sh.full[s], C::kEntry);
+          if (here || rank == 0) tc::mbar_arrive_expect_tx(&sh.full[s], here ? C::kEntry : 2 * C::kEntry);
+          else tc::mbar_arrive(&sh.full[s]);
           return smem + C::kRing + s * C::kEntry;
         };
         for (int j = 0; j <= t.tiles && ok; ++j) {
           if (j < t.tiles) {
-            if (uint8_t* dst = slot()) {
+            if (uint8_t* dst = slot(false)) {
               for (int kb = 0; kb < D / 64; ++kb)
-                tc::tma_load_3d(dst + kb * 8192, &tm_k, 64 * kb, t.kvh,
-                                t.k0 + j * kKeys + (int)rank * 64, &sh.full[e % C::kEntries]);
+                tc2::tma_load_3d(dst + kb * 8192, &tm_k, 64 * kb, t.kvh,
+                                 t.k0 + j * kKeys + (int)rank * 64, r_full + (e % C::kEntries) * 8);
               ++e;
             }
           }
           if (j > 0) {
-            if (uint8_t* dst = slot()) {
+            const bool edge = j * kKeys > whole;  // of key tile j - 1
+            if (uint8_t* dst = slot(edge)) {
+              const uint32_t bar = (edge ? tc2::in_cta(sh.full, rank) : r_full) + (e % C::kEntries) * 8;
               for (int kb = 0; kb < D / 128; ++kb)
-                tc::tma_load_3d(dst + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
-                                t.k0 + (j - 1) * kKeys, &sh.full[e % C::kEntries]);
+                tc2::tma_load_3d(dst + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
+                                 t.k0 + (j - 1) * kKeys, bar);
               ++e;
             }
           }
@@ -355,11 +382,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(kFullMask, ok);
       if (!ok) break;
     }
-    // copies still in flight land before the CTA ends (already so unless a wait expired)
+    // Copies still in flight land before the CTA ends: after an expired wait, the
+    // even CTA's barriers tell of both CTAs' copies (the odd one's own, of edge tiles).
     if (lane == 0) {
       for (int j = max(0, e - C::kEntries); j < e; ++j)
         if (!tc::mbar_wait(&sh.full[j % C::kEntries], (j / C::kEntries) & 1)) ok = false;
-      if (used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
+      if (rank == 0 && used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
@@ -372,37 +400,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dv = tc::smem_desc(sbase + C::kRing, 16384, 1024, tc::kLayoutSw128);
     const bool leader = tc::elect_one();
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool w = tc2::wait(bar, parity);
+      const bool w = tc::mbar_wait(bar, parity);
       tc::fence_after_sync();
       return __all_sync(kFullMask, w) != 0;
     };
-    const uint32_t r_full = tc2::in_cta(sh.pair_full, 0), r_q = tc2::in_cta(&sh.q_pair_full, 0);
-    auto entry = [&]() {  // the next ring entry has landed in both CTAs (odd CTA: passes that on)
-      const int s = e % C::kEntries;
-      const uint32_t ph = (e / C::kEntries) & 1;
-      bool w = warp_wait(&sh.full[s], ph);
-      if (rank == 0) {
-        w = w && warp_wait(&sh.pair_full[s], ph);
-      } else if (w && leader) {
-        tc::fence_proxy_async();
-        tc2::arrive_remote(r_full + s * 8);
-      }
-      return w;
-    };
-    for (int pass = 0; next_tile(pass, &t); ++pass) {
+    auto entry = [&]() { return warp_wait(&sh.full[e % C::kEntries], (e / C::kEntries) & 1); };
+    // the even CTA's warp issues for the pair
+    for (int pass = 0; rank == 0 && next_tile(pass, &t); ++pass) {
       if (t.tiles == 0) continue;
       ok = warp_wait(&sh.q_full, used & 1);
-      if (rank == 0) {
-        ok = ok && warp_wait(&sh.q_pair_full, used & 1);
-      } else if (ok && leader) {
-        tc::fence_proxy_async();
-        tc2::arrive_remote(r_q);
-      }
+      const int whole = t.off + t.tok0 + 1;
       for (int j = 0; j <= t.tiles && ok; ++j) {
         if (j < t.tiles) {  // S = Q K^T of key tile j
           if (!(ok = entry())) break;
           const int s = e % C::kEntries;
-          if (rank == 0 && leader) {
+          if (leader) {
             const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
 #pragma unroll
             for (int kk = 0; kk < C::kSteps; ++kk)
@@ -419,18 +431,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int h = g + j - 1;
           if (!(ok = entry())) break;
           const int s = e % C::kEntries;
-          if (rank == 0) {
-            if (!(ok = warp_wait(&sh.p_ready[h & 1], (h >> 1) & 1))) break;
-            if (j == 1 && used > 0 && !(ok = warp_wait(&sh.o_free, (used - 1) & 1))) break;
-            if (leader) {
-              const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
+          // an edge tile's V was edited in both CTAs (ordinary writes): acquire those
+          const bool edge = j * kKeys > whole;
+          bool w = edge ? tc2::wait(&sh.p_ready[h & 1], (h >> 1) & 1) : tc::mbar_wait(&sh.p_ready[h & 1], (h >> 1) & 1);
+          if (j == 1 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
+          tc::fence_after_sync();
+          if (!(ok = __all_sync(kFullMask, w) != 0)) break;
+          if (leader) {
+            const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
 #pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc2::mma_ts(tmem + C::kTmemO, tmem + (h & 1) * 128 + 8 * kk, dv + so + ((kk * 2048) >> 4),
-                            idesc_o, (j > 1) || (kk > 0));
-              tc2::commit(&sh.o_ready[h & 1]);
-              tc2::commit(&sh.empty[s]);
-            }
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              tc2::mma_ts(tmem + C::kTmemO, tmem + (h & 1) * 128 + 8 * kk, dv + so + ((kk * 2048) >> 4),
+                          idesc_o, (j > 1) || (kk > 0));
+            tc2::commit(&sh.o_ready[h & 1]);
+            tc2::commit(&sh.empty[s]);
           }
           __syncwarp();
           ++e;
@@ -440,12 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       g += t.tiles;
       ++used;
     }
-    // every product issued has completed before TMEM is released
+    // every product issued has completed before either CTA leaves the barrier at the end
     if (rank == 0) {
       if (leader) tc2::commit(&sh.drained);
       __syncwarp();
+      if (!warp_wait(&sh.drained, 0)) ok = false;
     }
-    if (!warp_wait(&sh.drained, 0)) ok = false;
   } else {
     // ------------------------------------------------------------ softmax
     Tile t;
@@ -511,16 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i] = i < left ? s[i] : none;
         }
-        float x;
-        if (!down) {
-          x = s[0];
-#pragma unroll
-          for (int i = 1; i < 64; ++i) x = fmaxf(x, s[i]);
-        } else {
-          x = s[0];
-#pragma unroll
-          for (int i = 1; i < 64; ++i) x = fminf(x, s[i]);
-        }
+        float x = down ? least64(s) : largest64(s);
         sh.red[h & 1][half][row] = x;
         tc::fence_before_sync();
         if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, w))) break;
@@ -554,30 +559,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = next;
         const float ref = m == -INFINITY ? 0.f : m;
         uint32_t pk[32];
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+        const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
-          float p0 = ex2(fmaf(s[i], c, -ref)), p1 = ex2(fmaf(s[i + 1], c, -ref));
-          float p2 = ex2(fmaf(s[i + 2], c, -ref)), p3 = ex2(fmaf(s[i + 3], c, -ref));
+          float2 p0 = tc2::fma2(make_float2(s[i], s[i + 1]), c2, r2);
+          float2 p1 = tc2::fma2(make_float2(s[i + 2], s[i + 3]), c2, r2);
+          p0 = make_float2(ex2(p0.x), ex2(p0.y));
+          p1 = make_float2(ex2(p1.x), ex2(p1.y));
           if (edge) {
-            p0 = i < left ? p0 : 0.f;
-            p1 = i + 1 < left ? p1 : 0.f;
-            p2 = i + 2 < left ? p2 : 0.f;
-            p3 = i + 3 < left ? p3 : 0.f;
+            p0.x = i < left ? p0.x : 0.f;
+            p0.y = i + 1 < left ? p0.y : 0.f;
+            p1.x = i + 2 < left ? p1.x : 0.f;
+            p1.y = i + 3 < left ? p1.y : 0.f;
           }
-          l0 += p0;
-          l1 += p1;
-          l2 += p2;
-          l3 += p3;
-          pk[i / 2] = pack_bf16(p0, p1);
-          pk[i / 2 + 1] = pack_bf16(p2, p3);
+          l0 = tc2::add2(l0, p0);
+          l1 = tc2::add2(l1, p1);
+          pk[i / 2] = pack_bf16(p0.x, p0.y);
+          pk[i / 2 + 1] = pack_bf16(p1.x, p1.y);
         }
-        l += (l0 + l1) + (l2 + l3);
+        l0 = tc2::add2(l0, l1);
+        l += l0.x + l0.y;
         tc2::tmem_st32(tmem + lanes + (h & 1) * 128 + 32 * half, pk);
-        if (edge) tc::fence_proxy_async();  // the edited V rows -> the tensor core
         tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc2::arrive_remote(r_p + (h & 1) * 8);
+        if (edge) {
+          tc::fence_proxy_async();  // the edited V rows -> the tensor core
+          __syncwarp();
+          if (lane == 0) tc2::arrive_remote(r_p + (h & 1) * 8);
+        } else {
+          __syncwarp();
+          if (lane == 0) tc2::arrive_remote_relaxed(r_p + (h & 1) * 8);
+        }
       }
       // ---- the pair's rows are through their keys
       float total = 0.f;
@@ -609,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t.tiles > 0 && i == D / 64 - 1) {
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc2::arrive_remote(r_free);  // O may be overwritten
+          if (lane == 0) tc2::arrive_remote_relaxed(r_free);  // O may be overwritten
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) ov[k] *= inv;

@@ -55,6 +55,17 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
+// 3-D tiled load into this CTA's shared memory whose bytes are counted on `bar`,
+// a barrier of either CTA of the pair (address from in_cta).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                            int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
 // Shared-memory address of `p`'s place in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
   uint32_t r;
@@ -63,6 +74,12 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
 }
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same without ordering this thread's ordinary memory writes (a release for
+// the whole cluster waits for them, about 500 cycles): for hand-offs of TMEM,
+// which tcgen05.wait and tcgen05.fence order.
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void store_remote(uint32_t addr, uint32_t value) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(value) : "memory");
@@ -85,6 +102,28 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     if (t0 == 0) t0 = t;
     if (t - t0 > 1000000000ull) return false;
   }
+}
+
+// Pairs of fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return reinterpret_cast<const float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return reinterpret_cast<const float2&>(d);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // 64 columns of the thread's TMEM lane; waits for completion.
