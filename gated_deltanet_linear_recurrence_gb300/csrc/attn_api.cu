@@ -66,6 +66,8 @@ gdn_status check_pages(const gdn::PagedCache& c) {
   if (any && c.dtype == GDN_CACHE_E4M3 && (!c.k_exp || !c.v_exp)) return GDN_ERR_NULL_POINTER;
   if (!aligned(c.k_pages, 16) || !aligned(c.v_pages, 16) || !aligned(c.table, 4))
     return GDN_ERR_MISALIGNED;
+  if (c.dtype == GDN_CACHE_E4M3 && (!aligned(c.k_exp, 8) || !aligned(c.v_exp, 8)))
+    return GDN_ERR_MISALIGNED;
   return GDN_OK;
 }
 

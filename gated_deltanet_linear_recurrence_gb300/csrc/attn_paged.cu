@@ -30,6 +30,8 @@
 // With an e4m3 cache a key's unit 2^ke scales its score, and a value's unit 2^ve
 // joins the exponent, 2^(t_i + ve_i - m') with m' = max_i (t_i + ve_i), so that
 // the f16 weights use their range whatever the units are; l keeps its own m.
+// (Products of e4m3 operands themselves, with q and P as sums of e4m3 parts,
+// measured slower: at warp level they run as f16 products after a widening.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -47,12 +49,24 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = 64;  // rows in a unit of work: one 16-row tile for each warp
-constexpr int kTileRows = 16;
 constexpr int kHeads = 8;  // query heads of a KV head, padded (N of the products)
-constexpr uint32_t kRing = 24576;  // bytes of a warp's ring: two CTAs fit on an SM
-constexpr int kTileSlots = 8;      // tiles whose row validity and units are kept
+constexpr int kSlots = 4;          // tiles whose row counts and units are kept
+
+// CTAs on an SM, as registers allow (O and Q of a warp: 6 or 3 KB), bytes of a
+// warp's ring, and rows of its tile.
+__host__ __device__ constexpr int ctas_per_sm(int D, bool fp8) { return D == 128 ? 4 : 2; }
+__host__ __device__ constexpr uint32_t ring_bytes(int D, bool fp8) { return D == 128 ? 12288 : 24576; }
+__host__ __device__ constexpr int tile_rows(int D, bool fp8) { return fp8 ? 32 : 16; }
+// Rows of a unit of work: a tile for each warp.
+__host__ __device__ constexpr int unit_rows(int D, bool fp8) { return kWarps * tile_rows(D, fp8); }
+
+struct TileInfo {     // of a tile on its way through a warp's ring
+  uint32_t rows;      // rows to use in each group of eight, a byte a group
+  uint32_t pad;
+  uint8_t k_unit[32], v_unit[32];  // exponent bytes
+};
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;  // log2 of the largest weight before a reference moves
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -89,28 +103,33 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-template <bool kF16>
-__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                      uint32_t a3, uint32_t b0, uint32_t b1) {
-  if (kF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two e4m3 codes (the low 16 bits) widened to f16
-__device__ __forceinline__ uint32_t widen(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// four e4m3 codes widened to two pairs of f16 (exact)
+__device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// an exponent byte as the unit itself, and as the exponent
+__device__ __forceinline__ float unit_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+__device__ __forceinline__ float exponent_of(uint32_t byte) {
+  return __uint_as_float(0x4b000000u | byte) - (8388608.f + 127.f);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -128,18 +147,23 @@ __device__ __forceinline__ int length_of(const PagedAttnArgs& p, int b) {
   const int len = __ldg(p.cache_len + b);
   return (len < 0 || (int64_t)len > ((int64_t)p.cache.max_pages << p.cache.page_shift)) ? 0 : len;
 }
-__device__ __forceinline__ int64_t units_of(const PagedAttnArgs& p, int len) {
-  return (int64_t)p.cache.h_kv * ((len + (int64_t)kUnit - 1) / kUnit);
+// Work of one (sequence, KV head): its units, and kPieceCost more for taking it up
+// (q and the first rows arrive, the warps join), so that a CTA with many short
+// sequences is not given more than it can do in the same time.
+constexpr int kPieceCost = 2;
+template <int kUnit>
+__device__ __forceinline__ int64_t span_of(int len) {
+  return len > 0 ? kPieceCost + (uint32_t)(len + kUnit - 1) / kUnit : 0;
 }
 
-// Units of the sequences before `upto`, and of the whole batch, on every thread.
-template <int kT>
-__device__ __forceinline__ void count_units(const PagedAttnArgs& p, int upto, int64_t* before,
+// Work of the sequences before `upto`, and of the whole batch, on every thread.
+template <int kT, int kUnit>
+__device__ __forceinline__ void count_work(const PagedAttnArgs& p, int upto, int64_t* before,
                                             int64_t* total) {
   __shared__ int64_t sums[2][kT / 32];
   int64_t s = 0, all = 0;
   for (int b = threadIdx.x; b < p.batch; b += kT) {
-    const int64_t u = units_of(p, length_of(p, b));
+    const int64_t u = p.cache.h_kv * span_of<kUnit>(length_of(p, b));
     all += u;
     if (b < upto) s += u;
   }
@@ -163,8 +187,7 @@ __device__ __forceinline__ void count_units(const PagedAttnArgs& p, int upto, in
   *total = all;
 }
 
-// The units of CTA c: the first `more` CTAs have size + 1 of them, the others size
-// (CTAs beyond the number of units none).
+// The work of CTA c: the first `more` CTAs have size + 1 of it, the others size.
 struct Shares {
   int64_t size, more, split;
   __device__ __forceinline__ Shares(int64_t total, int ctas) {
@@ -179,27 +202,30 @@ struct Shares {
 };
 
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttnArgs p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_kernel(const PagedAttnArgs p) {
   constexpr int kRowBytes = kFp8 ? D : 2 * D;
-  constexpr uint32_t kEntry = kTileRows * kRowBytes;  // K or V of a tile
+  constexpr uint32_t kRing = ring_bytes(D, kFp8);
+  constexpr int kRows = tile_rows(D, kFp8), kUnit = unit_rows(D, kFp8);
+  constexpr int kM = kRows / 16;              // row blocks of the products
+  constexpr int kGroups = kRows / 8;          // groups of rows within a page
+  constexpr uint32_t kEntry = kRows * kRowBytes;  // K or V of a tile
   constexpr int kEntries = kRing / kEntry;
   constexpr int kRowLanes = kRowBytes / 16;   // lanes copying a row
   constexpr int kRowsAtOnce = 32 / kRowLanes;
   constexpr int kQ = D / 16;                  // k-steps of S
-  constexpr int kPad = D + 4;                 // floats between heads in the warps' join
-  static_assert(kEntries >= 3 && kEntries / 2 + 1 < kTileSlots, "ring");
-  static_assert(kHeads * kPad * 4 <= kRing, "join buffer");
+  constexpr int kChunk = D / 4, kPad = kChunk + 4;  // dims the warps join at once
+  static_assert(kEntries >= 3 && kEntries <= 6, "ring");
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint8_t row_unit[kWarps][kTileSlots][32];  // exponent bytes: 16 keys, 16 values
-  __shared__ uint32_t row_ok[kWarps][kTileSlots];       // rows of a tile that hold a key
+  __shared__ __align__(8) TileInfo infos[kWarps][kSlots];
   __shared__ float wm[kWarps][kHeads], wv[kWarps][kHeads], wl[kWarps][kHeads];
+  __shared__ __align__(16) float joined[kWarps][kHeads][kPad];
   __shared__ int64_t at_units;
   __shared__ int at_seq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   tc::wait_prerequisites();  // q, the cache, its table and lengths come from earlier kernels
   tc::allow_dependents();    // the joining pass may be scheduled; it reads only the lengths early
 
-  // ---- this CTA's units
+  // ---- this CTA's share
   const int G = p.h_q / p.cache.h_kv;
   const int per = (p.batch + kThreads - 1) / kThreads;  // sequences a thread counts
   const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
@@ -207,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttn
   for (int b = b_lo; b < b_hi; ++b) {
     const int len = length_of(p, b);
     if (blockIdx.x == 0 && len != __ldg(p.cache_len + b)) raise_error(p.err, kErrBadCacheLen);
-    mine += units_of(p, len);
+    mine += p.cache.h_kv * span_of<kUnit>(len);
   }
   __shared__ int64_t scan[kWarps];
   int64_t incl = mine;
@@ -231,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttn
   if (before <= u && u < before + mine) {
     int b = b_lo;
     for (;; ++b) {
-      const int64_t n = units_of(p, length_of(p, b));
+      const int64_t n = p.cache.h_kv * span_of<kUnit>(length_of(p, b));
       if (u < before + n) break;
       before += n;
     }
@@ -244,28 +270,128 @@ __global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttn
 
   const uint32_t ring = tc::smem_u32(smem) + warp * kRing;
   const int quad = lane >> 2, pair = lane & 3;  // fragment row, and column pair
-  const uint32_t swz_k = lane & 7, swz_v = lane & 7;
+  const uint32_t swz = lane & 7;
   const float score_unit = p.scale * kLog2e;
 
-  while (u < u_end) {
-    int len = length_of(p, b);
-    while (u >= base + units_of(p, len)) {
-      base += units_of(p, len);
-      len = length_of(p, ++b);
+  // ---- pieces: this CTA's part of one (sequence, KV head) after the other
+  int len = length_of(p, b);
+  int j = 0, k_lo = 0, k_hi = 0;
+  bool from_start = false, whole = false;  // has the first unit; has all of them
+  int seq = 0;
+  auto next_piece = [&]() {
+    while (u < u_end) {
+      const int64_t span = span_of<kUnit>(len);
+      if (u >= base + p.cache.h_kv * span) {
+        base += p.cache.h_kv * span;
+        len = length_of(p, ++b);
+        continue;
+      }
+      j = (int)((u - base) / span);
+      const int64_t r0 = u - base - j * span, r1 = min(span, r0 + (u_end - u));
+      u += r1 - r0;
+      if (r1 <= kPieceCost) continue;
+      const int64_t c0 = max((int64_t)0, r0 - kPieceCost), c1 = r1 - kPieceCost;
+      k_lo = (int)(c0 * kUnit);
+      k_hi = (int)min((int64_t)len, c1 * kUnit);
+      from_start = c0 == 0;
+      whole = from_start && r1 == span;
+      seq = b;
+      return true;
     }
-    const int64_t tiles = (len + kUnit - 1) / kUnit;  // units of one KV head
-    const int j = (int)((u - base) / tiles);
-    const int64_t c0 = (u - base) % tiles;
-    const int64_t c1 = min(tiles, c0 + (u_end - u));
-    const int k_lo = (int)(c0 * kUnit), k_hi = (int)min((int64_t)len, c1 * kUnit);
-    const int64_t head0 = (int64_t)b * p.h_q + (int64_t)j * G;
-    const int32_t* table = p.cache.table + (int64_t)b * p.cache.max_pages;
+    return false;
+  };
 
+  // ---- the warp's tiles: rows k_lo + kRows (warp + kWarps i) ..
+  // Tiles start at multiples of 16 rows, so eight rows lie side by side in a page:
+  // lane x looks up and keeps group x of the tile being copied.
+  int count = 0, first_key = 0;
+  const int32_t* table = nullptr;
+  TileInfo* info = infos[warp];
+  auto page_of = [&](int i) {
+    const int key = first_key + kRows * kWarps * i;
+    return (i < count && key < k_hi) ? __ldg(table + (key >> p.cache.page_shift)) : -1;
+  };
+  int next_page = -1;
+  uint32_t row = 0;  // first cached row of the lane's group
+  int valid = 0;     // rows of the group that hold keys
+  uint2 ku = make_uint2(0, 0), vu = ku;  // its exponent bytes, on their way to info
+  uint32_t put = 0;  // ring entry to fill
+  auto copy = [&](const void* pages) {
+    const uint32_t dst = ring + put * kEntry + (lane / kRowLanes) * kRowBytes;
+    const int c = lane % kRowLanes, sub = lane / kRowLanes;
+    const uint8_t* base = static_cast<const uint8_t*>(pages) + 16 * c + sub * kRowBytes;
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) {
+      const uint32_t from = __shfl_sync(kFullMask, row, x);
+      const int n = __shfl_sync(kFullMask, valid, x);
+      const uint8_t* src = base + (size_t)from * kRowBytes;
+#pragma unroll
+      for (int s = 0; s < 8 / kRowsAtOnce; ++s) {
+        const int r = s * kRowsAtOnce + sub;  // row of the group
+        copy16(dst + (8 * x + s * kRowsAtOnce) * kRowBytes + ((c ^ r) << 4), src + s * kRowsAtOnce * kRowBytes,
+               r < n);
+      }
+    }
+  };
+  auto issue_k = [&](int i) {  // a commit group even when no tile is left
+    if (kFp8 && i > 0 && i <= count && lane < kGroups) {
+      TileInfo& t = info[(i - 1) % kSlots];
+      *reinterpret_cast<uint2*>(t.k_unit + 8 * lane) = ku;
+      *reinterpret_cast<uint2*>(t.v_unit + 8 * lane) = vu;
+    }
+    if (i < count) {
+      const int key = first_key + kRows * kWarps * i;
+      const int page = next_page;
+      const bool ok = page >= 0 && page < p.cache.num_pages;
+      valid = min(8, max(0, k_hi - key));
+      if (valid > 0 && !ok) {
+        raise_error(p.err, kErrBadPage);
+        valid = 0;
+      }
+      row = valid > 0 ? (((uint32_t)page * p.cache.h_kv + j) << p.cache.page_shift) +
+                            (key & ((1 << p.cache.page_shift) - 1))
+                      : 0u;
+      if (lane < kGroups) reinterpret_cast<uint8_t*>(&info[i % kSlots].rows)[lane] = (uint8_t)valid;
+      if (kFp8 && valid > 0 && lane < kGroups) {
+        ku = __ldg(reinterpret_cast<const uint2*>(p.cache.k_exp + row));
+        vu = __ldg(reinterpret_cast<const uint2*>(p.cache.v_exp + row));
+      }
+      next_page = page_of(i + 1);
+      copy(p.cache.k_pages);
+      if (++put == kEntries) put = 0;
+    }
+    copy_commit();
+  };
+  auto issue_v = [&](int i) {
+    if (i < count) {
+      copy(p.cache.v_pages);
+      if (++put == kEntries) put = 0;
+    }
+    copy_commit();
+  };
+  auto open = [&]() {  // the piece's first copies
+    const int n_tiles = (k_hi - k_lo + kRows - 1) / kRows;
+    count = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
+    first_key = k_lo + kRows * warp + 8 * (lane & (kGroups - 1));
+    table = p.cache.table + (int64_t)seq * p.cache.max_pages;
+    next_page = page_of(0);
+#pragma unroll
+    for (int e = 0; e < kEntries - 1; ++e) {
+      if (e & 1) issue_v(e >> 1);
+      else issue_k(e >> 1);
+    }
+  };
+
+  uint32_t get = 0;  // ring entry to use
+  bool more = next_piece();
+  if (more) open();
+  while (more) {
+    const int64_t head0 = (int64_t)seq * p.h_q + (int64_t)j * G;
     // ---- Q^T as the products' B operand: head `quad`, zeros past G
     uint32_t qf[kQ][2];
     float unit0 = score_unit, unit1 = score_unit;  // of heads 2 pair, 2 pair + 1
     {
-      const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)b * p.q_stride +
+      const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)seq * p.q_stride +
                                   ((int64_t)j * G + quad) * D;
       if (!kFp8) {
 #pragma unroll
@@ -290,150 +416,146 @@ __global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttn
         }
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-        const int e = min(max((int)((__float_as_uint(top) >> 23) & 0xff), 16), 240) - 127 - 14;
-        const float inv = pow2(-e);
+        const int e = min(max((int)(__float_as_uint(top) >> 23), 16), 240) - 127 - 14;
+        const float inv = pow2(-e), unit = pow2(e);
 #pragma unroll
         for (int kk = 0; kk < kQ; ++kk)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
             qf[kk][r] = pack_f16(__uint_as_float(qf[kk][r] << 16) * inv,
                                  __uint_as_float(qf[kk][r] & 0xffff0000u) * inv);
-        unit0 *= __shfl_sync(kFullMask, pow2(e), 8 * pair);
-        unit1 *= __shfl_sync(kFullMask, pow2(e), 8 * pair + 4);
+        unit0 *= __shfl_sync(kFullMask, unit, 8 * pair);
+        unit1 *= __shfl_sync(kFullMask, unit, 8 * pair + 4);
       }
     }
-
-    // ---- the warp's tiles: rows k_lo + 16 (warp + kWarps i) ..
-    const int n_tiles = (k_hi - k_lo + kTileRows - 1) / kTileRows;
-    const int count = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
-    const int last = count * 2;  // ring entries: K, V, K, V, ...
-    const int my_row = lane & 15;
-    auto page_of = [&](int i) {  // page of this lane's row of tile i; -1: no row
-      const int key = k_lo + kTileRows * (warp + kWarps * i) + my_row;
-      return (i < count && key < k_hi) ? __ldg(table + (key >> p.cache.page_shift)) : -1;
-    };
-    int next_page = page_of(0);
-    uint32_t row = 0;         // this lane's cached row of the tile being copied
-    bool row_valid = false;
-    uint32_t unit_byte = 0;   // exponent byte on its way to row_unit
-    auto issue = [&](int e) {  // copy entry e (a commit group even when there is none left)
-      const int i = e >> 1;
-      if ((e & 1) == 0) {
-        if (kFp8 && i > 0 && i <= count) row_unit[warp][(i - 1) % kTileSlots][lane] = (uint8_t)unit_byte;
-        if (i < count) {
-          const int key = k_lo + kTileRows * (warp + kWarps * i) + my_row;
-          const int page = next_page;
-          row_valid = key < k_hi && page >= 0 && page < p.cache.num_pages;
-          if (key < k_hi && !row_valid) raise_error(p.err, kErrBadPage);
-          row = row_valid ? (((uint32_t)page * p.cache.h_kv + j) << p.cache.page_shift) +
-                                (key & ((1 << p.cache.page_shift) - 1))
-                          : 0u;
-          const unsigned ok = __ballot_sync(kFullMask, row_valid);
-          if (lane == 0) row_ok[warp][i % kTileSlots] = ok & 0xffffu;
-          if (kFp8) unit_byte = row_valid ? (lane < 16 ? p.cache.k_exp[row] : p.cache.v_exp[row]) : 127u;
-          next_page = page_of(i + 1);
-        }
-      }
-      if (e < last) {
-        const uint8_t* src = static_cast<const uint8_t*>((e & 1) ? p.cache.v_pages : p.cache.k_pages);
-        const uint32_t dst = ring + (uint32_t)(e % kEntries) * kEntry;
-        const int c = lane % kRowLanes;
-#pragma unroll
-        for (int s = 0; s < kTileRows / kRowsAtOnce; ++s) {
-          const int r = s * kRowsAtOnce + lane / kRowLanes;
-          const uint32_t from = __shfl_sync(kFullMask, row, r);
-          const bool ok = __shfl_sync(kFullMask, (int)row_valid, r) != 0;
-          copy16(dst + r * kRowBytes + ((c ^ (r & 7)) << 4), src + (size_t)from * kRowBytes + 16 * c, ok);
-        }
-      }
-      copy_commit();
-    };
-#pragma unroll
-    for (int e = 0; e < kEntries - 1; ++e) issue(e);
 
     float o[kQ][4];
 #pragma unroll
     for (int t = 0; t < kQ; ++t)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[t][c] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY;  // of heads 2 pair, 2 pair + 1
-    float v0 = -INFINITY, v1 = -INFINITY;  // maxima with the values' units (e4m3)
+    float m0 = -INFINITY, m1 = -INFINITY;  // references of heads 2 pair, 2 pair + 1
+    float v0 = -INFINITY, v1 = -INFINITY;  // those with the values' units (e4m3)
     float l0 = 0.f, l1 = 0.f;              // this lane's rows only
 
     for (int i = 0; i < count; ++i) {
-      // ---- S^T = K Q^T: rows quad and quad + 8, heads 2 pair and 2 pair + 1
+      // ---- S^T = K Q^T: rows quad and quad + 8 of each block, heads 2 pair, 2 pair + 1
       copy_wait<kEntries - 2>();
       __syncwarp();
-      issue(2 * i + kEntries - 1);
-      float s[4];
+      if (((kEntries - 1) & 1) == 0) issue_k(i + (kEntries - 1) / 2);
+      else issue_v(i + (kEntries - 1) / 2);
+      __syncwarp();
+      float s[kM][4];
       {
-        float acc[4][4];
+        float acc[2][kM][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[x][c] = 0.f;
-        const uint32_t tile = ring + (uint32_t)((2 * i) % kEntries) * kEntry +
-                              ((lane & 7) + 8 * ((lane >> 3) & 1)) * kRowBytes;
+          for (int m = 0; m < kM; ++m)
 #pragma unroll
-        for (int kk = 0; kk < (kFp8 ? kQ / 2 : kQ); ++kk) {
-          uint32_t r[4];
-          ldsm4(tile + (((2 * kk + (lane >> 4)) ^ swz_k) << 4), r);
-          if (!kFp8) {
-            mma16<false>(acc[kk & 3], r[0], r[1], r[2], r[3], qf[kk][0], qf[kk][1]);
-          } else {
-            mma16<true>(acc[(2 * kk) & 3], widen(r[0]), widen(r[1]), widen(r[0] >> 16), widen(r[1] >> 16),
-                        qf[2 * kk][0], qf[2 * kk][1]);
-            mma16<true>(acc[(2 * kk + 1) & 3], widen(r[2]), widen(r[3]), widen(r[2] >> 16),
-                        widen(r[3] >> 16), qf[2 * kk + 1][0], qf[2 * kk + 1][1]);
+            for (int c = 0; c < 4; ++c) acc[x][m][c] = 0.f;
+        const uint32_t tile = ring + get * kEntry + ((lane & 7) + 8 * ((lane >> 3) & 1)) * kRowBytes;
+#pragma unroll
+        for (int kk = 0; kk < kRowBytes / 32; ++kk)  // 32 bytes of each row
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            uint32_t r[4];
+            ldsm4(tile + 16 * m * kRowBytes + (((2 * kk + (lane >> 4)) ^ swz) << 4), r);
+            if (!kFp8) {
+              mma_bf16(acc[kk & 1][m], r, qf[kk][0], qf[kk][1]);
+            } else {
+              uint32_t a[4];
+              widen(r[0], a[0], a[2]);
+              widen(r[1], a[1], a[3]);
+              mma_f16(acc[0][m], a, qf[2 * kk][0], qf[2 * kk][1]);
+              widen(r[2], a[0], a[2]);
+              widen(r[3], a[1], a[3]);
+              mma_f16(acc[1][m], a, qf[2 * kk + 1][0], qf[2 * kk + 1][1]);
+            }
           }
-        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[c] = (acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c]);
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[m][c] = acc[0][m][c] + acc[1][m][c];
       }
-      const uint32_t ok = row_ok[warp][i % kTileSlots];
-      const bool ok0 = (ok >> quad) & 1, ok1 = (ok >> (quad + 8)) & 1;
-      float ve0 = 0.f, ve1 = 0.f;
-      if (kFp8) {
-        const uint8_t* ub = row_unit[warp][i % kTileSlots];
-        const float k0 = pow2((int)ub[quad] - 127), k1 = pow2((int)ub[quad + 8] - 127);
-        ve0 = (float)((int)ub[16 + quad] - 127);
-        ve1 = (float)((int)ub[24 + quad] - 127);
-        s[0] *= k0;
-        s[1] *= k0;
-        s[2] *= k1;
-        s[3] *= k1;
+      if (++get == kEntries) get = 0;
+      const TileInfo& ti = info[i % kSlots];
+      const uint32_t rows = ti.rows;
+      float ve[kM][2];  // the values' exponents (rows quad, quad + 8)
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        float f0 = 1.f, f1 = 1.f;
+        if (kFp8) {
+          f0 = unit_of(ti.k_unit[16 * m + quad]);
+          f1 = unit_of(ti.k_unit[16 * m + 8 + quad]);
+          ve[m][0] = exponent_of(ti.v_unit[16 * m + quad]);
+          ve[m][1] = exponent_of(ti.v_unit[16 * m + 8 + quad]);
+        }
+        const bool ok0 = quad < (int)((rows >> (16 * m)) & 0xff), ok1 = quad < (int)((rows >> (16 * m + 8)) & 0xff);
+        s[m][0] = ok0 ? s[m][0] * f0 * unit0 : -INFINITY;
+        s[m][1] = ok0 ? s[m][1] * f0 * unit1 : -INFINITY;
+        s[m][2] = ok1 ? s[m][2] * f1 * unit0 : -INFINITY;
+        s[m][3] = ok1 ? s[m][3] * f1 * unit1 : -INFINITY;
       }
-      s[0] = ok0 ? s[0] * unit0 : -INFINITY;
-      s[1] = ok0 ? s[1] * unit1 : -INFINITY;
-      s[2] = ok1 ? s[2] * unit0 : -INFINITY;
-      s[3] = ok1 ? s[3] * unit1 : -INFINITY;
-      // ---- online softmax
+      // ---- online softmax; a reference moves when it is exceeded by more than kSlack
       auto col_max = [&](float x) {
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, off));
         return x;
       };
-      const float n0 = fmaxf(m0, col_max(fmaxf(s[0], s[2])));
-      const float n1 = fmaxf(m1, col_max(fmaxf(s[1], s[3])));
-      const float g0 = n0 == -INFINITY ? 0.f : n0, g1 = n1 == -INFINITY ? 0.f : n1;
-      float e0 = ex2(s[0] - g0), e1 = ex2(s[1] - g1), e2 = ex2(s[2] - g0), e3 = ex2(s[3] - g1);
-      float a0 = ex2(m0 - g0), a1 = ex2(m1 - g1);
-      l0 = fmaf(l0, a0, e0 + e2);
-      l1 = fmaf(l1, a1, e1 + e3);
+      auto moved = [&](float ref, float top) { return top > ref + kSlack || ref == -INFINITY ? top : ref; };
+      float t0 = fmaxf(s[0][0], s[0][2]), t1 = fmaxf(s[0][1], s[0][3]);
+#pragma unroll
+      for (int m = 1; m < kM; ++m) {
+        t0 = fmaxf(t0, fmaxf(s[m][0], s[m][2]));
+        t1 = fmaxf(t1, fmaxf(s[m][1], s[m][3]));
+      }
+      const float n0 = moved(m0, col_max(t0)), n1 = moved(m1, col_max(t1));
+      float g0 = n0 == -INFINITY ? 0.f : n0, g1 = n1 == -INFINITY ? 0.f : n1;
+      float a0 = 1.f, a1 = 1.f;
+      if (__any_sync(kFullMask, n0 != m0 || n1 != m1)) {
+        a0 = ex2(m0 - g0);
+        a1 = ex2(m1 - g1);
+        l0 *= a0;
+        l1 *= a1;
+      }
       m0 = n0;
       m1 = n1;
+      float w[kM][4];
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        w[m][0] = ex2(s[m][0] - g0);
+        w[m][1] = ex2(s[m][1] - g1);
+        w[m][2] = ex2(s[m][2] - g0);
+        w[m][3] = ex2(s[m][3] - g1);
+        l0 += w[m][0] + w[m][2];
+        l1 += w[m][1] + w[m][3];
+      }
       if (kFp8) {
-        const float x0 = fmaxf(v0, col_max(fmaxf(s[0] + ve0, s[2] + ve1)));
-        const float x1 = fmaxf(v1, col_max(fmaxf(s[1] + ve0, s[3] + ve1)));
-        const float h0 = x0 == -INFINITY ? 0.f : x0, h1 = x1 == -INFINITY ? 0.f : x1;
-        e0 = ex2(s[0] + ve0 - h0);
-        e1 = ex2(s[1] + ve0 - h1);
-        e2 = ex2(s[2] + ve1 - h0);
-        e3 = ex2(s[3] + ve1 - h1);
-        a0 = ex2(v0 - h0);
-        a1 = ex2(v1 - h1);
-        v0 = x0;
-        v1 = x1;
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+          s[m][0] += ve[m][0];
+          s[m][1] += ve[m][0];
+          s[m][2] += ve[m][1];
+          s[m][3] += ve[m][1];
+          x0 = fmaxf(x0, fmaxf(s[m][0], s[m][2]));
+          x1 = fmaxf(x1, fmaxf(s[m][1], s[m][3]));
+        }
+        const float h0 = moved(v0, col_max(x0)), h1 = moved(v1, col_max(x1));
+        g0 = h0 == -INFINITY ? 0.f : h0;
+        g1 = h1 == -INFINITY ? 0.f : h1;
+        a0 = ex2(v0 - g0);
+        a1 = ex2(v1 - g1);
+        v0 = h0;
+        v1 = h1;
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+          w[m][0] = ex2(s[m][0] - g0);
+          w[m][1] = ex2(s[m][1] - g1);
+          w[m][2] = ex2(s[m][2] - g0);
+          w[m][3] = ex2(s[m][3] - g1);
+        }
       }
       if (__any_sync(kFullMask, a0 != 1.f || a1 != 1.f)) {
 #pragma unroll
@@ -445,50 +567,62 @@ __global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttn
         }
       }
       // ---- P^T as the B operand
-      uint32_t b0, b1, c0 = 0, c1 = 0;
-      if (kFp8) {
-        b0 = transpose8x8(pack_f16(e0, e1));
-        b1 = transpose8x8(pack_f16(e2, e3));
-      } else {
-        const uint32_t x = pack_bf16(e0, e1), y = pack_bf16(e2, e3);
-        b0 = transpose8x8(x);
-        b1 = transpose8x8(y);
-        c0 = transpose8x8(pack_bf16(lo_part(x, e0), hi_part(x, e1)));
-        c1 = transpose8x8(pack_bf16(lo_part(y, e2), hi_part(y, e3)));
+      uint32_t ph[kM][2], pl[kM][2];
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        if (kFp8) {
+          ph[m][0] = transpose8x8(pack_f16(w[m][0], w[m][1]));
+          ph[m][1] = transpose8x8(pack_f16(w[m][2], w[m][3]));
+        } else {
+          const uint32_t x = pack_bf16(w[m][0], w[m][1]), y = pack_bf16(w[m][2], w[m][3]);
+          ph[m][0] = transpose8x8(x);
+          ph[m][1] = transpose8x8(y);
+          pl[m][0] = transpose8x8(pack_bf16(lo_part(x, w[m][0]), hi_part(x, w[m][1])));
+          pl[m][1] = transpose8x8(pack_bf16(lo_part(y, w[m][2]), hi_part(y, w[m][3])));
+        }
       }
       // ---- O^T += V^T P^T
       copy_wait<kEntries - 2>();
       __syncwarp();
-      issue(2 * i + kEntries);
-      const uint32_t vt = ring + (uint32_t)((2 * i + 1) % kEntries) * kEntry;
+      if ((kEntries & 1) == 0) issue_k(i + kEntries / 2);
+      else issue_v(i + kEntries / 2);
+      const uint32_t vt = ring + get * kEntry;
+      if (++get == kEntries) get = 0;
       if (!kFp8) {
         const uint32_t tile = vt + ((lane & 7) + 8 * (lane >> 4)) * kRowBytes;
 #pragma unroll
-        for (int t = 0; t < kQ; ++t) {
-          uint32_t r[4];
-          ldsm4t(tile + (((2 * t + ((lane >> 3) & 1)) ^ swz_v) << 4), r);
-          mma16<false>(o[t], r[0], r[1], r[2], r[3], b0, b1);
-          mma16<false>(o[t], r[0], r[1], r[2], r[3], c0, c1);
-        }
+        for (int t = 0; t < kQ; ++t)
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            uint32_t r[4];
+            ldsm4t(tile + 16 * m * kRowBytes + (((2 * t + ((lane >> 3) & 1)) ^ swz) << 4), r);
+            mma_bf16(o[t], r, ph[m][0], ph[m][1]);
+            mma_bf16(o[t], r, pl[m][0], pl[m][1]);
+          }
       } else {
         const uint32_t tile = vt + ((lane & 7) + 8 * ((lane >> 3) & 1)) * kRowBytes;
 #pragma unroll
-        for (int t = 0; t < kQ; t += 2) {
-          uint32_t r[4];  // chunks t (r0: rows 0-7, r1: 8-15) and t + 1 (r2, r3)
-          ldsm4t(tile + (((t + (lane >> 4)) ^ swz_v) << 4), r);
+        for (int t = 0; t < kQ; t += 2)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // bytes (row 2 pair: dims 2 quad, 2 quad + 1; row 2 pair + 1: the same)
-            const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
-            mma16<true>(o[t + h], widen(x), widen(x >> 16), widen(y), widen(y >> 16), b0, b1);
+          for (int m = 0; m < kM; ++m) {
+            uint32_t r[4];  // chunks t (r0: rows 0-7, r1: 8-15) and t + 1 (r2, r3)
+            ldsm4t(tile + 16 * m * kRowBytes + (((t + (lane >> 4)) ^ swz) << 4), r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // bytes (row 2 pair: dims 2 quad, 2 quad + 1; row 2 pair + 1: the same)
+              uint32_t a[4];
+              widen(__byte_perm(r[2 * h], 0, 0x3120), a[0], a[1]);
+              widen(__byte_perm(r[2 * h + 1], 0, 0x3120), a[2], a[3]);
+              mma_f16(o[t + h], a, ph[m][0], ph[m][1]);
+            }
           }
-        }
       }
     }
     copy_wait<0>();
     __syncwarp();
 
-    // ---- join the warps
+    // ---- join the warps, a quarter of the dimensions at a time; the next piece's
+    // first copies are on their way meanwhile
 #pragma unroll
     for (int off = 4; off <= 16; off <<= 1) {
       l0 += __shfl_xor_sync(kFullMask, l0, off);
@@ -506,143 +640,206 @@ __global__ void __launch_bounds__(kThreads, 2) attn_paged_kernel(const PagedAttn
       wl[warp][2 * pair] = l0;
       wl[warp][2 * pair + 1] = l1;
     }
+    const bool to_o = whole;
+    const int64_t part = ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * G;
+    more = next_piece();
+    if (more) open();
     __syncthreads();
-    {
-      float t0 = wv[0][2 * pair], t1 = wv[0][2 * pair + 1];
+    float t0 = wv[0][2 * pair], t1 = wv[0][2 * pair + 1];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        t0 = fmaxf(t0, wv[w][2 * pair]);
-        t1 = fmaxf(t1, wv[w][2 * pair + 1]);
-      }
-      const float f0 = v0 == -INFINITY ? 0.f : ex2(v0 - t0), f1 = v1 == -INFINITY ? 0.f : ex2(v1 - t1);
-      float* buf = reinterpret_cast<float*>(smem + warp * kRing);
-#pragma unroll
-      for (int t = 0; t < kQ; ++t) {
-        // e4m3: rows of V^T interleave two dims (see the products above)
-        const int d0 = 16 * t + (kFp8 ? 2 * quad : quad), d1 = kFp8 ? d0 + 1 : d0 + 8;
-        buf[(2 * pair) * kPad + d0] = o[t][0] * f0;
-        buf[(2 * pair + 1) * kPad + d0] = o[t][1] * f1;
-        buf[(2 * pair) * kPad + d1] = o[t][2] * f0;
-        buf[(2 * pair + 1) * kPad + d1] = o[t][3] * f1;
-      }
+    for (int w = 1; w < kWarps; ++w) {
+      t0 = fmaxf(t0, wv[w][2 * pair]);
+      t1 = fmaxf(t1, wv[w][2 * pair + 1]);
     }
-    __syncthreads();
-    const bool whole = c0 == 0 && c1 == tiles;
-    const int slot = u_start > base + (int64_t)j * tiles ? 0 : 1;
-    float* part = p.partial + ((int64_t)blockIdx.x * 2 + slot) * G * (D + 2);
-    for (int x = tid; x < G * D; x += kThreads) {
-      const int h = x / D, d = x % D;
-      float M = wm[0][h], T = wv[0][h];
+    const float f0 = v0 == -INFINITY ? 0.f : ex2(v0 - t0), f1 = v1 == -INFINITY ? 0.f : ex2(v1 - t1);
+    // the head and the four dims that this thread finishes
+    const int h = tid / (kChunk / 4), d4 = tid % (kChunk / 4);
+    float M = -INFINITY, l = 0.f, r = 0.f;
+    if (h < G) {
+      float T = wv[0][h];
+      M = wm[0][h];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) {
         M = fmaxf(M, wm[w][h]);
         T = fmaxf(T, wv[w][h]);
       }
-      float l = 0.f, acc = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        l += wm[w][h] == -INFINITY ? 0.f : wl[w][h] * ex2(wm[w][h] - M);
-        acc += reinterpret_cast<const float*>(smem + w * kRing)[h * kPad + d];
-      }
+      for (int w = 0; w < kWarps; ++w) l += wm[w][h] == -INFINITY ? 0.f : wl[w][h] * ex2(wm[w][h] - M);
       // l > 0 whenever a row was seen; NaN stays NaN
-      const float r = l == 0.f ? 0.f : acc * (kFp8 ? ex2(T - M) : 1.f) / l;
-      if (whole) {
-        static_cast<__nv_bfloat16*>(p.o)[(head0 + h) * D + d] = __float2bfloat16_rn(r);
-      } else {
-        part[h * (D + 2) + d] = r;
-        if (d == 0) {
-          part[h * (D + 2) + D] = M;
-          part[h * (D + 2) + D + 1] = l;
-        }
-      }
+      r = l == 0.f ? 0.f : (kFp8 ? ex2(T - M) : 1.f) / l;
+      if (!to_o && d4 == 0)
+        reinterpret_cast<float2*>(p.partial + (int64_t)p.ctas * 2 * G * D)[part + h] = make_float2(M, l);
     }
-    __syncthreads();  // the buffers are refilled by the next (sequence, KV head)
-    u += c1 - c0;
+#pragma unroll
+    for (int x = 0; x < D / kChunk; ++x) {
+#pragma unroll
+      for (int y = 0; y < kQ / 4; ++y) {
+        const int t = x * (kQ / 4) + y;
+        // e4m3: rows of V^T interleave two dims (see the products above)
+        const int d0 = 16 * y + (kFp8 ? 2 * quad : quad), d1 = kFp8 ? d0 + 1 : d0 + 8;
+        joined[warp][2 * pair][d0] = o[t][0] * f0;
+        joined[warp][2 * pair + 1][d0] = o[t][1] * f1;
+        joined[warp][2 * pair][d1] = o[t][2] * f0;
+        joined[warp][2 * pair + 1][d1] = o[t][3] * f1;
+      }
+      __syncthreads();
+      if (h < G) {
+        float4 a = *reinterpret_cast<const float4*>(&joined[0][h][4 * d4]);
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(&joined[w][h][4 * d4]);
+          a.x += y.x;
+          a.y += y.y;
+          a.z += y.z;
+          a.w += y.w;
+        }
+        a = make_float4(a.x * r, a.y * r, a.z * r, a.w * r);
+        const int d = x * kChunk + 4 * d4;
+        if (to_o)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (head0 + h) * D + d) =
+              make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+        else
+          *reinterpret_cast<float4*>(p.partial + (part + h) * D + d) = a;
+      }
+      __syncthreads();
+    }
   }
 }
 
 // The results of a (sequence, KV head) whose units went to several CTAs:
 //     o = sum_s w_s o_s / sum_s w_s,   w_s = 2^(m_s - M) l_s,   M = max_s m_s
 // with each CTA's o_s already divided by its l_s.  Also writes the zeros of a
-// sequence without cached rows.  One block per (sequence, KV head, query head).
-constexpr int kJoinThreads = 256;
-template <int D>
+// sequence without cached rows.  One block per (sequence, KV head, query head):
+// with up to kFew splits the block of the first query head does all of them, a warp
+// each (batches: nearly every item has two); with more, each block its own, D / 4
+// lanes a row of four values each, the splits dealt to the groups of lanes, eight
+// loads in flight in each.
+constexpr int kFew = 16;
+template <int D, int kUnit, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const PagedAttnArgs p) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
   __shared__ float w_sm[kPagedMaxCtas];
-  __shared__ float red[kJoinThreads / 32];
-  __shared__ float sum_sm[kJoinThreads];
+  __shared__ float red[2][kJoinThreads / 32];
+  __shared__ float4 sum_sm[kGroups][kLanes];
   tc::allow_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h_kv = p.cache.h_kv, G = p.h_q / h_kv;
-  const int b = blockIdx.x / h_kv, j = blockIdx.x % h_kv, h = blockIdx.y;
+  const int b = blockIdx.x / h_kv, j = blockIdx.x % h_kv;
   int64_t base, total;
-  count_units<kJoinThreads>(p, b, &base, &total);
-  const int64_t tiles = (length_of(p, b) + (int64_t)kUnit - 1) / kUnit;
-  const int64_t first = base + (int64_t)j * tiles, end = first + tiles;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)b * p.h_q + (int64_t)j * G + h) * D;
+  count_work<kJoinThreads, kUnit>(p, b, &base, &total);
+  const int64_t span = span_of<kUnit>(length_of(p, b));
+  const int64_t first = base + (int64_t)j * span + kPieceCost, end = base + (int64_t)(j + 1) * span;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)b * p.h_q + (int64_t)j * G) * D;
+  const Shares sh(total, p.ctas);
+  const int c_lo = span > 0 ? sh.owner(first) : 0, c_hi = span > 0 ? sh.owner(end - 1) : 0;
+  const int n = c_hi - c_lo + 1;
   tc::wait_prerequisites();
-  if (tiles == 0) {
-    for (int d = tid; d < D; d += kJoinThreads) o[d] = __float2bfloat16_rn(0.f);
+  if (span == 0) {
+    if (tid < D) o[blockIdx.y * D + tid] = __float2bfloat16_rn(0.f);
     return;
   }
-  const Shares sh(total, p.ctas);
-  const int c_lo = sh.owner(first), c_hi = sh.owner(end - 1);
-  if (c_lo == c_hi) return;  // written by its CTA
-  const int n = c_hi - c_lo + 1;
+  if (n == 1) return;  // written by its CTA
   // the CTA with the first unit wrote slot 1, those that start inside it slot 0
-  auto part = [&](int s) {
-    return p.partial + (((int64_t)(c_lo + s) * 2 + (s == 0)) * G + h) * (D + 2);
+  auto part = [&](int s, int h) { return ((int64_t)(c_lo + s) * 2 + (s == 0)) * G + h; };
+  const float4* acc_in = reinterpret_cast<const float4*>(p.partial);
+  const float2* ml_in = reinterpret_cast<const float2*>(p.partial + (int64_t)p.ctas * 2 * G * D);
+  auto add = [](float4& a, float f, const float4& v) {
+    if (f != 0.f) {
+      a.x = fmaf(f, v.x, a.x);
+      a.y = fmaf(f, v.y, a.y);
+      a.z = fmaf(f, v.z, a.z);
+      a.w = fmaf(f, v.w, a.w);
+    }
   };
+  auto store = [&](int h, int d4, const float4& a, float den) {
+    const float r = den == 0.f ? 0.f : 1.f / den;
+    *reinterpret_cast<uint2*>(o + (int64_t)h * D + 4 * d4) =
+        make_uint2(pack_bf16(a.x * r, a.y * r), pack_bf16(a.z * r, a.w * r));
+  };
+  if (n <= kFew) {
+    const int h = warp;
+    if (blockIdx.y > 0 || h >= G) return;
+    float2 ml = lane < n ? ml_in[part(lane, h)] : make_float2(-INFINITY, 0.f);
+    float4 a[D / 128];
+#pragma unroll
+    for (int k = 0; k < D / 128; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float mx = ml.x;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, off));
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx) * ml.y;
+    float den = w;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(kFullMask, den, off);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float f = __shfl_sync(kFullMask, w, s);
+#pragma unroll
+      for (int k = 0; k < D / 128; ++k) add(a[k], f, acc_in[part(s, h) * kLanes + 32 * k + lane]);
+    }
+#pragma unroll
+    for (int k = 0; k < D / 128; ++k) store(h, 32 * k + lane, a[k], den);
+    return;
+  }
+  const int d4 = tid % kLanes, grp = tid / kLanes, h = blockIdx.y;
+  float4 x[8];  // the first loads go out before the weights are known
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int s = grp + k * kGroups;
+    x[k] = s < n ? acc_in[part(s, h) * kLanes + d4] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  constexpr int kMine = (kPagedMaxCtas + kJoinThreads - 1) / kJoinThreads;  // splits a thread
+  float2 ml[kMine];
   float mx = -INFINITY;
-  for (int s = tid; s < n; s += kJoinThreads) {
-    const float m = part(s)[D];
-    w_sm[s] = m;
-    mx = fmaxf(mx, m);
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int s = tid + k * kJoinThreads;
+    ml[k] = s < n ? ml_in[part(s, h)] : make_float2(-INFINITY, 0.f);
+    mx = fmaxf(mx, ml[k].x);
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, off));
-  if (lane == 0) red[warp] = mx;
+  if (lane == 0) red[0][warp] = mx;
   __syncthreads();
-  mx = red[0];
+  mx = red[0][0];
 #pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
-  __syncthreads();
+  for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[0][w]);
   float den = 0.f;
-  for (int s = tid; s < n; s += kJoinThreads) {
-    const float m = w_sm[s];
-    const float w = m == -INFINITY ? 0.f : ex2(m - mx) * part(s)[D + 1];
-    w_sm[s] = w;
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const float w = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - mx) * ml[k].y;
+    if (tid + k * kJoinThreads < n) w_sm[tid + k * kJoinThreads] = w;
     den += w;
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(kFullMask, den, off);
-  if (lane == 0) red[warp] = den;
+  if (lane == 0) red[1][warp] = den;
   __syncthreads();
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (grp + k * kGroups < n) add(a, w_sm[grp + k * kGroups], x[k]);
+#pragma unroll 8
+  for (int s = grp + 8 * kGroups; s < n; s += kGroups) add(a, w_sm[s], acc_in[part(s, h) * kLanes + d4]);
+  sum_sm[grp][d4] = a;
+  __syncthreads();
+  if (grp > 0) return;
   den = 0.f;
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) den += red[w];
-  constexpr int kGroups = kJoinThreads / D;
-  const int d = tid % D, grp = tid / D;
-  float acc = 0.f;
-#pragma unroll 8
-  for (int s = grp; s < n; s += kGroups) {
-    const float w = w_sm[s];
-    acc += w == 0.f ? 0.f : w * part(s)[d];
-  }
-  if (kGroups > 1) {
-    sum_sm[tid] = acc;
-    __syncthreads();
-    if (grp > 0) return;
+  for (int i = 0; i < kJoinThreads / 32; ++i) den += red[1][i];
 #pragma unroll
-    for (int g = 1; g < kGroups; ++g) acc += sum_sm[g * D + d];
+  for (int g = 1; g < kGroups; ++g) {
+    const float4 y = sum_sm[g][d4];
+    a.x += y.x;
+    a.y += y.y;
+    a.z += y.z;
+    a.w += y.w;
   }
-  o[d] = __float2bfloat16_rn(den == 0.f ? 0.f : acc / den);
+  store(h, d4, a, den);
 }
-
 template <int D, bool kFp8>
 cudaError_t launch_paged(const PagedAttnArgs& args, cudaStream_t stream) {
   static PerDeviceOnce attrs;
-  const size_t smem = kWarps * kRing;
+  const size_t smem = kWarps * ring_bytes(D, kFp8);
   cudaError_t e = attrs.run([&] {
     return cudaFuncSetAttribute(attn_paged_kernel<D, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem);
@@ -663,9 +860,15 @@ cudaError_t launch_paged(const PagedAttnArgs& args, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, attn_paged_kernel<D, kFp8>, args);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(args.batch * args.cache.h_kv), (unsigned)(args.h_q / args.cache.h_kv));
-  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, args);
+  // Few rows of o have many splits each: more loads in flight.  A batch's rows have
+  // few, and small blocks let more of them run at once.
+  if ((int64_t)args.batch * args.h_q <= 64) {
+    cfg.blockDim = dim3(1024);
+    return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 1024>, args);
+  }
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 256>, args);
 }
 
 }  // namespace
@@ -681,14 +884,15 @@ cudaError_t launch_attn_decode_paged(const PagedAttnArgs& a, cudaStream_t stream
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   PagedAttnArgs args = a;
-  // Two CTAs are resident on an SM; no more CTAs than units the table can reach.
-  const int64_t reach = ((int64_t)a.cache.max_pages << a.cache.page_shift) + kUnit - 1;
-  const int64_t units = (int64_t)a.batch * a.cache.h_kv * (reach / kUnit);
-  int64_t ctas = 2 * (int64_t)sms;
+  // As many CTAs as are resident at once, but no more than units the table can reach.
+  const bool fp8 = a.cache.dtype == kCacheE4M3;
+  const int unit = unit_rows(a.cache.head_dim, fp8);
+  const int64_t reach = ((int64_t)a.cache.max_pages << a.cache.page_shift) + unit - 1;
+  const int64_t units = (int64_t)a.batch * a.cache.h_kv * (reach / unit);
+  int64_t ctas = (int64_t)ctas_per_sm(a.cache.head_dim, fp8) * sms;
   if (ctas > kPagedMaxCtas) ctas = kPagedMaxCtas;
   if (ctas > units) ctas = units > 0 ? units : 1;
   args.ctas = (int32_t)ctas;
-  const bool fp8 = a.cache.dtype == kCacheE4M3;
   if (a.cache.head_dim == 256)
     return fp8 ? launch_paged<256, true>(args, stream) : launch_paged<256, false>(args, stream);
   return fp8 ? launch_paged<128, true>(args, stream) : launch_paged<128, false>(args, stream);

@@ -72,7 +72,7 @@ struct AttnPrefillArgs {
   int* err;
 };
 
-constexpr int32_t kPagedMaxCtas = 512;  // bounds the workspace of the paged decode
+constexpr int32_t kPagedMaxCtas = 640;  // bounds the workspace of the paged decode
 
 size_t paged_attn_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t head_dim);
 cudaError_t launch_kv_append(const KvRowsArgs& a, cudaStream_t stream);
