@@ -21,8 +21,8 @@
 //     Q 4 KB + K 2 KB a 64-cycle step; V 4 KB a 128-cycle step (D = 256)
 // to read and half of the writes.
 //
-// TMEM (512 columns): S of two key tiles (128 fp32 columns each, of which P's 64
-// columns of bf16 pairs then take the first half), O (D columns).  Shared memory:
+// TMEM (512 columns): S of two or three key tiles (128 fp32 columns each, of whose
+// two halves P then takes 32 columns of bf16 pairs), O (D columns).  Shared memory:
 // Q (64 KB at D = 256), a ring of K and V tile halves in the order of their use,
 // K0 K1 V0 K2 V1 ..: the products of tile j + 1's scores run while the softmax
 // warps work on tile j.
@@ -46,6 +46,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "attn_params.h"
 #include "attn_tc.cuh"
@@ -56,14 +57,10 @@
 namespace gdn {
 namespace {
 
-constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = 256;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kScheduleWarp = 10;
-constexpr int kThreads = 352;
-// Warps that read a scheduled tile: all but the schedule's own and, in the odd CTA, the products'.
-__device__ __forceinline__ uint32_t tile_readers(uint32_t rank) { return rank == 0 ? 10 : 9; }
 constexpr int kKeys = 128;          // keys a tile
 constexpr int kRows = 128;          // rows a CTA
-constexpr uint32_t kBarSoftmax = 1;
+constexpr int kSoftmaxThreads = 256, kTmaWarp = 8, kMmaWarp = 9, kScheduleWarp = 10, kThreads = 352;
+constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;  // log2 of the largest weight before m moves
 
@@ -77,25 +74,41 @@ struct Tile {  // one unit of work of a pair; tiles < 0 ends the schedule
 
 template <int D>
 struct Cfg {
+  // Eight softmax warps.  At D = 256 a tile's products take as long as its softmax,
+  // and O leaves room for two score tiles: all warps work on one key tile, two
+  // threads a row.  At D = 128 the products take half as long and there is room for
+  // three: two groups of four warps take the key tiles in turn, a thread a row, each
+  // with two tiles' time for one.
+  static constexpr int kGroups = D == 256 ? 1 : 2, kHalves = D == 256 ? 2 : 1;
+  static constexpr int kCols = kKeys / kHalves;  // scores a thread
+  static constexpr int kS = D == 256 ? 2 : 3;
+  static constexpr int kLag = kS - 1;  // key tiles that the scores are ahead of P V
+  static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
   static constexpr uint32_t kQBytes = kRows * D * 2;
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
   static constexpr int kEntries = D == 256 ? 5 : 10;
   static constexpr uint32_t kRing = kQBytes;
   static constexpr uint32_t kShared = kRing + kEntries * kEntry;  // the barriers and the rest
   static constexpr int kSteps = D / 16;
-  static constexpr uint32_t kTmemO = 256;
+  static constexpr uint32_t kTmemO = kS * kKeys;
   static constexpr uint32_t kTmemCols = 512;
+  static_assert(kTmemO + D <= kTmemCols, "TMEM");
 };
 
+template <int D>
 struct Shared {  // beside the tiles
-  uint64_t full[10], empty[10];
+  using C = Cfg<D>;
+  uint64_t full[C::kEntries], empty[C::kEntries];
   uint64_t q_full, q_empty;
-  uint64_t s_ready[2], p_ready[2], o_ready[2], o_free;
+  uint64_t s_ready[C::kS], p_ready[C::kS], o_ready[2], o_free;
+  uint64_t m_ready[2][4];  // two groups: a key tile's references are in m, by quarters of the rows
   uint64_t tile_full[2], tile_empty[2], flags_in, drained;
   Tile tile[2];
   uint32_t poison[2][2];  // [pass parity][half of the dimensions]: pass + 1 where V had a non-finite
   uint32_t tmem;
-  float red[2][2][128];   // row maxima (and at the end sums) of the two column halves
+  // halves: the row maxima of a key tile's halves, two key tiles (and row sums in the
+  // end); groups: the references of two key tiles
+  float red[2][2][128];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -111,22 +124,22 @@ __device__ __forceinline__ float poison_of(uint32_t bits16) {  // the value if i
   return (bits16 & 0x7f80u) == 0x7f80u ? __uint_as_float(bits16 << 16) : 0.f;
 }
 
-__device__ __forceinline__ float largest64(const float (&s)[64]) {
+template <int N>
+__device__ __forceinline__ float largest(const float (&s)[N]) {
   float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = tc2::max3(s[i], s[8 + i], s[16 + i]);
+  for (int i = 0; i < 8; ++i) x[i] = fmaxf(s[i], s[8 + i]);
 #pragma unroll
-  for (int k = 24; k < 56; k += 16)
+  for (int k = 16; k < N; k += 16)
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = tc2::max3(x[i], s[k + i], s[k + 8 + i]);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaxf(x[i], s[56 + i]);
   return tc2::max3(tc2::max3(x[0], x[1], x[2]), tc2::max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
 }
-__device__ __forceinline__ float least64(const float (&s)[64]) {
+template <int N>
+__device__ __forceinline__ float least(const float (&s)[N]) {
   float x = s[0];
 #pragma unroll
-  for (int i = 1; i < 64; ++i) x = fminf(x, s[i]);
+  for (int i = 1; i < N; ++i) x = fminf(x, s[i]);
   return x;
 }
 
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   // the tiles fill shared memory but for the 2.5 KB of Shared: no room to align them here
   extern __shared__ __align__(1024) uint8_t smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem + C::kShared);
+  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem + C::kShared);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = tc::cluster_rank();
   const int G = p.h_q / p.h_kv;
@@ -267,16 +280,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::mbar_init(&sh.q_full, 1);
     tc::mbar_init(&sh.q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kS; ++i) {
       tc::mbar_init(&sh.s_ready[i], 1);
-      tc::mbar_init(&sh.p_ready[i], 2 * kSoftmaxWarps);
+      tc::mbar_init(&sh.p_ready[i], 2 * C::kPWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sh.o_ready[i], 1);
+      for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
-      tc::mbar_init(&sh.tile_empty[i], tile_readers(rank));
+      // readers: the softmax and TMA warps, and in the even CTA the products'
+      tc::mbar_init(&sh.tile_empty[i], 8 + (rank == 0 ? 2 : 1));
       sh.poison[i][0] = sh.poison[i][1] = 0;
     }
-    tc::mbar_init(&sh.o_free, 2 * kSoftmaxWarps);
-    tc::mbar_init(&sh.flags_in, kSoftmaxWarps);
+    tc::mbar_init(&sh.o_free, 2 * 8);
+    tc::mbar_init(&sh.flags_in, 8);
     tc::mbar_init(&sh.drained, 1);
     tc::fence_mbar_init();
   }
@@ -357,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else tc::mbar_arrive(&sh.full[s]);
           return smem + C::kRing + s * C::kEntry;
         };
-        for (int j = 0; j <= t.tiles && ok; ++j) {
+        for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
           if (j < t.tiles) {
             if (uint8_t* dst = slot(false)) {
               for (int kb = 0; kb < D / 64; ++kb)
@@ -366,13 +383,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++e;
             }
           }
-          if (j > 0) {
-            const bool edge = j * kKeys > whole;  // of key tile j - 1
+          const int i = j - C::kLag;
+          if (i >= 0) {
+            const bool edge = (i + 1) * kKeys > whole;
             if (uint8_t* dst = slot(edge)) {
               const uint32_t bar = (edge ? tc2::in_cta(sh.full, rank) : r_full) + (e % C::kEntries) * 8;
               for (int kb = 0; kb < D / 128; ++kb)
                 tc2::tma_load_3d(dst + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
-                                 t.k0 + (j - 1) * kKeys, bar);
+                                 t.k0 + i * kKeys, bar);
               ++e;
             }
           }
@@ -410,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t.tiles == 0) continue;
       ok = warp_wait(&sh.q_full, used & 1);
       const int whole = t.off + t.tok0 + 1;
-      for (int j = 0; j <= t.tiles && ok; ++j) {
+      for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
         if (j < t.tiles) {  // S = Q K^T of key tile j
           if (!(ok = entry())) break;
           const int s = e % C::kEntries;
@@ -418,31 +436,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
 #pragma unroll
             for (int kk = 0; kk < C::kSteps; ++kk)
-              tc2::mma_ss(tmem + ((g + j) & 1) * 128, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+              tc2::mma_ss(tmem + ((g + j) % C::kS) * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                           dk + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-            tc2::commit(&sh.s_ready[(g + j) & 1]);
+            tc2::commit(&sh.s_ready[(g + j) % C::kS]);
             tc2::commit(&sh.empty[s]);
             if (j == t.tiles - 1) tc2::commit(&sh.q_empty);
           }
           __syncwarp();
           ++e;
         }
-        if (j > 0) {  // O += P V of key tile j - 1
-          const int h = g + j - 1;
+        const int i = j - C::kLag;
+        if (i >= 0) {  // O += P V of key tile i
+          const int h = g + i;
           if (!(ok = entry())) break;
           const int s = e % C::kEntries;
           // an edge tile's V was edited in both CTAs (ordinary writes): acquire those
-          const bool edge = j * kKeys > whole;
-          bool w = edge ? tc2::wait(&sh.p_ready[h & 1], (h >> 1) & 1) : tc::mbar_wait(&sh.p_ready[h & 1], (h >> 1) & 1);
-          if (j == 1 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
+          const bool edge = (i + 1) * kKeys > whole;
+          uint64_t* pr = &sh.p_ready[h % C::kS];
+          const uint32_t ph = (h / C::kS) & 1;
+          bool w = edge ? tc2::wait(pr, ph) : tc::mbar_wait(pr, ph);
+          if (i == 0 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
           tc::fence_after_sync();
           if (!(ok = __all_sync(kFullMask, w) != 0)) break;
           if (leader) {
             const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              tc2::mma_ts(tmem + C::kTmemO, tmem + (h & 1) * 128 + 8 * kk, dv + so + ((kk * 2048) >> 4),
-                          idesc_o, (j > 1) || (kk > 0));
+              tc2::mma_ts(tmem + C::kTmemO, tmem + (h % C::kS) * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), dv + so + ((kk * 2048) >> 4),
+                          idesc_o, (i > 0) || (kk > 0));
             tc2::commit(&sh.o_ready[h & 1]);
             tc2::commit(&sh.empty[s]);
           }
@@ -464,9 +485,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax
     Tile t;
     int e = 0, used = 0, g = 0;
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int grp = C::kGroups > 1 ? part : 0, half = C::kHalves > 1 ? part : 0;
+    constexpr int kPart = D / 2;  // columns of O that the thread finishes
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const float c = p.scale * kLog2e;
+    // (scale 0: all scores alike, by a factor that keeps a masked score infinite)
+    const float c = p.scale == 0.f ? 1e-30f : p.scale * kLog2e;
     const bool down = c < 0.f;  // the largest score is then the smallest product
     const uint32_t r_p = tc2::in_cta(sh.p_ready, 0), r_free = tc2::in_cta(&sh.o_free, 0);
     const uint32_t r_flags = tc2::in_cta(&sh.flags_in, rank ^ 1), r_poison = tc2::in_cta(sh.poison, rank ^ 1);
@@ -481,20 +505,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int whole = t.off + t.tok0 + 1;                // keys that every row of the pair sees
       float m = -INFINITY, l = 0.f;
       uint32_t* poison = sh.poison[used & 1];
-      for (int j = 0; j < t.tiles && ok; ++j) {
-        const int h = g + j, key0 = j * kKeys;
-        const bool edge = key0 + kKeys > whole;
-        bool w = carried && tc::mbar_wait(&sh.s_ready[h & 1], (h >> 1) & 1);
+      // with two groups, this one takes every other key tile (g counts them through)
+      // (a tile without an edge, most of them, in code of its own: selections for the
+      // mask would otherwise be issued with every tile)
+      auto key_tile = [&](int j, auto edge_tile) {
+        constexpr bool edge = decltype(edge_tile)::value;
+        const int h = g + j, key0 = j * kKeys, sb = h % C::kS;
+        bool w = carried && tc::mbar_wait(&sh.s_ready[sb], (h / C::kS) & 1);
         tc::fence_after_sync();
         if (edge) {  // this CTA's half of V: see the note at the top
-          const int v = e + (j < t.tiles - 1 ? 2 * j + 2 : 2 * j + 1);
+          const int v = e + min(t.tiles, j + C::kLag + 1) + j;  // ring entry of V
           w = w && tc::mbar_wait(&sh.full[v % C::kEntries], (v / C::kEntries) & 1);
           if (w) {
             uint8_t* vt = smem + C::kRing + (v % C::kEntries) * C::kEntry;
             bool found = false;
 #pragma unroll
-            for (int i = 0; i < (int)C::kEntry / 16 / kSoftmaxThreads; ++i) {
-              const int x = tid + i * kSoftmaxThreads, r = (x >> 3) & 127;
+            for (int i = 0; i < (int)C::kEntry / 16 / (32 * C::kPWarps); ++i) {
+              const int x = (tid % (32 * C::kPWarps)) + i * 32 * C::kPWarps, r = (x >> 3) & 127;
               uint4* at = reinterpret_cast<uint4*>(vt + (x >> 10) * 16384 + r * 128 + (x & 7) * 16);
               if (key0 + r >= t.sight) {
                 *at = make_uint4(0, 0, 0, 0);
@@ -517,32 +544,55 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         w = __all_sync(kFullMask, w);
-        float s[64];
-        tc2::tmem_ld64(tmem + lanes + (h & 1) * 128 + 64 * half, s);
-        const int left = lim - key0 - 64 * half;  // columns of this thread that the row sees
-        if (edge) {
-          const float none = down ? INFINITY : -INFINITY;
+        const int left = lim - key0 - C::kCols * half;  // columns of this thread that the row sees
+        const float none = down ? INFINITY : -INFINITY;
+        const uint32_t scores = tmem + lanes + sb * kKeys + C::kCols * half;
+        float s[64];  // 64 of the thread's scores
+        auto fetch = [&](int k) {
+          tc2::tmem_ld(scores + k, s);
+          if (edge) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = i < left ? s[i] : none;
+            for (int i = 0; i < 64; ++i) s[i] = k + i < left ? s[i] : none;
+          }
+        };
+        fetch(C::kCols - 64);
+        float x = down ? least(s) : largest(s);
+        if (C::kCols > 64) {
+          fetch(0);
+          x = down ? fminf(x, least(s)) : fmaxf(x, largest(s));
         }
-        float x = down ? least64(s) : largest64(s);
-        sh.red[h & 1][half][row] = x;
-        tc::fence_before_sync();
-        if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, w))) break;
-        tc::fence_after_sync();
-        const float y = sh.red[h & 1][half ^ 1][row];
-        x = down ? fminf(x, y) : fmaxf(x, y);
+        float now = m;  // the row's reference, which O and the tiles before go by
+        if (C::kHalves > 1) {
+          float(&red)[2][128] = sh.red[h & 1];
+          red[half][row] = x;
+          tc::fence_before_sync();
+          if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, w))) return;
+          tc::fence_after_sync();
+          const float y = red[half ^ 1][row];
+          x = down ? fminf(x, y) : fmaxf(x, y);
+        } else {
+          carried = w;
+          if (j > 0) {
+            carried = __all_sync(kFullMask, carried && tc::mbar_wait(&sh.m_ready[(h - 1) & 1][warp & 3], ((h - 1) >> 1) & 1));
+            now = sh.red[(h - 1) & 1][0][row];
+          }
+        }
         const bool any = x != (down ? INFINITY : -INFINITY);
         const float top = any ? x * c : -INFINITY;
-        const float next = top > m + kSlack || m == -INFINITY ? top : m;
-        const bool grow = next != m;
+        const float next = top > now + kSlack || now == -INFINITY ? top : now;
+        const bool grow = next != now;
+        if (C::kGroups > 1) {
+          sh.red[h & 1][0][row] = next;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sh.m_ready[h & 1][warp & 3]);
+        }
         if (j > 0 && __any_sync(kFullMask, grow)) {  // O holds the tiles before: rescale it
           const bool v = __all_sync(kFullMask, tc::mbar_wait(&sh.o_ready[(h - 1) & 1], ((h - 1) >> 1) & 1));
           tc::fence_after_sync();
-          const float f = m == -INFINITY ? 0.f : ex2(m - next);
+          const float f = now == -INFINITY ? 0.f : ex2(now - next);
           if (v) {
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
+            for (int i = 0; i < D / 32 / C::kHalves; ++i) {
               float ov[32];
               const uint32_t at = tmem + lanes + C::kTmemO + half * (D / 2) + 32 * i;
               tc::tmem_ld32(at, ov);
@@ -553,72 +603,81 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tmem_st32(at, ov);
             }
           }
-          carried = v;
-          if (grow) l *= f;
+          carried = carried && v;
         }
-        m = next;
+        if (next != m) {
+          l *= m == -INFINITY ? 0.f : ex2(m - next);
+          m = next;
+        }
         const float ref = m == -INFINITY ? 0.f : m;
-        uint32_t pk[32];
         const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          float2 p0 = tc2::fma2(make_float2(s[i], s[i + 1]), c2, r2);
-          float2 p1 = tc2::fma2(make_float2(s[i + 2], s[i + 3]), c2, r2);
-          p0 = make_float2(ex2(p0.x), ex2(p0.y));
-          p1 = make_float2(ex2(p1.x), ex2(p1.y));
-          if (edge) {
-            p0.x = i < left ? p0.x : 0.f;
-            p0.y = i + 1 < left ? p0.y : 0.f;
-            p1.x = i + 2 < left ? p1.x : 0.f;
-            p1.y = i + 3 < left ? p1.y : 0.f;
+        for (int k = 0; k < C::kCols; k += 64) {
+          if (k > 0) fetch(k);
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            float2 p0 = tc2::fma2(make_float2(s[i], s[i + 1]), c2, r2);
+            float2 p1 = tc2::fma2(make_float2(s[i + 2], s[i + 3]), c2, r2);
+            p0 = make_float2(ex2(p0.x), ex2(p0.y));
+            p1 = make_float2(ex2(p1.x), ex2(p1.y));
+            l0 = tc2::add2(l0, p0);
+            l1 = tc2::add2(l1, p1);
+            pk[i / 2] = pack_bf16(p0.x, p0.y);
+            pk[i / 2 + 1] = pack_bf16(p1.x, p1.y);
           }
-          l0 = tc2::add2(l0, p0);
-          l1 = tc2::add2(l1, p1);
-          pk[i / 2] = pack_bf16(p0.x, p0.y);
-          pk[i / 2 + 1] = pack_bf16(p1.x, p1.y);
+          tc2::tmem_st(scores + k, pk);  // over scores that are done with
         }
         l0 = tc2::add2(l0, l1);
         l += l0.x + l0.y;
-        tc2::tmem_st32(tmem + lanes + (h & 1) * 128 + 32 * half, pk);
         tc::fence_before_sync();
         if (edge) {
           tc::fence_proxy_async();  // the edited V rows -> the tensor core
           __syncwarp();
-          if (lane == 0) tc2::arrive_remote(r_p + (h & 1) * 8);
+          if (lane == 0) tc2::arrive_remote(r_p + sb * 8);
         } else {
           __syncwarp();
-          if (lane == 0) tc2::arrive_remote_relaxed(r_p + (h & 1) * 8);
+          if (lane == 0) tc2::arrive_remote_relaxed(r_p + sb * 8);
         }
+      };
+      for (int j = C::kGroups > 1 ? (g ^ grp) & 1 : 0; j < t.tiles && ok; j += C::kGroups) {
+        if ((j + 1) * kKeys > whole) key_tile(j, std::true_type());
+        else key_tile(j, std::false_type());
       }
       // ---- the pair's rows are through their keys
       float total = 0.f;
       if (t.tiles > 0) {
-        if (!ok) break;
         if (lane == 0) tc2::arrive_remote(r_flags);
-        bool w = carried && tc2::wait(&sh.flags_in, used & 1);
+        bool w = ok && carried && tc2::wait(&sh.flags_in, used & 1);
         const int h = g + t.tiles - 1;
         w = w && tc::mbar_wait(&sh.o_ready[h & 1], (h >> 1) & 1);
         tc::fence_after_sync();
-        float* lsum = &sh.red[(h + 1) & 1][0][0];  // last read before the last tile's barrier
-        lsum[half * 128 + row] = l;
+        float* sums = &sh.red[(h + 1) & 1][0][0];  // not in use: the last tile's is h & 1
+        if (C::kGroups > 1) {
+          w = w && tc::mbar_wait(&sh.m_ready[h & 1][warp & 3], (h >> 1) & 1);
+          const float last = sh.red[h & 1][0][row];  // of the last tile, which O goes by
+          if (m != last) l *= m == -INFINITY ? 0.f : ex2(m - last);
+          // the tile before's references: read by the other group before its last arrival
+        }
+        sums[part * 128 + row] = l;
         if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, w))) break;
-        total = lsum[row] + lsum[128 + row];
+        total = sums[row] + sums[128 + row];
       }
       const float inv = total == 0.f ? 0.f : 1.f / total;
       const bool dirty = t.tiles > 0 && (poison[0] == (uint32_t)used + 1 || poison[1] == (uint32_t)used + 1);
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) +
-                         (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D + half * (D / 2);
+                         (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D + part * kPart;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
+      for (int i = 0; i < kPart / 32; ++i) {
         float ov[32];
         if (t.tiles > 0) {
-          tc::tmem_ld32(tmem + lanes + C::kTmemO + half * (D / 2) + 32 * i, ov);
+          tc::tmem_ld32(tmem + lanes + C::kTmemO + part * kPart + 32 * i, ov);
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) ov[k] = 0.f;
         }
-        if (t.tiles > 0 && i == D / 64 - 1) {
+        if (t.tiles > 0 && i == kPart / 32 - 1) {
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc2::arrive_remote_relaxed(r_free);  // O may be overwritten
@@ -627,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 32; ++k) ov[k] *= inv;
         if (dirty && real) {
           const int first = max(0, whole) / kKeys * kKeys;  // first key of the tiles that were edited
-          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)t.kvh * D + half * (D / 2) + 32 * i;
+          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)t.kvh * D + part * kPart + 32 * i;
           for (int key = first; key < lim; ++key) {
             const uint32_t* src = reinterpret_cast<const uint32_t*>(vr + ((int64_t)t.k0 + key) * p.v_stride);
 #pragma unroll
@@ -704,8 +763,8 @@ cudaError_t launch(const AttnPrefillArgs& a, int sms, cudaStream_t stream) {
       !encode(&mv, keys ? a.v : a.q, D, keys ? a.h_kv : 1, keys ? a.total_k : 1, keys ? a.v_stride : a.q_stride,
               1, kKeys))
     return cudaErrorInvalidValue;
-  const int smem = (int)(C::kShared + sizeof(Shared));
-  static_assert(C::kShared + sizeof(Shared) <= 227 * 1024, "shared memory");
+  const int smem = (int)(C::kShared + sizeof(Shared<D>));
+  static_assert(C::kShared + sizeof(Shared<D>) <= 227 * 1024, "shared memory");
   static PerDeviceOnce attrs;
   cudaError_t e = attrs.run([&] {
     return cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
