@@ -86,9 +86,10 @@ struct Cfg {
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
   static constexpr uint32_t kQBytes = kRows * D * 2;
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
-  static constexpr int kEntries = D == 256 ? 5 : 10;
+  static constexpr int kEntries = D == 256 ? 4 : 8;
   static constexpr uint32_t kRing = kQBytes;
-  static constexpr uint32_t kShared = kRing + kEntries * kEntry;  // the barriers and the rest
+  static constexpr uint32_t kStage = kRing + kEntries * kEntry;  // o on its way out, 4 KB a softmax warp
+  static constexpr uint32_t kShared = kStage + 8 * 4096;         // the barriers and the rest
   static constexpr int kSteps = D / 16;
   static constexpr uint32_t kTmemO = kS * kKeys;
   static constexpr uint32_t kTmemCols = 512;
@@ -666,44 +667,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float inv = total == 0.f ? 0.f : 1.f / total;
       const bool dirty = t.tiles > 0 && (poison[0] == (uint32_t)used + 1 || poison[1] == (uint32_t)used + 1);
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) +
-                         (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D + part * kPart;
+      // o, 64 columns at a time, through shared memory: a thread has a row, but the rows
+      // leave as whole 128-byte lines (16 bytes a row and store cost 3 us a tile)
+      const int64_t out = (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D + part * kPart;
+      const unsigned rows = __ballot_sync(kFullMask, real);
+      uint8_t* stage = smem + C::kStage + warp * 4096;
 #pragma unroll
-      for (int i = 0; i < kPart / 32; ++i) {
-        float ov[32];
+      for (int i = 0; i < kPart; i += 64) {
+        float ov[64];
         if (t.tiles > 0) {
-          tc::tmem_ld32(tmem + lanes + C::kTmemO + part * kPart + 32 * i, ov);
+          tc2::tmem_ld(tmem + lanes + C::kTmemO + part * kPart + i, ov);
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) ov[k] = 0.f;
+          for (int k = 0; k < 64; ++k) ov[k] = 0.f;
         }
-        if (t.tiles > 0 && i == kPart / 32 - 1) {
+        if (t.tiles > 0 && i == kPart - 64) {
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc2::arrive_remote_relaxed(r_free);  // O may be overwritten
         }
 #pragma unroll
-        for (int k = 0; k < 32; ++k) ov[k] *= inv;
+        for (int k = 0; k < 64; ++k) ov[k] *= inv;
         if (dirty && real) {
           const int first = max(0, whole) / kKeys * kKeys;  // first key of the tiles that were edited
-          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)t.kvh * D + part * kPart + 32 * i;
+          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)t.kvh * D + part * kPart + i;
           for (int key = first; key < lim; ++key) {
             const uint32_t* src = reinterpret_cast<const uint32_t*>(vr + ((int64_t)t.k0 + key) * p.v_stride);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 32; ++k) {
               const uint32_t two = __ldg(src + k);
               ov[2 * k] += poison_of(two & 0xffffu);
               ov[2 * k + 1] += poison_of(two >> 16);
             }
           }
         }
-        if (real) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4*>(o + 32 * i + k) =
-                make_uint4(pack_bf16(ov[k], ov[k + 1]), pack_bf16(ov[k + 2], ov[k + 3]),
-                           pack_bf16(ov[k + 4], ov[k + 5]), pack_bf16(ov[k + 6], ov[k + 7]));
+        for (int k = 0; k < 64; k += 8)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + (((k / 8) ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16(ov[k], ov[k + 1]), pack_bf16(ov[k + 2], ov[k + 3]),
+                         pack_bf16(ov[k + 4], ov[k + 5]), pack_bf16(ov[k + 6], ov[k + 7]));
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3), x = lane & 7;
+          const int64_t to = __shfl_sync(kFullMask, out, r) + i + 8 * x;
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((x ^ (r & 7)) << 4));
+          if ((rows >> r) & 1) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + to) = y;
         }
+        __syncwarp();
       }
       if (t.tiles > 0) {
         e += 2 * t.tiles;
