@@ -27,18 +27,17 @@
 // K0 K1 V0 K2 V1 ..: the products of tile j + 1's scores run while the softmax
 // warps work on tile j.
 //
-// Roles (11 warps): 0-7 softmax (two threads a row, 64 columns each), 8 TMA, 9
-// products (the even CTA's issues them for the pair), 10 the schedule.  The pairs
-// are persistent.
+// Roles (16 warps): 0-7 softmax, 8-11 epilogue (O to o while the next tile's scores
+// are under way), 12 TMA, 13 products (the even CTA's issues them for the pair), 14
+// the schedule.  The pairs are persistent.
 //
 // Rounding: P is rounded to bf16 for the second product (relative 2^-9 a weight,
 // the same as the output's rounding; the sums l stay fp32 over unrounded weights).
 //
 // What a query does not see must not reach it even as NaN: its scores are masked,
-// and in a tile that some row sees in part, V rows past every row's sight are
-// zeroed in shared memory and non-finite values in the rest replaced by zero; the
-// epilogue adds those back to the rows that do see them (from global memory, only
-// in tiles where any was found).
+// and in a tile that some row sees in part, non-finite values of V are replaced by
+// zero in shared memory; the epilogue adds them back to the rows that do see them
+// (from global memory, only in tiles where any was found).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -59,7 +58,10 @@ namespace {
 
 constexpr int kKeys = 128;          // keys a tile
 constexpr int kRows = 128;          // rows a CTA
-constexpr int kSoftmaxThreads = 256, kTmaWarp = 8, kMmaWarp = 9, kScheduleWarp = 10, kThreads = 352;
+// Four warpgroups: softmax (two), epilogue, and the rest.  A thread of them has 168,
+// 112 and 64 registers (setmaxnreg; together the 65,536 that the CTA starts with).
+constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14;
+constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;  // log2 of the largest weight before m moves
@@ -88,8 +90,8 @@ struct Cfg {
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
   static constexpr int kEntries = D == 256 ? 4 : 8;
   static constexpr uint32_t kRing = kQBytes;
-  static constexpr uint32_t kStage = kRing + kEntries * kEntry;  // o on its way out, 4 KB a softmax warp
-  static constexpr uint32_t kShared = kStage + 8 * 4096;         // the barriers and the rest
+  static constexpr uint32_t kStage = kRing + kEntries * kEntry;  // o on its way out, 4 KB an epilogue warp
+  static constexpr uint32_t kShared = kStage + 4 * 4096;         // the barriers and the rest
   static constexpr int kSteps = D / 16;
   static constexpr uint32_t kTmemO = kS * kKeys;
   static constexpr uint32_t kTmemCols = 512;
@@ -103,13 +105,17 @@ struct Shared {  // beside the tiles
   uint64_t q_full, q_empty;
   uint64_t s_ready[C::kS], p_ready[C::kS], o_ready[2], o_free;
   uint64_t m_ready[2][4];  // two groups: a key tile's references are in m, by quarters of the rows
-  uint64_t tile_full[2], tile_empty[2], flags_in, drained;
+  // of two tiles, for the epilogue: the rows' sums; that the other CTA's softmax warps
+  // have told of what they found in V
+  uint64_t sums_in[2], flags_in[2];
+  uint64_t tile_full[2], tile_empty[2], drained;
   Tile tile[2];
   uint32_t poison[2][2];  // [pass parity][half of the dimensions]: pass + 1 where V had a non-finite
   uint32_t tmem;
-  // halves: the row maxima of a key tile's halves, two key tiles (and row sums in the
-  // end); groups: the references of two key tiles
+  // halves: the row maxima of a key tile's halves, two key tiles; groups: the
+  // references of two key tiles
   float red[2][2][128];
+  float sums[2][2][128];  // row sums of two tiles, in two parts
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -289,12 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sh.o_ready[i], 1);
       for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
-      // readers: the softmax and TMA warps, and in the even CTA the products'
-      tc::mbar_init(&sh.tile_empty[i], 8 + (rank == 0 ? 2 : 1));
+      tc::mbar_init(&sh.sums_in[i], 8);
+      tc::mbar_init(&sh.flags_in[i], 8);
+      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products'
+      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 2 : 1));
       sh.poison[i][0] = sh.poison[i][1] = 0;
     }
-    tc::mbar_init(&sh.o_free, 2 * 8);
-    tc::mbar_init(&sh.flags_in, 8);
+    tc::mbar_init(&sh.o_free, 2 * 4);
     tc::mbar_init(&sh.drained, 1);
     tc::fence_mbar_init();
   }
@@ -321,180 +328,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     return t->tiles >= 0;
   };
 
-  if (warp == kScheduleWarp) {
-    // ------------------------------------------------------------ schedule
-    const int pairs = gridDim.x / 2, me = blockIdx.x / 2;
-    Schedule sc;
-    sc.open(p, tokens, lane, blockIdx.x == 0);
-    for (int pass = 0;; ++pass) {
-      // pass by pass in alternating direction, so that the pairs' sums come out alike
-      const int64_t i = (int64_t)pass * pairs + ((pass & 1) ? pairs - 1 - me : me);
-      Tile t;
-      const bool more = sc.get(p, (int)(i / p.h_kv), (int)(i % p.h_kv), &t);
-      if (!more) t.tiles = -1;
-      if (pass >= 2 && !__all_sync(kFullMask, tc::mbar_wait(&sh.tile_empty[pass & 1], ((pass >> 1) - 1) & 1))) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        sh.tile[pass & 1] = t;
-        tc::mbar_arrive(&sh.tile_full[pass & 1]);
-      }
-      if (!more) break;
-    }
-  } else if (warp == kTmaWarp) {
-    // ------------------------------------------------------------ copies
-    Tile t;
-    int e = 0, used = 0;  // ring entries issued; tiles with Q
-    const uint32_t r_full = tc2::in_cta(sh.full, 0), r_q = tc2::in_cta(&sh.q_full, 0);
-    if (lane == 0) {
-      tc::prefetch_tmap(&tm_q);
-      tc::prefetch_tmap(&tm_k);
-      tc::prefetch_tmap(&tm_v);
-    }
-    for (int pass = 0; next_tile(pass, &t); ++pass) {
-      if (t.tiles == 0) continue;
-      if (lane == 0) {
-        const int whole = t.off + t.tok0 + 1;
-        if (used > 0) ok = tc::mbar_wait(&sh.q_empty, (used - 1) & 1);
-        if (ok) {
-          if (rank == 0) tc::mbar_arrive_expect_tx(&sh.q_full, 2u * (uint32_t)(tok_cta * G) * D * 2);
-          for (int kb = 0; kb < D / 64; ++kb)
-            tc2::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G,
-                             t.q0 + t.tok0 + (int)rank * tok_cta, r_q);
-        }
-        // The next ring entry, when it is empty.  The bytes of both CTAs count on
-        // the even CTA's barrier; those of V in an edge tile on the CTA's own, for
-        // the softmax warps that edit them there (whose arrival on p_ready then
-        // stands for the odd CTA's V).  The odd CTA's barrier keeps step.
-        auto slot = [&](bool here) -> uint8_t* {
-          const int s = e % C::kEntries;
-          if (e >= C::kEntries) ok = ok && tc::mbar_wait(&sh.empty[s], ((e / C::kEntries) - 1) & 1);
-          if (!ok) return nullptr;
-          if (here || rank == 0) tc::mbar_arrive_expect_tx(&sh.full[s], here ? C::kEntry : 2 * C::kEntry);
-          else tc::mbar_arrive(&sh.full[s]);
-          return smem + C::kRing + s * C::kEntry;
-        };
-        for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
-          if (j < t.tiles) {
-            if (uint8_t* dst = slot(false)) {
-              for (int kb = 0; kb < D / 64; ++kb)
-                tc2::tma_load_3d(dst + kb * 8192, &tm_k, 64 * kb, t.kvh,
-                                 t.k0 + j * kKeys + (int)rank * 64, r_full + (e % C::kEntries) * 8);
-              ++e;
-            }
-          }
-          const int i = j - C::kLag;
-          if (i >= 0) {
-            const bool edge = (i + 1) * kKeys > whole;
-            if (uint8_t* dst = slot(edge)) {
-              const uint32_t bar = (edge ? tc2::in_cta(sh.full, rank) : r_full) + (e % C::kEntries) * 8;
-              for (int kb = 0; kb < D / 128; ++kb)
-                tc2::tma_load_3d(dst + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
-                                 t.k0 + i * kKeys, bar);
-              ++e;
-            }
-          }
-        }
-      }
-      ++used;
-      ok = __all_sync(kFullMask, ok);
-      if (!ok) break;
-    }
-    // Copies still in flight land before the CTA ends: after an expired wait, the
-    // even CTA's barriers tell of both CTAs' copies (the odd one's own, of edge tiles).
-    if (lane == 0) {
-      for (int j = max(0, e - C::kEntries); j < e; ++j)
-        if (!tc::mbar_wait(&sh.full[j % C::kEntries], (j / C::kEntries) & 1)) ok = false;
-      if (rank == 0 && used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
-    }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ products
-    Tile t;
-    int e = 0, used = 0, g = 0;  // ring entries, tiles with Q, key tiles so far
-    const uint32_t idesc_s = tc::idesc_bf16_f32(256, kKeys, false, false);
-    const uint32_t idesc_o = tc::idesc_bf16_f32(256, D, false, true);
-    const uint64_t dq = tc::smem_desc(sbase, 16, 1024, tc::kLayoutSw128);
-    const uint64_t dk = tc::smem_desc(sbase + C::kRing, 16, 1024, tc::kLayoutSw128);
-    const uint64_t dv = tc::smem_desc(sbase + C::kRing, 16384, 1024, tc::kLayoutSw128);
-    const bool leader = tc::elect_one();
-    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool w = tc::mbar_wait(bar, parity);
-      tc::fence_after_sync();
-      return __all_sync(kFullMask, w) != 0;
-    };
-    auto entry = [&]() { return warp_wait(&sh.full[e % C::kEntries], (e / C::kEntries) & 1); };
-    // the even CTA's warp issues for the pair
-    for (int pass = 0; rank == 0 && next_tile(pass, &t); ++pass) {
-      if (t.tiles == 0) continue;
-      ok = warp_wait(&sh.q_full, used & 1);
-      const int whole = t.off + t.tok0 + 1;
-      for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
-        if (j < t.tiles) {  // S = Q K^T of key tile j
-          if (!(ok = entry())) break;
-          const int s = e % C::kEntries;
-          if (leader) {
-            const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
-#pragma unroll
-            for (int kk = 0; kk < C::kSteps; ++kk)
-              tc2::mma_ss(tmem + ((g + j) % C::kS) * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                          dk + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-            tc2::commit(&sh.s_ready[(g + j) % C::kS]);
-            tc2::commit(&sh.empty[s]);
-            if (j == t.tiles - 1) tc2::commit(&sh.q_empty);
-          }
-          __syncwarp();
-          ++e;
-        }
-        const int i = j - C::kLag;
-        if (i >= 0) {  // O += P V of key tile i
-          const int h = g + i;
-          if (!(ok = entry())) break;
-          const int s = e % C::kEntries;
-          // an edge tile's V was edited in both CTAs (ordinary writes): acquire those
-          const bool edge = (i + 1) * kKeys > whole;
-          uint64_t* pr = &sh.p_ready[h % C::kS];
-          const uint32_t ph = (h / C::kS) & 1;
-          bool w = edge ? tc2::wait(pr, ph) : tc::mbar_wait(pr, ph);
-          if (i == 0 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
-          tc::fence_after_sync();
-          if (!(ok = __all_sync(kFullMask, w) != 0)) break;
-          if (leader) {
-            const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              tc2::mma_ts(tmem + C::kTmemO, tmem + (h % C::kS) * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), dv + so + ((kk * 2048) >> 4),
-                          idesc_o, (i > 0) || (kk > 0));
-            tc2::commit(&sh.o_ready[h & 1]);
-            tc2::commit(&sh.empty[s]);
-          }
-          __syncwarp();
-          ++e;
-        }
-      }
-      if (!ok) break;
-      g += t.tiles;
-      ++used;
-    }
-    // every product issued has completed before either CTA leaves the barrier at the end
-    if (rank == 0) {
-      if (leader) tc2::commit(&sh.drained);
-      __syncwarp();
-      if (!warp_wait(&sh.drained, 0)) ok = false;
-    }
-  } else {
+  if (warp < kEpilogueWarp) {
+    tc2::more_registers<168>();
     // ------------------------------------------------------------ softmax
     Tile t;
     int e = 0, used = 0, g = 0;
     const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const int grp = C::kGroups > 1 ? part : 0, half = C::kHalves > 1 ? part : 0;
-    constexpr int kPart = D / 2;  // columns of O that the thread finishes
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     // (scale 0: all scores alike, by a factor that keeps a masked score infinite)
     const float c = p.scale == 0.f ? 1e-30f : p.scale * kLog2e;
     const bool down = c < 0.f;  // the largest score is then the smallest product
-    const uint32_t r_p = tc2::in_cta(sh.p_ready, 0), r_free = tc2::in_cta(&sh.o_free, 0);
-    const uint32_t r_flags = tc2::in_cta(&sh.flags_in, rank ^ 1), r_poison = tc2::in_cta(sh.poison, rank ^ 1);
+    const uint32_t r_p = tc2::in_cta(sh.p_ready, 0);
+    const uint32_t r_flags = tc2::in_cta(sh.flags_in, rank ^ 1), r_poison = tc2::in_cta(sh.poison, rank ^ 1);
     bool carried = true;  // no wait expired since the last barrier of these warps
     for (int pass = 0;; ++pass) {
       // all softmax warps go on or none: they meet at barriers without a limit
@@ -505,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = real ? max(0, t.off + tok + 1) : 0;  // keys this row sees
       const int whole = t.off + t.tok0 + 1;                // keys that every row of the pair sees
       float m = -INFINITY, l = 0.f;
-      uint32_t* poison = sh.poison[used & 1];
+      bool told = false;  // the other CTA was told of a non-finite value
       // with two groups, this one takes every other key tile (g counts them through)
       // (a tile without an edge, most of them, in code of its own: selections for the
       // mask would otherwise be issued with every tile)
@@ -514,35 +360,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = g + j, key0 = j * kKeys, sb = h % C::kS;
         bool w = carried && tc::mbar_wait(&sh.s_ready[sb], (h / C::kS) & 1);
         tc::fence_after_sync();
+        bool edited = false, seen = false;
         if (edge) {  // this CTA's half of V: see the note at the top
           const int v = e + min(t.tiles, j + C::kLag + 1) + j;  // ring entry of V
           w = w && tc::mbar_wait(&sh.full[v % C::kEntries], (v / C::kEntries) & 1);
           if (w) {
             uint8_t* vt = smem + C::kRing + (v % C::kEntries) * C::kEntry;
-            bool found = false;
 #pragma unroll
             for (int i = 0; i < (int)C::kEntry / 16 / (32 * C::kPWarps); ++i) {
               const int x = (tid % (32 * C::kPWarps)) + i * 32 * C::kPWarps, r = (x >> 3) & 127;
               uint4* at = reinterpret_cast<uint4*>(vt + (x >> 10) * 16384 + r * 128 + (x & 7) * 16);
-              if (key0 + r >= t.sight) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else {
-                uint4 y = *at;
-                const uint32_t a0 = __vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u),
-                               a1 = __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u),
-                               a2 = __vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u),
-                               a3 = __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u);
-                if (a0 | a1 | a2 | a3) {
-                  found = true;
-                  *at = make_uint4(y.x & ~a0, y.y & ~a1, y.z & ~a2, y.w & ~a3);
-                }
+              const uint4 y = *at;
+              const uint32_t a0 = __vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u), a1 = __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u),
+                             a2 = __vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u), a3 = __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u);
+              if (a0 | a1 | a2 | a3) {
+                edited = true;
+                seen = seen || key0 + r < t.sight;
+                *at = make_uint4(y.x & ~a0, y.y & ~a1, y.z & ~a2, y.w & ~a3);
               }
             }
-            if (found) {
-              poison[rank] = (uint32_t)used + 1;
+            if (seen) {
+              sh.poison[used & 1][rank] = (uint32_t)used + 1;
               tc2::store_remote(r_poison + ((used & 1) * 2 + rank) * 4, (uint32_t)used + 1);
             }
           }
+          edited = __any_sync(kFullMask, edited);
+          told = told || edited;
         }
         w = __all_sync(kFullMask, w);
         const int left = lim - key0 - C::kCols * half;  // columns of this thread that the row sees
@@ -633,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l0 = tc2::add2(l0, l1);
         l += l0.x + l0.y;
         tc::fence_before_sync();
-        if (edge) {
+        if (edge && edited) {
           tc::fence_proxy_async();  // the edited V rows -> the tensor core
           __syncwarp();
           if (lane == 0) tc2::arrive_remote(r_p + sb * 8);
@@ -646,51 +489,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((j + 1) * kKeys > whole) key_tile(j, std::true_type());
         else key_tile(j, std::false_type());
       }
-      // ---- the pair's rows are through their keys
-      float total = 0.f;
+      // ---- the pair's rows are through their keys: their sums go to the epilogue
       if (t.tiles > 0) {
-        if (lane == 0) tc2::arrive_remote(r_flags);
-        bool w = ok && carried && tc2::wait(&sh.flags_in, used & 1);
-        const int h = g + t.tiles - 1;
-        w = w && tc::mbar_wait(&sh.o_ready[h & 1], (h >> 1) & 1);
-        tc::fence_after_sync();
-        float* sums = &sh.red[(h + 1) & 1][0][0];  // not in use: the last tile's is h & 1
         if (C::kGroups > 1) {
-          w = w && tc::mbar_wait(&sh.m_ready[h & 1][warp & 3], (h >> 1) & 1);
+          const int h = g + t.tiles - 1;
+          carried = carried && tc::mbar_wait(&sh.m_ready[h & 1][warp & 3], (h >> 1) & 1);
           const float last = sh.red[h & 1][0][row];  // of the last tile, which O goes by
           if (m != last) l *= m == -INFINITY ? 0.f : ex2(m - last);
-          // the tile before's references: read by the other group before its last arrival
         }
-        sums[part * 128 + row] = l;
-        if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, w))) break;
-        total = sums[row] + sums[128 + row];
+        sh.sums[used & 1][part][row] = l;
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&sh.sums_in[used & 1]);
+          if (told) tc2::arrive_remote(r_flags + (used & 1) * 8);
+          else tc2::arrive_remote_relaxed(r_flags + (used & 1) * 8);
+        }
+        e += 2 * t.tiles;
+        g += t.tiles;
+        ++used;
       }
-      const float inv = total == 0.f ? 0.f : 1.f / total;
-      const bool dirty = t.tiles > 0 && (poison[0] == (uint32_t)used + 1 || poison[1] == (uint32_t)used + 1);
-      // o, 64 columns at a time, through shared memory: a thread has a row, but the rows
-      // leave as whole 128-byte lines (16 bytes a row and store cost 3 us a tile)
-      const int64_t out = (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D + part * kPart;
+    }
+  } else if (warp < kTmaWarp) {
+    tc2::fewer_registers<112>();
+    // ------------------------------------------------------------ epilogue
+    Tile t;
+    int used = 0, g = 0;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t r_free = tc2::in_cta(&sh.o_free, 0);
+    uint8_t* stage = smem + C::kStage + (warp & 3) * 4096;
+    for (int pass = 0; next_tile(pass, &t); ++pass) {
+      const int tok = t.tok0 + (int)rank * tok_cta + row / G;
+      const bool real = row < tok_cta * G && tok < t.a;
+      const int lim = real ? max(0, t.off + tok + 1) : 0;  // keys this row sees
       const unsigned rows = __ballot_sync(kFullMask, real);
-      uint8_t* stage = smem + C::kStage + warp * 4096;
-#pragma unroll
-      for (int i = 0; i < kPart; i += 64) {
+      const int64_t out = (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D;
+      float inv = 0.f;
+      bool dirty = false;
+      if (t.tiles > 0) {
+        const int h = g + t.tiles - 1;
+        bool w = tc::mbar_wait(&sh.sums_in[used & 1], (used >> 1) & 1) &&
+                 tc2::wait(&sh.flags_in[used & 1], (used >> 1) & 1);
+        const float total = sh.sums[used & 1][0][row] + sh.sums[used & 1][1][row];
+        inv = total == 0.f ? 0.f : 1.f / total;
+        dirty = sh.poison[used & 1][0] == (uint32_t)used + 1 || sh.poison[used & 1][1] == (uint32_t)used + 1;
+        w = w && tc::mbar_wait(&sh.o_ready[h & 1], (h >> 1) & 1);
+        tc::fence_after_sync();
+        if (!(ok = __all_sync(kFullMask, w) != 0)) break;
+      }
+      // 64 columns at a time, through shared memory: a thread has a row, but the rows
+      // leave as whole 128-byte lines (16 bytes a row and store cost 3 us a tile)
+#pragma unroll 1
+      for (int i = 0; i < D; i += 64) {
         float ov[64];
         if (t.tiles > 0) {
-          tc2::tmem_ld(tmem + lanes + C::kTmemO + part * kPart + i, ov);
+          tc2::tmem_ld(tmem + lanes + C::kTmemO + i, ov);
+          if (i == D - 64) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc2::arrive_remote_relaxed(r_free);  // O may be overwritten
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 64; ++k) ov[k] = 0.f;
         }
-        if (t.tiles > 0 && i == kPart - 64) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc2::arrive_remote_relaxed(r_free);  // O may be overwritten
-        }
 #pragma unroll
         for (int k = 0; k < 64; ++k) ov[k] *= inv;
         if (dirty && real) {
+          const int whole = t.off + t.tok0 + 1;
           const int first = max(0, whole) / kKeys * kKeys;  // first key of the tiles that were edited
-          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)t.kvh * D + part * kPart + i;
+          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)t.kvh * D + i;
           for (int key = first; key < lim; ++key) {
             const uint32_t* src = reinterpret_cast<const uint32_t*>(vr + ((int64_t)t.k0 + key) * p.v_stride);
 #pragma unroll
@@ -717,9 +585,172 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (t.tiles > 0) {
-        e += 2 * t.tiles;
         g += t.tiles;
         ++used;
+      }
+    }
+  } else {
+    tc2::fewer_registers<64>();
+    if (warp == kScheduleWarp) {
+      // ------------------------------------------------------------ schedule
+      const int pairs = gridDim.x / 2, me = blockIdx.x / 2;
+      Schedule sc;
+      sc.open(p, tokens, lane, blockIdx.x == 0);
+      for (int pass = 0;; ++pass) {
+        // pass by pass in alternating direction, so that the pairs' sums come out alike
+        const int64_t i = (int64_t)pass * pairs + ((pass & 1) ? pairs - 1 - me : me);
+        Tile t;
+        const bool more = sc.get(p, (int)(i / p.h_kv), (int)(i % p.h_kv), &t);
+        if (!more) t.tiles = -1;
+        if (pass >= 2 && !__all_sync(kFullMask, tc::mbar_wait(&sh.tile_empty[pass & 1], ((pass >> 1) - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          sh.tile[pass & 1] = t;
+          tc::mbar_arrive(&sh.tile_full[pass & 1]);
+        }
+        if (!more) break;
+      }
+    } else if (warp == kTmaWarp) {
+      // ------------------------------------------------------------ copies
+      Tile t;
+      int e = 0, used = 0;  // ring entries issued; tiles with Q
+      const uint32_t r_full = tc2::in_cta(sh.full, 0), r_q = tc2::in_cta(&sh.q_full, 0);
+      if (lane == 0) {
+        tc::prefetch_tmap(&tm_q);
+        tc::prefetch_tmap(&tm_k);
+        tc::prefetch_tmap(&tm_v);
+      }
+      for (int pass = 0; next_tile(pass, &t); ++pass) {
+        if (t.tiles == 0) continue;
+        if (lane == 0) {
+          const int whole = t.off + t.tok0 + 1;
+          if (used > 0) ok = tc::mbar_wait(&sh.q_empty, (used - 1) & 1);
+          if (ok) {
+            if (rank == 0) tc::mbar_arrive_expect_tx(&sh.q_full, 2u * (uint32_t)(tok_cta * G) * D * 2);
+            for (int kb = 0; kb < D / 64; ++kb)
+              tc2::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G,
+                               t.q0 + t.tok0 + (int)rank * tok_cta, r_q);
+          }
+          // The next ring entry, when it is empty.  The bytes of both CTAs count on
+          // the even CTA's barrier; those of V in an edge tile on the CTA's own, for
+          // the softmax warps that edit them there (whose arrival on p_ready then
+          // stands for the odd CTA's V).  The odd CTA's barrier keeps step.
+          auto slot = [&](bool here) -> uint8_t* {
+            const int s = e % C::kEntries;
+            if (e >= C::kEntries) ok = ok && tc::mbar_wait(&sh.empty[s], ((e / C::kEntries) - 1) & 1);
+            if (!ok) return nullptr;
+            if (here || rank == 0) tc::mbar_arrive_expect_tx(&sh.full[s], here ? C::kEntry : 2 * C::kEntry);
+            else tc::mbar_arrive(&sh.full[s]);
+            return smem + C::kRing + s * C::kEntry;
+          };
+          for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
+            if (j < t.tiles) {
+              if (uint8_t* dst = slot(false)) {
+                for (int kb = 0; kb < D / 64; ++kb)
+                  tc2::tma_load_3d(dst + kb * 8192, &tm_k, 64 * kb, t.kvh,
+                                   t.k0 + j * kKeys + (int)rank * 64, r_full + (e % C::kEntries) * 8);
+                ++e;
+              }
+            }
+            const int i = j - C::kLag;
+            if (i >= 0) {
+              const bool edge = (i + 1) * kKeys > whole;
+              if (uint8_t* dst = slot(edge)) {
+                const uint32_t bar = (edge ? tc2::in_cta(sh.full, rank) : r_full) + (e % C::kEntries) * 8;
+                for (int kb = 0; kb < D / 128; ++kb)
+                  tc2::tma_load_3d(dst + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
+                                   t.k0 + i * kKeys, bar);
+                ++e;
+              }
+            }
+          }
+        }
+        ++used;
+        ok = __all_sync(kFullMask, ok);
+        if (!ok) break;
+      }
+      // Copies still in flight land before the CTA ends: after an expired wait, the
+      // even CTA's barriers tell of both CTAs' copies (the odd one's own, of edge tiles).
+      if (lane == 0) {
+        for (int j = max(0, e - C::kEntries); j < e; ++j)
+          if (!tc::mbar_wait(&sh.full[j % C::kEntries], (j / C::kEntries) & 1)) ok = false;
+        if (rank == 0 && used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ products
+      Tile t;
+      int e = 0, used = 0, g = 0;  // ring entries, tiles with Q, key tiles so far
+      const uint32_t idesc_s = tc::idesc_bf16_f32(256, kKeys, false, false);
+      const uint32_t idesc_o = tc::idesc_bf16_f32(256, D, false, true);
+      const uint64_t dq = tc::smem_desc(sbase, 16, 1024, tc::kLayoutSw128);
+      const uint64_t dk = tc::smem_desc(sbase + C::kRing, 16, 1024, tc::kLayoutSw128);
+      const uint64_t dv = tc::smem_desc(sbase + C::kRing, 16384, 1024, tc::kLayoutSw128);
+      const bool leader = tc::elect_one();
+      auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool w = tc::mbar_wait(bar, parity);
+        tc::fence_after_sync();
+        return __all_sync(kFullMask, w) != 0;
+      };
+      auto entry = [&]() { return warp_wait(&sh.full[e % C::kEntries], (e / C::kEntries) & 1); };
+      // the even CTA's warp issues for the pair
+      for (int pass = 0; rank == 0 && next_tile(pass, &t); ++pass) {
+        if (t.tiles == 0) continue;
+        ok = warp_wait(&sh.q_full, used & 1);
+        const int whole = t.off + t.tok0 + 1;
+        for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
+          if (j < t.tiles) {  // S = Q K^T of key tile j
+            if (!(ok = entry())) break;
+            const int s = e % C::kEntries;
+            if (leader) {
+              const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
+#pragma unroll
+              for (int kk = 0; kk < C::kSteps; ++kk)
+                tc2::mma_ss(tmem + ((g + j) % C::kS) * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                            dk + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+              tc2::commit(&sh.s_ready[(g + j) % C::kS]);
+              tc2::commit(&sh.empty[s]);
+              if (j == t.tiles - 1) tc2::commit(&sh.q_empty);
+            }
+            __syncwarp();
+            ++e;
+          }
+          const int i = j - C::kLag;
+          if (i >= 0) {  // O += P V of key tile i
+            const int h = g + i;
+            if (!(ok = entry())) break;
+            const int s = e % C::kEntries;
+            // an edge tile's V was edited in both CTAs (ordinary writes): acquire those
+            const bool edge = (i + 1) * kKeys > whole;
+            uint64_t* pr = &sh.p_ready[h % C::kS];
+            const uint32_t ph = (h / C::kS) & 1;
+            bool w = edge ? tc2::wait(pr, ph) : tc::mbar_wait(pr, ph);
+            if (i == 0 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
+            tc::fence_after_sync();
+            if (!(ok = __all_sync(kFullMask, w) != 0)) break;
+            if (leader) {
+              const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                tc2::mma_ts(tmem + C::kTmemO, tmem + (h % C::kS) * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), dv + so + ((kk * 2048) >> 4),
+                            idesc_o, (i > 0) || (kk > 0));
+              tc2::commit(&sh.o_ready[h & 1]);
+              tc2::commit(&sh.empty[s]);
+            }
+            __syncwarp();
+            ++e;
+          }
+        }
+        if (!ok) break;
+        g += t.tiles;
+        ++used;
+      }
+      // every product issued has completed before either CTA leaves the barrier at the end
+      if (rank == 0) {
+        if (leader) tc2::commit(&sh.drained);
+        __syncwarp();
+        if (!warp_wait(&sh.drained, 0)) ok = false;
       }
     }
   }
