@@ -90,8 +90,7 @@ struct Cfg {
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
   static constexpr int kEntries = D == 256 ? 4 : 8;
   static constexpr uint32_t kRing = kQBytes;
-  static constexpr uint32_t kStage = kRing + kEntries * kEntry;  // o on its way out, 4 KB an epilogue warp
-  static constexpr uint32_t kShared = kStage + 4 * 4096;         // the barriers and the rest
+  static constexpr uint32_t kShared = kRing + kEntries * kEntry;  // the barriers and the rest
   static constexpr int kSteps = D / 16;
   static constexpr uint32_t kTmemO = kS * kKeys;
   static constexpr uint32_t kTmemCols = 512;
@@ -151,11 +150,23 @@ __device__ __forceinline__ float least(const float (&s)[N]) {
 }
 
 // ------------------------------------------------------------------ schedule
+// Division of non-negative numbers by the tokens of a tile (at least 2):
+// x floor(2^32 / d + 1) / 2^32 is at most one more than x / d.
+struct Divisor {
+  int d;
+  uint32_t inv;
+  __device__ __forceinline__ explicit Divisor(int by) : d(by), inv(0xffffffffu / (uint32_t)by + 1u) {}
+  __device__ __forceinline__ int divide(int x) const {
+    const int q = (int)__umulhi((uint32_t)x, inv);
+    return (int64_t)q * d > x ? q - 1 : q;
+  }
+};
+
 // One sequence's ranges (bad ones count no tiles; recorded once).
 struct Seq {
   int q0, k0, a, b, tiles;
 };
-__device__ __forceinline__ Seq sequence(const AttnPrefillArgs& p, int n, int tokens, bool report) {
+__device__ __forceinline__ Seq sequence(const AttnPrefillArgs& p, int n, Divisor tokens, bool report) {
   Seq s{0, 0, 0, 0, 0};
   if (n >= p.num_seqs) return s;
   const int q0 = __ldg(p.cu_q + n), q1 = __ldg(p.cu_q + n + 1);
@@ -169,15 +180,15 @@ __device__ __forceinline__ Seq sequence(const AttnPrefillArgs& p, int n, int tok
   s.k0 = k0;
   s.a = q1 - q0;
   s.b = k1 - k0;
-  s.tiles = (s.a + tokens - 1) / tokens;
+  s.tiles = s.a > 0 ? tokens.divide(s.a - 1) + 1 : 0;
   return s;
 }
 // Tiles of s that see at least x >= 1 keys (its later tiles see more); all of them for x <= 0.
-__device__ __forceinline__ int tiles_from(const Seq& s, int x, int tokens) {
+__device__ __forceinline__ int tiles_from(const Seq& s, int x, Divisor tokens) {
   if (x <= 0) return s.tiles;
   if (x > s.b || s.tiles == 0) return 0;
   const int need = x - (s.b - s.a);  // tokens up to the first one that sees x keys
-  const int skip = need <= 0 ? 0 : (need - 1) / tokens;
+  const int skip = need <= 0 ? 0 : tokens.divide(need - 1);
   return s.tiles - min(skip, s.tiles);
 }
 __device__ __forceinline__ Tile make_tile(const Seq& s, int i, int kvh, int tokens) {
@@ -218,17 +229,22 @@ struct Schedule {
   Seq s;       // this lane's sequence of the current 32
   int base;    // first sequence of the current 32
   int before;  // tiles of the sequences before them
-  int tokens, lane;
-  __device__ __forceinline__ void open(const AttnPrefillArgs& p, int toks, int ln, bool report) {
-    tokens = toks;
-    lane = ln;
-    base = before = 0;
+  int lane;
+  Divisor tokens;
+  __device__ __forceinline__ Schedule(const AttnPrefillArgs& p, int toks, int ln, bool report)
+      : base(0), before(0), lane(ln), tokens(toks) {
     s = sequence(p, lane, tokens, report);
     if (report)  // the other sequences' checks
       for (int n = 32 + lane; n < p.num_seqs; n += 32) sequence(p, n, tokens, true);
   }
   // tile number r (asked in increasing order) of KV head kvh; false past the end
   __device__ __forceinline__ bool get(const AttnPrefillArgs& p, int r, int kvh, Tile* t) {
+    if (p.num_seqs == 1) {  // one sequence: its last tile sees most
+      const Seq q = pick(s, 0);
+      if (r >= q.tiles) return false;
+      *t = make_tile(q, q.tiles - 1 - r, kvh, tokens.d);
+      return true;
+    }
     if (p.num_seqs <= 32) {
       if (r >= __reduce_add_sync(kFullMask, s.tiles)) return false;
       int lo = 0, hi = __reduce_max_sync(kFullMask, s.b) + 1;  // tiles_from(lo) > r >= tiles_from(hi)
@@ -244,7 +260,7 @@ struct Schedule {
       const int src = __ffs(hit) - 1;
       const Seq q = pick(s, src);
       *t = make_tile(q, q.tiles - __shfl_sync(kFullMask, at, src) + k - __shfl_sync(kFullMask, pre, src),
-                     kvh, tokens);
+                     kvh, tokens.d);
       return true;
     }
     for (;;) {
@@ -259,7 +275,7 @@ struct Schedule {
     const unsigned hit = __ballot_sync(kFullMask, r >= pre && r < pre + s.tiles);
     const int src = __ffs(hit) - 1;
     const Seq q = pick(s, src);
-    *t = make_tile(q, q.tiles - 1 - (r - __shfl_sync(kFullMask, pre, src)), kvh, tokens);
+    *t = make_tile(q, q.tiles - 1 - (r - __shfl_sync(kFullMask, pre, src)), kvh, tokens.d);
     return true;
   }
 };
@@ -305,6 +321,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&sh.drained, 1);
     tc::fence_mbar_init();
   }
+  if (warp == kScheduleWarp) {  // the first tile, while the pair gets ready
+    tc::wait_prerequisites();
+    Tile t;
+    if (!Schedule(p, tokens, lane, blockIdx.x == 0).get(p, (int)(blockIdx.x / 2) / p.h_kv, (int)(blockIdx.x / 2) % p.h_kv, &t))
+      t.tiles = -1;
+    if (lane == 0) sh.tile[0] = t;
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();
@@ -317,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // The warp's next tile (pass counts tiles); false at the end or when a wait expired.
   auto next_tile = [&](int pass, Tile* t) {
-    const bool w = __all_sync(kFullMask, tc::mbar_wait(&sh.tile_full[pass & 1], (pass >> 1) & 1));
+    // (the first is there from the start; of tile_full's phases it takes none)
+    const bool w = pass == 0 || __all_sync(kFullMask, tc::mbar_wait(&sh.tile_full[pass & 1], ((pass - 1) >> 1) & 1));
     if (!w) {
       ok = false;
       return false;
@@ -517,12 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t r_free = tc2::in_cta(&sh.o_free, 0);
-    uint8_t* stage = smem + C::kStage + (warp & 3) * 4096;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
     for (int pass = 0; next_tile(pass, &t); ++pass) {
       const int tok = t.tok0 + (int)rank * tok_cta + row / G;
       const bool real = row < tok_cta * G && tok < t.a;
       const int lim = real ? max(0, t.off + tok + 1) : 0;  // keys this row sees
-      const unsigned rows = __ballot_sync(kFullMask, real);
       const int64_t out = (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D;
       float inv = 0.f;
       bool dirty = false;
@@ -537,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         if (!(ok = __all_sync(kFullMask, w) != 0)) break;
       }
-      // 64 columns at a time, through shared memory: a thread has a row, but the rows
-      // leave as whole 128-byte lines (16 bytes a row and store cost 3 us a tile)
+      // 64 columns at a time; a thread has a row and stores 32 bytes of it at once
+      // (where o is aligned to that; its rows are)
 #pragma unroll 1
       for (int i = 0; i < D; i += 64) {
         float ov[64];
@@ -569,20 +592,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if (real) {
 #pragma unroll
-        for (int k = 0; k < 64; k += 8)
-          *reinterpret_cast<uint4*>(stage + lane * 128 + (((k / 8) ^ (lane & 7)) << 4)) =
-              make_uint4(pack_bf16(ov[k], ov[k + 1]), pack_bf16(ov[k + 2], ov[k + 3]),
-                         pack_bf16(ov[k + 4], ov[k + 5]), pack_bf16(ov[k + 6], ov[k + 7]));
-        __syncwarp();
+          for (int k = 0; k < 64; k += 16) {
+            uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = 4 * k + (lane >> 3), x = lane & 7;
-          const int64_t to = __shfl_sync(kFullMask, out, r) + i + 8 * x;
-          const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((x ^ (r & 7)) << 4));
-          if ((rows >> r) & 1) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + to) = y;
+            for (int x = 0; x < 8; ++x) w[x] = pack_bf16(ov[k + 2 * x], ov[k + 2 * x + 1]);
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + out + i + k;
+            if (wide) {
+              tc2::store32(to, w);
+            } else {
+              reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
         }
-        __syncwarp();
       }
       if (t.tiles > 0) {
         g += t.tiles;
@@ -594,13 +618,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kScheduleWarp) {
       // ------------------------------------------------------------ schedule
       const int pairs = gridDim.x / 2, me = blockIdx.x / 2;
-      Schedule sc;
-      sc.open(p, tokens, lane, blockIdx.x == 0);
-      for (int pass = 0;; ++pass) {
+      Schedule sc(p, tokens, lane, false);
+      bool more = sh.tile[0].tiles >= 0;
+      for (int pass = 1; more; ++pass) {
         // pass by pass in alternating direction, so that the pairs' sums come out alike
         const int64_t i = (int64_t)pass * pairs + ((pass & 1) ? pairs - 1 - me : me);
+        const int r = i <= INT32_MAX ? (int)i / p.h_kv : (int)(i / p.h_kv);
         Tile t;
-        const bool more = sc.get(p, (int)(i / p.h_kv), (int)(i % p.h_kv), &t);
+        more = sc.get(p, r, (int)(i - (int64_t)r * p.h_kv), &t);
         if (!more) t.tiles = -1;
         if (pass >= 2 && !__all_sync(kFullMask, tc::mbar_wait(&sh.tile_empty[pass & 1], ((pass >> 1) - 1) & 1))) {
           ok = false;
@@ -610,7 +635,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh.tile[pass & 1] = t;
           tc::mbar_arrive(&sh.tile_full[pass & 1]);
         }
-        if (!more) break;
       }
     } else if (warp == kTmaWarp) {
       // ------------------------------------------------------------ copies
@@ -681,7 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
       Tile t;
-      int e = 0, used = 0, g = 0;  // ring entries, tiles with Q, key tiles so far
+      int used = 0, g = 0;  // tiles with Q, key tiles so far
+      // next ring entry, score tiles to write and to read, and their barriers' phases
+      // (counted, not divided: the issue of a product waits for all of this)
+      uint32_t slot = 0, slot_ph = 0, sw = 0, sr = 0, sr_ph = 0;
       const uint32_t idesc_s = tc::idesc_bf16_f32(256, kKeys, false, false);
       const uint32_t idesc_o = tc::idesc_bf16_f32(256, D, false, true);
       const uint64_t dq = tc::smem_desc(sbase, 16, 1024, tc::kLayoutSw128);
@@ -693,7 +720,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         return __all_sync(kFullMask, w) != 0;
       };
-      auto entry = [&]() { return warp_wait(&sh.full[e % C::kEntries], (e / C::kEntries) & 1); };
+      auto next_slot = [&]() {
+        if (++slot == C::kEntries) {
+          slot = 0;
+          slot_ph ^= 1;
+        }
+      };
       // the even CTA's warp issues for the pair
       for (int pass = 0; rank == 0 && next_tile(pass, &t); ++pass) {
         if (t.tiles == 0) continue;
@@ -701,45 +733,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int whole = t.off + t.tok0 + 1;
         for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
           if (j < t.tiles) {  // S = Q K^T of key tile j
-            if (!(ok = entry())) break;
-            const int s = e % C::kEntries;
+            if (!(ok = warp_wait(&sh.full[slot], slot_ph))) break;
             if (leader) {
-              const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
+              const uint64_t kd = dk + ((slot * C::kEntry) >> 4);
 #pragma unroll
               for (int kk = 0; kk < C::kSteps; ++kk)
-                tc2::mma_ss(tmem + ((g + j) % C::kS) * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                            dk + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-              tc2::commit(&sh.s_ready[(g + j) % C::kS]);
-              tc2::commit(&sh.empty[s]);
+                tc2::mma_ss(tmem + sw * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                            kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+              tc2::commit(&sh.s_ready[sw]);
+              tc2::commit(&sh.empty[slot]);
               if (j == t.tiles - 1) tc2::commit(&sh.q_empty);
             }
             __syncwarp();
-            ++e;
+            if (++sw == C::kS) sw = 0;
+            next_slot();
           }
           const int i = j - C::kLag;
           if (i >= 0) {  // O += P V of key tile i
             const int h = g + i;
-            if (!(ok = entry())) break;
-            const int s = e % C::kEntries;
-            // an edge tile's V was edited in both CTAs (ordinary writes): acquire those
+            // an edge tile's V may have been edited in both CTAs (ordinary writes): acquire those
             const bool edge = (i + 1) * kKeys > whole;
-            uint64_t* pr = &sh.p_ready[h % C::kS];
-            const uint32_t ph = (h / C::kS) & 1;
-            bool w = edge ? tc2::wait(pr, ph) : tc::mbar_wait(pr, ph);
+            bool w = tc::mbar_wait(&sh.full[slot], slot_ph);
+            w = w && (edge ? tc2::wait(&sh.p_ready[sr], sr_ph) : tc::mbar_wait(&sh.p_ready[sr], sr_ph));
             if (i == 0 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
             tc::fence_after_sync();
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
             if (leader) {
-              const uint64_t so = (uint64_t)(s * C::kEntry) >> 4;
+              const uint64_t vd = dv + ((slot * C::kEntry) >> 4);
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc2::mma_ts(tmem + C::kTmemO, tmem + (h % C::kS) * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), dv + so + ((kk * 2048) >> 4),
+                tc2::mma_ts(tmem + C::kTmemO, tmem + sr * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), vd + ((kk * 2048) >> 4),
                             idesc_o, (i > 0) || (kk > 0));
               tc2::commit(&sh.o_ready[h & 1]);
-              tc2::commit(&sh.empty[s]);
+              tc2::commit(&sh.empty[slot]);
             }
             __syncwarp();
-            ++e;
+            if (++sr == C::kS) {
+              sr = 0;
+              sr_ph ^= 1;
+            }
+            next_slot();
           }
         }
         if (!ok) break;

@@ -104,6 +104,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// 32 bytes to a 32-byte aligned place in global memory.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Change the registers of every thread of the (converged) warpgroup.
 template <int N>
 __device__ __forceinline__ void more_registers() {
