@@ -23,9 +23,9 @@
 //
 // TMEM (512 columns): S of two or three key tiles (128 fp32 columns each, of whose
 // two halves P then takes 32 columns of bf16 pairs), O (D columns).  Shared memory:
-// Q (64 KB at D = 256), a ring of K and V tile halves in the order of their use,
-// K0 K1 V0 K2 V1 ..: the products of tile j + 1's scores run while the softmax
-// warps work on tile j.
+// Q (64 KB at D = 256), K and V halves of two or four key
+// tiles.  The scores of the next key tiles are computed while the softmax warps work
+// on one, and the products with V follow one or two key tiles behind.
 //
 // Roles (16 warps): 0-7 softmax, 8-11 epilogue (O to o while the next tile's scores
 // are under way), 12 TMA, 13 products (the even CTA's issues them for the pair), 14
@@ -88,9 +88,9 @@ struct Cfg {
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
   static constexpr uint32_t kQBytes = kRows * D * 2;
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
-  static constexpr int kEntries = D == 256 ? 4 : 8;
-  static constexpr uint32_t kRing = kQBytes;
-  static constexpr uint32_t kShared = kRing + kEntries * kEntry;  // the barriers and the rest
+  static constexpr int kSlots = D == 256 ? 2 : 4;  // key tiles of K, and of V, in shared memory
+  static constexpr uint32_t kK = kQBytes, kV = kK + kSlots * kEntry;
+  static constexpr uint32_t kShared = kV + kSlots * kEntry;  // the barriers and the rest
   static constexpr int kSteps = D / 16;
   static constexpr uint32_t kTmemO = kS * kKeys;
   static constexpr uint32_t kTmemCols = 512;
@@ -100,9 +100,10 @@ struct Cfg {
 template <int D>
 struct Shared {  // beside the tiles
   using C = Cfg<D>;
-  uint64_t full[C::kEntries], empty[C::kEntries];
-  uint64_t q_full, q_empty;
-  uint64_t s_ready[C::kS], p_ready[C::kS], o_ready[2], o_free;
+  // by key tile h: K, V of h % kSlots have landed; the scores of h, the product with V
+  // of h are done (h % kSlots; this frees their slots too); P of h is in TMEM (h % kS)
+  uint64_t k_full[C::kSlots], v_full[C::kSlots], s_done[C::kSlots], o_done[C::kSlots], p_ready[C::kS];
+  uint64_t q_full, q_empty, o_free;
   uint64_t m_ready[2][4];  // two groups: a key tile's references are in m, by quarters of the rows
   // of two tiles, for the epilogue: the rows' sums; that the other CTA's softmax warps
   // have told of what they found in V
@@ -297,18 +298,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc2::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < C::kEntries; ++i) {
-      tc::mbar_init(&sh.full[i], 1);
-      tc::mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(&sh.k_full[i], 1);
+      tc::mbar_init(&sh.v_full[i], 1);
+      tc::mbar_init(&sh.s_done[i], 1);
+      tc::mbar_init(&sh.o_done[i], 1);
     }
     tc::mbar_init(&sh.q_full, 1);
     tc::mbar_init(&sh.q_empty, 1);
-    for (int i = 0; i < C::kS; ++i) {
-      tc::mbar_init(&sh.s_ready[i], 1);
-      tc::mbar_init(&sh.p_ready[i], 2 * C::kPWarps);
-    }
+    for (int i = 0; i < C::kS; ++i) tc::mbar_init(&sh.p_ready[i], 2 * C::kPWarps);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sh.o_ready[i], 1);
       for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
       tc::mbar_init(&sh.sums_in[i], 8);
@@ -338,6 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::wait_prerequisites();  // q, k, v and the offsets come from earlier kernels
   tc::allow_dependents();
 
+  // wait for what a barrier by key tile says of key tile h
+  auto of_tile = [&](uint64_t* bars, int h) { return tc::mbar_wait(&bars[h % C::kSlots], (h / C::kSlots) & 1); };
+
   // The warp's next tile (pass counts tiles); false at the end or when a wait expired.
   auto next_tile = [&](int pass, Tile* t) {
     // (the first is there from the start; of tile_full's phases it takes none)
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc2::more_registers<168>();
     // ------------------------------------------------------------ softmax
     Tile t;
-    int e = 0, used = 0, g = 0;
+    int used = 0, g = 0;
     const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const int grp = C::kGroups > 1 ? part : 0, half = C::kHalves > 1 ? part : 0;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -382,14 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto key_tile = [&](int j, auto edge_tile) {
         constexpr bool edge = decltype(edge_tile)::value;
         const int h = g + j, key0 = j * kKeys, sb = h % C::kS;
-        bool w = carried && tc::mbar_wait(&sh.s_ready[sb], (h / C::kS) & 1);
+        bool w = carried && of_tile(sh.s_done, h);
         tc::fence_after_sync();
         bool edited = false, seen = false;
         if (edge) {  // this CTA's half of V: see the note at the top
-          const int v = e + min(t.tiles, j + C::kLag + 1) + j;  // ring entry of V
-          w = w && tc::mbar_wait(&sh.full[v % C::kEntries], (v / C::kEntries) & 1);
+          w = w && of_tile(sh.v_full, h);
           if (w) {
-            uint8_t* vt = smem + C::kRing + (v % C::kEntries) * C::kEntry;
+            uint8_t* vt = smem + C::kV + (h % C::kSlots) * C::kEntry;
 #pragma unroll
             for (int i = 0; i < (int)C::kEntry / 16 / (32 * C::kPWarps); ++i) {
               const int x = (tid % (32 * C::kPWarps)) + i * 32 * C::kPWarps, r = (x >> 3) & 127;
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) tc::mbar_arrive(&sh.m_ready[h & 1][warp & 3]);
         }
         if (j > 0 && __any_sync(kFullMask, grow)) {  // O holds the tiles before: rescale it
-          const bool v = __all_sync(kFullMask, tc::mbar_wait(&sh.o_ready[(h - 1) & 1], ((h - 1) >> 1) & 1));
+          const bool v = __all_sync(kFullMask, of_tile(sh.o_done, h - 1));
           tc::fence_after_sync();
           const float f = now == -INFINITY ? 0.f : ex2(now - next);
           if (v) {
@@ -528,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (told) tc2::arrive_remote(r_flags + (used & 1) * 8);
           else tc2::arrive_remote_relaxed(r_flags + (used & 1) * 8);
         }
-        e += 2 * t.tiles;
         g += t.tiles;
         ++used;
       }
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float total = sh.sums[used & 1][0][row] + sh.sums[used & 1][1][row];
         inv = total == 0.f ? 0.f : 1.f / total;
         dirty = sh.poison[used & 1][0] == (uint32_t)used + 1 || sh.poison[used & 1][1] == (uint32_t)used + 1;
-        w = w && tc::mbar_wait(&sh.o_ready[h & 1], (h >> 1) & 1);
+        w = w && of_tile(sh.o_done, h);
         tc::fence_after_sync();
         if (!(ok = __all_sync(kFullMask, w) != 0)) break;
       }
@@ -639,8 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kTmaWarp) {
       // ------------------------------------------------------------ copies
       Tile t;
-      int e = 0, used = 0;  // ring entries issued; tiles with Q
-      const uint32_t r_full = tc2::in_cta(sh.full, 0), r_q = tc2::in_cta(&sh.q_full, 0);
+      int g = 0, used = 0;  // key tiles, tiles with Q so far
+      int kc = 0, vc = 0;   // key tiles whose K, V were asked for
+      const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0);
+      const uint32_t my_v = tc2::in_cta(sh.v_full, rank), r_q = tc2::in_cta(&sh.q_full, 0);
       if (lane == 0) {
         tc::prefetch_tmap(&tm_q);
         tc::prefetch_tmap(&tm_k);
@@ -657,40 +659,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc2::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G,
                                t.q0 + t.tok0 + (int)rank * tok_cta, r_q);
           }
-          // The next ring entry, when it is empty.  The bytes of both CTAs count on
-          // the even CTA's barrier; those of V in an edge tile on the CTA's own, for
-          // the softmax warps that edit them there (whose arrival on p_ready then
-          // stands for the odd CTA's V).  The odd CTA's barrier keeps step.
-          auto slot = [&](bool here) -> uint8_t* {
-            const int s = e % C::kEntries;
-            if (e >= C::kEntries) ok = ok && tc::mbar_wait(&sh.empty[s], ((e / C::kEntries) - 1) & 1);
-            if (!ok) return nullptr;
-            if (here || rank == 0) tc::mbar_arrive_expect_tx(&sh.full[s], here ? C::kEntry : 2 * C::kEntry);
-            else tc::mbar_arrive(&sh.full[s]);
-            return smem + C::kRing + s * C::kEntry;
-          };
           for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
             if (j < t.tiles) {
-              if (uint8_t* dst = slot(false)) {
-                for (int kb = 0; kb < D / 64; ++kb)
-                  tc2::tma_load_3d(dst + kb * 8192, &tm_k, 64 * kb, t.kvh,
-                                   t.k0 + j * kKeys + (int)rank * 64, r_full + (e % C::kEntries) * 8);
-                ++e;
-              }
+              const int h = g + j, s = h % C::kSlots;
+              if (h >= C::kSlots && !(ok = of_tile(sh.s_done, h - C::kSlots))) break;
+              // the bytes of both CTAs count on the even CTA's barrier
+              if (rank == 0) tc::mbar_arrive_expect_tx(&sh.k_full[s], 2 * C::kEntry);
+#pragma unroll
+              for (int kb = 0; kb < D / 64; ++kb)
+                tc2::tma_load_3d(smem + C::kK + s * C::kEntry + kb * 8192, &tm_k, 64 * kb, t.kvh,
+                                 t.k0 + j * kKeys + (int)rank * 64, r_k + s * 8);
+              kc = h + 1;
             }
             const int i = j - C::kLag;
             if (i >= 0) {
+              const int h = g + i, s = h % C::kSlots;
+              if (h >= C::kSlots && !(ok = of_tile(sh.o_done, h - C::kSlots))) break;
+              // So do those of V, but in an edge tile they count on the CTA's own, for the
+              // softmax warps that look through them there (whose arrival on p_ready then
+              // stands for the odd CTA's V).  The odd CTA's barrier keeps step.
               const bool edge = (i + 1) * kKeys > whole;
-              if (uint8_t* dst = slot(edge)) {
-                const uint32_t bar = (edge ? tc2::in_cta(sh.full, rank) : r_full) + (e % C::kEntries) * 8;
-                for (int kb = 0; kb < D / 128; ++kb)
-                  tc2::tma_load_3d(dst + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
-                                   t.k0 + i * kKeys, bar);
-                ++e;
-              }
+              if (edge || rank == 0) tc::mbar_arrive_expect_tx(&sh.v_full[s], edge ? C::kEntry : 2 * C::kEntry);
+              else tc::mbar_arrive(&sh.v_full[s]);
+#pragma unroll
+              for (int kb = 0; kb < D / 128; ++kb)
+                tc2::tma_load_3d(smem + C::kV + s * C::kEntry + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
+                                 t.k0 + i * kKeys, (edge ? my_v : r_v) + s * 8);
+              vc = h + 1;
             }
           }
         }
+        g += t.tiles;
         ++used;
         ok = __all_sync(kFullMask, ok);
         if (!ok) break;
@@ -698,32 +697,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Copies still in flight land before the CTA ends: after an expired wait, the
       // even CTA's barriers tell of both CTAs' copies (the odd one's own, of edge tiles).
       if (lane == 0) {
-        for (int j = max(0, e - C::kEntries); j < e; ++j)
-          if (!tc::mbar_wait(&sh.full[j % C::kEntries], (j / C::kEntries) & 1)) ok = false;
+        for (int h = max(0, kc - C::kSlots); rank == 0 && h < kc; ++h) ok = of_tile(sh.k_full, h) && ok;
+        for (int h = max(0, vc - C::kSlots); h < vc; ++h) ok = of_tile(sh.v_full, h) && ok;
         if (rank == 0 && used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
       Tile t;
-      int used = 0, g = 0;  // tiles with Q, key tiles so far
-      // next ring entry, score tiles to write and to read, and their barriers' phases
+      int used = 0;  // tiles with Q so far
+      // slots of K and V, score tiles to write and to read, and their barriers' phases
       // (counted, not divided: the issue of a product waits for all of this)
-      uint32_t slot = 0, slot_ph = 0, sw = 0, sr = 0, sr_ph = 0;
+      uint32_t ks = 0, k_ph = 0, vs = 0, v_ph = 0, sw = 0, sr = 0, sr_ph = 0;
       const uint32_t idesc_s = tc::idesc_bf16_f32(256, kKeys, false, false);
       const uint32_t idesc_o = tc::idesc_bf16_f32(256, D, false, true);
       const uint64_t dq = tc::smem_desc(sbase, 16, 1024, tc::kLayoutSw128);
-      const uint64_t dk = tc::smem_desc(sbase + C::kRing, 16, 1024, tc::kLayoutSw128);
-      const uint64_t dv = tc::smem_desc(sbase + C::kRing, 16384, 1024, tc::kLayoutSw128);
+      const uint64_t dk = tc::smem_desc(sbase + C::kK, 16, 1024, tc::kLayoutSw128);
+      const uint64_t dv = tc::smem_desc(sbase + C::kV, 16384, 1024, tc::kLayoutSw128);
       const bool leader = tc::elect_one();
       auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
         const bool w = tc::mbar_wait(bar, parity);
         tc::fence_after_sync();
         return __all_sync(kFullMask, w) != 0;
       };
-      auto next_slot = [&]() {
-        if (++slot == C::kEntries) {
-          slot = 0;
-          slot_ph ^= 1;
+      auto step = [](uint32_t& i, uint32_t& ph, uint32_t n) {
+        if (++i == n) {
+          i = 0;
+          ph ^= 1;
         }
       };
       // the even CTA's warp issues for the pair
@@ -733,50 +732,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int whole = t.off + t.tok0 + 1;
         for (int j = 0; j < t.tiles + C::kLag && ok; ++j) {
           if (j < t.tiles) {  // S = Q K^T of key tile j
-            if (!(ok = warp_wait(&sh.full[slot], slot_ph))) break;
+            if (!(ok = warp_wait(&sh.k_full[ks], k_ph))) break;
             if (leader) {
-              const uint64_t kd = dk + ((slot * C::kEntry) >> 4);
+              const uint64_t kd = dk + ((ks * C::kEntry) >> 4);
 #pragma unroll
               for (int kk = 0; kk < C::kSteps; ++kk)
                 tc2::mma_ss(tmem + sw * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                             kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-              tc2::commit(&sh.s_ready[sw]);
-              tc2::commit(&sh.empty[slot]);
+              tc2::commit(&sh.s_done[ks]);
               if (j == t.tiles - 1) tc2::commit(&sh.q_empty);
             }
             __syncwarp();
             if (++sw == C::kS) sw = 0;
-            next_slot();
+            step(ks, k_ph, C::kSlots);
           }
           const int i = j - C::kLag;
           if (i >= 0) {  // O += P V of key tile i
-            const int h = g + i;
             // an edge tile's V may have been edited in both CTAs (ordinary writes): acquire those
             const bool edge = (i + 1) * kKeys > whole;
-            bool w = tc::mbar_wait(&sh.full[slot], slot_ph);
+            bool w = tc::mbar_wait(&sh.v_full[vs], v_ph);
             w = w && (edge ? tc2::wait(&sh.p_ready[sr], sr_ph) : tc::mbar_wait(&sh.p_ready[sr], sr_ph));
             if (i == 0 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
             tc::fence_after_sync();
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
             if (leader) {
-              const uint64_t vd = dv + ((slot * C::kEntry) >> 4);
+              const uint64_t vd = dv + ((vs * C::kEntry) >> 4);
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
                 tc2::mma_ts(tmem + C::kTmemO, tmem + sr * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), vd + ((kk * 2048) >> 4),
                             idesc_o, (i > 0) || (kk > 0));
-              tc2::commit(&sh.o_ready[h & 1]);
-              tc2::commit(&sh.empty[slot]);
+              tc2::commit(&sh.o_done[vs]);
             }
             __syncwarp();
-            if (++sr == C::kS) {
-              sr = 0;
-              sr_ph ^= 1;
-            }
-            next_slot();
+            step(sr, sr_ph, C::kS);
+            step(vs, v_ph, C::kSlots);
           }
         }
         if (!ok) break;
-        g += t.tiles;
         ++used;
       }
       // every product issued has completed before either CTA leaves the barrier at the end
