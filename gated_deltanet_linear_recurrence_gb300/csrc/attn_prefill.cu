@@ -58,8 +58,6 @@ namespace {
 
 constexpr int kKeys = 128;          // keys a tile
 constexpr int kRows = 128;          // rows a CTA
-// Four warpgroups: softmax (two), epilogue, and the rest.  A thread of them has 168,
-// 112 and 64 registers (setmaxnreg; together the 65,536 that the CTA starts with).
 constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14;
 constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
@@ -86,6 +84,13 @@ struct Cfg {
   static constexpr int kS = D == 256 ? 2 : 3;
   static constexpr int kLag = kS - 1;  // key tiles that the scores are ahead of P V
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
+  // Registers of a thread of the four warpgroups: softmax (two), epilogue, and 64 for
+  // the rest; together the 65,536 that the CTA starts with (setmaxnreg takes them
+  // from there).  At D = 128 a softmax thread's 128 scores want more than 168 (198
+  // against 222 us for seven packed prompts), and the epilogue reads fewer columns at once.
+  static constexpr int kSoftmaxRegs = D == 256 ? 168 : 184, kEpilogueRegs = D == 256 ? 112 : 80;
+  static constexpr int kOut = D == 256 ? 64 : 32;  // columns of O that the epilogue holds
+  static_assert(2 * kSoftmaxRegs + kEpilogueRegs + 64 == 512, "registers");
   static constexpr uint32_t kQBytes = kRows * D * 2;
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
   static constexpr int kSlots = D == 256 ? 2 : 4;  // key tiles of K, and of V, in shared memory
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < kEpilogueWarp) {
-    tc2::more_registers<168>();
+    tc2::more_registers<C::kSoftmaxRegs>();
     // ------------------------------------------------------------ softmax
     Tile t;
     int used = 0, g = 0;
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kTmaWarp) {
-    tc2::fewer_registers<112>();
+    tc2::fewer_registers<C::kEpilogueRegs>();
     // ------------------------------------------------------------ epilogue
     Tile t;
     int used = 0, g = 0;
@@ -560,24 +565,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         if (!(ok = __all_sync(kFullMask, w) != 0)) break;
       }
-      // 64 columns at a time; a thread has a row and stores 32 bytes of it at once
+      // kOut columns at a time; a thread has a row and stores 32 bytes of it at once
       // (where o is aligned to that; its rows are)
 #pragma unroll 1
-      for (int i = 0; i < D; i += 64) {
-        float ov[64];
+      for (int i = 0; i < D; i += C::kOut) {
+        float ov[C::kOut];
         if (t.tiles > 0) {
           tc2::tmem_ld(tmem + lanes + C::kTmemO + i, ov);
-          if (i == D - 64) {
+          if (i == D - C::kOut) {
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc2::arrive_remote_relaxed(r_free);  // O may be overwritten
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) ov[k] = 0.f;
+          for (int k = 0; k < C::kOut; ++k) ov[k] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < 64; ++k) ov[k] *= inv;
+        for (int k = 0; k < C::kOut; ++k) ov[k] *= inv;
         if (dirty && real) {
           const int whole = t.off + t.tok0 + 1;
           const int first = max(0, whole) / kKeys * kKeys;  // first key of the tiles that were edited
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int key = first; key < lim; ++key) {
             const uint32_t* src = reinterpret_cast<const uint32_t*>(vr + ((int64_t)t.k0 + key) * p.v_stride);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
+            for (int k = 0; k < C::kOut / 2; ++k) {
               const uint32_t two = __ldg(src + k);
               ov[2 * k] += poison_of(two & 0xffffu);
               ov[2 * k + 1] += poison_of(two >> 16);
@@ -594,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (real) {
 #pragma unroll
-          for (int k = 0; k < 64; k += 16) {
+          for (int k = 0; k < C::kOut; k += 16) {
             uint32_t w[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) w[x] = pack_bf16(ov[k + 2 * x], ov[k + 2 * x + 1]);
