@@ -386,69 +386,6 @@ def gdn_attn_decode(q, k_cache, v_cache, cache_len, scale=None, o=None, layout="
     return o
 
 
-_CACHE_DTYPES = {torch.bfloat16: _lib.GDN_CACHE_BF16, torch.float8_e4m3fn: _lib.GDN_CACHE_E4M3}
-
-
-def _token_stride(t, name):
-    """Elements between the tokens of t [T, heads, D]: the heads of a token lie side
-    by side, the tokens may be apart (a slice of a fused projection)."""
-    T, H, D = t.shape
-    if t.is_contiguous() or T <= 1 and H == 1 and t.stride(2) == 1:
-        return H * D
-    step, head, one = t.stride()
-    if one != 1 or (H > 1 and head != D):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return step if T > 1 else H * D
-
-
-def _int32_on_gpu(t, shape, name):
-    if not (t.dtype is torch.int32 and t.is_cuda and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{name} must be {list(shape)} int32 on the GPU, contiguous")
-
-
-def _bf16_on_gpu(t, shape, name, dense=False):
-    if not (t.dtype is torch.bfloat16 and t.is_cuda and t.shape == shape
-            and (not dense or t.is_contiguous())):
-        raise ValueError(f"{name} must be {list(shape)} bfloat16 on the GPU"
-                         + (", contiguous" if dense else ""))
-
-
-def _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp):
-    """(num_pages, h_kv, page_size, D, N, max_pages, dtype code) of a paged cache."""
-    shape, dtype = k_pages.shape, k_pages.dtype
-    code = _CACHE_DTYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {dtype}")
-    if not (len(shape) == 4 and v_pages.shape == shape and v_pages.dtype is dtype
-            and k_pages.is_contiguous() and v_pages.is_contiguous() and k_pages.is_cuda
-            and v_pages.is_cuda):
-        raise ValueError("k_pages / v_pages must be [num_pages, h_kv, page_size, D] of one dtype "
-                         "on the GPU, contiguous")
-    if code == _lib.GDN_CACHE_E4M3:
-        rows = shape[:3]
-        if (k_exp is None or v_exp is None
-                or not (k_exp.shape == rows and v_exp.shape == rows and k_exp.is_cuda
-                        and v_exp.is_cuda and k_exp.dtype is torch.uint8
-                        and v_exp.dtype is torch.uint8 and k_exp.is_contiguous()
-                        and v_exp.is_contiguous())):
-            raise ValueError("k_exp / v_exp must be [num_pages, h_kv, page_size] uint8 on the "
-                             "GPU, contiguous")
-    if not (page_table.dim() == 2 and page_table.dtype is torch.int32 and page_table.is_cuda
-            and page_table.is_contiguous()):
-        raise ValueError("page_table must be [num_seqs, max_pages] int32 on the GPU, contiguous")
-    return (*shape, *page_table.shape, code)
-
-
-def _keep_for(stream, *tensors):
-    """Tensors allocated here for a call on another stream than the current one must
-    not be given out again before that stream has passed the call."""
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        for t in tensors:
-            t.record_stream(stream)
-
-
 def gdn_kv_append(k, v, k_pages, v_pages, page_table, cu_seqlens, start_pos, k_exp=None,
                   v_exp=None, stream=None):
     """Write packed new rows into a paged cache, in place (gdn_kv_append in include/gdn.h):
@@ -457,19 +394,8 @@ def gdn_kv_append(k, v, k_pages, v_pages, page_table, cu_seqlens, start_pos, k_e
     or float8_e4m3fn with k_exp, v_exp [num_pages, h_kv, page_size] uint8 (each row's
     power of two, bias 127); page_table [N, max_pages], cu_seqlens [N+1], start_pos [N]
     int32 on the device.  k and v may be slices of a fused projection."""
-    lib = _lib.load()
-    P, h_kv, page, D, N, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
-    T = k.shape[0]
-    _bf16_on_gpu(k, (T, h_kv, D), "k")
-    _bf16_on_gpu(v, (T, h_kv, D), "v")
-    _int32_on_gpu(cu_seqlens, (N + 1,), "cu_seqlens")
-    _int32_on_gpu(start_pos, (N,), "start_pos")
-    st = lib.gdn_kv_append(k.data_ptr(), v.data_ptr(), _token_stride(k, "k"),
-                           _token_stride(v, "v"), k_pages.data_ptr(), v_pages.data_ptr(),
-                           _ptr(k_exp), _ptr(v_exp), page_table.data_ptr(), cu_seqlens.data_ptr(),
-                           start_pos.data_ptr(), N, T, h_kv, D, page, P, max_pages, dt,
-                           _stream(stream))
-    _lib.check(st, "gdn_kv_append")
+    _lib.binding().kv_append(k, v, k_pages, v_pages, page_table, cu_seqlens, start_pos, k_exp, v_exp,
+                             stream)
 
 
 def gdn_kv_gather(k_pages, v_pages, page_table, cu_seqlens, start_pos, total_tokens, k_exp=None,
@@ -477,26 +403,8 @@ def gdn_kv_gather(k_pages, v_pages, page_table, cu_seqlens, start_pos, total_tok
     """Read cached rows back as packed bf16 (gdn_kv_gather in include/gdn.h): rows
     start_pos[n] .. of each sequence, cu_seqlens[n+1] - cu_seqlens[n] of them, total_tokens
     in all.  Returns (k, v) [total_tokens, h_kv, D]; arguments as for gdn_kv_append."""
-    lib = _lib.load()
-    P, h_kv, page, D, N, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
-    T = int(total_tokens)
-    _int32_on_gpu(cu_seqlens, (N + 1,), "cu_seqlens")
-    _int32_on_gpu(start_pos, (N,), "start_pos")
-    made = []
-    if k is None:
-        made.append(k := torch.empty((T, h_kv, D), dtype=torch.bfloat16, device=k_pages.device))
-    if v is None:
-        made.append(v := torch.empty((T, h_kv, D), dtype=torch.bfloat16, device=k_pages.device))
-    _bf16_on_gpu(k, (T, h_kv, D), "k")
-    _bf16_on_gpu(v, (T, h_kv, D), "v")
-    st = lib.gdn_kv_gather(k.data_ptr(), v.data_ptr(), _token_stride(k, "k"),
-                           _token_stride(v, "v"), k_pages.data_ptr(), v_pages.data_ptr(),
-                           _ptr(k_exp), _ptr(v_exp), page_table.data_ptr(), cu_seqlens.data_ptr(),
-                           start_pos.data_ptr(), N, T, h_kv, D, page, P, max_pages, dt,
-                           _stream(stream))
-    _lib.check(st, "gdn_kv_gather")
-    _keep_for(stream, *made)
-    return k, v
+    return _lib.binding().kv_gather(k_pages, v_pages, page_table, cu_seqlens, start_pos, total_tokens,
+                                    k_exp, v_exp, k, v, stream)
 
 
 def gdn_attn_decode_paged_workspace_size(h_q, h_kv, head_dim):
@@ -510,28 +418,8 @@ def gdn_attn_decode_paged(q, k_pages, v_pages, page_table, cache_len, k_exp=None
     as for gdn_kv_append; cache_len [B] int32 on the device.  ``scale`` defaults to
     1/sqrt(D).  A workspace of gdn_attn_decode_paged_workspace_size() bytes is allocated
     when none is given.  Returns o [B, h_q, D] bf16."""
-    lib = _lib.load()
-    P, h_kv, page, D, B, max_pages, dt = _cache_shape(k_pages, v_pages, page_table, k_exp, v_exp)
-    h_q = q.shape[1]
-    _bf16_on_gpu(q, (B, h_q, D), "q")
-    _int32_on_gpu(cache_len, (B,), "cache_len")
-    made = []
-    if o is None:
-        made.append(o := torch.empty((B, h_q, D), dtype=torch.bfloat16, device=q.device))
-    _bf16_on_gpu(o, (B, h_q, D), "o", dense=True)
-    if workspace is None:
-        need = lib.gdn_attn_decode_paged_workspace_size(h_q, h_kv, D)
-        made.append(workspace := torch.empty(need, dtype=torch.uint8, device=q.device))
-    st = lib.gdn_attn_decode_paged(q.data_ptr(), _token_stride(q, "q"), k_pages.data_ptr(),
-                                   v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp),
-                                   page_table.data_ptr(), cache_len.data_ptr(), o.data_ptr(), B,
-                                   h_q, h_kv, D, page, P, max_pages, dt,
-                                   float(D ** -0.5 if scale is None else scale),
-                                   workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(stream))
-    _lib.check(st, "gdn_attn_decode_paged")
-    _keep_for(stream, *made)
-    return o
+    return _lib.binding().attn_decode_paged(q, k_pages, v_pages, page_table, cache_len, k_exp, v_exp,
+                                            scale, o, workspace, stream)
 
 
 def gdn_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=None, stream=None):
@@ -540,29 +428,7 @@ def gdn_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=Non
     the queries of sequence n (cu_seqlens_q) are the last of its positions (cu_seqlens_k,
     by default the same offsets: whole prompts).  q, k and v may be slices of a fused
     projection.  ``scale`` defaults to 1/sqrt(D).  Returns o [Tq, h_q, D]."""
-    lib = _lib.load()
-    if cu_seqlens_k is None:
-        cu_seqlens_k = cu_seqlens_q
-    Tq, h_q, D = q.shape
-    Tk, h_kv, _ = k.shape
-    N = cu_seqlens_q.numel() - 1
-    _bf16_on_gpu(q, (Tq, h_q, D), "q")
-    _bf16_on_gpu(k, (Tk, h_kv, D), "k")
-    _bf16_on_gpu(v, (Tk, h_kv, D), "v")
-    _int32_on_gpu(cu_seqlens_q, (N + 1,), "cu_seqlens_q")
-    _int32_on_gpu(cu_seqlens_k, (N + 1,), "cu_seqlens_k")
-    made = []
-    if o is None:
-        made.append(o := torch.empty((Tq, h_q, D), dtype=q.dtype, device=q.device))
-    _bf16_on_gpu(o, (Tq, h_q, D), "o", dense=True)
-    st = lib.gdn_attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                              cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), N, Tq, Tk, h_q,
-                              h_kv, D, _token_stride(q, "q"), _token_stride(k, "k"),
-                              _token_stride(v, "v"), _lib.GDN_BF16,
-                              float(D ** -0.5 if scale is None else scale), _stream(stream))
-    _lib.check(st, "gdn_attn_prefill")
-    _keep_for(stream, *made)
-    return o
+    return _lib.binding().attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, o, stream)
 
 
 def gdn_stream_status(stream=None):

@@ -1,13 +1,16 @@
-"""ctypes binding of the C ABI in include/gdn.h (argument marshalling only).
+"""Binding of the C ABI in include/gdn.h (argument marshalling only): ctypes, and for the
+attention layers' operators the extension built from csrc/attn_binding.cpp.
 
 Every step of the recurrence runs in the CUDA library; this module passes
 pointers, sizes and the stream handle through and turns status codes into
 exceptions.  There is no CPU path: if the library is missing, loading fails.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
-from .build import lib_path
+from .build import binding_path, lib_path
 
 GDN_OK = 0
 STATUS_NAMES = {
@@ -109,6 +112,27 @@ def load(path=None):
     if path is None:
         _LIB = lib
     return lib
+
+
+_BINDING = None
+
+
+def binding():
+    """The extension of the attention layers' operators (loaded once), calling the library."""
+    global _BINDING
+    if _BINDING is None:
+        lib, p = load(), binding_path()
+        if not os.path.exists(p):
+            raise RuntimeError(f"extension {p} is missing; build it first (python -c 'import "
+                               f"__graft_entry__ as g; g.build()')")
+        loader = importlib.machinery.ExtensionFileLoader("_attn_binding", p)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn_binding", loader))
+        loader.exec_module(mod)
+        mod.init(check, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                          ("gdn_kv_append", "gdn_kv_gather", "gdn_attn_decode_paged",
+                           "gdn_attn_decode_paged_workspace_size", "gdn_attn_prefill")))
+        _BINDING = mod
+    return _BINDING
 
 
 def check(status, where):

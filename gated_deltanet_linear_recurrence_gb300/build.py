@@ -3,12 +3,15 @@
 Compiles every ``csrc/*.cu`` translation unit with nvcc in parallel and links
 them into ``_build/libgdn_gb300.so``, an in-tree shared library exporting the
 C ABI of ``include/gdn.h``.  The CUDA runtime is linked statically; the
-library depends on the driver (libcuda) only at run time.
+library depends on the driver (libcuda) only at run time.  Beside it, with g++,
+``_build/_attn_binding.so``: the CPython extension through which torch tensors
+reach the attention layers' operators (``csrc/attn_binding.cpp``).
 """
 import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libgdn_gb300.so"
+BINDING_NAME = "_attn_binding.so"
+BINDING_SRC = os.path.join(CSRC, "attn_binding.cpp")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -23,6 +28,25 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompil
 
 def lib_path():
     return os.path.join(BUILD_DIR, LIB_NAME)
+
+
+def binding_path():
+    return os.path.join(BUILD_DIR, BINDING_NAME)
+
+
+def _binding_command(out):
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cxx = shutil.which("g++") or "c++"
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(base, "include"),
+            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", out,
+            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _nvcc():
@@ -73,9 +97,14 @@ def build(force=False, verbose=False, extra_flags=()):
             print(r.stdout + r.stderr)
         return r
 
+    binding, binding_tmp = binding_path(), binding_path() + f".tmp{os.getpid()}"
+    if force or _stale(binding, [BINDING_SRC] + headers):
+        jobs.append(_binding_command(binding_tmp))
     if jobs:
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
+    if os.path.exists(binding_tmp):
+        os.replace(binding_tmp, binding)
     out = lib_path()
     if force or jobs or _stale(out, objs):
         tmp = out + f".tmp{os.getpid()}"

@@ -99,7 +99,7 @@ def test_prompt_attention_refuses(lib):
     assert prompt(lib, tq=0) == 0 and prompt(lib, n=0, tq=0, tk=0, cq=None, ck=None) == 0
 
 
-def test_binding_refuses_before_the_library():
+def test_binding_refuses_before_the_library(lib):
     """Shapes, types and places that the binding checks (tensors on the CPU are refused)."""
     bf, i32 = torch.bfloat16, torch.int32
     pages = torch.zeros((4, 2, 16, 128), dtype=bf)
@@ -119,12 +119,17 @@ def test_binding_refuses_before_the_library():
         gdn.gdn_attn_prefill(k.float(), k.float(), k.float(), cu)
 
 
-def test_token_stride():
+def test_token_stride(lib):
+    stride = _lib.binding().token_stride
     fused = torch.zeros((5, 12, 128))
-    assert gdn._token_stride(fused, "x") == 12 * 128
-    assert gdn._token_stride(fused[:, 2:6], "x") == 12 * 128
-    assert gdn._token_stride(fused[:1, 2:6], "x") == 4 * 128  # one token: no step is taken
-    assert gdn._token_stride(fused[::2, 3:4], "x") == 24 * 128
-    for bad in (fused[..., ::2], fused[:, ::2], fused.transpose(0, 1)[:, :, :]):
+    assert stride(fused) == 12 * 128
+    assert stride(fused[:, 2:6]) == 12 * 128
+    assert stride(fused[:1, 2:6]) == 4 * 128  # one token: no step is taken
+    assert stride(fused[::2, 3:4]) == 24 * 128
+    for bad in (fused[..., ::2], fused[:, ::2], fused.transpose(0, 1)):
         with pytest.raises(ValueError):
-            gdn._token_stride(bad, "x")
+            stride(bad)
+    with pytest.raises(ValueError):
+        stride(fused[0])
+    with pytest.raises(TypeError):
+        stride(5)
