@@ -156,48 +156,61 @@ __device__ __forceinline__ int64_t span_of(int len) {
   return len > 0 ? kPieceCost + (uint32_t)(len + kUnit - 1) / kUnit : 0;
 }
 
-// Work of the sequences before `upto`, and of the whole batch, on every thread.
-template <int kT, int kUnit>
-__device__ __forceinline__ void count_work(const PagedAttnArgs& p, int upto, int64_t* before,
-                                            int64_t* total) {
-  __shared__ int64_t sums[2][kT / 32];
-  int64_t s = 0, all = 0;
-  for (int b = threadIdx.x; b < p.batch; b += kT) {
-    const int64_t u = p.cache.h_kv * span_of<kUnit>(length_of(p, b));
-    all += u;
-    if (b < upto) s += u;
-  }
+// Sums and largest values over a block's warps, on every thread (two barriers apart
+// from each other's use of `at`, one value a warp).
+template <int kT>
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* at) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    s += __shfl_xor_sync(kFullMask, s, off);
-    all += __shfl_xor_sync(kFullMask, all, off);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    sums[0][threadIdx.x >> 5] = s;
-    sums[1][threadIdx.x >> 5] = all;
-  }
+  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
+  if (lane == 0) at[threadIdx.x >> 5] = x;
   __syncthreads();
-  s = all = 0;
+  x = lane < kT / 32 ? at[lane] : 0;
 #pragma unroll
-  for (int w = 0; w < kT / 32; ++w) {
-    s += sums[0][w];
-    all += sums[1][w];
-  }
-  *before = s;
-  *total = all;
+  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
+  return x;
+}
+template <int kT>
+__device__ __forceinline__ float block_max(float x, float* at) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, off));
+  if (lane == 0) at[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = lane < kT / 32 ? at[lane] : -INFINITY;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, off));
+  return x;
+}
+template <int kT>
+__device__ __forceinline__ float block_sum(float x, float* at) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
+  if (lane == 0) at[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = lane < kT / 32 ? at[lane] : 0.f;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
+  return x;
+}
+
+// Quotient of non-negative numbers (those of 32 bits, nearly all, take the short way).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // The work of CTA c: the first `more` CTAs have size + 1 of it, the others size.
 struct Shares {
   int64_t size, more, split;
   __device__ __forceinline__ Shares(int64_t total, int ctas) {
-    size = total / ctas;
+    size = quotient(total, ctas);
     more = total - size * ctas;
     split = more * (size + 1);
   }
   __device__ __forceinline__ int64_t start(int c) const { return c * size + min((int64_t)c, more); }
   __device__ __forceinline__ int owner(int64_t u) const {
-    return u < split ? (int)(u / (size + 1)) : (int)(more + (u - split) / size);
+    return u < split ? (int)quotient(u, size + 1) : (int)(more + quotient(u - split, size));
   }
 };
 
@@ -219,54 +232,74 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
   __shared__ __align__(8) TileInfo infos[kWarps][kSlots];
   __shared__ float wm[kWarps][kHeads], wv[kWarps][kHeads], wl[kWarps][kHeads];
   __shared__ __align__(16) float joined[kWarps][kHeads][kPad];
-  __shared__ int64_t at_units;
-  __shared__ int at_seq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   tc::wait_prerequisites();  // q, the cache, its table and lengths come from earlier kernels
   tc::allow_dependents();    // the joining pass may be scheduled; it reads only the lengths early
 
   // ---- this CTA's share
   const int G = p.h_q / p.cache.h_kv;
-  const int per = (p.batch + kThreads - 1) / kThreads;  // sequences a thread counts
-  const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const int len = length_of(p, b);
-    if (blockIdx.x == 0 && len != __ldg(p.cache_len + b)) raise_error(p.err, kErrBadCacheLen);
-    mine += p.cache.h_kv * span_of<kUnit>(len);
-  }
-  __shared__ int64_t scan[kWarps];
-  int64_t incl = mine;
+  int64_t total = 0, u, u_end, base;  // all work, this CTA's, and that before its first sequence
+  int b;                              // its first sequence
+  if (p.batch <= 32) {  // a lane counts a sequence, each warp for itself
+    const int len = lane < p.batch ? length_of(p, lane) : 0;
+    if (blockIdx.x == 0 && lane < p.batch && len != __ldg(p.cache_len + lane)) raise_error(p.err, kErrBadCacheLen);
+    const int64_t mine = p.cache.h_kv * span_of<kUnit>(len);
+    int64_t incl = mine;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t y = __shfl_up_sync(kFullMask, incl, off);
-    if (lane >= off) incl += y;
-  }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  int64_t total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const Shares sh(total, gridDim.x);
-  const int64_t u_start = sh.start(blockIdx.x), u_end = sh.start(blockIdx.x + 1);
-  if (u_start == u_end) return;
-  int64_t u = u_start;
-  if (before <= u && u < before + mine) {
-    int b = b_lo;
-    for (;; ++b) {
-      const int64_t n = p.cache.h_kv * span_of<kUnit>(length_of(p, b));
-      if (u < before + n) break;
-      before += n;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(kFullMask, incl, off);
+      if (lane >= off) incl += y;
     }
-    at_seq = b;
-    at_units = before;
+    total = __shfl_sync(kFullMask, incl, 31);
+    const Shares sh(total, gridDim.x);
+    u = sh.start(blockIdx.x);
+    u_end = sh.start(blockIdx.x + 1);
+    if (u == u_end) return;
+    b = __ffs(__ballot_sync(kFullMask, incl > u)) - 1;
+    base = __shfl_sync(kFullMask, incl - mine, b);
+  } else {
+    __shared__ int64_t scan[kWarps], at_units;
+    __shared__ int at_seq;
+    const int per = (p.batch + kThreads - 1) / kThreads;  // sequences a thread counts
+    const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
+    int64_t mine = 0;
+    for (int i = b_lo; i < b_hi; ++i) {
+      const int len = length_of(p, i);
+      if (blockIdx.x == 0 && len != __ldg(p.cache_len + i)) raise_error(p.err, kErrBadCacheLen);
+      mine += p.cache.h_kv * span_of<kUnit>(len);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(kFullMask, incl, off);
+      if (lane >= off) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    const Shares sh(total, gridDim.x);
+    u = sh.start(blockIdx.x);
+    u_end = sh.start(blockIdx.x + 1);
+    if (u == u_end) return;
+    if (before <= u && u < before + mine) {
+      int i = b_lo;
+      for (;; ++i) {
+        const int64_t n = p.cache.h_kv * span_of<kUnit>(length_of(p, i));
+        if (u < before + n) break;
+        before += n;
+      }
+      at_seq = i;
+      at_units = before;
+    }
+    __syncthreads();
+    b = at_seq;
+    base = at_units;
   }
-  __syncthreads();
-  int b = at_seq;
-  int64_t base = at_units;
 
   const uint32_t ring = tc::smem_u32(smem) + warp * kRing;
   const int quad = lane >> 2, pair = lane & 3;  // fragment row, and column pair
@@ -286,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
         len = length_of(p, ++b);
         continue;
       }
-      j = (int)((u - base) / span);
+      j = (int)quotient(u - base, span);
       const int64_t r0 = u - base - j * span, r1 = min(span, r0 + (u_end - u));
       u += r1 - r0;
       if (r1 <= kPieceCost) continue;
@@ -382,51 +415,59 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
     }
   };
 
+  // The piece's q, as it is: pairs of dims in the order in which a row's arrive
+  // (bf16 2 pair, + 1, 2 pair + 8, + 9 of sixteen; e4m3 4 pair .. + 3).
+  uint32_t qf[kQ][2];
+  auto load_q = [&]() {
+    const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)seq * p.q_stride +
+                                ((int64_t)j * G + quad) * D;
+#pragma unroll
+    for (int kk = 0; kk < kQ; ++kk) {
+      uint2 x = make_uint2(0, 0);
+      if (quad < G) {
+        if (kFp8) {
+          x = __ldg(reinterpret_cast<const uint2*>(qrow + 16 * kk + 4 * pair));
+        } else {
+          x.x = __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 2 * pair));
+          x.y = __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 2 * pair + 8));
+        }
+      }
+      qf[kk][0] = x.x;
+      qf[kk][1] = x.y;
+    }
+  };
+
   uint32_t get = 0;  // ring entry to use
   bool more = next_piece();
-  if (more) open();
+  if (more) {
+    load_q();  // ahead of the copies: behind every CTA's first ones it took 2 us
+    open();
+  }
   while (more) {
     const int64_t head0 = (int64_t)seq * p.h_q + (int64_t)j * G;
     // ---- Q^T as the products' B operand: head `quad`, zeros past G
-    uint32_t qf[kQ][2];
     float unit0 = score_unit, unit1 = score_unit;  // of heads 2 pair, 2 pair + 1
-    {
-      const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)seq * p.q_stride +
-                                  ((int64_t)j * G + quad) * D;
-      if (!kFp8) {
+    if (kFp8) {
+      // scaled by a power of two per head so that f16 holds what bf16 held (down to
+      // 2^-38 of the head's largest)
+      float top = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < kQ; ++kk) {
-          const uint32_t* s = reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 2 * pair);
-          qf[kk][0] = quad < G ? __ldg(s) : 0u;
-          qf[kk][1] = quad < G ? __ldg(s + 4) : 0u;
-        }
-      } else {
-        // dims 16 kk + 4 pair .. + 3 in two registers, the order in which the
-        // widened codes of a row arrive; scaled by a power of two per head so
-        // that f16 holds what bf16 held (down to 2^-38 of the head's largest)
-        float top = 0.f;
+      for (int kk = 0; kk < kQ; ++kk)
 #pragma unroll
-        for (int kk = 0; kk < kQ; ++kk) {
-          uint2 x = make_uint2(0, 0);
-          if (quad < G) x = __ldg(reinterpret_cast<const uint2*>(qrow + 16 * kk + 4 * pair));
-          qf[kk][0] = x.x;
-          qf[kk][1] = x.y;
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(x.x << 16)), fabsf(__uint_as_float(x.x & 0xffff0000u))),
-                                 fmaxf(fabsf(__uint_as_float(x.y << 16)), fabsf(__uint_as_float(x.y & 0xffff0000u)))));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-        const int e = min(max((int)(__float_as_uint(top) >> 23), 16), 240) - 127 - 14;
-        const float inv = pow2(-e), unit = pow2(e);
+        for (int r = 0; r < 2; ++r)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[kk][r] << 16)), fabsf(__uint_as_float(qf[kk][r] & 0xffff0000u))));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+      const int e = min(max((int)(__float_as_uint(top) >> 23), 16), 240) - 127 - 14;
+      const float inv = pow2(-e), unit = pow2(e);
 #pragma unroll
-        for (int kk = 0; kk < kQ; ++kk)
+      for (int kk = 0; kk < kQ; ++kk)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            qf[kk][r] = pack_f16(__uint_as_float(qf[kk][r] << 16) * inv,
-                                 __uint_as_float(qf[kk][r] & 0xffff0000u) * inv);
-        unit0 *= __shfl_sync(kFullMask, unit, 8 * pair);
-        unit1 *= __shfl_sync(kFullMask, unit, 8 * pair + 4);
-      }
+        for (int r = 0; r < 2; ++r)
+          qf[kk][r] = pack_f16(__uint_as_float(qf[kk][r] << 16) * inv,
+                               __uint_as_float(qf[kk][r] & 0xffff0000u) * inv);
+      unit0 *= __shfl_sync(kFullMask, unit, 8 * pair);
+      unit1 *= __shfl_sync(kFullMask, unit, 8 * pair + 4);
     }
 
     float o[kQ][4];
@@ -703,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
       }
       __syncthreads();
     }
+    if (more) load_q();
   }
 }
 
@@ -711,22 +753,29 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
 // with each CTA's o_s already divided by its l_s.  Also writes the zeros of a
 // sequence without cached rows.  One block per (sequence, KV head, query head):
 // with up to kFew splits the block of the first query head does all of them, a warp
-// each (batches: nearly every item has two); with more, each block its own, D / 4
-// lanes a row of four values each, the splits dealt to the groups of lanes, eight
-// loads in flight in each.
+// each (batches: nearly every item has two); with more, each block its own (kSlices
+// blocks, a part of the dims each), a lane four values of a row, the splits dealt to
+// the groups of lanes, eight loads in flight in each.
 constexpr int kFew = 16;
-template <int D, int kUnit, int kJoinThreads>
+template <int D, int kUnit, int kJoinThreads, int kSlices>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const PagedAttnArgs p) {
-  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  constexpr int kRow = D / 4, kLanes = kRow / kSlices, kGroups = kJoinThreads / kLanes;
   __shared__ float w_sm[kPagedMaxCtas];
+  __shared__ int64_t sums[2][kJoinThreads / 32];
   __shared__ float red[2][kJoinThreads / 32];
   __shared__ float4 sum_sm[kGroups][kLanes];
   tc::allow_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h_kv = p.cache.h_kv, G = p.h_q / h_kv;
   const int b = blockIdx.x / h_kv, j = blockIdx.x % h_kv;
-  int64_t base, total;
-  count_work<kJoinThreads, kUnit>(p, b, &base, &total);
+  int64_t base = 0, total = 0;  // work of the sequences before this one, and of all
+  for (int i = tid; i < p.batch; i += kJoinThreads) {
+    const int64_t u = h_kv * span_of<kUnit>(length_of(p, i));
+    total += u;
+    if (i < b) base += u;
+  }
+  if (p.batch > 1) base = block_sum<kJoinThreads>(base, sums[0]);
+  total = p.batch > 1 ? block_sum<kJoinThreads>(total, sums[1]) : h_kv * span_of<kUnit>(length_of(p, 0));
   const int64_t span = span_of<kUnit>(length_of(p, b));
   const int64_t first = base + (int64_t)j * span + kPieceCost, end = base + (int64_t)(j + 1) * span;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)b * p.h_q + (int64_t)j * G) * D;
@@ -735,7 +784,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
   const int n = c_hi - c_lo + 1;
   tc::wait_prerequisites();
   if (span == 0) {
-    if (tid < D) o[blockIdx.y * D + tid] = __float2bfloat16_rn(0.f);
+    if (tid < D && blockIdx.z == 0) o[blockIdx.y * D + tid] = __float2bfloat16_rn(0.f);
     return;
   }
   if (n == 1) return;  // written by its CTA
@@ -758,7 +807,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
   };
   if (n <= kFew) {
     const int h = warp;
-    if (blockIdx.y > 0 || h >= G) return;
+    if (blockIdx.y > 0 || blockIdx.z > 0 || h >= G) return;
     float2 ml = lane < n ? ml_in[part(lane, h)] : make_float2(-INFINITY, 0.f);
     float4 a[D / 128];
 #pragma unroll
@@ -774,18 +823,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
     for (int s = 0; s < n; ++s) {
       const float f = __shfl_sync(kFullMask, w, s);
 #pragma unroll
-      for (int k = 0; k < D / 128; ++k) add(a[k], f, acc_in[part(s, h) * kLanes + 32 * k + lane]);
+      for (int k = 0; k < D / 128; ++k) add(a[k], f, acc_in[part(s, h) * kRow + 32 * k + lane]);
     }
 #pragma unroll
     for (int k = 0; k < D / 128; ++k) store(h, 32 * k + lane, a[k], den);
     return;
   }
-  const int d4 = tid % kLanes, grp = tid / kLanes, h = blockIdx.y;
+  const int d4 = tid % kLanes + blockIdx.z * kLanes, grp = tid / kLanes, h = blockIdx.y;
   float4 x[8];  // the first loads go out before the weights are known
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int s = grp + k * kGroups;
-    x[k] = s < n ? acc_in[part(s, h) * kLanes + d4] : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[k] = s < n ? acc_in[part(s, h) * kRow + d4] : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   constexpr int kMine = (kPagedMaxCtas + kJoinThreads - 1) / kJoinThreads;  // splits a thread
   float2 ml[kMine];
@@ -796,13 +845,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
     ml[k] = s < n ? ml_in[part(s, h)] : make_float2(-INFINITY, 0.f);
     mx = fmaxf(mx, ml[k].x);
   }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, off));
-  if (lane == 0) red[0][warp] = mx;
-  __syncthreads();
-  mx = red[0][0];
-#pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[0][w]);
+  mx = block_max<kJoinThreads>(mx, red[0]);
   float den = 0.f;
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
@@ -810,25 +853,19 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
     if (tid + k * kJoinThreads < n) w_sm[tid + k * kJoinThreads] = w;
     den += w;
   }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(kFullMask, den, off);
-  if (lane == 0) red[1][warp] = den;
-  __syncthreads();
+  den = block_sum<kJoinThreads>(den, red[1]);  // and every thread's weights are in w_sm
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     if (grp + k * kGroups < n) add(a, w_sm[grp + k * kGroups], x[k]);
 #pragma unroll 8
-  for (int s = grp + 8 * kGroups; s < n; s += kGroups) add(a, w_sm[s], acc_in[part(s, h) * kLanes + d4]);
-  sum_sm[grp][d4] = a;
+  for (int s = grp + 8 * kGroups; s < n; s += kGroups) add(a, w_sm[s], acc_in[part(s, h) * kRow + d4]);
+  sum_sm[grp][tid % kLanes] = a;
   __syncthreads();
   if (grp > 0) return;
-  den = 0.f;
-#pragma unroll
-  for (int i = 0; i < kJoinThreads / 32; ++i) den += red[1][i];
 #pragma unroll
   for (int g = 1; g < kGroups; ++g) {
-    const float4 y = sum_sm[g][d4];
+    const float4 y = sum_sm[g][tid % kLanes];
     a.x += y.x;
     a.y += y.y;
     a.z += y.z;
@@ -864,11 +901,12 @@ cudaError_t launch_paged(const PagedAttnArgs& args, cudaStream_t stream) {
   // Few rows of o have many splits each: more loads in flight.  A batch's rows have
   // few, and small blocks let more of them run at once.
   if ((int64_t)args.batch * args.h_q <= 64) {
-    cfg.blockDim = dim3(1024);
-    return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 1024>, args);
+    cfg.gridDim.z = 4;
+    cfg.blockDim = dim3(512);
+    return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 512, 4>, args);
   }
   cfg.blockDim = dim3(256);
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 256>, args);
+  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 256, 1>, args);
 }
 
 }  // namespace
