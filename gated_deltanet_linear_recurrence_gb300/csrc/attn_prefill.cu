@@ -29,15 +29,15 @@
 //
 // Roles (16 warps): 0-7 softmax, 8-11 epilogue (O to o while the next tile's scores
 // are under way), 12 TMA, 13 products (the even CTA's issues them for the pair), 14
-// the schedule.  The pairs are persistent.
+// the schedule, 15 V of edge tiles.  The pairs are persistent.
 //
 // Rounding: P is rounded to bf16 for the second product (relative 2^-9 a weight,
 // the same as the output's rounding; the sums l stay fp32 over unrounded weights).
 //
 // What a query does not see must not reach it even as NaN: its scores are masked,
-// and in a tile that some row sees in part, non-finite values of V are replaced by
-// zero in shared memory; the epilogue adds them back to the rows that do see them
-// (from global memory, only in tiles where any was found).
+// and in a tile that some row sees in part (an edge tile), warp 15 replaces non-finite
+// values of V by zero in shared memory; the epilogue adds them back to the rows that do
+// see them (from global memory, only in tiles where any was found).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -45,7 +45,6 @@
 #include <stdint.h>
 
 #include <mutex>
-#include <type_traits>
 
 #include "attn_params.h"
 #include "attn_tc.cuh"
@@ -58,7 +57,7 @@ namespace {
 
 constexpr int kKeys = 128;          // keys a tile
 constexpr int kRows = 128;          // rows a CTA
-constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14;
+constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14, kEdgeWarp = 15;
 constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
 constexpr float kLog2e = 1.4426950408889634f;
@@ -110,12 +109,16 @@ struct Shared {  // beside the tiles
   uint64_t k_full[C::kSlots], v_full[C::kSlots], s_done[C::kSlots], o_done[C::kSlots], p_ready[C::kS];
   uint64_t q_full, q_empty, o_free;
   uint64_t m_ready[2][4];  // two groups: a key tile's references are in m, by quarters of the rows
-  // of two tiles, for the epilogue: the rows' sums; that the other CTA's softmax warps
-  // have told of what they found in V
-  uint64_t sums_in[2], flags_in[2];
+  // edge tiles, counted through (% kSlots): the CTA's V has landed; V is finite in both CTAs
+  uint64_t v_edge[C::kSlots], v_clean[C::kSlots];
+  uint64_t sums_in[2];          // the rows' sums of two tiles are there, for the epilogue
+  // What was found in V in the edge tiles of a tile (by number & 3: the schedule's two
+  // tiles bound how far this runs ahead of the epilogue): the number + 1 where that was
+  // a non-finite value, by halves of the dimensions; that both CTAs have told of it.
+  uint64_t flags_in[4];
+  uint32_t poison[4][2];
   uint64_t tile_full[2], tile_empty[2], drained;
   Tile tile[2];
-  uint32_t poison[2][2];  // [pass parity][half of the dimensions]: pass + 1 where V had a non-finite
   uint32_t tmem;
   // halves: the row maxima of a key tile's halves, two key tiles; groups: the
   // references of two key tiles
@@ -316,10 +319,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
       tc::mbar_init(&sh.sums_in[i], 8);
-      tc::mbar_init(&sh.flags_in[i], 8);
-      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products'
-      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 2 : 1));
+      // readers: the softmax, epilogue, TMA and edge warps, and in the even CTA the products'
+      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : 2));
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sh.flags_in[i], 2);
       sh.poison[i][0] = sh.poison[i][1] = 0;
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(&sh.v_edge[i], 1);
+      tc::mbar_init(&sh.v_clean[i], 2);
     }
     tc::mbar_init(&sh.o_free, 2 * 4);
     tc::mbar_init(&sh.drained, 1);
@@ -371,7 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale == 0.f ? 1e-30f : p.scale * kLog2e;
     const bool down = c < 0.f;  // the largest score is then the smallest product
     const uint32_t r_p = tc2::in_cta(sh.p_ready, 0);
-    const uint32_t r_flags = tc2::in_cta(sh.flags_in, rank ^ 1), r_poison = tc2::in_cta(sh.poison, rank ^ 1);
     bool carried = true;  // no wait expired since the last barrier of these warps
     for (int pass = 0;; ++pass) {
       // all softmax warps go on or none: they meet at barriers without a limit
@@ -382,53 +390,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = real ? max(0, t.off + tok + 1) : 0;  // keys this row sees
       const int whole = t.off + t.tok0 + 1;                // keys that every row of the pair sees
       float m = -INFINITY, l = 0.f;
-      bool told = false;  // the other CTA was told of a non-finite value
       // with two groups, this one takes every other key tile (g counts them through)
-      // (a tile without an edge, most of them, in code of its own: selections for the
-      // mask would otherwise be issued with every tile)
-      auto key_tile = [&](int j, auto edge_tile) {
-        constexpr bool edge = decltype(edge_tile)::value;
+      auto key_tile = [&](int j) {
         const int h = g + j, key0 = j * kKeys, sb = h % C::kS;
         bool w = carried && of_tile(sh.s_done, h);
         tc::fence_after_sync();
-        bool edited = false, seen = false;
-        if (edge) {  // this CTA's half of V: see the note at the top
-          w = w && of_tile(sh.v_full, h);
-          if (w) {
-            uint8_t* vt = smem + C::kV + (h % C::kSlots) * C::kEntry;
-#pragma unroll
-            for (int i = 0; i < (int)C::kEntry / 16 / (32 * C::kPWarps); ++i) {
-              const int x = (tid % (32 * C::kPWarps)) + i * 32 * C::kPWarps, r = (x >> 3) & 127;
-              uint4* at = reinterpret_cast<uint4*>(vt + (x >> 10) * 16384 + r * 128 + (x & 7) * 16);
-              const uint4 y = *at;
-              const uint32_t a0 = __vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u), a1 = __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u),
-                             a2 = __vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u), a3 = __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u);
-              if (a0 | a1 | a2 | a3) {
-                edited = true;
-                seen = seen || key0 + r < t.sight;
-                *at = make_uint4(y.x & ~a0, y.y & ~a1, y.z & ~a2, y.w & ~a3);
-              }
-            }
-            if (seen) {
-              sh.poison[used & 1][rank] = (uint32_t)used + 1;
-              tc2::store_remote(r_poison + ((used & 1) * 2 + rank) * 4, (uint32_t)used + 1);
-            }
-          }
-          edited = __any_sync(kFullMask, edited);
-          told = told || edited;
-        }
         w = __all_sync(kFullMask, w);
-        const int left = lim - key0 - C::kCols * half;  // columns of this thread that the row sees
         const float none = down ? INFINITY : -INFINITY;
         const uint32_t scores = tmem + lanes + sb * kKeys + C::kCols * half;
-        float s[64];  // 64 of the thread's scores
-        auto fetch = [&](int k) {
-          tc2::tmem_ld(scores + k, s);
-          if (edge) {
+        if (key0 + kKeys > whole) {
+          // An edge tile: the scores that a row does not see are overwritten.  One short
+          // loop before code that all tiles share: with the masks inside an unrolled copy
+          // of that code, its instructions (run once a tile of queries, so never near)
+          // took 4,500 cycles where a tile without an edge takes 1,700.
+          const int left = lim - key0 - C::kCols * half;  // columns of this thread that the row sees
+          const int all = __reduce_min_sync(kFullMask, left);
+#pragma unroll 1
+          for (int k = max(0, all) & ~31; k < C::kCols; k += 32) {
+            float x[32];
+            tc::tmem_ld32(scores + k, x);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = k + i < left ? s[i] : none;
+            for (int i = 0; i < 32; ++i) x[i] = i < left - k ? x[i] : none;
+            tc::tmem_st32(scores + k, x);
           }
-        };
+        }
+        float s[64];  // 64 of the thread's scores
+        auto fetch = [&](int k) { tc2::tmem_ld(scores + k, s); };
         fetch(C::kCols - 64);
         float x = down ? least(s) : largest(s);
         if (C::kCols > 64) {
@@ -506,19 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         l0 = tc2::add2(l0, l1);
         l += l0.x + l0.y;
         tc::fence_before_sync();
-        if (edge && edited) {
-          tc::fence_proxy_async();  // the edited V rows -> the tensor core
-          __syncwarp();
-          if (lane == 0) tc2::arrive_remote(r_p + sb * 8);
-        } else {
-          __syncwarp();
-          if (lane == 0) tc2::arrive_remote_relaxed(r_p + sb * 8);
-        }
+        __syncwarp();
+        if (lane == 0) tc2::arrive_remote_relaxed(r_p + sb * 8);
       };
-      for (int j = C::kGroups > 1 ? (g ^ grp) & 1 : 0; j < t.tiles && ok; j += C::kGroups) {
-        if ((j + 1) * kKeys > whole) key_tile(j, std::true_type());
-        else key_tile(j, std::false_type());
-      }
+      for (int j = C::kGroups > 1 ? (g ^ grp) & 1 : 0; j < t.tiles && ok; j += C::kGroups) key_tile(j);
       // ---- the pair's rows are through their keys: their sums go to the epilogue
       if (t.tiles > 0) {
         if (C::kGroups > 1) {
@@ -529,11 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         sh.sums[used & 1][part][row] = l;
         __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&sh.sums_in[used & 1]);
-          if (told) tc2::arrive_remote(r_flags + (used & 1) * 8);
-          else tc2::arrive_remote_relaxed(r_flags + (used & 1) * 8);
-        }
+        if (lane == 0) tc::mbar_arrive(&sh.sums_in[used & 1]);
         g += t.tiles;
         ++used;
       }
@@ -557,10 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t.tiles > 0) {
         const int h = g + t.tiles - 1;
         bool w = tc::mbar_wait(&sh.sums_in[used & 1], (used >> 1) & 1) &&
-                 tc2::wait(&sh.flags_in[used & 1], (used >> 1) & 1);
+                 tc2::wait(&sh.flags_in[used & 3], (used >> 2) & 1);
         const float total = sh.sums[used & 1][0][row] + sh.sums[used & 1][1][row];
         inv = total == 0.f ? 0.f : 1.f / total;
-        dirty = sh.poison[used & 1][0] == (uint32_t)used + 1 || sh.poison[used & 1][1] == (uint32_t)used + 1;
+        dirty = sh.poison[used & 3][0] == (uint32_t)used + 1 || sh.poison[used & 3][1] == (uint32_t)used + 1;
         w = w && of_tile(sh.o_done, h);
         tc::fence_after_sync();
         if (!(ok = __all_sync(kFullMask, w) != 0)) break;
@@ -646,8 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       Tile t;
       int g = 0, used = 0;  // key tiles, tiles with Q so far
       int kc = 0, vc = 0;   // key tiles whose K, V were asked for
+      int ve = 0;           // edge tiles among the latter
       const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0);
-      const uint32_t my_v = tc2::in_cta(sh.v_full, rank), r_q = tc2::in_cta(&sh.q_full, 0);
+      const uint32_t my_v = tc2::in_cta(sh.v_edge, rank), r_q = tc2::in_cta(&sh.q_full, 0);
       if (lane == 0) {
         tc::prefetch_tmap(&tm_q);
         tc::prefetch_tmap(&tm_k);
@@ -680,17 +655,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= 0) {
               const int h = g + i, s = h % C::kSlots;
               if (h >= C::kSlots && !(ok = of_tile(sh.o_done, h - C::kSlots))) break;
-              // So do those of V, but in an edge tile they count on the CTA's own, for the
-              // softmax warps that look through them there (whose arrival on p_ready then
-              // stands for the odd CTA's V).  The odd CTA's barrier keeps step.
+              // So do those of V, but in an edge tile they count on the CTA's own v_edge, for
+              // its edge warp (whose arrival on v_clean then stands for them); v_full keeps step.
               const bool edge = (i + 1) * kKeys > whole;
-              if (edge || rank == 0) tc::mbar_arrive_expect_tx(&sh.v_full[s], edge ? C::kEntry : 2 * C::kEntry);
-              else tc::mbar_arrive(&sh.v_full[s]);
+              const int e = ve % C::kSlots;
+              if (edge) tc::mbar_arrive_expect_tx(&sh.v_edge[e], C::kEntry);
+              if (edge || rank != 0) tc::mbar_arrive(&sh.v_full[s]);
+              else tc::mbar_arrive_expect_tx(&sh.v_full[s], 2 * C::kEntry);
 #pragma unroll
               for (int kb = 0; kb < D / 128; ++kb)
                 tc2::tma_load_3d(smem + C::kV + s * C::kEntry + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
-                                 t.k0 + i * kKeys, (edge ? my_v : r_v) + s * 8);
+                                 t.k0 + i * kKeys, edge ? my_v + e * 8 : r_v + s * 8);
               vc = h + 1;
+              ve += edge;
             }
           }
         }
@@ -700,10 +677,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       // Copies still in flight land before the CTA ends: after an expired wait, the
-      // even CTA's barriers tell of both CTAs' copies (the odd one's own, of edge tiles).
+      // even CTA's barriers tell of both CTAs' copies (v_edge of the CTA's own).
       if (lane == 0) {
         for (int h = max(0, kc - C::kSlots); rank == 0 && h < kc; ++h) ok = of_tile(sh.k_full, h) && ok;
         for (int h = max(0, vc - C::kSlots); h < vc; ++h) ok = of_tile(sh.v_full, h) && ok;
+        for (int e = max(0, ve - C::kSlots); e < ve; ++e) ok = of_tile(sh.v_edge, e) && ok;
         if (rank == 0 && used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
       }
     } else if (warp == kMmaWarp) {
@@ -730,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
       };
+      int edges = 0;  // edge tiles so far
       // the even CTA's warp issues for the pair
       for (int pass = 0; rank == 0 && next_tile(pass, &t); ++pass) {
         if (t.tiles == 0) continue;
@@ -753,10 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int i = j - C::kLag;
           if (i >= 0) {  // O += P V of key tile i
-            // an edge tile's V may have been edited in both CTAs (ordinary writes): acquire those
-            const bool edge = (i + 1) * kKeys > whole;
             bool w = tc::mbar_wait(&sh.v_full[vs], v_ph);
-            w = w && (edge ? tc2::wait(&sh.p_ready[sr], sr_ph) : tc::mbar_wait(&sh.p_ready[sr], sr_ph));
+            if ((i + 1) * kKeys > whole) {  // V may have been edited in both CTAs (ordinary writes): acquire those
+              w = w && tc2::wait(&sh.v_clean[edges % C::kSlots], (edges / C::kSlots) & 1);
+              ++edges;
+            }
+            w = w && tc::mbar_wait(&sh.p_ready[sr], sr_ph);
             if (i == 0 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
             tc::fence_after_sync();
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
@@ -764,8 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t vd = dv + ((vs * C::kEntry) >> 4);
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc2::mma_ts(tmem + C::kTmemO, tmem + sr * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), vd + ((kk * 2048) >> 4),
-                            idesc_o, (i > 0) || (kk > 0));
+                if (16 * kk < t.sight - i * kKeys)  // no weight beyond
+                  tc2::mma_ts(tmem + C::kTmemO, tmem + sr * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), vd + ((kk * 2048) >> 4),
+                              idesc_o, (i > 0) || (kk > 0));
               tc2::commit(&sh.o_done[vs]);
             }
             __syncwarp();
@@ -781,6 +763,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) tc2::commit(&sh.drained);
         __syncwarp();
         if (!warp_wait(&sh.drained, 0)) ok = false;
+      }
+    } else if (warp == kEdgeWarp) {
+      // ------------------------------------------------------------ edge tiles
+      // This CTA's half of V: see the note at the top.
+      Tile t;
+      int g = 0, used = 0, edges = 0;
+      const uint32_t r_clean = tc2::in_cta(sh.v_clean, 0);
+      const uint32_t r_flags = tc2::in_cta(sh.flags_in, rank ^ 1), r_poison = tc2::in_cta(sh.poison, rank ^ 1);
+      for (int pass = 0; next_tile(pass, &t); ++pass) {
+        if (t.tiles == 0) continue;
+        bool told = false;  // a non-finite value that a row sees
+        for (int j = max(0, t.off + t.tok0 + 1) / kKeys; j < t.tiles && ok; ++j) {
+          const int h = g + j, rows = t.sight - j * kKeys;  // rows of V that some query sees
+          if (!(ok = __all_sync(kFullMask, of_tile(sh.v_edge, edges)))) break;
+          uint8_t* vt = smem + C::kV + (h % C::kSlots) * C::kEntry + lane * 16;
+          bool edited = false, seen = false;
+#pragma unroll 2
+          for (int r = 0; r < min(rows, kKeys); r += 16) {  // those that the product takes
+#pragma unroll
+            for (int kb = 0; kb < D / 128; ++kb) {
+              uint4 y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint4*>(vt + kb * 16384 + r * 128 + i * 512);
+              // a half's bit 15 is set where its exponent is all ones
+              auto full = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
+              uint32_t any = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) any |= full(y[i].x) | full(y[i].y) | full(y[i].z) | full(y[i].w);
+              if (any & 0x80008000u) {
+                edited = true;
+                auto finite = [](uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); };
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint4 z = make_uint4(finite(y[i].x), finite(y[i].y), finite(y[i].z), finite(y[i].w));
+                  if (z.x != y[i].x || z.y != y[i].y || z.z != y[i].z || z.w != y[i].w) {
+                    *reinterpret_cast<uint4*>(vt + kb * 16384 + r * 128 + i * 512) = z;
+                    seen = seen || r + 4 * i + (lane >> 3) < rows;
+                  }
+                }
+              }
+            }
+          }
+          if (seen) {
+            sh.poison[used & 3][rank] = (uint32_t)used + 1;
+            tc2::store_remote(r_poison + ((used & 3) * 2 + rank) * 4, (uint32_t)used + 1);
+          }
+          edited = __any_sync(kFullMask, edited);
+          told = told || edited;
+          if (edited) tc::fence_proxy_async();  // the edited V rows -> the tensor core
+          __syncwarp();
+          if (lane == 0) {
+            if (edited) tc2::arrive_remote(r_clean + edges % C::kSlots * 8);
+            else tc2::arrive_remote_relaxed(r_clean + edges % C::kSlots * 8);
+          }
+          ++edges;
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&sh.flags_in[used & 3]);
+          if (told) tc2::arrive_remote(r_flags + (used & 3) * 8);
+          else tc2::arrive_remote_relaxed(r_flags + (used & 3) * 8);
+        }
+        g += t.tiles;
+        ++used;
       }
     }
   }
