@@ -94,7 +94,8 @@ struct Cfg {
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
   static constexpr int kSlots = D == 256 ? 2 : 4;  // key tiles of K, and of V, in shared memory
   static constexpr uint32_t kK = kQBytes, kV = kK + kSlots * kEntry;
-  static constexpr uint32_t kShared = kV + kSlots * kEntry;  // the barriers and the rest
+  static constexpr uint32_t kStage = kV + kSlots * kEntry;  // 64 columns of o on their way out
+  static constexpr uint32_t kShared = kStage + kRows * 128;  // the barriers and the rest
   static constexpr int kSteps = D / 16;
   static constexpr uint32_t kTmemO = kS * kKeys;
   static constexpr uint32_t kTmemCols = 512;
@@ -520,12 +521,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t r_free = tc2::in_cta(&sh.o_free, 0);
-    const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+    // 32 rows of 128 bytes for each warp, 16-byte pieces c of row r at c ^ (r & 7)
+    uint8_t* stage = smem + C::kStage + (warp & 3) * 4096;
+    int32_t to[8];  // which row of o rows 4 i + lane / 8 of the warp's are, from the first one
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = (warp & 3) * 32 + 4 * i + (lane >> 3);
+      to[i] = r / G * p.h_q + r % G;
+    }
     for (int pass = 0; next_tile(pass, &t); ++pass) {
-      const int tok = t.tok0 + (int)rank * tok_cta + row / G;
-      const bool real = row < tok_cta * G && tok < t.a;
-      const int lim = real ? max(0, t.off + tok + 1) : 0;  // keys this row sees
-      const int64_t out = (((int64_t)t.q0 + tok) * p.h_q + (int64_t)t.kvh * G + row % G) * D;
+      const int tok0 = t.tok0 + (int)rank * tok_cta;
+      const int rows = min(tok_cta, t.a - tok0) * G - (warp & 3) * 32;  // that are there, of the warp's
+      const bool real = lane < rows;
+      const int lim = real ? max(0, t.off + tok0 + row / G + 1) : 0;  // keys this row sees
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
+                           (((int64_t)t.q0 + tok0) * p.h_q + (int64_t)t.kvh * G) * D + (lane & 7) * 8;
       float inv = 0.f;
       bool dirty = false;
       if (t.tiles > 0) {
@@ -539,8 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         if (!(ok = __all_sync(kFullMask, w) != 0)) break;
       }
-      // kOut columns at a time; a thread has a row and stores 32 bytes of it at once
-      // (where o is aligned to that; its rows are)
+      // kOut columns at a time (a thread has a row), through shared memory: stored from
+      // there in rows of 128 bytes.  (With 32 bytes a row, as the threads hold them, 64
+      // KB took 3,900 cycles, in which the softmax warps' next tile took 3,400 for 1,450.)
 #pragma unroll 1
       for (int i = 0; i < D; i += C::kOut) {
         float ov[C::kOut];
@@ -555,11 +566,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < C::kOut; ++k) ov[k] = 0.f;
         }
+        const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-        for (int k = 0; k < C::kOut; ++k) ov[k] *= inv;
+        for (int k = 0; k < C::kOut; k += 2) {
+          const float2 y = tc2::mul2(make_float2(ov[k], ov[k + 1]), inv2);
+          ov[k] = y.x;
+          ov[k + 1] = y.y;
+        }
         if (dirty && real) {
           const int whole = t.off + t.tok0 + 1;
-          const int first = max(0, whole) / kKeys * kKeys;  // first key of the tiles that were edited
+          const int first = max(0, whole) & ~15;  // first key of those that were edited
           const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)t.kvh * D + i;
           for (int key = first; key < lim; ++key) {
             const uint32_t* src = reinterpret_cast<const uint32_t*>(vr + ((int64_t)t.k0 + key) * p.v_stride);
@@ -571,20 +587,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (real) {
 #pragma unroll
-          for (int k = 0; k < C::kOut; k += 16) {
-            uint32_t w[8];
+        for (int k = 0; k < C::kOut; k += 8) {
+          const uint4 x = make_uint4(pack_bf16(ov[k], ov[k + 1]), pack_bf16(ov[k + 2], ov[k + 3]),
+                                     pack_bf16(ov[k + 4], ov[k + 5]), pack_bf16(ov[k + 6], ov[k + 7]));
+          *reinterpret_cast<uint4*>(stage + lane * 128 + (((((i + k) >> 3) & 7) ^ (lane & 7)) << 4)) = x;
+        }
+        if (((i + C::kOut) & 63) == 0) {
+          __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 8; ++x) w[x] = pack_bf16(ov[k + 2 * x], ov[k + 2 * x + 1]);
-            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + out + i + k;
-            if (wide) {
-              tc2::store32(to, w);
-            } else {
-              reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+          for (int x = 0; x < 8; ++x) {
+            const int r = 4 * x + (lane >> 3);
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            if (r < rows) *reinterpret_cast<uint4*>(out + (int64_t)to[x] * D + i + C::kOut - 64) = y;
           }
+          __syncwarp();
         }
       }
       if (t.tiles > 0) {
@@ -776,32 +793,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool told = false;  // a non-finite value that a row sees
         for (int j = max(0, t.off + t.tok0 + 1) / kKeys; j < t.tiles && ok; ++j) {
           const int h = g + j, rows = t.sight - j * kKeys;  // rows of V that some query sees
+          // the first that some does not (rounded down); those before need no care
+          const int row0 = max(0, t.off + t.tok0 + 1 - j * kKeys) & ~15;
           if (!(ok = __all_sync(kFullMask, of_tile(sh.v_edge, edges)))) break;
           uint8_t* vt = smem + C::kV + (h % C::kSlots) * C::kEntry + lane * 16;
-          bool edited = false, seen = false;
-#pragma unroll 2
-          for (int r = 0; r < min(rows, kKeys); r += 16) {  // those that the product takes
+          // the largest of the magnitudes, as 16-bit integers (a non-finite one is 0x7f80 or more)
+          uint32_t most = 0;
+          for (int r = row0; r < min(rows, kKeys); r += 16) {
 #pragma unroll
-            for (int kb = 0; kb < D / 128; ++kb) {
-              uint4 y[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint4*>(vt + kb * 16384 + r * 128 + i * 512);
-              // a half's bit 15 is set where its exponent is all ones
-              auto full = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
-              uint32_t any = 0;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) any |= full(y[i].x) | full(y[i].y) | full(y[i].z) | full(y[i].w);
-              if (any & 0x80008000u) {
-                edited = true;
-                auto finite = [](uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); };
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint4 z = make_uint4(finite(y[i].x), finite(y[i].y), finite(y[i].z), finite(y[i].w));
-                  if (z.x != y[i].x || z.y != y[i].y || z.z != y[i].z || z.w != y[i].w) {
-                    *reinterpret_cast<uint4*>(vt + kb * 16384 + r * 128 + i * 512) = z;
-                    seen = seen || r + 4 * i + (lane >> 3) < rows;
-                  }
-                }
+            for (int i = 0; i < D / 32; ++i) {
+              const uint4 y = *reinterpret_cast<const uint4*>(vt + (i >> 2) * 16384 + r * 128 + (i & 3) * 512);
+              most = __vimax3_u16x2(most, y.x & 0x7fff7fffu, y.y & 0x7fff7fffu);
+              most = __vimax3_u16x2(most, y.z & 0x7fff7fffu, y.w & 0x7fff7fffu);
+            }
+          }
+          bool seen = false;
+          const bool edited = __any_sync(kFullMask, (most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u);
+          if (edited) {
+#pragma unroll 1
+            for (int i = 0; i < (int)C::kEntry / 512; ++i) {  // four rows at a time
+              if (4 * (i & 31) < row0) continue;
+              uint4* at = reinterpret_cast<uint4*>(vt + i * 512);
+              auto finite = [](uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); };
+              const uint4 y = *at, z = make_uint4(finite(y.x), finite(y.y), finite(y.z), finite(y.w));
+              if (z.x != y.x || z.y != y.y || z.z != y.z || z.w != y.w) {
+                *at = z;
+                seen = seen || 4 * (i & 31) + (lane >> 3) < rows;
               }
             }
           }
@@ -809,7 +826,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh.poison[used & 3][rank] = (uint32_t)used + 1;
             tc2::store_remote(r_poison + ((used & 3) * 2 + rank) * 4, (uint32_t)used + 1);
           }
-          edited = __any_sync(kFullMask, edited);
           told = told || edited;
           if (edited) tc::fence_proxy_async();  // the edited V rows -> the tensor core
           __syncwarp();
