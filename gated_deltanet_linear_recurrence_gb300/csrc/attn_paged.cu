@@ -10,15 +10,15 @@
 //
 // Bound by HBM: every cached row is read once (8 flops per value and head).
 // What the layout is for:
-//   * A CTA's share of the batch is a range of 64-row units in (sequence, KV
-//     head, row) order, the same number for every CTA whatever the lengths are:
+//   * A CTA's share of the batch is a range of units of 64 rows (e4m3: 128) in
+//     (sequence, KV head, row) order, as much work for every CTA whatever the lengths are:
 //     ragged batches and single long sequences fill the GPU alike.  The shares
 //     follow from the device's lengths alone, so each CTA (and the joining pass)
 //     works them out for itself, and the workspace is two partial results a CTA.
-//   * A warp owns its 16-row tiles end to end: a ring of its own in shared
-//     memory filled by 16-byte asynchronous copies, warp-level matrix products
-//     (m16n8k16: 16 rows x 8 query heads), no CTA barrier before the end of a
-//     (sequence, KV head).  Rows are addressed one by one through the page table,
+//   * A warp owns its tiles of 16 rows (e4m3: 32) end to end: a ring of its own in shared
+//     memory (24 KB at D = 256, 12 KB at D = 128, two or four CTAs an SM) filled by
+//     16-byte asynchronous copies, warp-level matrix products (m16n8k16: 16 rows x 8
+//     query heads), no CTA barrier before the end of a (sequence, KV head).  Rows are addressed one by one through the page table,
 //     so a page may be smaller than a tile or end anywhere inside it.
 //   * The products are S^T = K Q^T and O^T = V^T P^T, whose N = 8 is the number
 //     of query heads on a KV head, so no multiply is padding at eight heads; one
@@ -32,6 +32,14 @@
 // the f16 weights use their range whatever the units are; l keeps its own m.
 // (Products of e4m3 operands themselves, with q and P as sums of e4m3 parts,
 // measured slower: at warp level they run as f16 products after a widening.)
+//
+// Measured (calls back to back, both kernels): 64 sequences of 8,192 bf16 keys, 16
+// query heads of 256 on 2, 162 us = 6.6 TB/s, 98 % of a plain copy's rate; one
+// sequence of 131,072 e4m3 keys 30 us = 4.5 TB/s, one eight times as long 168 us =
+// 6.4; 40 ragged e4m3 sequences on 8 KV heads of 128 91 us = 5.4, four times as long
+// 314 us = 6.3; one of 4,096 keys 9 us.  So rows stream at 6.6 to 6.9 TB/s, and a call
+// costs 10 to 15 us beside that: lengths, table and first rows one after the other
+// (3 us), the last rows' weights, the warps' join, and the joining pass (4 to 5 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

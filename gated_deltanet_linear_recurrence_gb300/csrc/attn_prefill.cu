@@ -13,26 +13,38 @@
 // the rows of a KV head keeps the causal edge short (G tokens' rows end at the
 // same key) and fills tiles of short sequences.
 //
-// Bound by the tensor pipe: 4 D flops per row and key, 2 D/128 x 1024 cycles a
-// pair and 128 keys, against 64 exponentials a row and key-half.  With one CTA the
-// operands would not fit the shared-memory bandwidth: Q and K tiles read at 128
-// bytes a cycle and K and V written at 64.  cta_group::2 lets each CTA hold half
-// of K (keys) and of V (dimensions), and P stays in TMEM, which leaves
+// Bound by the tensor pipe at D = 256: a pair's products take 8 D cycles a key tile
+// (4 D flops a row and key), its softmax about 1,450.  With one CTA the operands
+// would not fit the shared-memory bandwidth: Q and K tiles read at 128 bytes a cycle
+// and K and V written at 64.  cta_group::2 lets each CTA hold half of K (keys) and of
+// V (dimensions), and P stays in TMEM, which leaves
 //     Q 4 KB + K 2 KB a 64-cycle step; V 4 KB a 128-cycle step (D = 256)
-// to read and half of the writes.
+// to read and half of the writes.  At D = 128 the products take half as long (1,024
+// cycles) and the softmax of a tile still 1,800, so two groups of warps take the
+// tiles in turn: about 1,150 cycles a tile.  Between two tiles of queries the tensor
+// pipe pauses 2,500 cycles (the last P, its product, O read out, the next product),
+// which is what short sequences pay.
+//
+// Measured (calls back to back; flops of the visible keys only): 16,384 tokens with
+// 16 query heads of 256 on 2 KV heads 1.14 ms, 1.93 PFLOP/s, as fast as a plain
+// library product and limited by the board's power; 4,096 tokens 78 us, 1.77; 2,048
+// new tokens on 16,000 keys 270 us, 1.86.  At D = 128, 8,192 tokens 155 us, 1.77;
+// seven prompts of 1 to 4,096 tokens with 32 query heads on 8, 183 us, 1.49; seven
+// of 1 to 200 tokens 13 us (launch and latency).
 //
 // TMEM (512 columns): S of two or three key tiles (128 fp32 columns each, of whose
 // two halves P then takes 32 columns of bf16 pairs), O (D columns).  Shared memory:
-// Q (64 KB at D = 256), K and V halves of two or four key
-// tiles.  The scores of the next key tiles are computed while the softmax warps work
+// Q (64 KB at D = 256), K and V halves of two or four key tiles, 64 columns of O.
+// The scores of the next key tiles are computed while the softmax warps work
 // on one, and the products with V follow one or two key tiles behind.
 //
 // Roles (16 warps): 0-7 softmax, 8-11 epilogue (O to o while the next tile's scores
 // are under way), 12 TMA, 13 products (the even CTA's issues them for the pair), 14
 // the schedule, 15 V of edge tiles.  The pairs are persistent.
 //
-// Rounding: P is rounded to bf16 for the second product (relative 2^-9 a weight,
-// the same as the output's rounding; the sums l stay fp32 over unrounded weights).
+// Rounding: P is rounded to bf16 for the second product (by at most 2^-8 of a weight,
+// as the output is; the sums l stay fp32 over unrounded weights).  Weights as bf16
+// pairs would double the second product, which is half of all the work.
 //
 // What a query does not see must not reach it even as NaN: its scores are masked,
 // and in a tile that some row sees in part (an edge tile), warp 15 replaces non-finite
@@ -85,7 +97,8 @@ struct Cfg {
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
   // Registers of a thread of the four warpgroups: softmax (two), epilogue, and 64 for
   // the rest; together the 65,536 that the CTA starts with (setmaxnreg takes them
-  // from there).  At D = 128 a softmax thread's 128 scores want more than 168 (198
+  // from   // from there).  At D = 128 a softmax thread's 128 scores want more than 168 (198
+  // against 222 us for seven packed prompts, when that was tried)
   // against 222 us for seven packed prompts), and the epilogue reads fewer columns at once.
   static constexpr int kSoftmaxRegs = D == 256 ? 168 : 184, kEpilogueRegs = D == 256 ? 112 : 80;
   static constexpr int kOut = D == 256 ? 64 : 32;  // columns of O that the epilogue holds
@@ -403,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // An edge tile: the scores that a row does not see are overwritten.  One short
           // loop before code that all tiles share: with the masks inside an unrolled copy
           // of that code, its instructions (run once a tile of queries, so never near)
-          // took 4,500 cycles where a tile without an edge takes 1,700.
+          // took 4,500 cycles where a tile without an edge takes 1,800 (seven packed
+          // prompts 196 us, now 184; with this loop an edge tile takes 2,400).
           const int left = lim - key0 - C::kCols * half;  // columns of this thread that the row sees
           const int all = __reduce_min_sync(kFullMask, left);
 #pragma unroll 1

@@ -459,8 +459,9 @@ typedef enum { GDN_CACHE_BF16 = 1, GDN_CACHE_E4M3 = 2 } gdn_cache_dtype;
  * of 8, at least h_kv x head_dim: a slice of a fused projection needs no copy).
  * Sequences must not share the pages that a call writes.  cu_seqlens
  * [num_seqs + 1], start_pos [num_seqs] int32 on the device.  Tensors 16-byte
- * aligned (int32 arrays 4-byte, exponent bytes 8-byte).  The rows of a token that cu_seqlens gives to no
- * sequence are not written (GDN_ERR_BAD_CU_SEQLENS in the error word).
+ * aligned (int32 arrays 4-byte, exponent bytes 8-byte).  The rows of a token that
+ * cu_seqlens gives to no sequence are not written (GDN_ERR_BAD_CU_SEQLENS in the
+ * error word).
  */
 gdn_status gdn_kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                          void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
