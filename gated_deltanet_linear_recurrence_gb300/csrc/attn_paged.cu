@@ -36,10 +36,11 @@
 // Measured (calls back to back, both kernels): 64 sequences of 8,192 bf16 keys, 16
 // query heads of 256 on 2, 162 us = 6.6 TB/s, 98 % of a plain copy's rate; one
 // sequence of 131,072 e4m3 keys 30 us = 4.5 TB/s, one eight times as long 168 us =
-// 6.4; 40 ragged e4m3 sequences on 8 KV heads of 128 91 us = 5.4, four times as long
-// 314 us = 6.3; one of 4,096 keys 9 us.  So rows stream at 6.6 to 6.9 TB/s, and a call
-// costs 10 to 15 us beside that: lengths, table and first rows one after the other
-// (3 us), the last rows' weights, the warps' join, and the joining pass (4 to 5 us).
+// 6.4; e4m3 with 8 KV heads of 128: 40 ragged sequences 86 us = 5.8, 304 of 792 keys
+// 84 us = 5.9, 608 of 396 keys 91 us = 5.6; one of 4,096 keys 9 us.  So rows stream at
+// 6.6 to 6.9 TB/s, and a call costs about 10 us beside that: lengths, table and first
+// rows one after the other (3 us), the last rows' weights, the warps' join, and the
+// joining pass (4 to 5 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -155,10 +156,12 @@ __device__ __forceinline__ int length_of(const PagedAttnArgs& p, int b) {
   const int len = __ldg(p.cache_len + b);
   return (len < 0 || (int64_t)len > ((int64_t)p.cache.max_pages << p.cache.page_shift)) ? 0 : len;
 }
-// Work of one (sequence, KV head): its units, and kPieceCost more for taking it up
+// Work of one (sequence, KV head): its units, and kPieceCost units more for taking it up
 // (q and the first rows arrive, the warps join), so that a CTA with many short
-// sequences is not given more than it can do in the same time.
-constexpr int kPieceCost = 2;
+// sequences is not given more than it can do in the same time (40 ragged sequences on 8
+// KV heads of 128: 86 us with one unit, 89 with two, 87 with three; without any, a sixth
+// more when that was tried).
+constexpr int kPieceCost = 1;
 template <int kUnit>
 __device__ __forceinline__ int64_t span_of(int len) {
   return len > 0 ? kPieceCost + (uint32_t)(len + kUnit - 1) / kUnit : 0;
@@ -166,18 +169,6 @@ __device__ __forceinline__ int64_t span_of(int len) {
 
 // Sums and largest values over a block's warps, on every thread (two barriers apart
 // from each other's use of `at`, one value a warp).
-template <int kT>
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* at) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
-  if (lane == 0) at[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = lane < kT / 32 ? at[lane] : 0;
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
-  return x;
-}
 template <int kT>
 __device__ __forceinline__ float block_max(float x, float* at) {
   const int lane = threadIdx.x & 31;
@@ -222,6 +213,79 @@ struct Shares {
   }
 };
 
+// For up to 32 sequences: all work, and on each lane that before the lane's sequence.
+template <int kUnit>
+__device__ __forceinline__ int64_t count_work(const PagedAttnArgs& p, int lane, int64_t& total, int64_t& before) {
+  const int64_t mine = lane < p.batch ? p.cache.h_kv * span_of<kUnit>(length_of(p, lane)) : 0;
+  int64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(kFullMask, incl, off);
+    if (lane >= off) incl += y;
+  }
+  total = __shfl_sync(kFullMask, incl, 31);
+  before = incl - mine;
+  return incl;
+}
+// For a whole block: all work, where that of CTA c starts, the sequence b that it falls
+// into and the work before that one.  False when there is none for c.
+template <int kT, int kUnit>
+__device__ __forceinline__ bool find_work(const PagedAttnArgs& p, int c, bool report, int64_t& total, int64_t& u,
+                                          int& b, int64_t& base) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (p.batch <= 32) {  // a lane counts a sequence, each warp for itself
+    if (report && lane < p.batch && length_of(p, lane) != __ldg(p.cache_len + lane)) raise_error(p.err, kErrBadCacheLen);
+    int64_t before;
+    const int64_t incl = count_work<kUnit>(p, lane, total, before);
+    u = Shares(total, p.ctas).start(c);
+    if (u >= total) return false;
+    b = __ffs(__ballot_sync(kFullMask, incl > u)) - 1;
+    base = __shfl_sync(kFullMask, before, b);
+    return true;
+  }
+  const int per = (p.batch + kT - 1) / kT;  // sequences a thread counts
+  const int lo = min(p.batch, tid * per), hi = min(p.batch, lo + per);
+  int64_t mine = 0;
+  for (int i = lo; i < hi; ++i) {
+    const int len = length_of(p, i);
+    if (report && len != __ldg(p.cache_len + i)) raise_error(p.err, kErrBadCacheLen);
+    mine += p.cache.h_kv * span_of<kUnit>(len);
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(kFullMask, incl, off);
+    if (lane >= off) incl += y;
+  }
+  __shared__ int64_t scan[kT / 32], found_work;
+  __shared__ int found;
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kT / 32; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  u = Shares(total, p.ctas).start(c);
+  if (u >= total) return false;
+  if (before <= u && u < before + mine) {
+    int i = lo;
+    for (;; ++i) {
+      const int64_t n = p.cache.h_kv * span_of<kUnit>(length_of(p, i));
+      if (u < before + n) break;
+      before += n;
+    }
+    found = i;
+    found_work = before;
+  }
+  __syncthreads();
+  b = found;
+  base = found_work;
+  return true;
+}
+
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_kernel(const PagedAttnArgs p) {
   constexpr int kRowBytes = kFp8 ? D : 2 * D;
@@ -246,68 +310,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
 
   // ---- this CTA's share
   const int G = p.h_q / p.cache.h_kv;
-  int64_t total = 0, u, u_end, base;  // all work, this CTA's, and that before its first sequence
-  int b;                              // its first sequence
-  if (p.batch <= 32) {  // a lane counts a sequence, each warp for itself
-    const int len = lane < p.batch ? length_of(p, lane) : 0;
-    if (blockIdx.x == 0 && lane < p.batch && len != __ldg(p.cache_len + lane)) raise_error(p.err, kErrBadCacheLen);
-    const int64_t mine = p.cache.h_kv * span_of<kUnit>(len);
-    int64_t incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(kFullMask, incl, off);
-      if (lane >= off) incl += y;
-    }
-    total = __shfl_sync(kFullMask, incl, 31);
-    const Shares sh(total, gridDim.x);
-    u = sh.start(blockIdx.x);
-    u_end = sh.start(blockIdx.x + 1);
-    if (u == u_end) return;
-    b = __ffs(__ballot_sync(kFullMask, incl > u)) - 1;
-    base = __shfl_sync(kFullMask, incl - mine, b);
-  } else {
-    __shared__ int64_t scan[kWarps], at_units;
-    __shared__ int at_seq;
-    const int per = (p.batch + kThreads - 1) / kThreads;  // sequences a thread counts
-    const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
-    int64_t mine = 0;
-    for (int i = b_lo; i < b_hi; ++i) {
-      const int len = length_of(p, i);
-      if (blockIdx.x == 0 && len != __ldg(p.cache_len + i)) raise_error(p.err, kErrBadCacheLen);
-      mine += p.cache.h_kv * span_of<kUnit>(len);
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(kFullMask, incl, off);
-      if (lane >= off) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
-    }
-    const Shares sh(total, gridDim.x);
-    u = sh.start(blockIdx.x);
-    u_end = sh.start(blockIdx.x + 1);
-    if (u == u_end) return;
-    if (before <= u && u < before + mine) {
-      int i = b_lo;
-      for (;; ++i) {
-        const int64_t n = p.cache.h_kv * span_of<kUnit>(length_of(p, i));
-        if (u < before + n) break;
-        before += n;
-      }
-      at_seq = i;
-      at_units = before;
-    }
-    __syncthreads();
-    b = at_seq;
-    base = at_units;
-  }
+  int64_t total, u, base;  // all work, this CTA's, and that before its first sequence
+  int b;                   // its first sequence
+  if (!find_work<kThreads, kUnit>(p, blockIdx.x, blockIdx.x == 0, total, u, b, base)) return;
+  const int64_t u_end = Shares(total, p.ctas).start(blockIdx.x + 1);
 
   const uint32_t ring = tc::smem_u32(smem) + warp * kRing;
   const int quad = lane >> 2, pair = lane & 3;  // fragment row, and column pair
@@ -758,44 +764,63 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
 
 // The results of a (sequence, KV head) whose units went to several CTAs:
 //     o = sum_s w_s o_s / sum_s w_s,   w_s = 2^(m_s - M) l_s,   M = max_s m_s
-// with each CTA's o_s already divided by its l_s.  Also writes the zeros of a
-// sequence without cached rows.  One block per (sequence, KV head, query head):
-// with up to kFew splits the block of the first query head does all of them, a warp
-// each (batches: nearly every item has two); with more, each block its own (kSlices
-// blocks, a part of the dims each), a lane four values of a row, the splits dealt to
-// the groups of lanes, eight loads in flight in each.
+// with each CTA's o_s already divided by its l_s.  Also writes the zeros of sequences
+// without cached rows.  With up to kFew splits of an item (a sequence's KV head) one
+// block does all query heads, a warp each; with more, several share out the heads and
+// kSlices parts of their dims, a lane four values of a row, the splits dealt to the
+// groups of lanes, eight loads in flight in each.
+// Few rows of o (kByItem): a block for every item, head and part.  Else a block for
+// every boundary between two CTAs' shares: what the boundaries that fall into an item
+// show is all that there is to join, and they are its blocks.  (A block for every item
+// and head, most of them with nothing to join, took 110 of 187 us for 608 sequences
+// with 8 KV heads; now 9.)
 constexpr int kFew = 16;
 template <int D, int kUnit, int kJoinThreads, int kSlices>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const PagedAttnArgs p) {
   constexpr int kRow = D / 4, kLanes = kRow / kSlices, kGroups = kJoinThreads / kLanes;
+  constexpr bool kByItem = kSlices > 1;
   __shared__ float w_sm[kPagedMaxCtas];
-  __shared__ int64_t sums[2][kJoinThreads / 32];
   __shared__ float red[2][kJoinThreads / 32];
   __shared__ float4 sum_sm[kGroups][kLanes];
-  tc::allow_dependents();
+  // (The next call's kernel is not let in early: with its CTAs taking their places
+  // between these blocks, 40 sequences with 8 KV heads took 105 for 89 us.)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h_kv = p.cache.h_kv, G = p.h_q / h_kv;
-  const int b = blockIdx.x / h_kv, j = blockIdx.x % h_kv;
-  int64_t base = 0, total = 0;  // work of the sequences before this one, and of all
-  for (int i = tid; i < p.batch; i += kJoinThreads) {
-    const int64_t u = h_kv * span_of<kUnit>(length_of(p, i));
-    total += u;
-    if (i < b) base += u;
+  int64_t total = 0, u, base;
+  int b = 0, j = 0, c_lo = 0, n = 1;  // the block's item; its first CTA, its splits
+  int mine = 0, blocks = G * kSlices;  // the block's number among the item's
+  if (kByItem) {  // at most 32 sequences
+    mine = blockIdx.x % blocks;
+    j = blockIdx.x / blocks % h_kv;
+    b = blockIdx.x / blocks / h_kv;
+    count_work<kUnit>(p, lane, total, base);
+    base = __shfl_sync(kFullMask, base, b);
+  } else if (blockIdx.x + 1 >= p.ctas || !find_work<kJoinThreads, kUnit>(p, blockIdx.x + 1, false, total, u, b, base)) {
+    total = 0;
   }
-  if (p.batch > 1) base = block_sum<kJoinThreads>(base, sums[0]);
-  total = p.batch > 1 ? block_sum<kJoinThreads>(total, sums[1]) : h_kv * span_of<kUnit>(length_of(p, 0));
-  const int64_t span = span_of<kUnit>(length_of(p, b));
-  const int64_t first = base + (int64_t)j * span + kPieceCost, end = base + (int64_t)(j + 1) * span;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)b * p.h_q + (int64_t)j * G) * D;
-  const Shares sh(total, p.ctas);
-  const int c_lo = span > 0 ? sh.owner(first) : 0, c_hi = span > 0 ? sh.owner(end - 1) : 0;
-  const int n = c_hi - c_lo + 1;
+  const int64_t span = total > 0 ? span_of<kUnit>(length_of(p, b)) : 0;
+  if (span > 0) {
+    if (!kByItem) j = (int)quotient(u - base, span);
+    const int64_t first = base + (int64_t)j * span + kPieceCost, end = base + (int64_t)(j + 1) * span;
+    const Shares sh(total, p.ctas);
+    c_lo = sh.owner(first);
+    n = sh.owner(end - 1) - c_lo + 1;
+    if (!kByItem) {
+      mine = (int)blockIdx.x - c_lo;
+      blocks = n - 1;
+      if (mine < 0) n = 1;  // not inside the item's units
+    }
+  }
+  int empty = blockIdx.x;  // a sequence without cached rows
+  while (empty < p.batch && length_of(p, empty) > 0) empty += gridDim.x;
+  // every block waits: the kernel after this one takes its end for that of both
   tc::wait_prerequisites();
-  if (span == 0) {
-    if (tid < D && blockIdx.z == 0) o[blockIdx.y * D + tid] = __float2bfloat16_rn(0.f);
-    return;
-  }
+  for (; empty < p.batch; empty += gridDim.x)
+    if (length_of(p, empty) == 0)
+      for (int d = tid; d < p.h_q * D / 8; d += kJoinThreads)
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (int64_t)empty * p.h_q * D)[d] = make_uint4(0, 0, 0, 0);
   if (n == 1) return;  // written by its CTA
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)b * p.h_q + (int64_t)j * G) * D;
   // the CTA with the first unit wrote slot 1, those that start inside it slot 0
   auto part = [&](int s, int h) { return ((int64_t)(c_lo + s) * 2 + (s == 0)) * G + h; };
   const float4* acc_in = reinterpret_cast<const float4*>(p.partial);
@@ -815,7 +840,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
   };
   if (n <= kFew) {
     const int h = warp;
-    if (blockIdx.y > 0 || blockIdx.z > 0 || h >= G) return;
+    if (mine > 0 || h >= G) return;
     float2 ml = lane < n ? ml_in[part(lane, h)] : make_float2(-INFINITY, 0.f);
     float4 a[D / 128];
 #pragma unroll
@@ -837,50 +862,55 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
     for (int k = 0; k < D / 128; ++k) store(h, 32 * k + lane, a[k], den);
     return;
   }
-  const int d4 = tid % kLanes + blockIdx.z * kLanes, grp = tid / kLanes, h = blockIdx.y;
-  float4 x[8];  // the first loads go out before the weights are known
+  for (int x = mine; x < G * kSlices; x += blocks) {  // query head, part of its dims
+    const int h = x % G, grp = tid / kLanes, d4 = tid % kLanes + x / G * kLanes;
+    float4 in[8];  // the first loads go out before the weights are known
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int s = grp + k * kGroups;
-    x[k] = s < n ? acc_in[part(s, h) * kRow + d4] : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  constexpr int kMine = (kPagedMaxCtas + kJoinThreads - 1) / kJoinThreads;  // splits a thread
-  float2 ml[kMine];
-  float mx = -INFINITY;
+    for (int k = 0; k < 8; ++k) {
+      const int s = grp + k * kGroups;
+      in[k] = s < n ? acc_in[part(s, h) * kRow + d4] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    constexpr int kMine = (kPagedMaxCtas + kJoinThreads - 1) / kJoinThreads;  // splits a thread
+    float2 ml[kMine];
+    float mx = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const int s = tid + k * kJoinThreads;
-    ml[k] = s < n ? ml_in[part(s, h)] : make_float2(-INFINITY, 0.f);
-    mx = fmaxf(mx, ml[k].x);
-  }
-  mx = block_max<kJoinThreads>(mx, red[0]);
-  float den = 0.f;
+    for (int k = 0; k < kMine; ++k) {
+      const int s = tid + k * kJoinThreads;
+      ml[k] = s < n ? ml_in[part(s, h)] : make_float2(-INFINITY, 0.f);
+      mx = fmaxf(mx, ml[k].x);
+    }
+    mx = block_max<kJoinThreads>(mx, red[0]);
+    float den = 0.f;
 #pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const float w = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - mx) * ml[k].y;
-    if (tid + k * kJoinThreads < n) w_sm[tid + k * kJoinThreads] = w;
-    den += w;
-  }
-  den = block_sum<kJoinThreads>(den, red[1]);  // and every thread's weights are in w_sm
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < kMine; ++k) {
+      const float w = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - mx) * ml[k].y;
+      if (tid + k * kJoinThreads < n) w_sm[tid + k * kJoinThreads] = w;
+      den += w;
+    }
+    den = block_sum<kJoinThreads>(den, red[1]);  // and every thread's weights are in w_sm
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (grp + k * kGroups < n) add(a, w_sm[grp + k * kGroups], x[k]);
+    for (int k = 0; k < 8; ++k)
+      if (grp + k * kGroups < n) add(a, w_sm[grp + k * kGroups], in[k]);
 #pragma unroll 8
-  for (int s = grp + 8 * kGroups; s < n; s += kGroups) add(a, w_sm[s], acc_in[part(s, h) * kRow + d4]);
-  sum_sm[grp][tid % kLanes] = a;
-  __syncthreads();
-  if (grp > 0) return;
+    for (int s = grp + 8 * kGroups; s < n; s += kGroups) add(a, w_sm[s], acc_in[part(s, h) * kRow + d4]);
+    sum_sm[grp][tid % kLanes] = a;
+    __syncthreads();
+    if (grp == 0) {
 #pragma unroll
-  for (int g = 1; g < kGroups; ++g) {
-    const float4 y = sum_sm[g][tid % kLanes];
-    a.x += y.x;
-    a.y += y.y;
-    a.z += y.z;
-    a.w += y.w;
+      for (int g = 1; g < kGroups; ++g) {
+        const float4 y = sum_sm[g][tid % kLanes];
+        a.x += y.x;
+        a.y += y.y;
+        a.z += y.z;
+        a.w += y.w;
+      }
+      store(h, d4, a, den);
+    }
+    __syncthreads();
   }
-  store(h, d4, a, den);
 }
+
 template <int D, bool kFp8>
 cudaError_t launch_paged(const PagedAttnArgs& args, cudaStream_t stream) {
   static PerDeviceOnce attrs;
@@ -904,15 +934,13 @@ cudaError_t launch_paged(const PagedAttnArgs& args, cudaStream_t stream) {
   cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, attn_paged_kernel<D, kFp8>, args);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(args.batch * args.cache.h_kv), (unsigned)(args.h_q / args.cache.h_kv));
   cfg.dynamicSmemBytes = 0;
-  // Few rows of o have many splits each: more loads in flight.  A batch's rows have
-  // few, and small blocks let more of them run at once.
-  if ((int64_t)args.batch * args.h_q <= 64) {
-    cfg.gridDim.z = 4;
+  if ((int64_t)args.batch * args.h_q <= 64 && args.batch <= 32) {  // few rows, with many splits each
+    cfg.gridDim = dim3((unsigned)(args.batch * args.h_q * 4));
     cfg.blockDim = dim3(512);
     return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 512, 4>, args);
   }
+  cfg.gridDim = dim3((unsigned)(args.ctas > 1 ? args.ctas - 1 : 1));
   cfg.blockDim = dim3(256);
   return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 256, 1>, args);
 }

@@ -116,6 +116,39 @@ def test_one_sequence_on_every_cta(D, fp8):
 
 
 @pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("h_q,h_kv", [(8, 8), (16, 2)])
+def test_one_long_sequence_among_many(h_q, h_kv, D, fp8):
+    """One sequence on many CTAs (more of them than query heads and parts of a row, and in
+    other layouts fewer), every other one on a part of a CTA or empty; and a batch of more
+    than 32 with less work than there are CTAs."""
+    r = np.random.default_rng(3)
+    lens = [int(x) for x in r.integers(0, 40, 150)]
+    lens[70] = 12000
+    lens[71] = lens[149] = 0
+    agrees(lens, h_q, h_kv, D, 16, fp8, seed=42)
+    agrees([0] * 20 + [1, 700, 0] + [2] * 15, h_q, h_kv, D, 16, fp8, seed=43)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+def test_calls_one_after_the_other(D, fp8):
+    """Calls that follow each other without a wait between, with very
+    different shares, give what each gives alone."""
+    cases = []
+    for seed, lens in ((44, [3000, 50]), (45, [60] * 90), (46, [9000]), (47, [0, 1, 500] * 15)):
+        c = build(lens, 2, D, 16, fp8, seed=seed)
+        q = normal(gen(seed), len(lens), 8, D).cuda()
+        cases.append((c, q, call(c, q)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, q, alone in cases:
+            assert torch.equal(call(c, q), alone)
+    outs = [[call(c, q) for c, q, _ in cases] for _ in range(10)]
+    for got in outs:
+        for (_, _, alone), o in zip(cases, got):
+            assert torch.equal(o, alone)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
 def test_all_empty(D, fp8):
     _, _, o = agrees([0, 0, 0], 8, 2, D, 16, fp8, seed=24)
     assert (o == 0).all()
