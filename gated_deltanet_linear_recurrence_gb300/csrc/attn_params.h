@@ -69,6 +69,7 @@ struct AttnPrefillArgs {
   int32_t h_q, h_kv, head_dim;
   int64_t q_stride, k_stride, v_stride;
   float scale;
+  int32_t by_sequence;  // order of the tiles, chosen at the launch
   int* err;
 };
 

@@ -245,9 +245,11 @@ __device__ __forceinline__ int prefix(int x, int lane) {  // of the lanes before
   return y - x;
 }
 
-// Tiles in the order of the schedule, for one warp.  Up to 32 sequences: by how
-// many keys they see, most first.  More: sequence by sequence, last tile first
-// (their number evens the pairs' shares out).
+// Tiles in the order of the schedule, for one warp.  Either by how many keys they see,
+// most first, which makes the pairs' shares even; or sequence by sequence, last tile
+// first, so that pairs at work at the same time share keys and values.  The latter for
+// more than 32 sequences (their number evens the shares out too) and where the launch
+// asks for it.
 struct Schedule {
   Seq s;       // this lane's sequence of the current 32
   int base;    // first sequence of the current 32
@@ -268,7 +270,7 @@ struct Schedule {
       *t = make_tile(q, q.tiles - 1 - r, kvh, tokens.d);
       return true;
     }
-    if (p.num_seqs <= 32) {
+    if (p.num_seqs <= 32 && !p.by_sequence) {
       if (r >= __reduce_add_sync(kFullMask, s.tiles)) return false;
       int lo = 0, hi = __reduce_max_sync(kFullMask, s.b) + 1;  // tiles_from(lo) > r >= tiles_from(hi)
       while (hi - lo > 1) {
@@ -920,6 +922,13 @@ cudaError_t launch(const AttnPrefillArgs& a, int sms, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   int64_t pairs = (a.total_q / (2 * tok_cta) + a.num_seqs) * a.h_kv;  // at least as many as tiles
+  AttnPrefillArgs args = a;
+  // Sequence by sequence where no pair has two tiles (their order does not matter then;
+  // seven short prompts 10.9 -> 9.8 us), and where keys and values exceed half of L2, as
+  // they would be read from DRAM by tile after tile (16 prompts of 1,024 tokens, 32
+  // heads of 256 on 8: 190 -> 160 us; 8 of 4,096, heads of 128: 190 -> 176).  Below that
+  // even shares are worth more (seven prompts of 1 to 4,096 tokens, 46 MB: 181, not 192).
+  args.by_sequence = pairs <= sms / 2 || a.total_k * a.h_kv * D * 4 > (int64_t)64 << 20;
   if (pairs > sms / 2) pairs = sms / 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -935,7 +944,7 @@ cudaError_t launch(const AttnPrefillArgs& a, int sms, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, mq, mk, mv, a);
+  return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, mq, mk, mv, args);
 }
 
 }  // namespace
