@@ -27,10 +27,10 @@
 //
 // Measured (calls back to back; flops of the visible keys only): 16,384 tokens with
 // 16 query heads of 256 on 2 KV heads 1.14 ms, 1.93 PFLOP/s, as fast as a plain
-// library product and limited by the board's power; 4,096 tokens 78 us, 1.77; 2,048
-// new tokens on 16,000 keys 270 us, 1.86.  At D = 128, 8,192 tokens 155 us, 1.77;
-// seven prompts of 1 to 4,096 tokens with 32 query heads on 8, 183 us, 1.49; seven
-// of 1 to 200 tokens 13 us (launch and latency).
+// library product and limited by the board's power; 4,096 tokens 77 us, 1.79; 2,048
+// new tokens on 16,000 keys 268 us, 1.87.  At D = 128, 8,192 tokens 155 us, 1.77;
+// seven prompts of 1 to 4,096 tokens with 32 query heads on 8, 180 us, 1.52; seven
+// of 1 to 200 tokens (D = 256) 10 us (launch and latency).
 //
 // TMEM (512 columns): S of two or three key tiles (128 fp32 columns each, of whose
 // two halves P then takes 32 columns of bf16 pairs), O (D columns).  Shared memory:
