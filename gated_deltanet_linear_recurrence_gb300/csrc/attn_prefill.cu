@@ -29,7 +29,7 @@
 // 16 query heads of 256 on 2 KV heads 1.14 ms, 1.93 PFLOP/s, as fast as a plain
 // library product and limited by the board's power; 4,096 tokens 77 us, 1.79; 2,048
 // new tokens on 16,000 keys 268 us, 1.87.  At D = 128, 8,192 tokens 155 us, 1.77;
-// seven prompts of 1 to 4,096 tokens with 32 query heads on 8, 180 us, 1.52; seven
+// seven prompts of 1 to 4,096 tokens with 32 query heads on 8, 177 us, 1.54; seven
 // of 1 to 200 tokens (D = 256) 10 us (launch and latency).
 //
 // TMEM (512 columns): S of two or three key tiles (128 fp32 columns each, of whose
@@ -414,6 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         w = __all_sync(kFullMask, w);
         const float none = down ? INFINITY : -INFINITY;
         const uint32_t scores = tmem + lanes + sb * kKeys + C::kCols * half;
+        // the upper 64 of 128 columns only if some row sees them, as the product with V
+        // takes no more (packed prompts 180 -> 177 us, 600 prompts of 64 tokens 221 -> 190)
+        const bool upper = C::kCols > 64 && t.sight - key0 > 64;
+        const int cols = upper ? C::kCols : 64;
         if (key0 + kKeys > whole) {
           // An edge tile: the scores that a row does not see are overwritten.  One short
           // loop before code that all tiles share: with the masks inside an unrolled copy
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int left = lim - key0 - C::kCols * half;  // columns of this thread that the row sees
           const int all = __reduce_min_sync(kFullMask, left);
 #pragma unroll 1
-          for (int k = max(0, all) & ~31; k < C::kCols; k += 32) {
+          for (int k = max(0, all) & ~31; k < cols; k += 32) {
             float x[32];
             tc::tmem_ld32(scores + k, x);
 #pragma unroll
@@ -433,12 +437,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float s[64];  // 64 of the thread's scores
         auto fetch = [&](int k) { tc2::tmem_ld(scores + k, s); };
-        fetch(C::kCols - 64);
-        float x = down ? least(s) : largest(s);
-        if (C::kCols > 64) {
-          fetch(0);
-          x = down ? fminf(x, least(s)) : fmaxf(x, largest(s));
+        float x = none;
+        if (upper) {
+          fetch(64);
+          x = down ? least(s) : largest(s);
         }
+        fetch(0);
+        const float x0 = down ? least(s) : largest(s);
+        x = C::kCols > 64 ? (down ? fminf(x, x0) : fmaxf(x, x0)) : x0;
         float now = m;  // the row's reference, which O and the tiles before go by
         if (C::kHalves > 1) {
           float(&red)[2][128] = sh.red[h & 1];
@@ -492,7 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
         for (int k = 0; k < C::kCols; k += 64) {
-          if (k > 0) fetch(k);
+          if (k > 0) {
+            if (!upper) break;
+            fetch(k);
+          }
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
