@@ -29,7 +29,7 @@
 // 16 query heads of 256 on 2 KV heads 1.14 ms, 1.93 PFLOP/s, as fast as a plain
 // library product and limited by the board's power; 4,096 tokens 77 us, 1.79; 2,048
 // new tokens on 16,000 keys 268 us, 1.87.  At D = 128, 8,192 tokens 155 us, 1.77;
-// seven prompts of 1 to 4,096 tokens with 32 query heads on 8, 177 us, 1.54; seven
+// seven prompts of 1 to 4,096 tokens with 32 query heads on 8, 176 us, 1.55; seven
 // of 1 to 200 tokens (D = 256) 10 us (launch and latency).
 //
 // TMEM (512 columns): S of two or three key tiles (128 fp32 columns each, of whose
