@@ -55,6 +55,15 @@ def test_lengths(lens, D):
     agrees(lens, D=D, seed=len(lens) + lens[0])
 
 
+@pytest.mark.parametrize("D,h_kv", [(128, 40), (256, 40)])
+@pytest.mark.parametrize("q_len,k_len", [([150, 0, 7], [150, 30, 200]), ([300, 20], [1300, 900]),
+                                         ([257, 1, 256, 255], [700, 700, 700, 700])])
+def test_orders_of_the_tiles(q_len, k_len, D, h_kv):
+    """More tiles than pairs of CTAs: with keys and values on either side of 64 MB, which
+    choose the order of the tiles."""
+    agrees(q_len, k_len, h_q=h_kv, h_kv=h_kv, D=D, seed=50)
+
+
 @pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("q_len,k_len", [([1], [300]), ([40, 1, 3], [41, 129, 1000]),
                                          ([130], [900]), ([33, 64], [161, 64])])
