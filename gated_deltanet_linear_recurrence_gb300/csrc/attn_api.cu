@@ -59,10 +59,12 @@ gdn::PagedCache make_cache(const void* k_pages, const void* v_pages, const uint8
   return c;
 }
 
-// The pages' pointers: needed only where the pool and the table have entries.
+// The pointers: the table wherever it has entries (a position's page is looked up before
+// it is compared with the pool's size), the pages where the pool has some too.
 gdn_status check_pages(const gdn::PagedCache& c) {
   const bool any = c.num_pages > 0 && c.max_pages > 0;
-  if (any && (!c.k_pages || !c.v_pages || !c.table)) return GDN_ERR_NULL_POINTER;
+  if (c.max_pages > 0 && !c.table) return GDN_ERR_NULL_POINTER;
+  if (any && (!c.k_pages || !c.v_pages)) return GDN_ERR_NULL_POINTER;
   if (any && c.dtype == GDN_CACHE_E4M3 && (!c.k_exp || !c.v_exp)) return GDN_ERR_NULL_POINTER;
   if (!aligned(c.k_pages, 16) || !aligned(c.v_pages, 16) || !aligned(c.table, 4))
     return GDN_ERR_MISALIGNED;
