@@ -24,19 +24,22 @@
 //     of query heads on a KV head, so no multiply is padding at eight heads; one
 //     8x8 register transpose turns S^T's layout into P^T's.
 // Rounding: the weights P go to the matrix unit as bf16 pairs hi + lo (16
-// significant bits; the second product is free next to the memory time), or with
-// an e4m3 cache as f16, to which e4m3 values widen exactly.  Scores, maxima, sums
-// and O are fp32.
-// With an e4m3 cache a key's unit 2^ke scales its score, and a value's unit 2^ve
-// joins the exponent, 2^(t_i + ve_i - m') with m' = max_i (t_i + ve_i), so that
-// the f16 weights use their range whatever the units are; l keeps its own m.
+// significant bits; the second product is free next to the memory time).  Scores,
+// maxima, sums and O are fp32.
+// With an e4m3 cache a key's unit 2^ke scales its score (the codes widen exactly to
+// f16), and a value's code times its unit 2^ve is widened exactly to the bf16 that
+// reading the row back gives (above 2^7 the weight takes the rest of the unit), so
+// that both caches share one second product with fp32's range of exponents.  (Weights
+// in f16, units included, lost rows beside one with a far larger unit, a row of zeros
+// beside small values among them; they took 29.8 us for 131,072 keys, where these take
+// 31.3, and 86 for 90 us with 40 ragged sequences: the arithmetic pipe is the busiest.)
 // (Products of e4m3 operands themselves, with q and P as sums of e4m3 parts,
 // measured slower: at warp level they run as f16 products after a widening.)
 //
 // Measured (calls back to back, both kernels): 64 sequences of 8,192 bf16 keys, 16
 // query heads of 256 on 2, 162 us = 6.6 TB/s, 98 % of a plain copy's rate; one
-// sequence of 131,072 e4m3 keys 30 us = 4.5 TB/s, one eight times as long 168 us =
-// 6.4; e4m3 with 8 KV heads of 128: 40 ragged sequences 86 us = 5.8, 304 of 792 keys
+// sequence of 131,072 e4m3 keys 31 us = 4.3 TB/s, one eight times as long 168 us =
+// 6.4; e4m3 with 8 KV heads of 128: 40 ragged sequences 90 us = 5.5, 304 of 792 keys
 // 84 us = 5.9, 608 of 396 keys 91 us = 5.6; one of 4,096 keys 9 us.  So rows stream at
 // 6.6 to 6.9 TB/s, and a call costs about 10 us beside that: lengths, table and first
 // rows one after the other (3 us), the last rows' weights, the warps' join, and the
@@ -135,10 +138,33 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// an exponent byte as the unit itself, and as the exponent
+// an exponent byte as the unit itself
 __device__ __forceinline__ float unit_of(uint32_t byte) { return __uint_as_float(byte << 23); }
-__device__ __forceinline__ float exponent_of(uint32_t byte) {
-  return __uint_as_float(0x4b000000u | byte) - (8388608.f + 127.f);
+// The unit of a row of V in two factors: 2^120 times the part up to 2^7 for the codes
+// below (of two rows, as bf16), the rest for the weight (1 for bytes up to 134).
+constexpr uint32_t kUnitTop = 134;
+__device__ __forceinline__ uint32_t value_units(uint32_t byte0, uint32_t byte1) {
+  return ((min(byte0, kUnitTop) + 120) << 7) | ((min(byte1, kUnitTop) + 120) << 23);
+}
+__device__ __forceinline__ float weight_unit(uint32_t byte) {
+  return __uint_as_float((max(byte, kUnitTop) - (kUnitTop - 127)) << 23);
+}
+// An e4m3 code's sign, exponent and significand bits put where bf16 has them are 2^-120
+// of its value, subnormal codes included: the magnitudes of the even and of the odd bytes
+// of a word (a NaN code as 480), and two such values times their units (exact).
+constexpr uint32_t kMagnitude = 0x07f007f0u, kSigns = 0x80008000u;
+__device__ __forceinline__ uint32_t even_magnitudes(uint32_t codes) { return (codes << 4) & kMagnitude; }
+__device__ __forceinline__ uint32_t odd_magnitudes(uint32_t codes) { return (codes >> 4) & kMagnitude; }
+__device__ __forceinline__ uint32_t times(uint32_t two, uint32_t units) {
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(two), "r"(units));
+  return y;
+}
+// of the largest magnitudes seen, by halves
+__device__ __forceinline__ bool nan_code(uint32_t most) { return most >= 0x07f00000u || (most & 0xffffu) >= 0x07f0u; }
+// bf16 NaN where a magnitude is that of a NaN code, else zero
+__device__ __forceinline__ uint32_t nan_where(uint32_t magnitudes) {
+  return __vcmpeq2(magnitudes, kMagnitude) & 0x7fc07fc0u;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -302,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
   static_assert(kEntries >= 3 && kEntries <= 6, "ring");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) TileInfo infos[kWarps][kSlots];
-  __shared__ float wm[kWarps][kHeads], wv[kWarps][kHeads], wl[kWarps][kHeads];
+  __shared__ float wm[kWarps][kHeads], wl[kWarps][kHeads];
   __shared__ __align__(16) float joined[kWarps][kHeads][kPad];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   tc::wait_prerequisites();  // q, the cache, its table and lengths come from earlier kernels
@@ -490,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[t][c] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY;  // references of heads 2 pair, 2 pair + 1
-    float v0 = -INFINITY, v1 = -INFINITY;  // those with the values' units (e4m3)
     float l0 = 0.f, l1 = 0.f;              // this lane's rows only
 
     for (int i = 0; i < count; ++i) {
@@ -536,15 +561,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
       if (++get == kEntries) get = 0;
       const TileInfo& ti = info[i % kSlots];
       const uint32_t rows = ti.rows;
-      float ve[kM][2];  // the values' exponents (rows quad, quad + 8)
+      uint32_t vu2[kM][2];  // units of V's rows 2 pair, 2 pair + 1 (and + 8) of each block
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         float f0 = 1.f, f1 = 1.f;
         if (kFp8) {
           f0 = unit_of(ti.k_unit[16 * m + quad]);
           f1 = unit_of(ti.k_unit[16 * m + 8 + quad]);
-          ve[m][0] = exponent_of(ti.v_unit[16 * m + quad]);
-          ve[m][1] = exponent_of(ti.v_unit[16 * m + 8 + quad]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            vu2[m][x] = value_units(ti.v_unit[16 * m + 8 * x + 2 * pair], ti.v_unit[16 * m + 8 * x + 2 * pair + 1]);
         }
         const bool ok0 = quad < (int)((rows >> (16 * m)) & 0xff), ok1 = quad < (int)((rows >> (16 * m + 8)) & 0xff);
         s[m][0] = ok0 ? s[m][0] * f0 * unit0 : -INFINITY;
@@ -587,29 +613,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
         l1 += w[m][1] + w[m][3];
       }
       if (kFp8) {
-        float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
-          s[m][0] += ve[m][0];
-          s[m][1] += ve[m][0];
-          s[m][2] += ve[m][1];
-          s[m][3] += ve[m][1];
-          x0 = fmaxf(x0, fmaxf(s[m][0], s[m][2]));
-          x1 = fmaxf(x1, fmaxf(s[m][1], s[m][3]));
-        }
-        const float h0 = moved(v0, col_max(x0)), h1 = moved(v1, col_max(x1));
-        g0 = h0 == -INFINITY ? 0.f : h0;
-        g1 = h1 == -INFINITY ? 0.f : h1;
-        a0 = ex2(v0 - g0);
-        a1 = ex2(v1 - g1);
-        v0 = h0;
-        v1 = h1;
-#pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          w[m][0] = ex2(s[m][0] - g0);
-          w[m][1] = ex2(s[m][1] - g1);
-          w[m][2] = ex2(s[m][2] - g0);
-          w[m][3] = ex2(s[m][3] - g1);
+          const float e0 = weight_unit(ti.v_unit[16 * m + quad]), e1 = weight_unit(ti.v_unit[16 * m + 8 + quad]);
+          w[m][0] *= e0;
+          w[m][1] *= e0;
+          w[m][2] *= e1;
+          w[m][3] *= e1;
         }
       }
       if (__any_sync(kFullMask, a0 != 1.f || a1 != 1.f)) {
@@ -625,16 +635,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
       uint32_t ph[kM][2], pl[kM][2];
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
-        if (kFp8) {
-          ph[m][0] = transpose8x8(pack_f16(w[m][0], w[m][1]));
-          ph[m][1] = transpose8x8(pack_f16(w[m][2], w[m][3]));
-        } else {
-          const uint32_t x = pack_bf16(w[m][0], w[m][1]), y = pack_bf16(w[m][2], w[m][3]);
-          ph[m][0] = transpose8x8(x);
-          ph[m][1] = transpose8x8(y);
-          pl[m][0] = transpose8x8(pack_bf16(lo_part(x, w[m][0]), hi_part(x, w[m][1])));
-          pl[m][1] = transpose8x8(pack_bf16(lo_part(y, w[m][2]), hi_part(y, w[m][3])));
-        }
+        const uint32_t x = pack_bf16(w[m][0], w[m][1]), y = pack_bf16(w[m][2], w[m][3]);
+        ph[m][0] = transpose8x8(x);
+        ph[m][1] = transpose8x8(y);
+        pl[m][0] = transpose8x8(pack_bf16(lo_part(x, w[m][0]), hi_part(x, w[m][1])));
+        pl[m][1] = transpose8x8(pack_bf16(lo_part(y, w[m][2]), hi_part(y, w[m][3])));
       }
       // ---- O^T += V^T P^T
       copy_wait<kEntries - 2>();
@@ -656,21 +661,48 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
           }
       } else {
         const uint32_t tile = vt + ((lane & 7) + 8 * ((lane >> 3) & 1)) * kRowBytes;
+        // (row blocks outside: the products of one accumulator far apart; the other way
+        // round 131,072 keys took 32.7 for 31.3 us)
+        uint32_t most = 0;
 #pragma unroll
-        for (int t = 0; t < kQ; t += 2)
+        for (int m = 0; m < kM; ++m)
 #pragma unroll
-          for (int m = 0; m < kM; ++m) {
+          for (int t = 0; t < kQ; t += 2) {
             uint32_t r[4];  // chunks t (r0: rows 0-7, r1: 8-15) and t + 1 (r2, r3)
             ldsm4t(tile + 16 * m * kRowBytes + (((t + (lane >> 4)) ^ swz) << 4), r);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               // bytes (row 2 pair: dims 2 quad, 2 quad + 1; row 2 pair + 1: the same)
               uint32_t a[4];
-              widen(__byte_perm(r[2 * h], 0, 0x3120), a[0], a[1]);
-              widen(__byte_perm(r[2 * h + 1], 0, 0x3120), a[2], a[3]);
-              mma_f16(o[t + h], a, ph[m][0], ph[m][1]);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t c = r[2 * h + x];
+                const uint32_t even = even_magnitudes(c), odd = odd_magnitudes(c);
+                most = __vimax3_u16x2(most, even, odd);
+                a[2 * x] = times(even | ((c << 8) & kSigns), vu2[m][x]);
+                a[2 * x + 1] = times(odd | (c & kSigns), vu2[m][x]);
+              }
+              mma_bf16(o[t + h], a, ph[m][0], ph[m][1]);
+              mma_bf16(o[t + h], a, pl[m][0], pl[m][1]);
             }
           }
+        // a value that is not finite makes its dimension of every head so
+        if (__any_sync(kFullMask, nan_code(most))) {
+#pragma unroll
+          for (int t = 0; t < kQ; t += 2)
+#pragma unroll 1
+            for (int m = 0; m < kM; ++m) {
+              uint32_t r[4];
+              ldsm4t(tile + 16 * m * kRowBytes + (((t + (lane >> 4)) ^ swz) << 4), r);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a[4] = {
+                    nan_where(even_magnitudes(r[2 * h])), nan_where(odd_magnitudes(r[2 * h])),
+                    nan_where(even_magnitudes(r[2 * h + 1])), nan_where(odd_magnitudes(r[2 * h + 1]))};
+                mma_bf16(o[t + h], a, 0x3f803f80u, 0x3f803f80u);
+              }
+            }
+        }
       }
     }
     copy_wait<0>();
@@ -683,15 +715,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
       l0 += __shfl_xor_sync(kFullMask, l0, off);
       l1 += __shfl_xor_sync(kFullMask, l1, off);
     }
-    if (!kFp8) {
-      v0 = m0;
-      v1 = m1;
-    }
     if (quad == 0) {
       wm[warp][2 * pair] = m0;
       wm[warp][2 * pair + 1] = m1;
-      wv[warp][2 * pair] = v0;
-      wv[warp][2 * pair + 1] = v1;
       wl[warp][2 * pair] = l0;
       wl[warp][2 * pair + 1] = l1;
     }
@@ -700,28 +726,24 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
     more = next_piece();
     if (more) open();
     __syncthreads();
-    float t0 = wv[0][2 * pair], t1 = wv[0][2 * pair + 1];
+    float t0 = wm[0][2 * pair], t1 = wm[0][2 * pair + 1];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
-      t0 = fmaxf(t0, wv[w][2 * pair]);
-      t1 = fmaxf(t1, wv[w][2 * pair + 1]);
+      t0 = fmaxf(t0, wm[w][2 * pair]);
+      t1 = fmaxf(t1, wm[w][2 * pair + 1]);
     }
-    const float f0 = v0 == -INFINITY ? 0.f : ex2(v0 - t0), f1 = v1 == -INFINITY ? 0.f : ex2(v1 - t1);
+    const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - t0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - t1);
     // the head and the four dims that this thread finishes
     const int h = tid / (kChunk / 4), d4 = tid % (kChunk / 4);
     float M = -INFINITY, l = 0.f, r = 0.f;
     if (h < G) {
-      float T = wv[0][h];
       M = wm[0][h];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        M = fmaxf(M, wm[w][h]);
-        T = fmaxf(T, wv[w][h]);
-      }
+      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, wm[w][h]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) l += wm[w][h] == -INFINITY ? 0.f : wl[w][h] * ex2(wm[w][h] - M);
       // l > 0 whenever a row was seen; NaN stays NaN
-      r = l == 0.f ? 0.f : (kFp8 ? ex2(T - M) : 1.f) / l;
+      r = l == 0.f ? 0.f : 1.f / l;
       if (!to_o && d4 == 0)
         reinterpret_cast<float2*>(p.partial + (int64_t)p.ctas * 2 * G * D)[part + h] = make_float2(M, l);
     }
