@@ -138,8 +138,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// an exponent byte as the unit itself
-__device__ __forceinline__ float unit_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+// an exponent byte's unit in two factors of half its exponent
+__device__ __forceinline__ float2 half_units(uint32_t byte) {
+  return make_float2(__uint_as_float((byte / 2 + 64) << 23), __uint_as_float((byte - byte / 2 + 63) << 23));
+}
 // The unit of a row of V in two factors: 2^120 times the part up to 2^7 for the codes
 // below (of two rows, as bf16), the rest for the weight (1 for bytes up to 134).
 constexpr uint32_t kUnitTop = 134;
@@ -487,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
     const int64_t head0 = (int64_t)seq * p.h_q + (int64_t)j * G;
     // ---- Q^T as the products' B operand: head `quad`, zeros past G
     float unit0 = score_unit, unit1 = score_unit;  // of heads 2 pair, 2 pair + 1
+    float rest0 = 1.f, rest1 = 1.f;                // (e4m3: half of q's exponent apart)
     if (kFp8) {
       // scaled by a power of two per head so that f16 holds what bf16 held (down to
       // 2^-38 of the head's largest)
@@ -498,16 +501,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
           top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[kk][r] << 16)), fabsf(__uint_as_float(qf[kk][r] & 0xffff0000u))));
       top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-      const int e = min(max((int)(__float_as_uint(top) >> 23), 16), 240) - 127 - 14;
-      const float inv = pow2(-e), unit = pow2(e);
+      const int e = min(max((int)(__float_as_uint(top) >> 23), 16), 254) - 127 - 14;
+      const float inv = pow2(-e);
 #pragma unroll
       for (int kk = 0; kk < kQ; ++kk)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
           qf[kk][r] = pack_f16(__uint_as_float(qf[kk][r] << 16) * inv,
                                __uint_as_float(qf[kk][r] & 0xffff0000u) * inv);
-      unit0 *= __shfl_sync(kFullMask, unit, 8 * pair);
-      unit1 *= __shfl_sync(kFullMask, unit, 8 * pair + 4);
+      const int e0 = __shfl_sync(kFullMask, e, 8 * pair), e1 = __shfl_sync(kFullMask, e, 8 * pair + 4);
+      unit0 *= pow2(e0 / 2);
+      unit1 *= pow2(e1 / 2);
+      rest0 = pow2(e0 - e0 / 2);
+      rest1 = pow2(e1 - e1 / 2);
     }
 
     float o[kQ][4];
@@ -564,19 +570,29 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
       uint32_t vu2[kM][2];  // units of V's rows 2 pair, 2 pair + 1 (and + 8) of each block
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
-        float f0 = 1.f, f1 = 1.f;
         if (kFp8) {
-          f0 = unit_of(ti.k_unit[16 * m + quad]);
-          f1 = unit_of(ti.k_unit[16 * m + 8 + quad]);
+          // the key's unit and the head's are multiplied in by halves of their exponents, in
+          // turn: a large one and a small one whose product is ordinary leave the range nowhere
+          const float2 f0 = half_units(ti.k_unit[16 * m + quad]), f1 = half_units(ti.k_unit[16 * m + 8 + quad]);
+          s[m][0] = s[m][0] * f0.x * unit0 * f0.y * rest0;
+          s[m][1] = s[m][1] * f0.x * unit1 * f0.y * rest1;
+          s[m][2] = s[m][2] * f1.x * unit0 * f1.y * rest0;
+          s[m][3] = s[m][3] * f1.x * unit1 * f1.y * rest1;
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             vu2[m][x] = value_units(ti.v_unit[16 * m + 8 * x + 2 * pair], ti.v_unit[16 * m + 8 * x + 2 * pair + 1]);
         }
         const bool ok0 = quad < (int)((rows >> (16 * m)) & 0xff), ok1 = quad < (int)((rows >> (16 * m + 8)) & 0xff);
-        s[m][0] = ok0 ? s[m][0] * f0 * unit0 : -INFINITY;
-        s[m][1] = ok0 ? s[m][1] * f0 * unit1 : -INFINITY;
-        s[m][2] = ok1 ? s[m][2] * f1 * unit0 : -INFINITY;
-        s[m][3] = ok1 ? s[m][3] * f1 * unit1 : -INFINITY;
+        if (!kFp8) {
+          s[m][0] *= unit0;
+          s[m][1] *= unit1;
+          s[m][2] *= unit0;
+          s[m][3] *= unit1;
+        }
+        s[m][0] = ok0 ? s[m][0] : -INFINITY;
+        s[m][1] = ok0 ? s[m][1] : -INFINITY;
+        s[m][2] = ok1 ? s[m][2] : -INFINITY;
+        s[m][3] = ok1 ? s[m][3] : -INFINITY;
       }
       // ---- online softmax; a reference moves when it is exceeded by more than kSlack
       auto col_max = [&](float x) {

@@ -1,6 +1,6 @@
 """Decode attention over the paged cache where sizes differ: rows of V next to rows of
-zeros or to one very large channel, a long tail of small weights, values at the ends of
-bf16's range, NaN codes.  Both cache types against the fp64 oracle over the cached values.
+zeros or to one very large channel, a long tail of small weights, values, and keys with
+queries, at the ends of bf16's range, NaN codes.  Both cache types against the fp64 oracle over the cached values.
 
 Bounds, by element, from the arithmetic (A = the oracle's attention over |v|, A >= |o|):
 o is stored in bf16, 2^-8 |o|; the weights are bf16 pairs, 2^-16 A, or one fp16, 2^-11 A;
@@ -80,6 +80,17 @@ def test_a_long_tail_of_small_weights(down, D, fp8):
     q = torch.zeros((1, 4, D), dtype=torch.bfloat16)
     q[..., 0] = 1.0
     close(c, q, lens, page, float(np.log(2.0)))
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("power", [116, -118])
+def test_keys_and_queries_at_the_ends_of_the_range(power, D, fp8):
+    """Ordinary scores from keys of 2^power and queries of 2^-power."""
+    def rows(name, x, g):
+        return (x.double() * 2.0 ** power).to(x.dtype) if name == "k" else x
+    lens = [200, 9]
+    q = (normal(gen(66), 2, 8, D).double() * 2.0 ** -power).to(torch.bfloat16)
+    close(build(lens, 1, D, 16, fp8, 65, rows), q, lens, 16, D ** -0.5)
 
 
 @pytest.mark.parametrize("D,fp8", FORMS)
