@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -125,25 +126,44 @@ struct Cache {  // a paged cache's tensors and sizes
   }
 };
 
-// The call's stream; tensors allocated for a call on another stream than the current
-// one must not be given out again before that stream has passed the call.
+// The call's stream, and the tensors that belong on it.  What a call on another stream
+// than the current one allocates comes from that stream's own memory: a block of the
+// current stream's may still be written by work queued there.  An output of such a call is
+// not given out again before the current stream, where the caller gets it, has passed the
+// point where it is freed; a tensor of the caller's not before the call's stream has.
 struct Stream {
   cudaStream_t handle;
-  bool given;
-  explicit Stream(PyObject* o) : given(o != Py_None) {
-    if (!given) {
-      handle = c10::cuda::getCurrentCUDAStream().stream();
-      return;
+  bool other;  // than the current one
+  explicit Stream(PyObject* o) {
+    const cudaStream_t current = c10::cuda::getCurrentCUDAStream().stream();
+    handle = current;
+    if (o != Py_None) {
+      PyObject* h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream")
+                                                             : PyNumber_Long(o);
+      if (!h) throw python_error();
+      handle = static_cast<cudaStream_t>(PyLong_AsVoidPtr(h));
+      Py_DECREF(h);
+      if (PyErr_Occurred()) throw python_error();
+      if (handle == cudaStreamLegacy) handle = nullptr;  // the same stream, as torch names it
     }
-    PyObject* h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream")
-                                                           : PyNumber_Long(o);
-    if (!h) throw python_error();
-    handle = static_cast<cudaStream_t>(PyLong_AsVoidPtr(h));
-    Py_DECREF(h);
-    if (PyErr_Occurred()) throw python_error();
+    other = handle != current;
   }
-  void keep(const at::Tensor& t) const {
-    if (given) t.record_stream(c10::cuda::getStreamFromExternal(handle, t.device().index()));
+  c10::cuda::CUDAStream of_torch(c10::DeviceIndex device) const {
+    return c10::cuda::getStreamFromExternal(handle, device);
+  }
+  at::Tensor scratch(c10::IntArrayRef shape, const at::TensorOptions& options) const {
+    if (!other) return at::empty(shape, options);
+    const c10::cuda::CUDAStreamGuard on(of_torch(options.device().index()));
+    return at::empty(shape, options);
+  }
+  at::Tensor output(c10::IntArrayRef shape, const at::TensorOptions& options) const {
+    at::Tensor t = scratch(shape, options);
+    if (other) t.record_stream(c10::cuda::getCurrentCUDAStream(t.device().index()));
+    return t;
+  }
+  const at::Tensor& given(const at::Tensor& t) const {
+    if (other) t.record_stream(of_torch(t.device().index()));
+    return t;
   }
   gdn_stream_t abi() const { return reinterpret_cast<gdn_stream_t>(handle); }
 };
@@ -214,15 +234,13 @@ PyObject* kv_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &cu = ints(a[3], {c.N + 1}, "cu_seqlens"), &st = ints(a[4], {c.N}, "start_pos");
     const Stream s(a[10]);
     auto out = [&](PyObject* o, const char* name) {
-      return o == Py_None ? at::empty({T, c.h_kv, c.D}, c.options) : rows(o, {T, c.h_kv, c.D}, name);
+      return o == Py_None ? s.output({T, c.h_kv, c.D}, c.options) : s.given(rows(o, {T, c.h_kv, c.D}, name));
     };
     const at::Tensor k = out(a[8], "k"), v = out(a[9], "v");
     check(p_gather(k.data_ptr(), v.data_ptr(), token_stride(k, "k"), token_stride(v, "v"), c.k, c.v, c.ke,
                    c.ve, c.table, i32_of(cu), i32_of(st), as32(c.N), T, as32(c.h_kv), as32(c.D),
                    as32(c.page), as32(c.P), as32(c.max_pages), c.dtype, s.abi()),
           "gdn_kv_gather");
-    s.keep(k);
-    s.keep(v);
     PyObject *pk = THPVariable_Wrap(k), *pv = THPVariable_Wrap(v);
     return pk && pv ? Py_BuildValue("(NN)", pk, pv) : nullptr;
   });
@@ -239,12 +257,11 @@ PyObject* attn_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& len = ints(a[4], {c.N}, "cache_len");
     const float scale = scale_of(a[7], c.D);
     const Stream s(a[10]);
-    const at::Tensor o = a[8] == Py_None ? at::empty({c.N, h_q, c.D}, c.options)
-                                         : rows(a[8], {c.N, h_q, c.D}, "o", true);
+    const at::Tensor o = a[8] == Py_None ? s.output({c.N, h_q, c.D}, c.options)
+                                         : s.given(rows(a[8], {c.N, h_q, c.D}, "o", true));
     at::Tensor ws;
     if (a[9] == Py_None) {
-      ws = at::empty({(int64_t)p_decode_ws(as32(h_q), as32(c.h_kv), as32(c.D))}, c.options.dtype(at::kByte));
-      s.keep(ws);
+      ws = s.scratch({(int64_t)p_decode_ws(as32(h_q), as32(c.h_kv), as32(c.D))}, c.options.dtype(at::kByte));
     } else {
       ws = tensor(a[9], "workspace");
       if (!(ws.is_cuda() && ws.is_contiguous())) value_error("workspace must be on the GPU, contiguous");
@@ -253,7 +270,6 @@ PyObject* attn_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    as32(c.N), as32(h_q), as32(c.h_kv), as32(c.D), as32(c.page), as32(c.P), as32(c.max_pages),
                    c.dtype, scale, ws.numel() ? ws.data_ptr() : nullptr, ws.nbytes(), s.abi()),
           "gdn_attn_decode_paged");
-    s.keep(o);
     return THPVariable_Wrap(o);
   });
 }
@@ -273,12 +289,12 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (N < 0) value_error("cu_seqlens_q must have at least one entry");
     const float scale = scale_of(a[5], D);
     const Stream s(a[7]);
-    const at::Tensor o = a[6] == Py_None ? at::empty({Tq, h_q, D}, q.options()) : rows(a[6], {Tq, h_q, D}, "o", true);
+    const at::Tensor o = a[6] == Py_None ? s.output({Tq, h_q, D}, q.options())
+                                         : s.given(rows(a[6], {Tq, h_q, D}, "o", true));
     check(p_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), i32_of(cq), i32_of(ck), as32(N), Tq,
                     Tk, as32(h_q), as32(h_kv), as32(D), token_stride(q, "q"), token_stride(k, "k"),
                     token_stride(v, "v"), GDN_BF16, scale, s.abi()),
           "gdn_attn_prefill");
-    s.keep(o);
     return THPVariable_Wrap(o);
   });
 }
