@@ -81,13 +81,26 @@ int64_t dim(const at::Tensor& t, int64_t n, const char* name, const char* what) 
   return 0;
 }
 
+// The tensors' common device: the call launches there, whatever the current one is.
+c10::Device one_device(std::initializer_list<const at::Tensor*> tensors) {
+  const c10::Device d = (*tensors.begin())->device();
+  for (const at::Tensor* t : tensors)
+    if (t->device() != d) value_error("tensors must be on one device, got " + d.str() + " and " + t->device().str());
+  return d;
+}
+
 struct Cache {  // a paged cache's tensors and sizes
+  c10::Device device = c10::Device(c10::kCPU);
   const void *k, *v;
   const uint8_t *ke = nullptr, *ve = nullptr;
   const int32_t* table;
   int64_t P, h_kv, page, D, N, max_pages;
   gdn_cache_dtype dtype;
   at::TensorOptions options;  // of rows read back
+  void with(std::initializer_list<const at::Tensor*> tensors) const {
+    if (one_device(tensors) != device)
+      value_error("tensors must be on the cache's device " + device.str() + ", got " + one_device(tensors).str());
+  }
   Cache(PyObject* k_pages, PyObject* v_pages, PyObject* page_table, PyObject* k_exp, PyObject* v_exp) {
     const at::Tensor &kp = tensor(k_pages, "k_pages"), &vp = tensor(v_pages, "v_pages");
     const at::Tensor& pt = tensor(page_table, "page_table");
@@ -123,19 +136,24 @@ struct Cache {  // a paged cache's tensors and sizes
     v = vp.data_ptr();
     table = static_cast<const int32_t*>(pt.data_ptr());
     options = kp.options().dtype(at::kBFloat16);
+    device = one_device({&kp, &vp, &pt});
+    if (dtype == GDN_CACHE_E4M3) one_device({&kp, &tensor(k_exp, "k_exp"), &tensor(v_exp, "v_exp")});
   }
 };
 
-// The call's stream, and the tensors that belong on it.  What a call on another stream
+// Where a call launches: on its tensors' device and the given stream, or that device's
+// current one; and the tensors that belong on the stream.  What a call on another stream
 // than the current one allocates comes from that stream's own memory: a block of the
 // current stream's may still be written by work queued there.  An output of such a call is
 // not given out again before the current stream, where the caller gets it, has passed the
 // point where it is freed; a tensor of the caller's not before the call's stream has.
-struct Stream {
+struct Launch {
+  c10::cuda::OptionalCUDAGuard on;  // only where another device is the current one
   cudaStream_t handle;
   bool other;  // than the current one
-  explicit Stream(PyObject* o) {
-    const cudaStream_t current = c10::cuda::getCurrentCUDAStream().stream();
+  Launch(c10::Device device, PyObject* o) {
+    if (c10::cuda::current_device() != device.index()) on.set_device(device);
+    const cudaStream_t current = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     handle = current;
     if (o != Py_None) {
       PyObject* h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream")
@@ -214,7 +232,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t T = k0.size(0);
     const at::Tensor &k = rows(a[0], {T, c.h_kv, c.D}, "k"), &v = rows(a[1], {T, c.h_kv, c.D}, "v");
     const at::Tensor &cu = ints(a[5], {c.N + 1}, "cu_seqlens"), &st = ints(a[6], {c.N}, "start_pos");
-    const Stream s(a[9]);
+    c.with({&k, &v, &cu, &st});
+    const Launch s(c.device, a[9]);
     check(p_append(k.data_ptr(), v.data_ptr(), token_stride(k, "k"), token_stride(v, "v"),
                    const_cast<void*>(c.k), const_cast<void*>(c.v), const_cast<uint8_t*>(c.ke),
                    const_cast<uint8_t*>(c.ve), c.table, i32_of(cu), i32_of(st), as32(c.N), T, as32(c.h_kv),
@@ -232,11 +251,13 @@ PyObject* kv_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyErr_Occurred()) throw python_error();
     if (T < 0) value_error("total_tokens must not be negative");
     const at::Tensor &cu = ints(a[3], {c.N + 1}, "cu_seqlens"), &st = ints(a[4], {c.N}, "start_pos");
-    const Stream s(a[10]);
+    c.with({&cu, &st});
+    const Launch s(c.device, a[10]);
     auto out = [&](PyObject* o, const char* name) {
       return o == Py_None ? s.output({T, c.h_kv, c.D}, c.options) : s.given(rows(o, {T, c.h_kv, c.D}, name));
     };
     const at::Tensor k = out(a[8], "k"), v = out(a[9], "v");
+    c.with({&k, &v});
     check(p_gather(k.data_ptr(), v.data_ptr(), token_stride(k, "k"), token_stride(v, "v"), c.k, c.v, c.ke,
                    c.ve, c.table, i32_of(cu), i32_of(st), as32(c.N), T, as32(c.h_kv), as32(c.D),
                    as32(c.page), as32(c.P), as32(c.max_pages), c.dtype, s.abi()),
@@ -256,7 +277,8 @@ PyObject* attn_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& q = rows(a[0], {c.N, h_q, c.D}, "q");
     const at::Tensor& len = ints(a[4], {c.N}, "cache_len");
     const float scale = scale_of(a[7], c.D);
-    const Stream s(a[10]);
+    c.with({&q, &len});
+    const Launch s(c.device, a[10]);
     const at::Tensor o = a[8] == Py_None ? s.output({c.N, h_q, c.D}, c.options)
                                          : s.given(rows(a[8], {c.N, h_q, c.D}, "o", true));
     at::Tensor ws;
@@ -266,6 +288,7 @@ PyObject* attn_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = tensor(a[9], "workspace");
       if (!(ws.is_cuda() && ws.is_contiguous())) value_error("workspace must be on the GPU, contiguous");
     }
+    c.with({&o, &ws});
     check(p_decode(q.data_ptr(), token_stride(q, "q"), c.k, c.v, c.ke, c.ve, c.table, i32_of(len), o.data_ptr(),
                    as32(c.N), as32(h_q), as32(c.h_kv), as32(c.D), as32(c.page), as32(c.P), as32(c.max_pages),
                    c.dtype, scale, ws.numel() ? ws.data_ptr() : nullptr, ws.nbytes(), s.abi()),
@@ -288,9 +311,10 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& ck = a[4] == Py_None ? cq : ints(a[4], {N + 1}, "cu_seqlens_k");
     if (N < 0) value_error("cu_seqlens_q must have at least one entry");
     const float scale = scale_of(a[5], D);
-    const Stream s(a[7]);
+    const Launch s(one_device({&q, &k, &v, &cq, &ck}), a[7]);
     const at::Tensor o = a[6] == Py_None ? s.output({Tq, h_q, D}, q.options())
                                          : s.given(rows(a[6], {Tq, h_q, D}, "o", true));
+    one_device({&q, &o});
     check(p_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), i32_of(cq), i32_of(ck), as32(N), Tq,
                     Tk, as32(h_q), as32(h_kv), as32(D), token_stride(q, "q"), token_stride(k, "k"),
                     token_stride(v, "v"), GDN_BF16, scale, s.abi()),
@@ -304,6 +328,14 @@ PyObject* token_stride_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 1, [&]() -> PyObject* {
     dim(tensor(a[0], "t"), 3, "t", "[T, heads, D]");
     return PyLong_FromLongLong(token_stride(tensor(a[0], "t"), "t"));
+  });
+}
+
+// one_device(t, u): None where the calls take both tensors together
+PyObject* one_device_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 2, [&]() -> PyObject* {
+    one_device({&tensor(a[0], "t"), &tensor(a[1], "u")});
+    Py_RETURN_NONE;
   });
 }
 
@@ -334,6 +366,7 @@ PyMethodDef methods[] = {FAST("init", init),
                          FAST("attn_decode_paged", attn_decode_paged),
                          FAST("attn_prefill", attn_prefill),
                          FAST("token_stride", token_stride_py),
+                         FAST("one_device", one_device_py),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
