@@ -35,7 +35,8 @@ namespace {
 constexpr int kKvWarps = 8;
 
 // Largest n in [0, N) with cu[n] <= t, for the whole warp (32 probes a step).
-// Entries out of order only make the answer wrong, which the caller checks.
+// Entries out of order only make the answer wrong, which the caller checks (and then
+// looks through all sequences).
 __device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int t, int lane) {
   int lo = 0, hi = N;
   while (hi - lo > 1) {
@@ -50,14 +51,32 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int t, in
   return lo;
 }
 
+// The first sequence whose range holds token t, by looking at each; -1 when none does.
+// For offsets out of order, among which the search by halves loses its way.
+__device__ __noinline__ int look_for_sequence(const KvRowsArgs& a, int t, int lane) {
+  for (int base = 0; base < a.num_seqs; base += 32) {
+    const int n = base + lane;
+    bool holds = false;
+    if (n < a.num_seqs) {
+      const int c0 = __ldg(a.cu_seqlens + n), c1 = __ldg(a.cu_seqlens + n + 1);
+      holds = c0 >= 0 && c0 <= t && t < c1 && c1 <= a.total_tokens;
+    }
+    const unsigned hit = __ballot_sync(kFullMask, holds);
+    if (hit) return base + __ffs(hit) - 1;
+  }
+  return -1;
+}
+
 // Index of the cached row of (token t, head 0), or -1 (with the error recorded).
 // Rows of the other heads follow page_size apart.
 __device__ __forceinline__ int64_t token_row(const KvRowsArgs& a, int t, int lane) {
-  const int n = find_sequence(a.cu_seqlens, a.num_seqs, t, lane);
-  const int c0 = __ldg(a.cu_seqlens + n), c1 = __ldg(a.cu_seqlens + n + 1);
+  int n = find_sequence(a.cu_seqlens, a.num_seqs, t, lane);
+  int c0 = __ldg(a.cu_seqlens + n), c1 = __ldg(a.cu_seqlens + n + 1);
   if (c0 < 0 || t < c0 || t >= c1) {
     if (lane == 0) raise_error(a.err, kErrBadCuSeqlens);
-    return -1;
+    n = look_for_sequence(a, t, lane);
+    if (n < 0) return -1;
+    c0 = __ldg(a.cu_seqlens + n);
   }
   const int64_t pos = (int64_t)__ldg(a.start + n) + (t - c0);
   const int64_t pi = pos >> a.cache.page_shift;
@@ -72,11 +91,14 @@ __device__ __forceinline__ int64_t token_row(const KvRowsArgs& a, int t, int lan
   return (((int64_t)page * a.cache.h_kv) << a.cache.page_shift) + slot;
 }
 
-// The packing itself: cu[0] = 0 and cu[N] = T (the first warp looks).
+// The packing itself: cu[0] = 0, no range decreases, cu[N] = T.  The warps share the
+// sequences out, 32 at a time: one that owns no token has no warp of its own to look.
 __device__ __forceinline__ void check_packing(const KvRowsArgs& a, int t, int lane) {
-  if (t == 0 && lane == 0 &&
-      (__ldg(a.cu_seqlens) != 0 || (int64_t)__ldg(a.cu_seqlens + a.num_seqs) != a.total_tokens))
-    raise_error(a.err, kErrBadCuSeqlens);
+  for (int64_t n = (int64_t)t * 32 + lane; n < a.num_seqs; n += a.total_tokens * 32) {
+    const int c0 = __ldg(a.cu_seqlens + n), c1 = __ldg(a.cu_seqlens + n + 1);
+    if (c1 < c0 || (n == 0 && c0 != 0) || (n == a.num_seqs - 1 && c1 != a.total_tokens))
+      raise_error(a.err, kErrBadCuSeqlens);
+  }
 }
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
@@ -147,7 +169,6 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_kernel(const KvRowsAr
   const int64_t tt = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
   if (tt >= a.total_tokens) return;
   const int t = (int)tt;
-  check_packing(a, t, lane);
   const int part = lane % kLanes, sub = lane / kLanes;
   const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + t * a.k_stride);
   const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + t * a.v_stride);
@@ -159,6 +180,7 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_kernel(const KvRowsAr
     vx = __ldg(vs + lane);
   }
   const int64_t row0 = token_row(a, t, lane);
+  check_packing(a, t, lane);
   if (row0 < 0) return;
   for (int j0 = 0; j0 < h_kv; j0 += kHeads) {
     const int j = j0 + sub;
@@ -200,11 +222,11 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_gather_kernel(const KvRowsAr
   const int64_t tt = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
   if (tt >= a.total_tokens) return;
   const int t = (int)tt;
-  check_packing(a, t, lane);
   const int part = lane % kLanes, sub = lane / kLanes;
   uint4* ks = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k) + t * a.k_stride);
   uint4* vs = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v) + t * a.v_stride);
   const int64_t row0 = token_row(a, t, lane);
+  check_packing(a, t, lane);
 #pragma unroll 4
   for (int j = sub; j < a.cache.h_kv; j += kHeads) {
     uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;  // a row without a page reads as zeros
