@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const int grp = C::kGroups > 1 ? part : 0, half = C::kHalves > 1 ? part : 0;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    // (scale 0: all scores alike, by a factor that keeps a masked score infinite)
-    const float c = p.scale == 0.f ? 1e-30f : p.scale * kLog2e;
+    // (scale 0: all scores alike, by the smallest factor that keeps a masked score infinite:
+    // 2^-149, with which the largest product is 2^-21)
+    const float c = p.scale == 0.f ? __uint_as_float(1) : p.scale * kLog2e;
     const bool down = c < 0.f;  // the largest score is then the smallest product
     const uint32_t r_p = tc2::in_cta(sh.p_ready, 0);
     bool carried = true;  // no wait expired since the last barrier of these warps
