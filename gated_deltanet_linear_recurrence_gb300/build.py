@@ -5,12 +5,14 @@ them into ``_build/libgdn_gb300.so``, an in-tree shared library exporting the
 C ABI of ``include/gdn.h``.  The CUDA runtime is linked statically; the
 library depends on the driver (libcuda) only at run time.  Beside it, with g++,
 ``_build/_attn_binding.so``: the CPython extension through which torch tensors
-reach the attention layers' operators (``csrc/attn_binding.cpp``).
+reach the attention layers' operators (``csrc/attn_binding.cpp``), compiled again when
+torch or Python is another version.
 """
 import concurrent.futures
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +49,21 @@ def _binding_command(out):
             "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
             "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", out,
             "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _binding_made_with():
+    """What the extension is compiled against: another torch or Python wants another one."""
+    import torch
+
+    return "\n".join([torch.__version__, sys.version, *_binding_command(binding_path())])
+
+
+def _binding_stale(headers):
+    stamp = binding_path() + ".made_with"
+    if _stale(binding_path(), [BINDING_SRC] + headers) or not os.path.exists(stamp):
+        return True
+    with open(stamp) as f:
+        return f.read() != _binding_made_with()
 
 
 def _nvcc():
@@ -98,13 +115,15 @@ def build(force=False, verbose=False, extra_flags=()):
         return r
 
     binding, binding_tmp = binding_path(), binding_path() + f".tmp{os.getpid()}"
-    if force or _stale(binding, [BINDING_SRC] + headers):
+    if force or _binding_stale(headers):
         jobs.append(_binding_command(binding_tmp))
     if jobs:
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
     if os.path.exists(binding_tmp):
         os.replace(binding_tmp, binding)
+        with open(binding + ".made_with", "w") as f:
+            f.write(_binding_made_with())
     out = lib_path()
     if force or jobs or _stale(out, objs):
         tmp = out + f".tmp{os.getpid()}"
@@ -114,5 +133,4 @@ def build(force=False, verbose=False, extra_flags=()):
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
