@@ -62,15 +62,15 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kHeads = 8;  // query heads of a KV head, padded (N of the products)
-constexpr int kSlots = 4;          // tiles whose row counts and units are kept
+constexpr int kSlots = 2;  // tiles whose row counts and units are kept: one at work, one on its way
 
-// CTAs on an SM, as registers allow (O and Q of a warp: 6 or 3 KB), bytes of a
-// warp's ring, and rows of its tile.
-__host__ __device__ constexpr int ctas_per_sm(int D, bool fp8) { return D == 128 ? 4 : 2; }
-__host__ __device__ constexpr uint32_t ring_bytes(int D, bool fp8) { return D == 128 ? 12288 : 24576; }
-__host__ __device__ constexpr int tile_rows(int D, bool fp8) { return fp8 ? 32 : 16; }
+// CTAs on an SM, as registers allow (O and Q of a warp: 12 KB at D = 256, 6 at 128),
+// bytes of a warp's ring, and rows of its tile.
+__host__ __device__ constexpr int ctas_per_sm(int D) { return D == 128 ? 4 : 2; }
+__host__ __device__ constexpr uint32_t ring_bytes(int D) { return D == 128 ? 12288 : 24576; }
+__host__ __device__ constexpr int tile_rows(bool fp8) { return fp8 ? 32 : 16; }
 // Rows of a unit of work: a tile for each warp.
-__host__ __device__ constexpr int unit_rows(int D, bool fp8) { return kWarps * tile_rows(D, fp8); }
+__host__ __device__ constexpr int unit_rows(bool fp8) { return kWarps * tile_rows(fp8); }
 
 struct TileInfo {     // of a tile on its way through a warp's ring
   uint32_t rows;      // rows to use in each group of eight, a byte a group
@@ -315,19 +315,19 @@ __device__ __forceinline__ bool find_work(const PagedAttnArgs& p, int c, bool re
 }
 
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_kernel(const PagedAttnArgs p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_paged_kernel(const PagedAttnArgs p) {
   constexpr int kRowBytes = kFp8 ? D : 2 * D;
-  constexpr uint32_t kRing = ring_bytes(D, kFp8);
-  constexpr int kRows = tile_rows(D, kFp8), kUnit = unit_rows(D, kFp8);
+  constexpr uint32_t kRing = ring_bytes(D);
+  constexpr int kRows = tile_rows(kFp8), kUnit = unit_rows(kFp8);
   constexpr int kM = kRows / 16;              // row blocks of the products
   constexpr int kGroups = kRows / 8;          // groups of rows within a page
   constexpr uint32_t kEntry = kRows * kRowBytes;  // K or V of a tile
-  constexpr int kEntries = kRing / kEntry;
+  constexpr int kEntries = 3;  // of the ring: K, V and the next K, or V, K and the next V
   constexpr int kRowLanes = kRowBytes / 16;   // lanes copying a row
   constexpr int kRowsAtOnce = 32 / kRowLanes;
   constexpr int kQ = D / 16;                  // k-steps of S
   constexpr int kChunk = D / 4, kPad = kChunk + 4;  // dims the warps join at once
-  static_assert(kEntries >= 3 && kEntries <= 6, "ring");
+  static_assert(kEntries * kEntry == kRing, "ring");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) TileInfo infos[kWarps][kSlots];
   __shared__ float wm[kWarps][kHeads], wl[kWarps][kHeads];
@@ -450,11 +450,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
     first_key = k_lo + kRows * warp + 8 * (lane & (kGroups - 1));
     table = p.cache.table + (int64_t)seq * p.cache.max_pages;
     next_page = page_of(0);
-#pragma unroll
-    for (int e = 0; e < kEntries - 1; ++e) {
-      if (e & 1) issue_v(e >> 1);
-      else issue_k(e >> 1);
-    }
+    issue_k(0);
+    issue_v(0);
   };
 
   // The piece's q, as it is: pairs of dims in the order in which a row's arrive
@@ -526,10 +523,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
 
     for (int i = 0; i < count; ++i) {
       // ---- S^T = K Q^T: rows quad and quad + 8 of each block, heads 2 pair, 2 pair + 1
-      copy_wait<kEntries - 2>();
+      copy_wait<1>();
       __syncwarp();
-      if (((kEntries - 1) & 1) == 0) issue_k(i + (kEntries - 1) / 2);
-      else issue_v(i + (kEntries - 1) / 2);
+      issue_k(i + 1);
       __syncwarp();
       float s[kM][4];
       {
@@ -658,10 +654,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
         pl[m][1] = transpose8x8(pack_bf16(lo_part(y, w[m][2]), hi_part(y, w[m][3])));
       }
       // ---- O^T += V^T P^T
-      copy_wait<kEntries - 2>();
+      copy_wait<1>();
       __syncwarp();
-      if ((kEntries & 1) == 0) issue_k(i + kEntries / 2);
-      else issue_v(i + kEntries / 2);
+      issue_v(i + 1);
       const uint32_t vt = ring + get * kEntry;
       if (++get == kEntries) get = 0;
       if (!kFp8) {
@@ -952,7 +947,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
 template <int D, bool kFp8>
 cudaError_t launch_paged(const PagedAttnArgs& args, cudaStream_t stream) {
   static PerDeviceOnce attrs;
-  const size_t smem = kWarps * ring_bytes(D, kFp8);
+  const size_t smem = kWarps * ring_bytes(D);
   cudaError_t e = attrs.run([&] {
     return cudaFuncSetAttribute(attn_paged_kernel<D, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem);
@@ -976,11 +971,11 @@ cudaError_t launch_paged(const PagedAttnArgs& args, cudaStream_t stream) {
   if ((int64_t)args.batch * args.h_q <= 64 && args.batch <= 32) {  // few rows, with many splits each
     cfg.gridDim = dim3((unsigned)(args.batch * args.h_q * 4));
     cfg.blockDim = dim3(512);
-    return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 512, 4>, args);
+    return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(kFp8), 512, 4>, args);
   }
   cfg.gridDim = dim3((unsigned)(args.ctas > 1 ? args.ctas - 1 : 1));
   cfg.blockDim = dim3(256);
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(D, kFp8), 256, 1>, args);
+  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(kFp8), 256, 1>, args);
 }
 
 }  // namespace
@@ -998,10 +993,10 @@ cudaError_t launch_attn_decode_paged(const PagedAttnArgs& a, cudaStream_t stream
   PagedAttnArgs args = a;
   // As many CTAs as are resident at once, but no more than units the table can reach.
   const bool fp8 = a.cache.dtype == kCacheE4M3;
-  const int unit = unit_rows(a.cache.head_dim, fp8);
+  const int unit = unit_rows(fp8);
   const int64_t reach = ((int64_t)a.cache.max_pages << a.cache.page_shift) + unit - 1;
   const int64_t units = (int64_t)a.batch * a.cache.h_kv * (reach / unit);
-  int64_t ctas = (int64_t)ctas_per_sm(a.cache.head_dim, fp8) * sms;
+  int64_t ctas = (int64_t)ctas_per_sm(a.cache.head_dim) * sms;
   if (ctas > kPagedMaxCtas) ctas = kPagedMaxCtas;
   if (ctas > units) ctas = units > 0 ? units : 1;
   args.ctas = (int32_t)ctas;
