@@ -807,7 +807,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_paged_kernel(co
 // show is all that there is to join, and they are its blocks.  (A block for every item
 // and head, most of them with nothing to join, took 110 of 187 us for 608 sequences
 // with 8 KV heads; now 9.)
-constexpr int kFew = 16;
+// Few splits, measured (bf16, 16 heads of 256 on 2): 16 sequences of 4,096 keys, 10 splits
+// an item, 29.9 us with a limit of 16, 27.6 with 8; one of 2,048 keys, 32 splits, 15.0 us
+// with a limit of 32, 7.9 with 8.
+constexpr int kFew = 8;
 template <int D, int kUnit, int kJoinThreads, int kSlices>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const PagedAttnArgs p) {
   constexpr int kRow = D / 4, kLanes = kRow / kSlices, kGroups = kJoinThreads / kLanes;
@@ -968,7 +971,11 @@ cudaError_t launch_paged(const PagedAttnArgs& args, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, attn_paged_kernel<D, kFp8>, args);
   if (e != cudaSuccess) return e;
   cfg.dynamicSmemBytes = 0;
-  if ((int64_t)args.batch * args.h_q <= 64 && args.batch <= 32) {  // few rows, with many splits each
+  // Few rows of o, with many splits each: by item.  Measured: 16 heads of 256 on 2, bf16, one
+  // sequence of 32,768 keys 13.5 us by item and 16.2 by boundary, four of 16,384 28.7 and
+  // 29.1; past 64 rows the other way, 32 heads of 128 on 8, e4m3, four of 16,384 keys 36.1
+  // and 31.3.
+  if ((int64_t)args.batch * args.h_q <= 64 && args.batch <= 32) {
     cfg.gridDim = dim3((unsigned)(args.batch * args.h_q * 4));
     cfg.blockDim = dim3(512);
     return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, unit_rows(kFp8), 512, 4>, args);
