@@ -123,14 +123,14 @@ struct Shared {  // beside the tiles
   uint64_t k_full[C::kSlots], v_full[C::kSlots], s_done[C::kSlots], o_done[C::kSlots], p_ready[C::kS];
   uint64_t q_full, q_empty, o_free;
   uint64_t m_ready[2][4];  // two groups: a key tile's references are in m, by quarters of the rows
-  // edge tiles, counted through (% kSlots): the CTA's V has landed; V is finite in both CTAs
+  // edge tiles, counted through (% kSlots): V has landed in both CTAs; is finite there
   uint64_t v_edge[C::kSlots], v_clean[C::kSlots];
   uint64_t sums_in[2];          // the rows' sums of two tiles are there, for the epilogue
   // What was found in V in the edge tiles of a tile (by number & 3: the schedule's two
   // tiles bound how far this runs ahead of the epilogue): the number + 1 where that was
-  // a non-finite value, by halves of the dimensions; that both CTAs have told of it.
+  // a non-finite value; that this has been told.
   uint64_t flags_in[4];
-  uint32_t poison[4][2];
+  uint32_t poison[4];
   uint64_t tile_full[2], tile_empty[2], drained;
   Tile tile[2];
   uint32_t tmem;
@@ -335,16 +335,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
       tc::mbar_init(&sh.sums_in[i], 8);
-      // readers: the softmax, epilogue, TMA and edge warps, and in the even CTA the products'
-      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : 2));
+      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products' and edge warps
+      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : 1));
     }
     for (int i = 0; i < 4; ++i) {
-      tc::mbar_init(&sh.flags_in[i], 2);
-      sh.poison[i][0] = sh.poison[i][1] = 0;
+      tc::mbar_init(&sh.flags_in[i], 1);
+      sh.poison[i] = 0;
     }
     for (int i = 0; i < C::kSlots; ++i) {
       tc::mbar_init(&sh.v_edge[i], 1);
-      tc::mbar_init(&sh.v_clean[i], 2);
+      tc::mbar_init(&sh.v_clean[i], 1);
     }
     tc::mbar_init(&sh.o_free, 2 * 4);
     tc::mbar_init(&sh.drained, 1);
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  tc2::wait(&sh.flags_in[used & 3], (used >> 2) & 1);
         const float total = sh.sums[used & 1][0][row] + sh.sums[used & 1][1][row];
         inv = total == 0.f ? 0.f : 1.f / total;
-        dirty = sh.poison[used & 3][0] == (uint32_t)used + 1 || sh.poison[used & 3][1] == (uint32_t)used + 1;
+        dirty = sh.poison[used & 3] == (uint32_t)used + 1;
         w = w && of_tile(sh.o_done, h);
         tc::fence_after_sync();
         if (!(ok = __all_sync(kFullMask, w) != 0)) break;
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kc = 0, vc = 0;   // key tiles whose K, V were asked for
       int ve = 0;           // edge tiles among the latter
       const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0);
-      const uint32_t my_v = tc2::in_cta(sh.v_edge, rank), r_q = tc2::in_cta(&sh.q_full, 0);
+      const uint32_t r_ve = tc2::in_cta(sh.v_edge, 0), r_q = tc2::in_cta(&sh.q_full, 0);
       if (lane == 0) {
         tc::prefetch_tmap(&tm_q);
         tc::prefetch_tmap(&tm_k);
@@ -701,17 +701,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= 0) {
               const int h = g + i, s = h % C::kSlots;
               if (h >= C::kSlots && !(ok = of_tile(sh.o_done, h - C::kSlots))) break;
-              // So do those of V, but in an edge tile they count on the CTA's own v_edge, for
-              // its edge warp (whose arrival on v_clean then stands for them); v_full keeps step.
+              // So do those of V, in an edge tile on a barrier of its own that the edge warp can
+              // count through; v_full keeps step.
               const bool edge = (i + 1) * kKeys > whole;
               const int e = ve % C::kSlots;
-              if (edge) tc::mbar_arrive_expect_tx(&sh.v_edge[e], C::kEntry);
-              if (edge || rank != 0) tc::mbar_arrive(&sh.v_full[s]);
-              else tc::mbar_arrive_expect_tx(&sh.v_full[s], 2 * C::kEntry);
+              if (rank == 0) {
+                tc::mbar_arrive_expect_tx(edge ? &sh.v_edge[e] : &sh.v_full[s], 2 * C::kEntry);
+                if (edge) tc::mbar_arrive(&sh.v_full[s]);
+              }
 #pragma unroll
               for (int kb = 0; kb < D / 128; ++kb)
                 tc2::tma_load_3d(smem + C::kV + s * C::kEntry + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, t.kvh,
-                                 t.k0 + i * kKeys, edge ? my_v + e * 8 : r_v + s * 8);
+                                 t.k0 + i * kKeys, edge ? r_ve + e * 8 : r_v + s * 8);
               vc = h + 1;
               ve += edge;
             }
@@ -723,12 +724,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       // Copies still in flight land before the CTA ends: after an expired wait, the
-      // even CTA's barriers tell of both CTAs' copies (v_edge of the CTA's own).
-      if (lane == 0) {
-        for (int h = max(0, kc - C::kSlots); rank == 0 && h < kc; ++h) ok = of_tile(sh.k_full, h) && ok;
+      // even CTA's barriers tell of both CTAs' copies.
+      if (lane == 0 && rank == 0) {
+        for (int h = max(0, kc - C::kSlots); h < kc; ++h) ok = of_tile(sh.k_full, h) && ok;
         for (int h = max(0, vc - C::kSlots); h < vc; ++h) ok = of_tile(sh.v_full, h) && ok;
         for (int e = max(0, ve - C::kSlots); e < ve; ++e) ok = of_tile(sh.v_edge, e) && ok;
-        if (rank == 0 && used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
+        if (used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
@@ -779,8 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int i = j - C::kLag;
           if (i >= 0) {  // O += P V of key tile i
             bool w = tc::mbar_wait(&sh.v_full[vs], v_ph);
-            if ((i + 1) * kKeys > whole) {  // V has landed in both CTAs, and may have been edited: acquire that
-              w = w && tc2::wait(&sh.v_clean[edges % C::kSlots], (edges / C::kSlots) & 1);
+            if ((i + 1) * kKeys > whole) {  // V may have been edited in both CTAs (ordinary writes): acquire those
+              w = w && of_tile(sh.v_edge, edges) && tc2::wait(&sh.v_clean[edges % C::kSlots], (edges / C::kSlots) & 1);
               ++edges;
             }
             w = w && tc::mbar_wait(&sh.p_ready[sr], sr_ph);
@@ -810,13 +811,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (!warp_wait(&sh.drained, 0)) ok = false;
       }
-    } else if (warp == kEdgeWarp) {
+    } else if (warp == kEdgeWarp && rank == 0) {
       // ------------------------------------------------------------ edge tiles
-      // This CTA's half of V: see the note at the top.
+      // V of both CTAs, whose bytes all count on this CTA's barriers: see the note at the top.
+      // (With a warp for each half, the odd CTA's has to hand over that V has landed there, with
+      // a release: 600 prompts of 64 tokens 193 us at D = 128, so 174, though 16 prompts of
+      // 1,024 tokens with 8 KV heads of 256 take 218 for 212.)
       Tile t;
       int g = 0, used = 0, edges = 0;
-      const uint32_t r_clean = tc2::in_cta(sh.v_clean, 0);
-      const uint32_t r_flags = tc2::in_cta(sh.flags_in, rank ^ 1), r_poison = tc2::in_cta(sh.poison, rank ^ 1);
+      const uint32_t r_flags = tc2::in_cta(sh.flags_in, 1), r_poison = tc2::in_cta(sh.poison, 1);
+      const uint32_t v_even = tc2::in_cta(smem + C::kV, 0) + lane * 16, v_odd = tc2::in_cta(smem + C::kV, 1) + lane * 16;
       for (int pass = 0; next_tile(pass, &t); ++pass) {
         if (t.tiles == 0) continue;
         bool told = false;  // a non-finite value that a row sees
@@ -824,51 +828,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int h = g + j, rows = t.sight - j * kKeys;  // rows of V that some query sees
           // the first that some does not (rounded down); those before need no care
           const int row0 = max(0, t.off + t.tok0 + 1 - j * kKeys) & ~15;
-          if (!(ok = __all_sync(kFullMask, of_tile(sh.v_edge, edges)))) break;
-          uint8_t* vt = smem + C::kV + (h % C::kSlots) * C::kEntry + lane * 16;
+          if (!(ok = __all_sync(kFullMask, tc2::wait(&sh.v_edge[edges % C::kSlots], (edges / C::kSlots) & 1)))) break;
+          const uint32_t slot = h % C::kSlots * C::kEntry;
           // the largest of the magnitudes, as 16-bit integers (a non-finite one is 0x7f80 or
           // more); in a short loop, as it runs once a tile of queries and not from a cache
           // (600 prompts of 64 tokens, D = 128: 188 us unrolled, 169 so)
           uint32_t most = 0;
 #pragma unroll 1
           for (int r = row0; r < min(rows, kKeys); r += 16) {
+            // eight loads in flight: both halves' rows at D = 128, a half's at 256
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              const uint4 y = *reinterpret_cast<const uint4*>(vt + (i >> 2) * 16384 + r * 128 + (i & 3) * 512);
-              most = __vimax3_u16x2(most, y.x & 0x7fff7fffu, y.y & 0x7fff7fffu);
-              most = __vimax3_u16x2(most, y.z & 0x7fff7fffu, y.w & 0x7fff7fffu);
+            for (int c = 0; c < D / 16; c += 8) {
+              uint4 y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int k = (c + i) % (D / 32);
+                const uint32_t at = slot + (k >> 2) * 16384 + r * 128 + (k & 3) * 512;
+                y[i] = c + i < D / 32 ? tc2::load_remote(v_odd + at)
+                                      : *reinterpret_cast<const uint4*>(smem + C::kV + at + lane * 16);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                most = __vimax3_u16x2(most, y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu);
+                most = __vimax3_u16x2(most, y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu);
+              }
             }
           }
           bool seen = false;
           const bool edited = __any_sync(kFullMask, (most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u);
           if (edited) {
 #pragma unroll 1
-            for (int i = 0; i < (int)C::kEntry / 512; ++i) {  // four rows at a time
-              if (4 * (i & 31) < row0) continue;
-              uint4* at = reinterpret_cast<uint4*>(vt + i * 512);
+            for (int i = 0; i < 2 * (int)C::kEntry / 512; ++i) {  // four rows at a time
+              const int k = i % ((int)C::kEntry / 512), r = 4 * (k & 31);
+              if (r < row0) continue;
+              const uint32_t at = (i == k ? v_even : v_odd) + slot + k * 512;
               auto finite = [](uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); };
-              const uint4 y = *at, z = make_uint4(finite(y.x), finite(y.y), finite(y.z), finite(y.w));
+              const uint4 y = tc2::load_remote(at), z = make_uint4(finite(y.x), finite(y.y), finite(y.z), finite(y.w));
               if (z.x != y.x || z.y != y.y || z.z != y.z || z.w != y.w) {
-                *at = z;
-                seen = seen || 4 * (i & 31) + (lane >> 3) < rows;
+                tc2::store_remote(at, z);
+                seen = seen || r + (lane >> 3) < rows;
               }
             }
           }
-          if (seen) {
-            sh.poison[used & 3][rank] = (uint32_t)used + 1;
-            tc2::store_remote(r_poison + ((used & 3) * 2 + rank) * 4, (uint32_t)used + 1);
-          }
-          told = told || edited;
-          if (edited) tc::fence_proxy_async();  // the edited V rows -> the tensor core
+          if (__any_sync(kFullMask, seen)) told = true;
+          if (edited) tc2::fence_proxy_async();  // the edited V rows -> the tensor cores of both CTAs
           __syncwarp();
-          // a release also without an edit: the even CTA's products read this CTA's V, whose
-          // landing only this warp has waited for (4,096 tokens 77.4 us relaxed, 78.4 so)
-          if (lane == 0) tc2::arrive_remote(r_clean + edges % C::kSlots * 8);
+          if (lane == 0) {
+            if (edited) tc2::arrive_remote(tc2::in_cta(&sh.v_clean[edges % C::kSlots], 0));
+            else tc::mbar_arrive(&sh.v_clean[edges % C::kSlots]);
+          }
           ++edges;
         }
         if (!ok) break;
-        __syncwarp();
         if (lane == 0) {
+          if (told) {
+            sh.poison[used & 3] = (uint32_t)used + 1;
+            tc2::store_remote(r_poison + (used & 3) * 4, (uint32_t)used + 1);
+          }
           tc::mbar_arrive(&sh.flags_in[used & 3]);
           if (told) tc2::arrive_remote(r_flags + (used & 3) * 8);
           else tc2::arrive_remote_relaxed(r_flags + (used & 3) * 8);
