@@ -64,9 +64,10 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kHeads = 8;  // query heads of a KV head, padded (N of the products)
 constexpr int kSlots = 2;  // tiles whose row counts and units are kept: one at work, one on its way
 
-// CTAs on an SM, as registers allow (O and Q of a warp: 12 KB at D = 256, 6 at 128),
-// bytes of a warp's ring, and rows of its tile.
-__host__ __device__ constexpr int ctas_per_sm(int D) { return D == 128 ? 4 : 2; }
+// CTAs on an SM, as registers allow (O and Q of a warp: 12 KB at D = 256, 6 at 128; with
+// e4m3 at 128 a fourth CTA leaves 128 registers, and 40 ragged sequences take 90 for 86 us,
+// though 608 of 396 keys 112 for 113), bytes of a warp's ring, and rows of its tile.
+__host__ __device__ constexpr int ctas_per_sm(int D, bool fp8) { return D == 128 ? (fp8 ? 3 : 4) : 2; }
 __host__ __device__ constexpr uint32_t ring_bytes(int D) { return D == 128 ? 12288 : 24576; }
 __host__ __device__ constexpr int tile_rows(bool fp8) { return fp8 ? 32 : 16; }
 // Rows of a unit of work: a tile for each warp.
@@ -315,7 +316,7 @@ __device__ __forceinline__ bool find_work(const PagedAttnArgs& p, int c, bool re
 }
 
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_paged_kernel(const PagedAttnArgs p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_kernel(const PagedAttnArgs p) {
   constexpr int kRowBytes = kFp8 ? D : 2 * D;
   constexpr uint32_t kRing = ring_bytes(D);
   constexpr int kRows = tile_rows(kFp8), kUnit = unit_rows(kFp8);
@@ -1003,7 +1004,7 @@ cudaError_t launch_attn_decode_paged(const PagedAttnArgs& a, cudaStream_t stream
   const int unit = unit_rows(fp8);
   const int64_t reach = ((int64_t)a.cache.max_pages << a.cache.page_shift) + unit - 1;
   const int64_t units = (int64_t)a.batch * a.cache.h_kv * (reach / unit);
-  int64_t ctas = (int64_t)ctas_per_sm(a.cache.head_dim) * sms;
+  int64_t ctas = (int64_t)ctas_per_sm(a.cache.head_dim, fp8) * sms;
   if (ctas > kPagedMaxCtas) ctas = kPagedMaxCtas;
   if (ctas > units) ctas = units > 0 ? units : 1;
   args.ctas = (int32_t)ctas;
