@@ -11,39 +11,46 @@
 // Bound by HBM: every cached row is read once (8 flops per value and head).
 // What the layout is for:
 //   * A CTA's share of the batch is a range of units of 64 rows (e4m3: 128) in
-//     (sequence, KV head, row) order, as much work for every CTA whatever the lengths are:
-//     ragged batches and single long sequences fill the GPU alike.  The shares
+//     (sequence, KV head, row) order, as much work for every CTA whatever the lengths
+//     are: ragged batches and single long sequences fill the GPU alike.  The shares
 //     follow from the device's lengths alone, so each CTA (and the joining pass)
 //     works them out for itself, and the workspace is two partial results a CTA.
 //   * A warp owns its tiles of 16 rows (e4m3: 32) end to end: a ring of its own in shared
-//     memory (24 KB at D = 256, 12 KB at D = 128, two or four CTAs an SM) filled by
-//     16-byte asynchronous copies, warp-level matrix products (m16n8k16: 16 rows x 8
-//     query heads), no CTA barrier before the end of a (sequence, KV head).  Rows are addressed one by one through the page table,
-//     so a page may be smaller than a tile or end anywhere inside it.
+//     memory (24 KB at D = 256 and two CTAs an SM, 12 KB at D = 128 and four, with e4m3
+//     three) filled by 16-byte asynchronous copies, warp-level matrix products (m16n8k16:
+//     16 rows x 8 query heads), no CTA barrier before the end of a (sequence, KV head).
+//     Rows are addressed by eights through the page table, so a page may be smaller than a
+//     tile or end anywhere inside it.
 //   * The products are S^T = K Q^T and O^T = V^T P^T, whose N = 8 is the number
 //     of query heads on a KV head, so no multiply is padding at eight heads; one
 //     8x8 register transpose turns S^T's layout into P^T's.
 // Rounding: the weights P go to the matrix unit as bf16 pairs hi + lo (16
 // significant bits; the second product is free next to the memory time).  Scores,
 // maxima, sums and O are fp32.
-// With an e4m3 cache a key's unit 2^ke scales its score (the codes widen exactly to
-// f16), and a value's code times its unit 2^ve is widened exactly to the bf16 that
-// reading the row back gives (above 2^7 the weight takes the rest of the unit), so
-// that both caches share one second product with fp32's range of exponents.  (Weights
-// in f16, units included, lost rows beside one with a far larger unit, a row of zeros
-// beside small values among them; they took 29.8 us for 131,072 keys, where these take
-// 31.3, and 86 for 90 us with 40 ragged sequences: the arithmetic pipe is the busiest.)
+// With an e4m3 cache a key's unit 2^ke scales its score; the codes widen exactly to f16,
+// and q is scaled into f16 by a power of two for each head: exact down to 2^-31 of the
+// head's largest, to within 2^-39 of it below, which moves no score that fp32 sums would
+// resolve unless the keys are zero where q is large.  A value's code times its unit 2^ve
+// is widened exactly to the bf16 that reading the row back gives (above 2^7 the weight
+// takes the rest of the unit), so that both caches share one second product with fp32's
+// range of exponents.  (Weights in f16, units included, lost rows beside one with a far larger unit, a row of zeros beside small
+// values among them.  They took 29.8 us for 131,072 keys, where these take 31.3, and 90
+// for 608 sequences of 396 keys, where these take 113: 350,000 instructions an SM then,
+// 475,000 now, with latency to match; long batches are as fast.)
 // (Products of e4m3 operands themselves, with q and P as sums of e4m3 parts,
 // measured slower: at warp level they run as f16 products after a widening.)
 //
-// Measured (calls back to back, both kernels): 64 sequences of 8,192 bf16 keys, 16
-// query heads of 256 on 2, 162 us = 6.6 TB/s, 98 % of a plain copy's rate; one
-// sequence of 131,072 e4m3 keys 31 us = 4.3 TB/s, one eight times as long 168 us =
-// 6.4; e4m3 with 8 KV heads of 128: 40 ragged sequences 90 us = 5.5, 304 of 792 keys
-// 84 us = 5.9, 608 of 396 keys 91 us = 5.6; one of 4,096 keys 9 us.  So rows stream at
-// 6.6 to 6.9 TB/s, and a call costs about 10 us beside that: lengths, table and first
-// rows one after the other (3 us), the last rows' weights, the warps' join, and the
-// joining pass (4 to 5 us).
+// Measured (calls back to back, both kernels).  bf16: 64 sequences of 8,192 keys, 16 query
+// heads of 256 on 2, 161 us = 6.7 TB/s, 98 % of a plain copy's rate; 48 heads of 128 on 8,
+// 40 ragged sequences 154 us = 6.4; 32 on 8, 64 of 4,096 keys 166 us = 6.5, one of 32,768
+// 30 us, one of 4,096 10 us (heads of 256 on 2: 9 us).  e4m3: 16 heads of 256 on 2, one
+// sequence of 131,072 keys 31 us = 4.3 TB/s, one eight times as long 170 us = 6.3; 48
+// heads of 128 on 8, 40 ragged sequences 86 us = 5.8, 20 of 12,040 keys 84 us = 5.9, 152
+// of 1,584 keys 91 us = 5.5, 304 of 792 keys 97 us = 5.1, 608 of 396 keys 113 us = 4.4.
+// So rows of long sequences stream at 6.5 to 6.9 TB/s, and a call costs about 10 us beside
+// that: lengths, table and first rows one after the other (3 us), the last rows' weights,
+// the warps' join, and the joining pass (4 to 5 us).  Short sequences of e4m3 rows also
+// show a piece's whole tiles: four warps with 13 tiles of 32 rows wait for the one with 4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -188,8 +195,8 @@ __device__ __forceinline__ int length_of(const PagedAttnArgs& p, int b) {
 // Work of one (sequence, KV head): its units, and kPieceCost units more for taking it up
 // (q and the first rows arrive, the warps join), so that a CTA with many short
 // sequences is not given more than it can do in the same time (40 ragged sequences on 8
-// KV heads of 128: 86 us with one unit, 89 with two, 87 with three; without any, a sixth
-// more when that was tried).
+// KV heads of 128: 86.0 us with one unit, 86.2 with two, 87.6 with three; without any, a
+// sixth more when that was tried).
 constexpr int kPieceCost = 1;
 template <int kUnit>
 __device__ __forceinline__ int64_t span_of(int len) {
@@ -489,8 +496,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
     float unit0 = score_unit, unit1 = score_unit;  // of heads 2 pair, 2 pair + 1
     float rest0 = 1.f, rest1 = 1.f;                // (e4m3: half of q's exponent apart)
     if (kFp8) {
-      // scaled by a power of two per head so that f16 holds what bf16 held (down to
-      // 2^-38 of the head's largest)
+      // scaled by a power of two per head so that f16 holds what bf16 held (see the top)
       float top = 0.f;
 #pragma unroll
       for (int kk = 0; kk < kQ; ++kk)
@@ -807,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, kFp8)) attn_paged_ker
 // every boundary between two CTAs' shares: what the boundaries that fall into an item
 // show is all that there is to join, and they are its blocks.  (A block for every item
 // and head, most of them with nothing to join, took 110 of 187 us for 608 sequences
-// with 8 KV heads; now 9.)
+// with 8 KV heads, when that was tried; these take 9.)
 // Few splits, measured (bf16, 16 heads of 256 on 2): 16 sequences of 4,096 keys, 10 splits
 // an item, 29.9 us with a limit of 16, 27.6 with 8; one of 2,048 keys, 32 splits, 15.0 us
 // with a limit of 32, 7.9 with 8.
@@ -820,7 +826,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
   __shared__ float red[2][kJoinThreads / 32];
   __shared__ float4 sum_sm[kGroups][kLanes];
   // (The next call's kernel is not let in early: with its CTAs taking their places
-  // between these blocks, 40 sequences with 8 KV heads took 105 for 89 us.)
+  // between these blocks, 40 sequences with 8 KV heads took 105 for 89 us, when tried.)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h_kv = p.cache.h_kv, G = p.h_q / h_kv;
   int64_t total = 0, u, base;

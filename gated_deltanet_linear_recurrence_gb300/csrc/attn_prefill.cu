@@ -25,12 +25,14 @@
 // pipe pauses 2,500 cycles (the last P, its product, O read out, the next product),
 // which is what short sequences pay.
 //
-// Measured (calls back to back; flops of the visible keys only): 16,384 tokens with
-// 16 query heads of 256 on 2 KV heads 1.14 ms, 1.93 PFLOP/s, as fast as a plain
-// library product and limited by the board's power; 4,096 tokens 77 us, 1.79; 2,048
-// new tokens on 16,000 keys 268 us, 1.87.  At D = 128, 8,192 tokens 155 us, 1.77;
-// seven prompts of 1 to 4,096 tokens with 32 query heads on 8, 176 us, 1.55; seven
-// of 1 to 200 tokens (D = 256) 10 us (launch and latency).
+// Measured, calls back to back for a second (in brackets runs of some milliseconds,
+// before the board's power limit sets in); flops of the visible keys only: 16,384 tokens
+// with 16 query heads of 256 on 2 KV heads 1.20 ms, 1.83 PFLOP/s (1.16, 1.90), the rate of
+// a plain library product; 4,096 tokens 87 us, 1.58 (78.5, 1.75); 2,048 new tokens on
+// 16,000 keys 291 us, 1.73 (280, 1.79).  At D = 128, seven prompts of 1 to 4,096 tokens
+// with 32 query heads on 8, 200 us, 1.37 (189, 1.45); 8,192 tokens with 16 on 2 (168,
+// 1.64); 600 prompts of 64 tokens with 32 on 8 (174 us).  Seven prompts of 1 to 200 tokens
+// (D = 256) 9.7 us (launch and latency).
 //
 // TMEM (512 columns): S of two or three key tiles (128 fp32 columns each, of whose
 // two halves P then takes 32 columns of bf16 pairs), O (D columns).  Shared memory:
@@ -40,7 +42,7 @@
 //
 // Roles (16 warps): 0-7 softmax, 8-11 epilogue (O to o while the next tile's scores
 // are under way), 12 TMA, 13 products (the even CTA's issues them for the pair), 14
-// the schedule, 15 V of edge tiles.  The pairs are persistent.
+// the schedule, 15 V of edge tiles (the even CTA's, of both).  The pairs are persistent.
 //
 // Rounding: P is rounded to bf16 for the second product (by at most 2^-8 of a weight,
 // as the output is; the sums l stay fp32 over unrounded weights).  Weights as bf16
@@ -95,11 +97,10 @@ struct Cfg {
   static constexpr int kS = D == 256 ? 2 : 3;
   static constexpr int kLag = kS - 1;  // key tiles that the scores are ahead of P V
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
-  // Registers of a thread of the four warpgroups: softmax (two), epilogue, and 64 for
-  // the rest; together the 65,536 that the CTA starts with (setmaxnreg takes them
-  // from   // from there).  At D = 128 a softmax thread's 128 scores want more than 168 (198
-  // against 222 us for seven packed prompts, when that was tried)
-  // against 222 us for seven packed prompts), and the epilogue reads fewer columns at once.
+  // Registers of a thread of the four warpgroups: softmax (two), epilogue, and 64 for the
+  // rest; together the 65,536 that the CTA starts with (setmaxnreg takes them from there).
+  // At D = 128 a softmax thread's 128 scores want more than 168 (198 against 222 us for
+  // seven packed prompts, when that was tried), and the epilogue reads fewer columns at once.
   static constexpr int kSoftmaxRegs = D == 256 ? 168 : 184, kEpilogueRegs = D == 256 ? 112 : 80;
   static constexpr int kOut = D == 256 ? 64 : 32;  // columns of O that the epilogue holds
   static_assert(2 * kSoftmaxRegs + kEpilogueRegs + 64 == 512, "registers");
@@ -310,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const AttnPrefillArgs p) {
   using C = Cfg<D>;
-  // the tiles fill shared memory but for the 2.5 KB of Shared: no room to align them here
+  // (the tiles' swizzle needs this alignment; there is no other shared memory, and the
+  // barriers and the rest, 4.5 KB, follow the tiles)
   extern __shared__ __align__(1024) uint8_t smem[];
   Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem + C::kShared);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -416,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float none = down ? INFINITY : -INFINITY;
         const uint32_t scores = tmem + lanes + sb * kKeys + C::kCols * half;
         // the upper 64 of 128 columns only if some row sees them, as the product with V
-        // takes no more (packed prompts 180 -> 177 us, 600 prompts of 64 tokens 221 -> 190)
+        // takes no more (packed prompts 180 -> 177 us, 600 prompts of 64 tokens 221 -> 190,
+        // when that was tried)
         const bool upper = C::kCols > 64 && t.sight - key0 > 64;
         const int cols = upper ? C::kCols : 64;
         if (key0 + kKeys > whole) {
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // loop before code that all tiles share: with the masks inside an unrolled copy
           // of that code, its instructions (run once a tile of queries, so never near)
           // took 4,500 cycles where a tile without an edge takes 1,800 (seven packed
-          // prompts 196 us, now 184; with this loop an edge tile takes 2,400).
+          // prompts 196 us, then 184; with this loop an edge tile takes 2,400).
           const int left = lim - key0 - C::kCols * half;  // columns of this thread that the row sees
           const int all = __reduce_min_sync(kFullMask, left);
 #pragma unroll 1
@@ -832,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t slot = h % C::kSlots * C::kEntry;
           // the largest of the magnitudes, as 16-bit integers (a non-finite one is 0x7f80 or
           // more); in a short loop, as it runs once a tile of queries and not from a cache
-          // (600 prompts of 64 tokens, D = 128: 188 us unrolled, 169 so)
+          // (600 prompts of 64 tokens, D = 128: 188 us unrolled, 169 so, when that was tried)
           uint32_t most = 0;
 #pragma unroll 1
           for (int r = row0; r < min(rows, kKeys); r += 16) {
@@ -955,10 +958,12 @@ cudaError_t launch(const AttnPrefillArgs& a, int sms, cudaStream_t stream) {
   int64_t pairs = (a.total_q / (2 * tok_cta) + a.num_seqs) * a.h_kv;  // at least as many as tiles
   AttnPrefillArgs args = a;
   // Sequence by sequence where no pair has two tiles (their order does not matter then;
-  // seven short prompts 10.9 -> 9.8 us), and where keys and values exceed half of L2, as
-  // they would be read from DRAM by tile after tile (16 prompts of 1,024 tokens, 32
-  // heads of 256 on 8: 190 -> 160 us; 8 of 4,096, heads of 128: 190 -> 176).  Below that
-  // even shares are worth more (seven prompts of 1 to 4,096 tokens, 46 MB: 181, not 192).
+  // seven short prompts 10.8 us by sight, 9.8 so), and where keys and values exceed half of
+  // L2, as they would be read from DRAM by tile after tile (16 prompts of 1,024 tokens, 32
+  // heads of 256 on 8: 242 us by sight, 224 so; 16 pieces of 576 tokens on 1,024 keys 192
+  // and 167; 8 on 4,096 keys, heads of 128, 210 and 181; 28 ragged prompts 858 and 740).
+  // Below that even shares are worth more (seven prompts of 1 to 4,096 tokens, 46 MB: 176
+  // by sight, 187 by sequence).
   args.by_sequence = pairs <= sms / 2 || a.total_k * a.h_kv * D * 4 > (int64_t)64 << 20;
   if (pairs > sms / 2) pairs = sms / 2;
   cudaLaunchAttribute attr[2];

@@ -16,10 +16,10 @@
 // row (8 values), so a row is 32 lanes at D = 256 and 16 at D = 128.
 //
 // Measured, append and gather together, calls back to back: 48,262 rows of 8 e4m3
-// heads of 128 in ragged batches 95 us for 595 MB = 6.2 TB/s, 92 % of a plain copy's
+// heads of 128 in ragged batches 96 us for 595 MB = 6.2 TB/s, 91 % of a plain copy's
 // rate (the append also issues in three quarters of its cycles: 13 instructions a
-// value for maximum, scaling and rounding); 4,096 rows of 2 bf16 heads of 256 10 us
-// and one row of each of 256 sequences 9 us, which is two launches.
+// value for maximum, scaling and rounding); 4,096 rows of 2 bf16 heads of 256 9 to 10 us
+// (8.6 in a graph) and one row of each of 256 sequences 9 us (5.5), which is two launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -445,7 +445,8 @@ int32_t gdn_attn_decode_block_keys(int32_t batch, int32_t h_q, int32_t h_kv, int
  * c x 2^(byte - 127).  gdn_kv_append picks the smallest power of two that brings
  * the row's largest finite magnitude to 448 or less (never below 2^-126; 1 for a
  * row of zeros) and rounds each quotient, which is exact, to the nearest e4m3
- * (ties to even); a value that is not finite is stored as NaN.  With
+ * (ties to even); a value that is not finite is stored as NaN.  It writes bytes 1
+ * to 247; 0 and 255 stand for no unit and must not reach a row that is read.  With
  * GDN_CACHE_BF16 rows are copied and k_exp, v_exp are not used (may be NULL).
  */
 typedef enum { GDN_CACHE_BF16 = 1, GDN_CACHE_E4M3 = 2 } gdn_cache_dtype;
@@ -459,9 +460,10 @@ typedef enum { GDN_CACHE_BF16 = 1, GDN_CACHE_E4M3 = 2 } gdn_cache_dtype;
  * of 8, at least h_kv x head_dim: a slice of a fused projection needs no copy).
  * Sequences must not share the pages that a call writes.  cu_seqlens
  * [num_seqs + 1], start_pos [num_seqs] int32 on the device.  Tensors 16-byte
- * aligned (int32 arrays 4-byte, exponent bytes 8-byte).  The rows of a token that
- * cu_seqlens gives to no sequence are not written (GDN_ERR_BAD_CU_SEQLENS in the
- * error word).
+ * aligned (int32 arrays 4-byte, exponent bytes 8-byte); page_table may be NULL only
+ * where max_pages is 0.  Offsets that break the conditions set
+ * GDN_ERR_BAD_CU_SEQLENS in the error word, wherever they are; the rows of a token
+ * that no sequence's range holds are not written.
  */
 gdn_status gdn_kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                          void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
@@ -492,8 +494,12 @@ gdn_status gdn_kv_gather(void* k, void* v, int64_t k_stride, int64_t v_stride,
  * (o = 0).  q [batch][h_q][head_dim] bf16 with q_stride elements between
  * sequences (a multiple of 8), o dense; cache_len [batch] int32 on the device,
  * 0 <= cache_len[b] <= max_pages x page_size (a value outside sets
- * GDN_ERR_BAD_CACHE_LEN and gives o = 0).  Slots at or past cache_len[b] are
- * never read.  The rows of the whole batch are dealt evenly to the CTAs whatever
+ * GDN_ERR_BAD_CACHE_LEN and gives o = 0).  Rows at or past cache_len[b] are never
+ * read, and what their exponent bytes hold (read eight at a time) has no effect.
+ * Over e4m3 rows the result is that of the rows read back as bf16, within the
+ * rounding of the weights (bf16 pairs, 2^-16) and of q values below 2^-31 of
+ * their head's largest (by at most 2^-39 of that).  A visible value that is not finite makes its dimension of o
+ * NaN or infinite.  The rows of the whole batch are dealt evenly to the CTAs whatever
  * the lengths; sequences that several CTAs share are joined through `workspace`
  * (at least gdn_attn_decode_paged_workspace_size(...) bytes, 16-byte aligned, any
  * contents; else GDN_ERR_NULL_POINTER or GDN_ERR_WORKSPACE_TOO_SMALL) in a fixed
