@@ -18,7 +18,7 @@ __all__ = ["gdn_prefill", "gdn_prefill_streamed", "gdn_prefill_streamed_workspac
            "gdn_output_rmsnorm", "gdn_decode_multi", "gdn_attn_decode",
            "gdn_attn_decode_workspace_size", "gdn_attn_decode_block_keys",
            "gdn_attn_prefill", "gdn_kv_append", "gdn_kv_gather", "gdn_attn_decode_paged",
-           "gdn_attn_decode_paged_workspace_size",
+           "gdn_attn_decode_paged_workspace_size", "gdn_qk_norm_rope", "gdn_kv_append_rope",
            "gdn_prefill_workspace_size",
            "gdn_stream_status", "gdn_status_string", "gdn_prefill_crossover_tokens",
            "gdn_prefill_form", "gdn_selftest_wait_timeout", "GdnError",
@@ -405,6 +405,32 @@ def gdn_kv_gather(k_pages, v_pages, page_table, cu_seqlens, start_pos, total_tok
     in all.  Returns (k, v) [total_tokens, h_kv, D]; arguments as for gdn_kv_append."""
     return _lib.binding().kv_gather(k_pages, v_pages, page_table, cu_seqlens, start_pos, total_tokens,
                                     k_exp, v_exp, k, v, stream)
+
+
+def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, norm_eps=None,
+                     axes=None, interleaved=False, q_out=None, k_out=None, stream=None):
+    """RMS norms of the heads of q and k and their rotation by position (gdn_qk_norm_rope in
+    include/gdn.h): q [T, h_q, D], k [T, h_kv, D] bf16, D 128 or 256; positions [T] int32;
+    inv_freq [rotary_dim / 2] fp32: the first rotary_dim values of a head turn in pairs
+    (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with ``interleaved``.  ``norm_eps``: normalise
+    first, with weights [D] fp32 (ones when None); no norm when None.  ``axes``: with
+    positions [A, T], the axis that each frequency goes by (bytes, or a list of
+    rotary_dim / 2 numbers below A).  q, k and the outputs may be slices of a fused
+    projection, an output also its input itself.  Returns (q_out, k_out)."""
+    return _lib.binding().qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, norm_eps, axes,
+                                       interleaved, q_out, k_out, stream)
+
+
+def gdn_kv_append_rope(q, k, v, k_pages, v_pages, page_table, cu_seqlens, start_pos, inv_freq,
+                       positions=None, q_weight=None, k_weight=None, norm_eps=None, axes=None,
+                       interleaved=False, k_exp=None, v_exp=None, q_out=None, stream=None):
+    """gdn_qk_norm_rope and gdn_kv_append in one launch (gdn_kv_append_rope in include/gdn.h):
+    the normalised and rotated k and v as it is go to the cache, the normalised and rotated q
+    is returned (None for q None).  ``positions`` default to those in the cache, start_pos[n]
+    + place; other arguments as for the two calls."""
+    return _lib.binding().kv_append_rope(q, k, v, k_pages, v_pages, page_table, cu_seqlens,
+                                         start_pos, positions, inv_freq, q_weight, k_weight,
+                                         norm_eps, axes, interleaved, k_exp, v_exp, q_out, stream)
 
 
 def gdn_attn_decode_paged_workspace_size(h_q, h_kv, head_dim):

@@ -22,6 +22,7 @@ STATUS_NAMES = {
 GDN_F32, GDN_BF16 = 0, 1
 GDN_CACHE_BF16, GDN_CACHE_E4M3 = 1, 2
 GDN_OPT_QK_L2NORM = 1
+GDN_ROPE_RMSNORM, GDN_ROPE_INTERLEAVED = 1, 2
 ALGOS = {"auto": 0, "scan": 1, "chunked": 2, "chunked_fused": 3, "chunked_split": 4,
          "chunked_coop": 5}
 ATTN_LAYOUTS = {"auto": 0, "general": 1, "fixed_block": 2}
@@ -76,6 +77,13 @@ SIGNATURES = {
     "gdn_attn_decode_paged_workspace_size": (_sz, [_i32, _i32, _i32]),
     "gdn_attn_prefill": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i32,
                                         _i32, _i32, _i64, _i64, _i64, ctypes.c_int, _f32, _vp]),
+    "gdn_qk_norm_rope": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i32, _vp,
+                                        _vp, _i32, _vp, _vp, _f32, _i64, _i32, _i32, _i32,
+                                        ctypes.c_int, ctypes.c_uint32, _vp]),
+    "gdn_kv_append_rope": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
+                                          _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
+                                          _f32, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                                          ctypes.c_int, ctypes.c_uint32, _vp]),
     "gdn_stream_status": (ctypes.c_int, [_vp]),
     "gdn_selftest_wait_timeout": (ctypes.c_int, [_i32, _vp]),
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -130,7 +138,8 @@ def binding():
         loader.exec_module(mod)
         mod.init(check, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
                           ("gdn_kv_append", "gdn_kv_gather", "gdn_attn_decode_paged",
-                           "gdn_attn_decode_paged_workspace_size", "gdn_attn_prefill")))
+                           "gdn_attn_decode_paged_workspace_size", "gdn_attn_prefill",
+                           "gdn_qk_norm_rope", "gdn_kv_append_rope")))
         _BINDING = mod
     return _BINDING
 

@@ -1,5 +1,5 @@
-// attn_api.cu — the C ABI of the paged cache and of prompt attention: argument
-// validation and launches.  Declarations and contracts: include/gdn.h.
+// attn_api.cu — the C ABI of the attention layers' operators (norms and rotation, the
+// paged cache, attention of prompts and over the cache): argument validation and launches.  Declarations and contracts: include/gdn.h.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -105,9 +105,129 @@ gdn_status rows_call(const void* k, const void* v, int64_t k_stride, int64_t v_s
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// Heads, rotation and norm of the two calls below; what they share goes into a.
+gdn_status check_rope(gdn::RopeArgs& a, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t rotary_dim,
+                      const int32_t* positions, int32_t num_axes, const uint8_t* axis_of, const float* inv_freq,
+                      const float* q_weight, const float* k_weight, float norm_eps, uint32_t options) {
+  if (head_dim <= 0 || rotary_dim <= 0 || num_axes < 1) return GDN_ERR_INVALID_ARG;
+  if (options & ~(uint32_t)(GDN_ROPE_RMSNORM | GDN_ROPE_INTERLEAVED)) return GDN_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || h_q > 65535 || h_kv > 65535 || num_axes > 4) return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (rotary_dim > head_dim || rotary_dim % 8 != 0) return GDN_ERR_UNSUPPORTED_SHAPE;
+  a.norm = (options & GDN_ROPE_RMSNORM) != 0;
+  if (a.norm ? !(norm_eps >= 0.f) : q_weight != nullptr || k_weight != nullptr) return GDN_ERR_INVALID_ARG;
+  if (num_axes > 1 && (!axis_of || !positions)) return GDN_ERR_NULL_POINTER;
+  for (int i = 0; num_axes > 1 && i < rotary_dim / 2; ++i) {
+    if (axis_of[i] >= num_axes) return GDN_ERR_INVALID_ARG;
+    a.axis_of[i] = axis_of[i];
+  }
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.head_dim = head_dim;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.rotary = rotary_dim;
+  a.axes = num_axes;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = norm_eps;
+  a.pairs = (options & GDN_ROPE_INTERLEAVED) != 0;
+  return GDN_OK;
+}
+
+gdn_status check_rope_pointers(const gdn::RopeArgs& a) {
+  if (!a.inv_freq) return GDN_ERR_NULL_POINTER;
+  if (!aligned(a.q, 16) || !aligned(a.q_out, 16) || !aligned(a.q_weight, 16) || !aligned(a.k_weight, 16) ||
+      !aligned(a.positions, 4) || !aligned(a.inv_freq, 4))
+    return GDN_ERR_MISALIGNED;
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+gdn_status gdn_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, void* q_out,
+                            void* k_out, int64_t q_out_stride, int64_t k_out_stride, const int32_t* positions,
+                            int32_t num_axes, const uint8_t* axis_of, const float* inv_freq, int32_t rotary_dim,
+                            const float* q_weight, const float* k_weight, float norm_eps, int64_t total_tokens,
+                            int32_t h_q, int32_t h_kv, int32_t head_dim, gdn_dtype dtype, uint32_t options,
+                            gdn_stream_t stream) {
+  if (total_tokens < 0 || h_q <= 0 || h_kv <= 0) return GDN_ERR_INVALID_ARG;
+  gdn::RopeArgs a{};
+  gdn_status st = check_rope(a, h_q, h_kv, head_dim, rotary_dim, positions, num_axes, axis_of, inv_freq, q_weight,
+                             k_weight, norm_eps, options);
+  if (st == GDN_OK) st = check_stride(q_stride, (int64_t)h_q * head_dim);
+  if (st == GDN_OK) st = check_stride(k_stride, (int64_t)h_kv * head_dim);
+  if (st == GDN_OK) st = check_stride(q_out_stride, (int64_t)h_q * head_dim);
+  if (st == GDN_OK) st = check_stride(k_out_stride, (int64_t)h_kv * head_dim);
+  if (st != GDN_OK) return st;
+  if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED_DTYPE;
+  if (total_tokens > INT32_MAX) return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (total_tokens == 0) return GDN_OK;
+  if (!q || !k || !q_out || !k_out || !positions) return GDN_ERR_NULL_POINTER;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.q_out = q_out;
+  a.q_out_stride = q_out_stride;
+  a.k_out = k_out;
+  a.k_out_stride = k_out_stride;
+  a.rows.k = const_cast<void*>(k);
+  a.rows.k_stride = k_stride;
+  a.rows.total_tokens = total_tokens;
+  st = check_rope_pointers(a);
+  if (st != GDN_OK) return st;
+  if (!aligned(k, 16) || !aligned(k_out, 16)) return GDN_ERR_MISALIGNED;
+  return gdn::launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_kv_append_rope(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, void* q_out, int64_t q_out_stride, void* k_pages, void* v_pages,
+                              uint8_t* k_exp, uint8_t* v_exp, const int32_t* page_table, const int32_t* cu_seqlens,
+                              const int32_t* start_pos, const int32_t* positions, int32_t num_axes,
+                              const uint8_t* axis_of, const float* inv_freq, int32_t rotary_dim,
+                              const float* q_weight, const float* k_weight, float norm_eps, int32_t num_seqs,
+                              int64_t total_tokens, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t page_size,
+                              int32_t num_pages, int32_t max_pages, gdn_cache_dtype cache_dtype, uint32_t options,
+                              gdn_stream_t stream) {
+  if (total_tokens < 0 || h_q < 0) return GDN_ERR_INVALID_ARG;
+  gdn_status st = check_cache(num_seqs, h_kv, head_dim, page_size, num_pages, max_pages, cache_dtype);
+  if (st != GDN_OK) return st;
+  gdn::RopeArgs a{};
+  st = check_rope(a, h_q, h_kv, head_dim, rotary_dim, positions, num_axes, axis_of, inv_freq, q_weight, k_weight,
+                  norm_eps, options);
+  if (st == GDN_OK && h_q > 0) st = check_stride(q_stride, (int64_t)h_q * head_dim);
+  if (st == GDN_OK && h_q > 0) st = check_stride(q_out_stride, (int64_t)h_q * head_dim);
+  if (st == GDN_OK) st = check_stride(k_stride, (int64_t)h_kv * head_dim);
+  if (st == GDN_OK) st = check_stride(v_stride, (int64_t)h_kv * head_dim);
+  if (st != GDN_OK) return st;
+  if (total_tokens > INT32_MAX) return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (num_seqs == 0) return total_tokens == 0 ? GDN_OK : GDN_ERR_INVALID_ARG;
+  if (!cu_seqlens || !start_pos) return GDN_ERR_NULL_POINTER;
+  if (total_tokens == 0) return GDN_OK;
+  if (!k || !v || (h_q > 0 && (!q || !q_out))) return GDN_ERR_NULL_POINTER;
+  a.q = h_q > 0 ? q : nullptr;
+  a.q_stride = q_stride;
+  a.q_out = h_q > 0 ? q_out : nullptr;
+  a.q_out_stride = q_out_stride;
+  a.rows.k = const_cast<void*>(k);
+  a.rows.v = const_cast<void*>(v);
+  a.rows.k_stride = k_stride;
+  a.rows.v_stride = v_stride;
+  a.rows.cache = make_cache(k_pages, v_pages, k_exp, v_exp, page_table, h_kv, head_dim, page_size, num_pages,
+                            max_pages, cache_dtype);
+  a.rows.cu_seqlens = cu_seqlens;
+  a.rows.start = start_pos;
+  a.rows.num_seqs = num_seqs;
+  a.rows.total_tokens = total_tokens;
+  st = check_pages(a.rows.cache);
+  if (st == GDN_OK) st = check_rope_pointers(a);
+  if (st != GDN_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_seqlens, 4) || !aligned(start_pos, 4))
+    return GDN_ERR_MISALIGNED;
+  if (!gdn::device_error_word(&a.rows.err)) return GDN_ERR_CUDA;
+  return gdn::launch_kv_append_rope(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK
+                                                                                             : GDN_ERR_CUDA;
+}
 
 gdn_status gdn_kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                          void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,

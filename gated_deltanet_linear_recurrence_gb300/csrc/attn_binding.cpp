@@ -26,6 +26,8 @@ decltype(&gdn_kv_gather) p_gather;
 decltype(&gdn_attn_decode_paged) p_decode;
 decltype(&gdn_attn_decode_paged_workspace_size) p_decode_ws;
 decltype(&gdn_attn_prefill) p_prefill;
+decltype(&gdn_qk_norm_rope) p_rope;
+decltype(&gdn_kv_append_rope) p_append_rope;
 PyObject* g_check;  // check(status, name): raises GdnError
 
 struct Refused {  // a Python exception to raise
@@ -323,6 +325,138 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+struct Rotation {  // how heads are normalised and turned, and the positions
+  const at::Tensor* tensors[4];  // those given, for one_device
+  int given = 0;
+  const int32_t* positions = nullptr;
+  const float *freq, *qw = nullptr, *kw = nullptr;
+  int64_t axes = 1, rotary;
+  float eps = 0.f;
+  uint32_t options = 0;
+  std::string axis_of;  // a byte for each frequency
+  Rotation(PyObject* pos, PyObject* inv_freq, PyObject* q_weight, PyObject* k_weight, PyObject* norm_eps,
+           PyObject* axes_, PyObject* interleaved, int64_t T, int64_t D) {
+    auto floats = [&](PyObject* o, int64_t n, const char* name) {
+      const at::Tensor& t = tensor(o, name);
+      if (!(t.scalar_type() == at::kFloat && t.is_cuda() && t.dim() == 1 && (n < 0 || t.numel() == n) && t.is_contiguous()))
+        value_error(std::string(name) + " must be [" + (n < 0 ? "rotary_dim / 2" : std::to_string(n)) +
+                    "] float32 on the GPU, contiguous");
+      tensors[given++] = &t;
+      return static_cast<const float*>(t.data_ptr());
+    };
+    freq = floats(inv_freq, -1, "inv_freq");
+    rotary = 2 * tensors[0]->numel();
+    if (axes_ != Py_None) {
+      PyObject* bytes = PyBytes_FromObject(axes_);
+      if (!bytes) throw python_error();
+      axis_of.assign(PyBytes_AS_STRING(bytes), static_cast<size_t>(PyBytes_GET_SIZE(bytes)));
+      Py_DECREF(bytes);
+      if (static_cast<int64_t>(axis_of.size()) != rotary / 2)
+        value_error("axes must have an entry for each of the " + std::to_string(rotary / 2) + " frequencies");
+    }
+    if (pos != Py_None) {
+      const at::Tensor& t = tensor(pos, "positions");
+      if (axes_ != Py_None && t.dim() == 2) axes = t.size(0);
+      const bool shape = axes_ == Py_None ? has_shape(t, {T}) : has_shape(t, {axes, T});
+      if (!(t.scalar_type() == at::kInt && t.is_cuda() && shape && t.is_contiguous()))
+        value_error(std::string("positions must be ") + (axes_ == Py_None ? list({T}) : "[axes, " + std::to_string(T) + "]") +
+                    " int32 on the GPU, contiguous");
+      for (const char c : axis_of)
+        if (static_cast<uint8_t>(c) >= axes) value_error("axes must be below " + std::to_string(axes) + ", the axes of positions");
+      tensors[given++] = &t;
+      positions = static_cast<const int32_t*>(t.data_ptr());
+    } else if (axes_ != Py_None) {
+      value_error("axes need positions");
+    }
+    if (norm_eps != Py_None) {
+      eps = static_cast<float>(PyFloat_AsDouble(norm_eps));
+      if (PyErr_Occurred()) throw python_error();
+      options |= GDN_ROPE_RMSNORM;
+      if (q_weight != Py_None) qw = floats(q_weight, D, "q_weight");
+      if (k_weight != Py_None) kw = floats(k_weight, D, "k_weight");
+    } else if (q_weight != Py_None || k_weight != Py_None) {
+      value_error("q_weight / k_weight need norm_eps");
+    }
+    const int yes = PyObject_IsTrue(interleaved);
+    if (yes < 0) throw python_error();
+    if (yes) options |= GDN_ROPE_INTERLEAVED;
+  }
+  const uint8_t* of() const { return axis_of.empty() ? nullptr : reinterpret_cast<const uint8_t*>(axis_of.data()); }
+  void on(c10::Device d) const {
+    for (int i = 0; i < given; ++i)
+      if (tensors[i]->device() != d) value_error("tensors must be on one device, got " + d.str() + " and " + tensors[i]->device().str());
+  }
+};
+
+// qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, norm_eps, axes, interleaved, q_out, k_out, stream)
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const at::Tensor &q0 = tensor(a[0], "q"), &k0 = tensor(a[1], "k");
+    dim(q0, 3, "q", "[T, h_q, D]");
+    dim(k0, 3, "k", "[T, h_kv, D]");
+    const int64_t T = q0.size(0), h_q = q0.size(1), D = q0.size(2), h_kv = k0.size(1);
+    const at::Tensor &q = rows(a[0], {T, h_q, D}, "q"), &k = rows(a[1], {T, h_kv, D}, "k");
+    if (a[2] == Py_None) value_error("positions must be given");
+    const Rotation r(a[2], a[3], a[4], a[5], a[6], a[7], a[8], T, D);
+    const c10::Device device = one_device({&q, &k});
+    r.on(device);
+    const Launch s(device, a[11]);
+    auto out = [&](PyObject* o, int64_t h, const char* name) {
+      return o == Py_None ? s.output({T, h, D}, q.options()) : s.given(rows(o, {T, h, D}, name));
+    };
+    const at::Tensor qo = out(a[9], h_q, "q_out"), ko = out(a[10], h_kv, "k_out");
+    one_device({&q, &qo, &ko});
+    check(p_rope(q.data_ptr(), k.data_ptr(), token_stride(q, "q"), token_stride(k, "k"), qo.data_ptr(), ko.data_ptr(),
+                 token_stride(qo, "q_out"), token_stride(ko, "k_out"), r.positions, as32(r.axes), r.of(), r.freq,
+                 as32(r.rotary), r.qw, r.kw, r.eps, T, as32(h_q), as32(h_kv), as32(D), GDN_BF16, r.options, s.abi()),
+          "gdn_qk_norm_rope");
+    PyObject *pq = THPVariable_Wrap(qo), *pk = THPVariable_Wrap(ko);
+    return pq && pk ? Py_BuildValue("(NN)", pq, pk) : nullptr;
+  });
+}
+
+// kv_append_rope(q, k, v, k_pages, v_pages, page_table, cu_seqlens, start_pos, positions, inv_freq, q_weight,
+//                k_weight, norm_eps, axes, interleaved, k_exp, v_exp, q_out, stream)
+PyObject* kv_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 19, [&]() -> PyObject* {
+    const Cache c(a[3], a[4], a[5], a[15], a[16]);
+    const at::Tensor& k0 = tensor(a[1], "k");
+    dim(k0, 3, "k", "[T, h_kv, D]");
+    const int64_t T = k0.size(0);
+    const at::Tensor &k = rows(a[1], {T, c.h_kv, c.D}, "k"), &v = rows(a[2], {T, c.h_kv, c.D}, "v");
+    const at::Tensor &cu = ints(a[6], {c.N + 1}, "cu_seqlens"), &st = ints(a[7], {c.N}, "start_pos");
+    int64_t h_q = 0, q_stride = 0, o_stride = 0;
+    if (a[0] != Py_None) {
+      dim(tensor(a[0], "q"), 3, "q", "[T, h_q, D]");
+      h_q = tensor(a[0], "q").size(1);
+      const at::Tensor& q = rows(a[0], {T, h_q, c.D}, "q");
+      c.with({&q});
+      q_stride = token_stride(q, "q");
+    } else if (a[17] != Py_None) {
+      value_error("q_out needs q");
+    }
+    const Rotation r(a[8], a[9], a[10], a[11], a[12], a[13], a[14], T, c.D);
+    c.with({&k, &v, &cu, &st});
+    r.on(c.device);
+    const Launch s(c.device, a[18]);
+    at::Tensor qo;
+    if (h_q > 0) {
+      qo = a[17] == Py_None ? s.output({T, h_q, c.D}, c.options) : s.given(rows(a[17], {T, h_q, c.D}, "q_out"));
+      c.with({&qo});
+      o_stride = token_stride(qo, "q_out");
+    }
+    check(p_append_rope(h_q > 0 ? tensor(a[0], "q").data_ptr() : nullptr, k.data_ptr(), v.data_ptr(), q_stride,
+                        token_stride(k, "k"), token_stride(v, "v"), h_q > 0 ? qo.data_ptr() : nullptr, o_stride,
+                        const_cast<void*>(c.k), const_cast<void*>(c.v), const_cast<uint8_t*>(c.ke),
+                        const_cast<uint8_t*>(c.ve), c.table, i32_of(cu), i32_of(st), r.positions, as32(r.axes), r.of(),
+                        r.freq, as32(r.rotary), r.qw, r.kw, r.eps, as32(c.N), T, as32(h_q), as32(c.h_kv), as32(c.D),
+                        as32(c.page), as32(c.P), as32(c.max_pages), c.dtype, r.options, s.abi()),
+          "gdn_kv_append_rope");
+    if (h_q == 0) Py_RETURN_NONE;
+    return THPVariable_Wrap(qo);
+  });
+}
+
 // token_stride(t): what the calls take for the distance of t's tokens
 PyObject* token_stride_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 1, [&]() -> PyObject* {
@@ -339,11 +473,12 @@ PyObject* one_device_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// init(check, addresses of the five functions)
+// init(check, addresses of the functions)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 6, [&]() -> PyObject* {
-    void* p[5];
-    for (int i = 0; i < 5; ++i) {
+  constexpr int kFunctions = 7;
+  return guarded(n, 1 + kFunctions, [&]() -> PyObject* {
+    void* p[kFunctions];
+    for (int i = 0; i < kFunctions; ++i) {
       p[i] = PyLong_AsVoidPtr(a[i + 1]);
       if (PyErr_Occurred()) throw python_error();
     }
@@ -352,6 +487,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p_decode = reinterpret_cast<decltype(p_decode)>(p[2]);
     p_decode_ws = reinterpret_cast<decltype(p_decode_ws)>(p[3]);
     p_prefill = reinterpret_cast<decltype(p_prefill)>(p[4]);
+    p_rope = reinterpret_cast<decltype(p_rope)>(p[5]);
+    p_append_rope = reinterpret_cast<decltype(p_append_rope)>(p[6]);
     Py_INCREF(a[0]);
     Py_XDECREF(g_check);
     g_check = a[0];
@@ -365,6 +502,8 @@ PyMethodDef methods[] = {FAST("init", init),
                          FAST("kv_gather", kv_gather),
                          FAST("attn_decode_paged", attn_decode_paged),
                          FAST("attn_prefill", attn_prefill),
+                         FAST("qk_norm_rope", qk_norm_rope),
+                         FAST("kv_append_rope", kv_append_rope),
                          FAST("token_stride", token_stride_py),
                          FAST("one_device", one_device_py),
                          {nullptr, nullptr, 0, nullptr}};

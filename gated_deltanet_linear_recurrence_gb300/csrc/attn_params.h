@@ -41,6 +41,29 @@ struct KvRowsArgs {
   int* err;
 };
 
+// Norms and rotation of the heads of q and k: dense outputs, or k with v into the cache
+// (rows.k, rows.v and their strides are the inputs there).
+constexpr int kMaxRotated = 256;  // rotary_dim
+struct RopeArgs {
+  const void* q;  // [T][h_q][D] bf16; strides in elements between tokens
+  int64_t q_stride;
+  void* q_out;
+  int64_t q_out_stride;
+  void* k_out;  // dense outputs only
+  int64_t k_out_stride;
+  int32_t h_q, h_kv, head_dim;
+  const int32_t* positions;  // [axes][T]; nullptr: the positions in the cache
+  const float* inv_freq;     // [rotary / 2]
+  int32_t rotary, axes;
+  const float* q_weight;  // [D] or nullptr (ones)
+  const float* k_weight;
+  float eps;
+  bool norm, pairs;
+  int32_t groups;  // of a token's rows, taken by a warp: chosen at the launch
+  KvRowsArgs rows;
+  uint8_t axis_of[kMaxRotated / 2];  // axis of each frequency's positions
+};
+
 // One query of each sequence over its cache_len[b] cached rows.
 struct PagedAttnArgs {
   const void* q;  // [B][h_q][D] bf16, q_stride elements between sequences
@@ -78,6 +101,8 @@ constexpr int32_t kPagedMaxCtas = 640;  // bounds the workspace of the paged dec
 size_t paged_attn_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t head_dim);
 cudaError_t launch_kv_append(const KvRowsArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_gather(const KvRowsArgs& a, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_append_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_decode_paged(const PagedAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const AttnPrefillArgs& a, cudaStream_t stream);
 

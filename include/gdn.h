@@ -488,6 +488,63 @@ gdn_status gdn_kv_gather(void* k, void* v, int64_t k_stride, int64_t v_stride,
                          gdn_stream_t stream);
 
 /*
+ * gdn_qk_norm_rope — RMS norms of the heads of q and k and their rotation by the
+ * tokens' positions, between a layer's projections and its attention.  A head's row x
+ * of head_dim values, in fp32, rounded once to bf16:
+ *     y = w x / sqrt(mean of x^2 + norm_eps)      with GDN_ROPE_RMSNORM, else y = x
+ *     the first rotary_dim values of y are pairs; pair i turns by p inv_freq[i]:
+ *     (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
+ * with a, b = i, i + rotary_dim / 2, or 2 i, 2 i + 1 with GDN_ROPE_INTERLEAVED; the
+ * other values stay.  rotary_dim: a multiple of 8 from 8 to head_dim.  inv_freq
+ * [rotary_dim / 2] fp32 (device), any finite values (a pair whose value is not finite
+ * becomes NaN); angles are right to 2^-25 of a turn for every 32-bit position while
+ * |inv_freq| < 2^40.  Weights w [head_dim] fp32 for q's heads and for k's, or NULL for
+ * ones; they must be NULL without GDN_ROPE_RMSNORM; norm_eps >= 0.
+ *
+ * Positions: [num_axes][total_tokens] int32 (device), 1 to 4 axes; pair i goes by axis
+ * axis_of[i] (host memory, rotary_dim / 2 bytes, each below num_axes; may be NULL for one
+ * axis), for example time, height and width of a picture's patches.
+ *
+ * q [total_tokens][h_q][head_dim], k [..][h_kv][..] and their outputs bf16 with strides
+ * between tokens as for gdn_kv_append; head_dim 128 or 256, any numbers of heads up to
+ * 65535.  An output may be its own input (same address and stride); otherwise it must not
+ * overlap an input.  Tensors and weights 16-byte aligned.
+ */
+#define GDN_ROPE_RMSNORM 1u
+#define GDN_ROPE_INTERLEAVED 2u
+
+gdn_status gdn_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                            void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride,
+                            const int32_t* positions, int32_t num_axes, const uint8_t* axis_of,
+                            const float* inv_freq, int32_t rotary_dim, const float* q_weight,
+                            const float* k_weight, float norm_eps, int64_t total_tokens,
+                            int32_t h_q, int32_t h_kv, int32_t head_dim, gdn_dtype dtype,
+                            uint32_t options, gdn_stream_t stream);
+
+/*
+ * gdn_kv_append_rope — gdn_qk_norm_rope and gdn_kv_append in one launch, for the rows that
+ * gdn_attn_prefill_paged or gdn_attn_decode_paged then attend to: the cache receives k,
+ * normalised and rotated, and v as it is, and q_out receives q normalised and rotated.
+ * All bit for bit what the two calls leave (an e4m3 row of k is quantised from its bf16
+ * rounding).  positions as above, or NULL (with one axis): the positions in the cache,
+ * start_pos[n] + place.  With h_q = 0 there is no q (q and q_out are not used).  A token
+ * that no sequence's range holds is left out whole; one whose page is missing still has
+ * its q.  Other arguments, conditions and errors as for the two calls.
+ */
+gdn_status gdn_kv_append_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, void* q_out,
+                              int64_t q_out_stride, void* k_pages, void* v_pages, uint8_t* k_exp,
+                              uint8_t* v_exp, const int32_t* page_table,
+                              const int32_t* cu_seqlens, const int32_t* start_pos,
+                              const int32_t* positions, int32_t num_axes, const uint8_t* axis_of,
+                              const float* inv_freq, int32_t rotary_dim, const float* q_weight,
+                              const float* k_weight, float norm_eps, int32_t num_seqs,
+                              int64_t total_tokens, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                              int32_t page_size, int32_t num_pages, int32_t max_pages,
+                              gdn_cache_dtype cache_dtype, uint32_t options,
+                              gdn_stream_t stream);
+
+/*
  * gdn_attn_decode_paged — gdn_attn_decode over the paged cache: one query of
  * each of `batch` sequences over its cache_len[b] cached rows, same formula,
  * head mapping (1 to 8 query heads per KV head) and result for an empty cache
