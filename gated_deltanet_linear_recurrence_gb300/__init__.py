@@ -18,7 +18,8 @@ __all__ = ["gdn_prefill", "gdn_prefill_streamed", "gdn_prefill_streamed_workspac
            "gdn_output_rmsnorm", "gdn_decode_multi", "gdn_attn_decode",
            "gdn_attn_decode_workspace_size", "gdn_attn_decode_block_keys",
            "gdn_attn_prefill", "gdn_kv_append", "gdn_kv_gather", "gdn_attn_decode_paged",
-           "gdn_attn_decode_paged_workspace_size", "gdn_qk_norm_rope", "gdn_kv_append_rope",
+           "gdn_attn_decode_paged_workspace_size", "gdn_attn_prefill_paged",
+           "gdn_attn_prefill_paged_workspace_size", "gdn_qk_norm_rope", "gdn_kv_append_rope",
            "gdn_prefill_workspace_size",
            "gdn_stream_status", "gdn_status_string", "gdn_prefill_crossover_tokens",
            "gdn_prefill_form", "gdn_selftest_wait_timeout", "GdnError",
@@ -455,6 +456,25 @@ def gdn_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=Non
     by default the same offsets: whole prompts).  q, k and v may be slices of a fused
     projection.  ``scale`` defaults to 1/sqrt(D).  Returns o [Tq, h_q, D]."""
     return _lib.binding().attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, o, stream)
+
+
+def gdn_attn_prefill_paged_workspace_size(h_q, h_kv, head_dim):
+    return int(_lib.load().gdn_attn_prefill_paged_workspace_size(h_q, h_kv, head_dim))
+
+
+def gdn_attn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens_q, cache_len, k_exp=None,
+                           v_exp=None, window=None, sinks=0, scale=None, o=None, workspace=None,
+                           stream=None):
+    """Attention of packed new tokens over a paged cache (gdn_attn_prefill_paged in
+    include/gdn.h): q [T, h_q, D] bf16, the tokens of sequence n = cu_seqlens_q[n] ..
+    cu_seqlens_q[n+1]-1, which are the last of its cache_len[n] cached positions; pages,
+    exponent bytes and page_table as for gdn_kv_append.  ``window``: a token sees itself and
+    the window - 1 positions before, and the first ``sinks`` positions; all before it when
+    None.  ``scale`` defaults to 1/sqrt(D).  A workspace of
+    gdn_attn_prefill_paged_workspace_size() bytes is allocated when none is given.  Returns o
+    [T, h_q, D] bf16."""
+    return _lib.binding().attn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens_q, cache_len,
+                                             k_exp, v_exp, window, sinks, scale, o, workspace, stream)
 
 
 def gdn_stream_status(stream=None):

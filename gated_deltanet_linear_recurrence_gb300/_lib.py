@@ -84,6 +84,10 @@ SIGNATURES = {
                                           _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
                                           _f32, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
                                           ctypes.c_int, ctypes.c_uint32, _vp]),
+    "gdn_attn_prefill_paged": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                                              ctypes.c_int, _f32, _i32, _i32, _vp, _sz, _vp]),
+    "gdn_attn_prefill_paged_workspace_size": (_sz, [_i32, _i32, _i32]),
     "gdn_stream_status": (ctypes.c_int, [_vp]),
     "gdn_selftest_wait_timeout": (ctypes.c_int, [_i32, _vp]),
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -139,7 +143,8 @@ def binding():
         mod.init(check, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
                           ("gdn_kv_append", "gdn_kv_gather", "gdn_attn_decode_paged",
                            "gdn_attn_decode_paged_workspace_size", "gdn_attn_prefill",
-                           "gdn_qk_norm_rope", "gdn_kv_append_rope")))
+                           "gdn_qk_norm_rope", "gdn_kv_append_rope", "gdn_attn_prefill_paged",
+                           "gdn_attn_prefill_paged_workspace_size")))
         _BINDING = mod
     return _BINDING
 

@@ -105,7 +105,7 @@ gdn_status rows_call(const void* k, const void* v, int64_t k_stride, int64_t v_s
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// Heads, rotation and norm of the two calls below; what they share goes into a.
+// Heads, rotation and norm of gdn_qk_norm_rope and gdn_kv_append_rope; what they share goes into a.
 gdn_status check_rope(gdn::RopeArgs& a, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t rotary_dim,
                       const int32_t* positions, int32_t num_axes, const uint8_t* axis_of, const float* inv_freq,
                       const float* q_weight, const float* k_weight, float norm_eps, uint32_t options) {
@@ -306,6 +306,57 @@ gdn_status gdn_attn_decode_paged(const void* q, int64_t q_stride, const void* k_
   return gdn::launch_attn_decode_paged(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? GDN_OK
              : GDN_ERR_CUDA;
+}
+
+size_t gdn_attn_prefill_paged_workspace_size(int32_t h_q, int32_t h_kv, int32_t head_dim) {
+  if (check_heads(h_q, h_kv, head_dim) != GDN_OK) return 0;
+  return gdn::paged_prefill_workspace_bytes(head_dim);
+}
+
+gdn_status gdn_attn_prefill_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                                  const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* page_table,
+                                  const int32_t* cu_seqlens_q, const int32_t* cache_len, void* o, int32_t num_seqs,
+                                  int64_t total_q, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t page_size,
+                                  int32_t num_pages, int32_t max_pages, gdn_cache_dtype cache_dtype, float scale,
+                                  int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                                  gdn_stream_t stream) {
+  if (total_q < 0 || window < 0 || sinks < 0) return GDN_ERR_INVALID_ARG;
+  gdn_status st = check_heads(h_q, h_kv, head_dim);
+  if (st == GDN_OK)
+    st = check_cache(num_seqs, h_kv, head_dim, page_size, num_pages, max_pages, cache_dtype);
+  if (st == GDN_OK) st = check_stride(q_stride, (int64_t)h_q * head_dim);
+  if (st != GDN_OK) return st;
+  if (total_q > INT32_MAX) return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (num_seqs == 0) return total_q == 0 ? GDN_OK : GDN_ERR_INVALID_ARG;
+  if (!cu_seqlens_q || !cache_len) return GDN_ERR_NULL_POINTER;
+  if (total_q == 0) return GDN_OK;
+  if (!q || !o || !workspace) return GDN_ERR_NULL_POINTER;
+  const gdn::PagedCache cache = make_cache(k_pages, v_pages, k_exp, v_exp, page_table, h_kv, head_dim, page_size,
+                                           num_pages, max_pages, cache_dtype);
+  st = check_pages(cache);
+  if (st != GDN_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(cache_len, 4))
+    return GDN_ERR_MISALIGNED;
+  if (workspace_bytes < gdn::paged_prefill_workspace_bytes(head_dim)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  gdn::PagedPrefillArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.cache = cache;
+  a.cu_q = cu_seqlens_q;
+  a.cache_len = cache_len;
+  a.o = o;
+  a.partial = static_cast<float*>(workspace);
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.h_q = h_q;
+  // a window that no position reaches past is none
+  a.window = window < (int64_t)max_pages * page_size ? window : 0;
+  a.sinks = a.window ? sinks : 0;
+  a.scale = scale;
+  if (!gdn::device_error_word(&a.err)) return GDN_ERR_CUDA;
+  return gdn::launch_attn_prefill_paged(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK
+                                                                                                 : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_attn_prefill(const void* q, const void* k, const void* v, void* o,

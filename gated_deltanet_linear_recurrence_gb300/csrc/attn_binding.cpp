@@ -28,6 +28,8 @@ decltype(&gdn_attn_decode_paged_workspace_size) p_decode_ws;
 decltype(&gdn_attn_prefill) p_prefill;
 decltype(&gdn_qk_norm_rope) p_rope;
 decltype(&gdn_kv_append_rope) p_append_rope;
+decltype(&gdn_attn_prefill_paged) p_prefill_paged;
+decltype(&gdn_attn_prefill_paged_workspace_size) p_prefill_paged_ws;
 PyObject* g_check;  // check(status, name): raises GdnError
 
 struct Refused {  // a Python exception to raise
@@ -325,6 +327,50 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A count that may be None (0); a negative one is refused.
+int32_t count_of(PyObject* o, const char* name) {
+  if (o == Py_None) return 0;
+  const int64_t n = PyLong_AsLongLong(o);
+  if (PyErr_Occurred()) throw python_error();
+  if (n < 0) value_error(std::string(name) + " must not be negative");
+  return as32(n);
+}
+
+// attn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens_q, cache_len, k_exp, v_exp, window, sinks, scale,
+//                    o, workspace, stream)
+PyObject* attn_prefill_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    const Cache c(a[1], a[2], a[3], a[6], a[7]);
+    const at::Tensor& q0 = tensor(a[0], "q");
+    dim(q0, 3, "q", "[T, h_q, D]");
+    const int64_t T = q0.size(0), h_q = q0.size(1);
+    const at::Tensor& q = rows(a[0], {T, h_q, c.D}, "q");
+    const at::Tensor &cu = ints(a[4], {c.N + 1}, "cu_seqlens_q"), &len = ints(a[5], {c.N}, "cache_len");
+    const int32_t window = count_of(a[8], "window"), sinks = count_of(a[9], "sinks");
+    if (a[8] != Py_None && window == 0) value_error("window must be positive, or None");
+    const float scale = scale_of(a[10], c.D);
+    c.with({&q, &cu, &len});
+    const Launch s(c.device, a[13]);
+    const at::Tensor o = a[11] == Py_None ? s.output({T, h_q, c.D}, c.options)
+                                          : s.given(rows(a[11], {T, h_q, c.D}, "o", true));
+    at::Tensor ws;
+    if (a[12] == Py_None) {
+      ws = s.scratch({(int64_t)p_prefill_paged_ws(as32(h_q), as32(c.h_kv), as32(c.D))}, c.options.dtype(at::kByte));
+    } else {
+      ws = tensor(a[12], "workspace");
+      if (!(ws.is_cuda() && ws.is_contiguous())) value_error("workspace must be on the GPU, contiguous");
+      s.given(ws);
+    }
+    c.with({&o, &ws});
+    check(p_prefill_paged(q.data_ptr(), token_stride(q, "q"), c.k, c.v, c.ke, c.ve, c.table, i32_of(cu), i32_of(len),
+                          o.data_ptr(), as32(c.N), T, as32(h_q), as32(c.h_kv), as32(c.D), as32(c.page), as32(c.P),
+                          as32(c.max_pages), c.dtype, scale, window, sinks, ws.numel() ? ws.data_ptr() : nullptr,
+                          ws.nbytes(), s.abi()),
+          "gdn_attn_prefill_paged");
+    return THPVariable_Wrap(o);
+  });
+}
+
 struct Rotation {  // how heads are normalised and turned, and the positions
   const at::Tensor* tensors[4];  // those given, for one_device
   int given = 0;
@@ -475,7 +521,7 @@ PyObject* one_device_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // init(check, addresses of the functions)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int kFunctions = 7;
+  constexpr int kFunctions = 9;
   return guarded(n, 1 + kFunctions, [&]() -> PyObject* {
     void* p[kFunctions];
     for (int i = 0; i < kFunctions; ++i) {
@@ -489,6 +535,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p_prefill = reinterpret_cast<decltype(p_prefill)>(p[4]);
     p_rope = reinterpret_cast<decltype(p_rope)>(p[5]);
     p_append_rope = reinterpret_cast<decltype(p_append_rope)>(p[6]);
+    p_prefill_paged = reinterpret_cast<decltype(p_prefill_paged)>(p[7]);
+    p_prefill_paged_ws = reinterpret_cast<decltype(p_prefill_paged_ws)>(p[8]);
     Py_INCREF(a[0]);
     Py_XDECREF(g_check);
     g_check = a[0];
@@ -502,6 +550,7 @@ PyMethodDef methods[] = {FAST("init", init),
                          FAST("kv_gather", kv_gather),
                          FAST("attn_decode_paged", attn_decode_paged),
                          FAST("attn_prefill", attn_prefill),
+                         FAST("attn_prefill_paged", attn_prefill_paged),
                          FAST("qk_norm_rope", qk_norm_rope),
                          FAST("kv_append_rope", kv_append_rope),
                          FAST("token_stride", token_stride_py),

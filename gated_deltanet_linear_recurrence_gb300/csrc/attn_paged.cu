@@ -57,6 +57,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "attn_common.cuh"
 #include "attn_params.h"
 #include "params.h"
 #include "per_device.h"
@@ -85,14 +86,7 @@ struct TileInfo {     // of a tile on its way through a warp's ring
   uint32_t pad;
   uint8_t k_unit[32], v_unit[32];  // exponent bytes
 };
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f;  // log2 of the largest weight before a reference moves
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 // 16 bytes from global to shared memory; zeros when !valid (nothing is read)
@@ -150,35 +144,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float2 half_units(uint32_t byte) {
   return make_float2(__uint_as_float((byte / 2 + 64) << 23), __uint_as_float((byte - byte / 2 + 63) << 23));
 }
-// The unit of a row of V in two factors: 2^120 times the part up to 2^7 for the codes
-// below (of two rows, as bf16), the rest for the weight (1 for bytes up to 134).
-constexpr uint32_t kUnitTop = 134;
-__device__ __forceinline__ uint32_t value_units(uint32_t byte0, uint32_t byte1) {
-  return ((min(byte0, kUnitTop) + 120) << 7) | ((min(byte1, kUnitTop) + 120) << 23);
-}
+// (the weight's part of a row's unit: see value_units)
 __device__ __forceinline__ float weight_unit(uint32_t byte) {
   return __uint_as_float((max(byte, kUnitTop) - (kUnitTop - 127)) << 23);
-}
-// An e4m3 code's sign, exponent and significand bits put where bf16 has them are 2^-120
-// of its value, subnormal codes included: the magnitudes of the even and of the odd bytes
-// of a word (a NaN code as 480), and two such values times their units (exact).
-constexpr uint32_t kMagnitude = 0x07f007f0u, kSigns = 0x80008000u;
-__device__ __forceinline__ uint32_t even_magnitudes(uint32_t codes) { return (codes << 4) & kMagnitude; }
-__device__ __forceinline__ uint32_t odd_magnitudes(uint32_t codes) { return (codes >> 4) & kMagnitude; }
-__device__ __forceinline__ uint32_t times(uint32_t two, uint32_t units) {
-  uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(two), "r"(units));
-  return y;
-}
-// of the largest magnitudes seen, by halves
-__device__ __forceinline__ bool nan_code(uint32_t most) { return most >= 0x07f00000u || (most & 0xffffu) >= 0x07f0u; }
-// bf16 NaN where a magnitude is that of a NaN code, else zero
-__device__ __forceinline__ uint32_t nan_where(uint32_t magnitudes) {
-  return __vcmpeq2(magnitudes, kMagnitude) & 0x7fc07fc0u;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float lo_part(uint32_t packed, float x) {
   return x - __uint_as_float(packed << 16);
@@ -229,25 +197,6 @@ __device__ __forceinline__ float block_sum(float x, float* at) {
   for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
   return x;
 }
-
-// Quotient of non-negative numbers (those of 32 bits, nearly all, take the short way).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// The work of CTA c: the first `more` CTAs have size + 1 of it, the others size.
-struct Shares {
-  int64_t size, more, split;
-  __device__ __forceinline__ Shares(int64_t total, int ctas) {
-    size = quotient(total, ctas);
-    more = total - size * ctas;
-    split = more * (size + 1);
-  }
-  __device__ __forceinline__ int64_t start(int c) const { return c * size + min((int64_t)c, more); }
-  __device__ __forceinline__ int owner(int64_t u) const {
-    return u < split ? (int)quotient(u, size + 1) : (int)(more + quotient(u - split, size));
-  }
-};
 
 // For up to 32 sequences: all work, and on each lane that before the lane's sequence.
 template <int kUnit>

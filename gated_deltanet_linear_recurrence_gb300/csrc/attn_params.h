@@ -96,6 +96,26 @@ struct AttnPrefillArgs {
   int* err;
 };
 
+// Attention of packed new tokens over the paged cache: the a queries of a sequence are the
+// last a of its cache_len[n] cached positions.
+struct PagedPrefillArgs {
+  const void* q;  // [Tq][h_q][D] bf16
+  int64_t q_stride;
+  PagedCache cache;
+  const int32_t* cu_q;
+  const int32_t* cache_len;
+  void* o;         // [Tq][h_q][D], dense
+  float* partial;  // [pairs][2][256][D + 2]
+  int32_t num_seqs;
+  int64_t total_q;
+  int32_t h_q;
+  int32_t window, sinks;  // keys a query sees of the last (0: all), and of the first
+  int32_t pairs;          // of CTAs that share the work
+  float scale;
+  int* err;
+};
+constexpr int32_t kPagedPrefillMaxPairs = 80;  // bounds the workspace
+
 constexpr int32_t kPagedMaxCtas = 640;  // bounds the workspace of the paged decode
 
 size_t paged_attn_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t head_dim);
@@ -105,6 +125,8 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_append_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_decode_paged(const PagedAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const AttnPrefillArgs& a, cudaStream_t stream);
+size_t paged_prefill_workspace_bytes(int32_t head_dim);
+cudaError_t launch_attn_prefill_paged(const PagedPrefillArgs& a, cudaStream_t stream);
 
 // The current device's error word (gdn_api.cu); false when it cannot be located.
 bool device_error_word(int** out);

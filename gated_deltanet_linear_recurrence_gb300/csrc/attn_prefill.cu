@@ -54,12 +54,10 @@
 // see them (from global memory, only in tiles where any was found).
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 #include <stdint.h>
 
-#include <mutex>
-
+#include "attn_common.cuh"
 #include "attn_params.h"
 #include "attn_tc.cuh"
 #include "params.h"
@@ -74,8 +72,6 @@ constexpr int kRows = 128;          // rows a CTA
 constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14, kEdgeWarp = 15;
 constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f;  // log2 of the largest weight before m moves
 
 struct Tile {  // one unit of work of a pair; tiles < 0 ends the schedule
   int32_t q0, k0;     // packed rows where the sequence's queries and keys start
@@ -141,51 +137,7 @@ struct Shared {  // beside the tiles
   float sums[2][2][128];  // row sums of two tiles, in two parts
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float poison_of(uint32_t bits16) {  // the value if it is not finite
-  return (bits16 & 0x7f80u) == 0x7f80u ? __uint_as_float(bits16 << 16) : 0.f;
-}
-
-template <int N>
-__device__ __forceinline__ float largest(const float (&s)[N]) {
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaxf(s[i], s[8 + i]);
-#pragma unroll
-  for (int k = 16; k < N; k += 16)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = tc2::max3(x[i], s[k + i], s[k + 8 + i]);
-  return tc2::max3(tc2::max3(x[0], x[1], x[2]), tc2::max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
-}
-template <int N>
-__device__ __forceinline__ float least(const float (&s)[N]) {
-  float x = s[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) x = fminf(x, s[i]);
-  return x;
-}
-
 // ------------------------------------------------------------------ schedule
-// Division of non-negative numbers by the tokens of a tile (at least 2):
-// x floor(2^32 / d + 1) / 2^32 is at most one more than x / d.
-struct Divisor {
-  int d;
-  uint32_t inv;
-  __device__ __forceinline__ explicit Divisor(int by) : d(by), inv(0xffffffffu / (uint32_t)by + 1u) {}
-  __device__ __forceinline__ int divide(int x) const {
-    const int q = (int)__umulhi((uint32_t)x, inv);
-    return (int64_t)q * d > x ? q - 1 : q;
-  }
-};
-
 // One sequence's ranges (bad ones count no tiles; recorded once).
 struct Seq {
   int q0, k0, a, b, tiles;
@@ -904,35 +856,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::cluster_sync();  // neither CTA's memory is in use by the other any more
   tc::fence_after_sync();
   if (warp == 0) tc2::tmem_dealloc(tmem, C::kTmemCols);
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-// [rows][heads][D] bf16, `stride` elements between rows; boxes of 64 dimensions
-// x box_heads x box_rows with the 128-byte swizzle
-bool encode(CUtensorMap* map, const void* base, int D, int64_t heads, int64_t rows, int64_t stride,
-            int box_heads, int box_rows) {
-  auto enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>

@@ -1,0 +1,1330 @@
+// attn_prefill_paged.cu — attention of packed new tokens over the paged cache, bf16 or
+// e4m3: prompts, pieces of them, a few drafted tokens and single ones in one call, over
+// all keys before them or a window and the first few.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_common.cuh"
+#include "attn_params.h"
+#include "attn_tc.cuh"
+#include "params.h"
+#include "per_device.h"
+#include "rows.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kKeys = 128;          // keys a tile
+constexpr int kRows = 128;          // rows a CTA
+constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14, kEdgeWarp = 15;
+constexpr int kThreads = 512;
+constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
+constexpr int kConverters = 8;       // warps of a pair that write an e4m3 tile's K or V
+constexpr int kNoted = 8;            // key tiles whose missing pages are noted
+
+// Work, in keys: a tile of queries counts the keys that its rows see, and kTileCost for
+// taking it up (Q in, the first scores, O out).  A share is at least kMinShare.
+constexpr int kTileCost = 256, kMinShare = 768;
+
+template <int D, bool kFp8>
+struct Cfg {
+  // Softmax warps, score tiles and slots as in the attention of packed prompts
+  // (attn_prefill.cu): at D = 256 all eight on one key tile, at D = 128 two groups in turn.
+  static constexpr int kGroups = D == 256 ? 1 : 2, kHalves = D == 256 ? 2 : 1;
+  static constexpr int kCols = kKeys / kHalves;  // scores a thread
+  static constexpr int kS = D == 256 ? 2 : 3;
+  static constexpr int kLag = kS - 1;  // key tiles that the scores are ahead of P V
+  static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
+  static constexpr int kSoftmaxRegs = D == 256 ? 168 : 184, kEpilogueRegs = D == 256 ? 112 : 80;
+  static constexpr int kOut = D == 256 ? 64 : 32;  // columns of O that the epilogue holds
+  static_assert(2 * kSoftmaxRegs + kEpilogueRegs + 64 == 512, "registers");
+  static constexpr uint32_t kQBytes = kRows * D * 2;
+  static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
+  static constexpr int kSlots = D == 256 ? 2 : 4;  // key tiles of K, and of V, in shared memory
+  static constexpr uint32_t kK = kQBytes, kV = kK + kSlots * kEntry;
+  static constexpr uint32_t kStage = kV + kSlots * kEntry;  // 64 columns of o on their way out
+  static constexpr uint32_t kShared = kStage + kRows * 128;  // the barriers and the rest
+  static constexpr int kSteps = D / 16;
+  static constexpr uint32_t kTmemO = kS * kKeys;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr int kItem = D / 32;  // 16-code loads of a thread for its half of K or V
+  static_assert(kTmemO + D <= kTmemCols, "TMEM");
+};
+
+// ------------------------------------------------------------------ work
+// One sequence's queries and keys (bad ones have no queries; recorded once).
+struct Seq {
+  int q0, a, off, tiles;  // first row of q, queries, keys before the first of them, tiles of queries
+};
+// One piece of a pair's work: keys of a tile of queries; count < 0 ends the schedule
+struct Piece {
+  int32_t q0, a, off;
+  int32_t seq, kvh;
+  int32_t tok0;        // first token of the pair's rows
+  int32_t sight;       // keys that the last row sees (its position + 1)
+  int32_t firsts, w0;  // key tiles that hold the first keys; number of the window's first one
+  int32_t v0, count;   // key tiles to go through, of both in this order
+  int32_t part;        // where its partial result goes (0, 1), or -1: all of the tile's keys
+};
+
+struct Work {
+  int64_t window, reach;  // reach = window + sinks
+  int sinks;
+  Divisor tokens;  // of a pair
+  __device__ __forceinline__ explicit Work(const PagedPrefillArgs& p)
+      : window(p.window), reach((int64_t)p.window + p.sinks), sinks(p.window ? p.sinks : 0),
+        tokens(2 * (kRows / (p.h_q / p.cache.h_kv))) {}
+
+  __device__ __forceinline__ Seq sequence(const PagedPrefillArgs& p, int n, bool report) const {
+    Seq s{0, 0, 0, 0};
+    if (n >= p.num_seqs) return s;
+    const int q0 = __ldg(p.cu_q + n), q1 = __ldg(p.cu_q + n + 1);
+    int len = __ldg(p.cache_len + n);
+    const bool bad = q0 < 0 || q1 < q0 || q1 > p.total_q;
+    const bool open = (n == 0 && q0 != 0) || (n == p.num_seqs - 1 && q1 != p.total_q);
+    const bool beyond = len < 0 || (int64_t)len > ((int64_t)p.cache.max_pages << p.cache.page_shift);
+    if (report && (bad || open)) raise_error(p.err, kErrBadCuSeqlens);
+    if (report && beyond) raise_error(p.err, kErrBadCacheLen);
+    if (bad) return s;
+    if (beyond) len = 0;
+    s.q0 = q0;
+    s.a = q1 - q0;
+    s.off = len - s.a;
+    s.tiles = s.a > 0 ? tokens.divide(s.a - 1) + 1 : 0;
+    return s;
+  }
+  // sum over i < m of max(0, x + i tokens)
+  __device__ __forceinline__ int64_t ramp(int64_t x, int m) const {
+    if (m <= 0 || x + (int64_t)(m - 1) * tokens.d <= 0) return 0;
+    // (-x < m tokens, which a sequence's queries bound)
+    const int k = x >= 0 ? 0 : (int)((uint32_t)(-x + tokens.d - 1) / (uint32_t)tokens.d);
+    const int64_t n = m - k;
+    return n * (x + (int64_t)k * tokens.d) + tokens.d * (n * (n - 1) / 2);
+  }
+  // of the first m tiles of a sequence, for one KV head
+  __device__ __forceinline__ int64_t before(const Seq& s, int m) const {
+    int64_t x = ramp((int64_t)s.off + tokens.d, m);
+    if (m > 0 && m == s.tiles)
+      x -= max((int64_t)0, s.off + (int64_t)m * tokens.d) - max((int64_t)0, (int64_t)s.off + s.a);
+    if (window) x -= ramp((int64_t)s.off + 1 - reach, m);
+    return x + (int64_t)m * kTileCost;
+  }
+  // keys that tile i counts
+  __device__ __forceinline__ int64_t keys(const Seq& s, int i) const {
+    const int64_t first = (int64_t)i * tokens.d, last = min((int64_t)s.a, first + tokens.d);
+    const int64_t x = max((int64_t)0, s.off + last);
+    return window ? x - max((int64_t)0, s.off + first + 1 - reach) : x;
+  }
+  __device__ __forceinline__ Piece piece(const Seq& s, int seq, int kvh, int i) const {
+    Piece t;
+    t.q0 = s.q0;
+    t.a = s.a;
+    t.off = s.off;
+    t.seq = seq;
+    t.kvh = kvh;
+    t.tok0 = i * tokens.d;
+    t.sight = max(0, s.off + t.tok0 + min(s.a - t.tok0, tokens.d));
+    const int lo = window ? (int)max((int64_t)0, s.off + t.tok0 + 1 - window) : 0;
+    t.w0 = lo / kKeys;
+    t.firsts = (int)min((int64_t)t.w0, ((int64_t)sinks + kKeys - 1) / kKeys);
+    t.v0 = 0;
+    t.count = t.firsts + (t.sight + kKeys - 1) / kKeys - t.w0;
+    t.part = -1;
+    return t;
+  }
+  // how many of a tile's `count` key tiles lie before work r of it
+  __device__ __forceinline__ int visits(int64_t r, int64_t keys, int count) const {
+    if (r <= kTileCost) return 0;
+    if (r >= kTileCost + keys) return count;
+    return (int)quotient((r - kTileCost) * count, keys);
+  }
+};
+// what the sequences come to, and where a share starts
+struct Found {
+  int64_t total, base;  // all work, that before sequence seq
+  int seq;
+};
+
+// A place in the work: tile i of KV head kvh of sequence n, which starts at `start`.
+struct Place {
+  Seq s;
+  int n, kvh, i;
+  int64_t start;
+  __device__ __forceinline__ void find(const PagedPrefillArgs& p, const Work& w, const Found& f, int64_t u, int lane) {
+    n = f.seq;
+    s = w.sequence(p, n, false);
+    const int64_t head = w.before(s, s.tiles);
+    kvh = (int)quotient(u - f.base, head);
+    const int64_t at = f.base + kvh * head;
+    // the last tile that starts at u or before: 32 probes a step
+    int lo = 0, hi = s.tiles;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, m = lo + lane * step;
+      const unsigned below = __ballot_sync(kFullMask, m < hi && w.before(s, m) <= u - at);
+      lo += (__popc(below) - 1) * step;
+      hi = min(hi, lo + step);
+    }
+    i = lo;
+    start = at + w.before(s, i);
+  }
+  __device__ __forceinline__ void next(const PagedPrefillArgs& p, const Work& w, int64_t end) {
+    start = end;
+    if (++i < s.tiles) return;
+    i = 0;
+    if (++kvh < p.cache.h_kv) return;
+    kvh = 0;
+    do {
+      if (++n >= p.num_seqs) return;
+      s = w.sequence(p, n, false);
+    } while (s.tiles == 0);
+  }
+};
+
+// The share of pair c: false when there is none.  With up to 32 sequences every warp that
+// asks counts them for itself; with more the whole block takes part.
+__device__ __forceinline__ int sharers(int64_t total, int pairs) {
+  return (int)min((int64_t)pairs, max((int64_t)1, quotient(total, kMinShare)));
+}
+__device__ __forceinline__ int64_t scan_up(int64_t x, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(kFullMask, x, off);
+    if (lane >= off) x += y;
+  }
+  return x;
+}
+// total, and the sequence that holds work u of share c (its first piece of work)
+__device__ __forceinline__ bool find_few(const PagedPrefillArgs& p, const Work& w, int c, bool report, int lane, Found* f) {
+  const Seq s = w.sequence(p, lane, report);
+  const int64_t mine = s.tiles > 0 ? p.cache.h_kv * w.before(s, s.tiles) : 0;
+  const int64_t incl = scan_up(mine, lane);
+  f->total = __shfl_sync(kFullMask, incl, 31);
+  const int n = sharers(f->total, p.pairs);
+  if (f->total == 0 || c >= n) return false;
+  const int64_t u = Shares(f->total, n).start(c);
+  f->seq = __ffs(__ballot_sync(kFullMask, incl > u)) - 1;
+  f->base = __shfl_sync(kFullMask, incl - mine, f->seq);
+  return true;
+}
+struct Sums {  // the block's, for this
+  int64_t of[16];
+  Found found;
+};
+template <int kT>
+__device__ __noinline__ bool find_many(const PagedPrefillArgs& p, const Work& w, int c, bool report, Sums& sh, Found* f) {
+  static_assert(kT <= 512, "sums");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.num_seqs - 1) / kT + 1;  // sequences a thread counts
+  const int lo = (int)min((int64_t)p.num_seqs, (int64_t)tid * per), hi = (int)min((int64_t)p.num_seqs, (int64_t)lo + per);
+  int64_t mine = 0;
+  for (int n = lo; n < hi; ++n) {
+    const Seq s = w.sequence(p, n, report);
+    if (s.tiles > 0) mine += p.cache.h_kv * w.before(s, s.tiles);
+  }
+  const int64_t incl = scan_up(mine, lane);
+  if (lane == 31) sh.of[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int k = 0; k < kT / 32; ++k) {
+    if (k < warp) before += sh.of[k];
+    total += sh.of[k];
+  }
+  const int sharing = sharers(total, p.pairs);
+  if (total == 0 || c >= sharing) return false;  // (for all threads alike)
+  const int64_t u = Shares(total, sharing).start(c);
+  if (before <= u && u < before + mine) {
+    for (int n = lo; n < hi; ++n) {
+      const Seq s = w.sequence(p, n, false);
+      const int64_t x = s.tiles > 0 ? p.cache.h_kv * w.before(s, s.tiles) : 0;
+      if (u < before + x) {
+        sh.found.seq = n;
+        sh.found.base = before;
+        break;
+      }
+      before += x;
+    }
+  }
+  __syncthreads();
+  *f = sh.found;
+  f->total = total;
+  return true;
+}
+
+// Key tile j of a piece: its first key, how many of its keys some row may see, and whether
+// some row does not see some of those (or the tile ends behind them).
+struct Keys {
+  int first, rows;
+  bool edge;
+};
+__device__ __forceinline__ Keys key_tile_of(const Piece& t, int j, int window, int sinks) {
+  Keys k;
+  const int v = t.v0 + j;
+  const bool firsts = v < t.firsts;
+  k.first = (firsts ? v : t.w0 + v - t.firsts) * kKeys;
+  k.rows = min(kKeys, (firsts ? sinks : t.sight) - k.first);
+  const int whole = t.off + t.tok0 + 1;  // keys that every row sees, but for the window
+  const int low = window ? max(0, t.sight - window) : 0;  // first key of the last row's window
+  k.edge = k.first + kKeys > whole || max(k.first, sinks) < min(k.first + kKeys, low);
+  return k;
+}
+// the first row of an edge tile's V that may need care (those before, every row sees)
+__device__ __forceinline__ int edge_row(const Piece& t, const Keys& k, int window, int sinks) {
+  const int low = window ? max(0, t.sight - window) : 0;
+  if (max(k.first, sinks) < min(k.first + kKeys, low)) return 0;
+  return max(0, t.off + t.tok0 + 1 - k.first) & ~15;
+}
+__device__ __forceinline__ uint32_t lowest(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
+
+template <int D, bool kFp8>
+struct Shared {  // beside the tiles
+  using C = Cfg<D, kFp8>;
+  // by key tile h: K, V of h % kSlots are there; the scores of h, the product with V
+  // of h are done (h % kSlots; this frees their slots too); P of h is in TMEM (h % kS)
+  uint64_t k_full[C::kSlots], v_full[C::kSlots], s_done[C::kSlots], o_done[C::kSlots], p_ready[C::kS];
+  uint64_t q_full, q_empty, o_free;
+  uint64_t m_ready[2][4];  // two groups: a key tile's references are in m, by quarters of the rows
+  // edge tiles, counted through (% kSlots): V is there in both CTAs; is finite there
+  uint64_t v_edge[C::kSlots], v_clean[C::kSlots];
+  uint64_t sums_in[2];     // the rows' sums of two pieces are there, for the epilogue
+  uint64_t noted[kNoted];  // groups of key tile h (% kNoted) are there
+  // What was found in V in the edge tiles of a piece (by number & 3): the number + 1 where
+  // that was a non-finite value; that this has been told.
+  uint64_t flags_in[4];
+  uint32_t poison[4];
+  uint64_t tile_full[2], tile_empty[2], drained;
+  Piece tile[2];
+  uint32_t tmem;
+  Sums work;
+  uint32_t groups[kNoted];  // which eights of a key tile's keys have a page
+  // halves: the row maxima of a key tile's halves, two key tiles; groups: the
+  // references of two key tiles
+  float red[2][2][128];
+  float sums[2][2][128];  // row sums of two pieces, in two parts
+  float refs[2][128];     // and the references that they go by
+};
+
+// Sixteen e4m3 codes of a row, times its unit, as bf16 (exact, and NaN for a NaN code).
+__device__ __forceinline__ void widen16(const uint4& x, uint32_t byte, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t unit = value_units(byte, byte);
+  uint32_t y[8], most = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t h = __byte_perm(w[i], 0, k == 0 ? 0x1404 : 0x3424);  // a code in each upper byte
+      const uint32_t m = (h >> 4) & kMagnitude;
+      most = __vmaxu2(most, m);
+      y[2 * i + k] = times(m | (h & kSigns), unit);
+    }
+  if (byte > kUnitTop) {  // the rest of a unit above 2^7
+    const uint32_t rest = (byte - kUnitTop + 127) << 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = times(y[i], rest | (rest << 16));
+  }
+  if (nan_code(most)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      y[i] |= nan_where((__byte_perm(w[i / 2], 0, i & 1 ? 0x3424 : 0x1404) >> 4) & kMagnitude);
+  }
+  lo = make_uint4(y[0], y[1], y[2], y[3]);
+  hi = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prefill_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedPrefillArgs p) {
+  using C = Cfg<D, kFp8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Shared<D, kFp8>& sh = *reinterpret_cast<Shared<D, kFp8>*>(smem + C::kShared);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int G = p.h_q / p.cache.h_kv;
+  const int tok_cta = kRows / G;  // tokens a CTA
+  const int window = p.window, sinks = window ? p.sinks : 0;
+  if (warp == 0) {
+    tc2::tmem_alloc(&sh.tmem, C::kTmemCols);
+    tc2::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(&sh.k_full[i], kFp8 ? kConverters : 1);
+      tc::mbar_init(&sh.v_full[i], kFp8 ? kConverters : 1);
+      tc::mbar_init(&sh.s_done[i], 1);
+      tc::mbar_init(&sh.o_done[i], 1);
+    }
+    tc::mbar_init(&sh.q_full, 1);
+    tc::mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < C::kS; ++i) tc::mbar_init(&sh.p_ready[i], 2 * C::kPWarps);
+    for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
+      tc::mbar_init(&sh.tile_full[i], 1);
+      tc::mbar_init(&sh.sums_in[i], 8);
+      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products' and edge warps
+      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : 1));
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sh.flags_in[i], 1);
+      sh.poison[i] = 0;
+    }
+    for (int i = 0; i < kNoted; ++i) tc::mbar_init(&sh.noted[i], 1);
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(&sh.v_edge[i], kFp8 ? kConverters : 1);
+      tc::mbar_init(&sh.v_clean[i], 1);
+    }
+    tc::mbar_init(&sh.o_free, 2 * 4);
+    tc::mbar_init(&sh.drained, 1);
+    tc::fence_mbar_init();
+  }
+  tc::wait_prerequisites();  // q, the cache, its table, the offsets and lengths come from earlier kernels
+  tc::allow_dependents();
+
+  // ---- this pair's share, and its pieces one after the other (for the schedule warp)
+  const Work work(p);
+  const int me = blockIdx.x / 2;
+  Found found{0, 0, 0};
+  bool any = false;
+  if (p.num_seqs > 32) any = find_many<kThreads>(p, work, me, blockIdx.x == 0, sh.work, &found);
+  else if (warp == kScheduleWarp) any = find_few(p, work, me, blockIdx.x == 0, lane, &found);
+  const Shares shares(found.total, any ? sharers(found.total, p.pairs) : 1);
+  int64_t u = any ? shares.start(me) : 0;
+  const int64_t u_end = any ? shares.start(me + 1) : 0;
+  auto next_piece = [&](Place& at, Piece* t) {
+    while (u < u_end) {
+      const int64_t keys = work.keys(at.s, at.i), end = at.start + kTileCost + keys;
+      const int64_t r0 = u - at.start, to = min(end, u_end);
+      *t = work.piece(at.s, at.n, at.kvh, at.i);
+      const int all = t->count, v0 = work.visits(r0, keys, all), v1 = work.visits(to - at.start, keys, all);
+      u = to;
+      if (to == end) at.next(p, work, end);
+      t->v0 = v0;
+      t->count = v1 - v0;
+      if (t->count < all) t->part = r0 > 0 ? 0 : 1;
+      if (t->count > 0 || (all == 0 && r0 == 0)) return true;
+    }
+    t->count = -1;
+    return false;
+  };
+  Place place;
+  if (warp == kScheduleWarp) {
+    Piece t;
+    if (any) place.find(p, work, found, u, lane);
+    next_piece(place, &t);
+    if (lane == 0) sh.tile[0] = t;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t sbase = tc::smem_u32(smem);
+  bool ok = true;
+
+  // wait for what a barrier by key tile says of key tile h
+  auto of_tile = [&](uint64_t* bars, int h) { return tc::mbar_wait(&bars[h % C::kSlots], (h / C::kSlots) & 1); };
+
+  // The warp's next piece (pass counts them); false at the end or when a wait expired.
+  auto next_tile = [&](int pass, Piece* t) {
+    // (the first is there from the start; of tile_full's phases it takes none)
+    const bool w = pass == 0 || __all_sync(kFullMask, tc::mbar_wait(&sh.tile_full[pass & 1], ((pass - 1) >> 1) & 1));
+    if (!w) {
+      ok = false;
+      return false;
+    }
+    *t = sh.tile[pass & 1];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sh.tile_empty[pass & 1]);
+    return t->count >= 0;
+  };
+  // The cached row of slot 0 of what holds key `key`, for the lane's eight keys from there: ~0
+  // without a page.
+  const int shift = p.cache.page_shift;
+  auto entry_of = [&](const Piece& t, int key, bool wanted) {
+    return wanted && (key >> shift) < p.cache.max_pages ? __ldg(p.cache.table + (int64_t)t.seq * p.cache.max_pages + (key >> shift)) : -1;
+  };
+  auto row_of = [&](const Piece& t, int key, int page) {
+    return page >= 0 && page < p.cache.num_pages
+               ? (((uint32_t)page * p.cache.h_kv + t.kvh) << shift) + (key & ((1 << shift) - 1))
+               : ~0u;
+  };
+
+  if (warp < kEpilogueWarp) {
+    tc2::more_registers<C::kSoftmaxRegs>();
+    // ------------------------------------------------------------ softmax
+    Piece t;
+    int used = 0, g = 0;
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int grp = C::kGroups > 1 ? part : 0, half = C::kHalves > 1 ? part : 0;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    // (scale 0: all scores alike, by the smallest factor that keeps a masked score infinite:
+    // 2^-149, with which the largest product is 2^-21)
+    const float c = p.scale == 0.f ? __uint_as_float(1) : p.scale * kLog2e;
+    const bool down = c < 0.f;  // the largest score is then the smallest product
+    const uint32_t r_p = tc2::in_cta(sh.p_ready, 0);
+    bool carried = true;  // no wait expired since the last barrier of these warps
+    for (int pass = 0;; ++pass) {
+      // all softmax warps go on or none: they meet at barriers without a limit
+      const bool more = next_tile(pass, &t);
+      if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, ok && carried)) || !more) break;
+      const int tok = t.tok0 + (int)rank * tok_cta + row / G;
+      const bool real = row < tok_cta * G && tok < t.a;
+      const int lim = real ? max(0, t.off + tok + 1) : 0;   // keys this row sees,
+      const int low = window ? max(0, lim - window) : 0;  // from this one, and the first ones
+      const bool idle = !__any_sync(kFullMask, real);  // no queries: their P may be anything
+      float m = -INFINITY, l = 0.f;
+      // with two groups, this one takes every other key tile (g counts them through)
+      auto key_tile = [&](int j) {
+        const int h = g + j, sb = h % C::kS;
+        const Keys keys = key_tile_of(t, j, window, sinks);
+        const int key0 = keys.first;
+        bool w = carried && of_tile(sh.s_done, h) && tc::mbar_wait(&sh.noted[h % kNoted], (h / kNoted) & 1);
+        const uint32_t paged = sh.groups[h % kNoted];
+        tc::fence_after_sync();
+        w = __all_sync(kFullMask, w);
+        const float none = down ? INFINITY : -INFINITY;
+        const uint32_t scores = tmem + lanes + sb * kKeys + C::kCols * half;
+        // the upper 64 of 128 columns only if some row sees them, as the product with V
+        // takes no more
+        const bool upper = C::kCols > 64 && keys.rows > 64;
+        const int cols = upper ? C::kCols : 64;
+        if ((keys.edge || paged != 0xffffu) && !idle) {
+          // The scores that a row does not see are overwritten, in one short loop before code
+          // that all tiles share.
+          const int left = lim - key0 - C::kCols * half;  // columns of this thread up to the row's last,
+          const int from = low - key0 - C::kCols * half;  // from the window's first,
+          const int first = sinks - key0 - C::kCols * half;  // and up to the first keys' last
+          const bool all = paged == 0xffffu && __all_sync(kFullMask, from <= 0 || !real);  // no other bound
+          const int skip = all ? max(0, __reduce_min_sync(kFullMask, left)) & ~31 : 0;
+#pragma unroll 1
+          for (int k = skip; k < cols; k += 32) {
+            uint32_t see = lowest(left - k) & (~lowest(from - k) | lowest(first - k));
+            if (paged != 0xffffu) {
+              const uint32_t eights = paged >> ((k + C::kCols * half) >> 3);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!((eights >> i) & 1)) see &= ~(0xffu << (8 * i));
+            }
+            float x[32];
+            tc::tmem_ld32(scores + k, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = (see >> i) & 1 ? x[i] : none;
+            tc::tmem_st32(scores + k, x);
+          }
+        }
+        float s[64];  // 64 of the thread's scores
+        auto fetch = [&](int k) { tc2::tmem_ld(scores + k, s); };
+        float x = none;
+        if (!idle) {
+          if (upper) {
+            fetch(64);
+            x = down ? least(s) : largest(s);
+          }
+          fetch(0);
+          const float x0 = down ? least(s) : largest(s);
+          x = C::kCols > 64 ? (down ? fminf(x, x0) : fmaxf(x, x0)) : x0;
+        }
+        float now = m;  // the row's reference, which O and the tiles before go by
+        if (C::kHalves > 1) {
+          float(&red)[2][128] = sh.red[h & 1];
+          red[half][row] = x;
+          tc::fence_before_sync();
+          if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, w))) return;
+          tc::fence_after_sync();
+          const float y = red[half ^ 1][row];
+          x = down ? fminf(x, y) : fmaxf(x, y);
+        } else {
+          carried = w;
+          if (j > 0) {
+            carried = __all_sync(kFullMask, carried && tc::mbar_wait(&sh.m_ready[(h - 1) & 1][warp & 3], ((h - 1) >> 1) & 1));
+            now = sh.red[(h - 1) & 1][0][row];
+          }
+        }
+        // Rows that are no queries hold other rows' q or what was there before: they never
+        // move a reference, and neither does one that is NaN already
+        const bool any = real && x != (down ? INFINITY : -INFINITY);
+        const float top = any ? x * c : -INFINITY;
+        const float next = top > now + kSlack || now == -INFINITY ? top : now;
+        const bool grow = next != now && now == now;
+        if (C::kGroups > 1) {
+          sh.red[h & 1][0][row] = next;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sh.m_ready[h & 1][warp & 3]);
+        }
+        if (j > 0 && __any_sync(kFullMask, grow)) {  // O holds the tiles before: rescale it
+          const bool v = __all_sync(kFullMask, of_tile(sh.o_done, h - 1));
+          tc::fence_after_sync();
+          const float f = now == -INFINITY ? 0.f : ex2(now - next);
+          if (v) {
+#pragma unroll
+            for (int i = 0; i < D / 32 / C::kHalves; ++i) {
+              float ov[32];
+              const uint32_t at = tmem + lanes + C::kTmemO + half * (D / 2) + 32 * i;
+              tc::tmem_ld32(at, ov);
+              if (grow) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) ov[k] *= f;
+              }
+              tc::tmem_st32(at, ov);
+            }
+          }
+          carried = carried && v;
+        }
+        if (next != m) {
+          l *= m == -INFINITY ? 0.f : ex2(m - next);
+          m = next;
+        }
+        if (!idle) {
+          const float ref = m == -INFINITY ? 0.f : m;
+          const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+          float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+#pragma unroll
+          for (int k = 0; k < C::kCols; k += 64) {
+            if (k > 0) {
+              if (!upper) break;
+              fetch(k);
+            }
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+              float2 p0 = tc2::fma2(make_float2(s[i], s[i + 1]), c2, r2);
+              float2 p1 = tc2::fma2(make_float2(s[i + 2], s[i + 3]), c2, r2);
+              p0 = make_float2(ex2(p0.x), ex2(p0.y));
+              p1 = make_float2(ex2(p1.x), ex2(p1.y));
+              l0 = tc2::add2(l0, p0);
+              l1 = tc2::add2(l1, p1);
+              pk[i / 2] = pack_bf16(p0.x, p0.y);
+              pk[i / 2 + 1] = pack_bf16(p1.x, p1.y);
+            }
+            tc2::tmem_st(scores + k, pk);  // over scores that are done with
+          }
+          l0 = tc2::add2(l0, l1);
+          l += l0.x + l0.y;
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc2::arrive_remote_relaxed(r_p + sb * 8);
+      };
+      for (int j = C::kGroups > 1 ? (g ^ grp) & 1 : 0; j < t.count && ok; j += C::kGroups) key_tile(j);
+      // ---- the pair's rows are through their keys: their sums go to the epilogue
+      if (t.count > 0) {
+        if (C::kGroups > 1) {
+          const int h = g + t.count - 1;
+          carried = carried && tc::mbar_wait(&sh.m_ready[h & 1][warp & 3], (h >> 1) & 1);
+          const float last = sh.red[h & 1][0][row];  // of the last tile, which O goes by
+          if (m != last) l *= m == -INFINITY ? 0.f : ex2(m - last);
+          m = last;
+        }
+        sh.sums[used & 1][part][row] = l;
+        if (part == 0) sh.refs[used & 1][row] = m;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.sums_in[used & 1]);
+        g += t.count;
+        ++used;
+      }
+    }
+  } else if (warp < kTmaWarp) {
+    tc2::fewer_registers<C::kEpilogueRegs>();
+    // ------------------------------------------------------------ epilogue, and widening of e4m3 rows
+    const int wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t r_free = tc2::in_cta(&sh.o_free, 0);
+    // 32 rows of 128 bytes for each warp, 16-byte pieces c of row r at c ^ (r & 7)
+    uint8_t* stage = smem + C::kStage + wq * 4096;
+    int32_t to[8];  // which row of o rows 4 i + lane / 8 of the warp's are, from the first one
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = wq * 32 + 4 * i + (lane >> 3);
+      to[i] = r / G * p.h_q + r % G;
+    }
+    // O of piece t, the used'th with keys, whose last key tile is h
+    auto epilogue = [&](const Piece& t, int used, int h) {
+      const int tok0 = t.tok0 + (int)rank * tok_cta;
+      const int rows = min(tok_cta, t.a - tok0) * G - wq * 32;  // that are there, of the warp's
+      const bool real = lane < rows;
+      const int lim = real ? max(0, t.off + tok0 + row / G + 1) : 0;  // keys this row sees
+      const int low = window ? max(0, lim - window) : 0;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
+                           (((int64_t)t.q0 + tok0) * p.h_q + (int64_t)t.kvh * G) * D + (lane & 7) * 8;
+      float inv = 0.f, total = 0.f, ref = 0.f;
+      bool dirty = false;
+      if (t.count > 0) {
+        bool w = tc::mbar_wait(&sh.sums_in[used & 1], (used >> 1) & 1) &&
+                 tc2::wait(&sh.flags_in[used & 3], (used >> 2) & 1);
+        total = sh.sums[used & 1][0][row] + sh.sums[used & 1][1][row];
+        ref = sh.refs[used & 1][row];
+        inv = total == 0.f ? 0.f : 1.f / total;
+        dirty = sh.poison[used & 3] == (uint32_t)used + 1;
+        w = w && of_tile(sh.o_done, h);
+        tc::fence_after_sync();
+        if (!(ok = __all_sync(kFullMask, w) != 0)) return;
+      }
+      float* part = nullptr;  // of a part of the keys: O as it is, four columns of all rows side by side
+      if (t.part >= 0) {
+        part = p.partial + (int64_t)(2 * me + t.part) * (2 * kRows * (D + 2));
+        if (real) {
+          part[2 * kRows * D + rank * kRows + row] = ref;
+          part[2 * kRows * (D + 1) + rank * kRows + row] = total;
+        }
+        part += (int)rank * kRows * D + row * 4;
+        inv = 1.f;
+      }
+      // kOut columns at a time (a thread has a row), through shared memory: stored from
+      // there in rows of 128 bytes
+#pragma unroll 1
+      for (int i = 0; i < D; i += C::kOut) {
+        float ov[C::kOut];
+        if (t.count > 0) {
+          tc2::tmem_ld(tmem + lanes + C::kTmemO + i, ov);
+          if (i == D - C::kOut) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc2::arrive_remote_relaxed(r_free);  // O may be overwritten
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < C::kOut; ++k) ov[k] = 0.f;
+        }
+        const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+        for (int k = 0; k < C::kOut; k += 2) {
+          const float2 y = tc2::mul2(make_float2(ov[k], ov[k + 1]), inv2);
+          ov[k] = y.x;
+          ov[k + 1] = y.y;
+        }
+        if (dirty && real) {  // non-finite values that the edge warp took out, for the rows that see them
+#pragma unroll 1
+          for (int j = 0; j < t.count; ++j) {
+            const Keys keys = key_tile_of(t, j, window, sinks);
+            if (!keys.edge) continue;
+#pragma unroll 1
+            for (int x = edge_row(t, keys, window, sinks); x < keys.rows; ++x) {
+              const int key = keys.first + x;
+              const uint32_t r = row_of(t, key, entry_of(t, key, true));
+              if (key >= lim || (key < low && key >= sinks) || r == ~0u) continue;
+              if (kFp8) {
+                const uint8_t* src = static_cast<const uint8_t*>(p.cache.v_pages) + (int64_t)r * D + i;
+#pragma unroll
+                for (int k = 0; k < C::kOut; ++k)
+                  if ((__ldg(src + k) & 0x7f) == 0x7f) ov[k] = NAN;
+              } else {
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.cache.v_pages) + (int64_t)r * D + i);
+#pragma unroll
+                for (int k = 0; k < C::kOut / 2; ++k) {
+                  const uint32_t two = __ldg(src + k);
+                  ov[2 * k] += poison_of(two & 0xffffu);
+                  ov[2 * k + 1] += poison_of(two >> 16);
+                }
+              }
+            }
+          }
+        }
+        if (part) {
+          if (real) {
+#pragma unroll
+            for (int k = 0; k < C::kOut; k += 4)
+              *reinterpret_cast<float4*>(part + (i + k) * kRows) = make_float4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+          }
+          continue;
+        }
+#pragma unroll
+        for (int k = 0; k < C::kOut; k += 8) {
+          const uint4 x = make_uint4(pack_bf16(ov[k], ov[k + 1]), pack_bf16(ov[k + 2], ov[k + 3]),
+                                     pack_bf16(ov[k + 4], ov[k + 5]), pack_bf16(ov[k + 6], ov[k + 7]));
+          *reinterpret_cast<uint4*>(stage + lane * 128 + (((((i + k) >> 3) & 7) ^ (lane & 7)) << 4)) = x;
+        }
+        if (((i + C::kOut) & 63) == 0) {
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int r = 4 * x + (lane >> 3);
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            if (r < rows) *reinterpret_cast<uint4*>(out + (int64_t)to[x] * D + i + C::kOut - 64) = y;
+          }
+          __syncwarp();
+        }
+      }
+    };
+    Piece t;
+    int used = 0, g = 0;
+    if (!kFp8) {
+      for (int pass = 0; next_tile(pass, &t); ++pass) {
+        epilogue(t, used, g + t.count - 1);
+        if (!ok) break;
+        if (t.count > 0) {
+          g += t.count;
+          ++used;
+        }
+      }
+    } else {
+      // The warps of both CTAs widen K and V into shared memory: eights of keys x 64
+      // dims at a time, which is a whole swizzle atom, in the order in which the products
+      // take them, the next ones' codes on their way meanwhile.  The epilogue of a piece
+      // follows the first V of the next one.
+      const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0), r_ve = tc2::in_cta(sh.v_edge, 0);
+      // within an atom: row, and which 16 of its 64 codes, such that eight lanes' stores
+      // fall into different banks
+      const int r8 = ((lane >> 1) & 1) | ((lane >> 2) & 2) | (lane & 4), c4 = (lane & 1) | ((lane >> 3) & 2);
+      const uint32_t put = r8 * 128 + (((2 * c4) ^ r8) << 4), put2 = r8 * 128 + (((2 * c4 + 1) ^ r8) << 4);
+      const uint8_t* k_codes = static_cast<const uint8_t*>(p.cache.k_pages) + r8 * D + 16 * c4;
+      const uint8_t* v_codes = static_cast<const uint8_t*>(p.cache.v_pages) + r8 * D + 16 * c4 + rank * (D / 2);
+      constexpr int kKShift = D == 256 ? 2 : 1, kVShift = kKShift - 1;  // blocks of 64 dims of a row, as powers
+      struct Item {  // half of K or of V of a key tile
+        bool v, there;
+        uint32_t rows;   // cached row of the lane's eight (lane & 15 of the tile)
+        uint32_t bytes;  // exponent byte of row lane % 8 of the warp's eight number lane / 8
+      };
+      uint4 x[C::kItem];
+      auto load = [&](const Item& it, int n) {
+        const int shf = it.v ? kVShift : kKShift;
+        const uint32_t r = __shfl_sync(kFullMask, it.rows, (it.v ? 0 : 8 * (int)rank) + wq + 4 * (n >> shf));
+        const uint8_t* src = (it.v ? v_codes : k_codes) + (int64_t)r * D + (n & ((1 << shf) - 1)) * 64;
+        return it.there && r != ~0u ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+      };
+      auto units = [&](Item& it) {
+        const uint32_t r = __shfl_sync(kFullMask, it.rows, (it.v ? 0 : 8 * (int)rank) + wq + 4 * ((lane >> 3) & (it.v ? 3 : 1)));
+        it.bytes = it.there && r != ~0u ? __ldg((it.v ? p.cache.v_exp : p.cache.k_exp) + r + (lane & 7)) : 127u;
+      };
+      Piece late;  // whose epilogue is due
+      int late_used = 0, late_h = 0, ve = 0;  // edge tiles so far
+      bool due = false;
+      for (int pass = 0; ok; ++pass) {
+        const bool more = next_tile(pass, &t);
+        if (!ok) break;
+        const int count = more ? t.count : 0, steps = count > 0 ? count + C::kLag : 0;
+        // the page of the lane's eight of key tile j, and their cached rows
+        auto look = [&](int j) {
+          if (j >= count) return -1;
+          const Keys k = key_tile_of(t, j, window, sinks);
+          return entry_of(t, k.first + 8 * (lane & 15), 8 * (lane & 15) < k.rows);
+        };
+        auto rows_of = [&](int j, int page) {
+          return j < count ? row_of(t, key_tile_of(t, j, window, sinks).first + 8 * (lane & 15), page) : ~0u;
+        };
+        uint32_t at[3] = {rows_of(0, look(0)), ~0u, ~0u};  // of key tiles j, j - 1, j - 2
+        int page = look(1);
+        Item it{false, count > 0, at[0], 0};
+        units(it);
+#pragma unroll
+        for (int n = 0; n < C::kItem; ++n) x[n] = load(it, n);
+        for (int j = 0; ok; ++j) {
+          const uint32_t ahead = rows_of(j + 1, page);
+          page = look(j + 2);
+#pragma unroll 1
+          for (int v = j < count ? 0 : 1; v < (j >= C::kLag && j < steps ? 2 : 1); ++v) {
+            const int i = v ? j - C::kLag : j, h = g + i, s = h % C::kSlots;
+            Item next;  // V of kLag tiles before, the next K, or the next V where there is no more K
+            if (!v && j >= C::kLag) next = Item{true, true, at[C::kLag], 0};
+            else if (j + 1 < count) next = Item{false, true, ahead, 0};
+            else if (!v) next = Item{true, true, j == 0 ? at[0] : at[1], 0};
+            else next = Item{true, i + 1 < count, at[C::kLag - 1], 0};
+            units(next);
+            const bool w = h < C::kSlots || of_tile(v ? sh.o_done : sh.s_done, h - C::kSlots);
+            if (!(ok = __all_sync(kFullMask, w) != 0)) break;
+            const int shf = v ? kVShift : kKShift;
+            uint8_t* to_slot = smem + (v ? C::kV : C::kK) + s * C::kEntry + wq * 1024;
+#pragma unroll
+            for (int n = 0; n < C::kItem; ++n) {
+              const uint32_t byte = __shfl_sync(kFullMask, it.bytes, 8 * (n >> shf) + r8);
+              uint4 lo, hi;
+              widen16(x[n], byte, lo, hi);
+              uint8_t* atom = to_slot + (n & ((1 << shf) - 1)) * (v ? 16384 : 8192) + (n >> shf) * 4096;
+              *reinterpret_cast<uint4*>(atom + put) = lo;
+              *reinterpret_cast<uint4*>(atom + put2) = hi;
+              x[n] = load(next, n);
+            }
+            tc2::fence_proxy_async();  // the rows -> the tensor cores
+            __syncwarp();
+            const bool edge = v && key_tile_of(t, i, window, sinks).edge;
+            if (lane == 0) {
+              if (edge) tc2::arrive_remote(r_ve + (ve % C::kSlots) * 8);
+              tc2::arrive_remote((v ? r_v : r_k) + s * 8);
+            }
+            ve += edge;
+            it = next;
+          }
+          if (!ok) break;
+          if (due && j == min(C::kLag, steps)) {
+            epilogue(late, late_used, late_h);
+            due = false;
+          }
+          if (j >= steps) break;
+          at[2] = at[1];
+          at[1] = at[0];
+          at[0] = ahead;
+        }
+        if (!ok || !more) break;
+        late = t;
+        late_used = used;
+        late_h = g + count - 1;
+        due = true;
+        if (count > 0) {
+          g += count;
+          ++used;
+        }
+      }
+    }
+  } else {
+    tc2::fewer_registers<64>();
+    if (warp == kScheduleWarp) {
+      // ------------------------------------------------------------ schedule
+      bool more = sh.tile[0].count >= 0;
+      for (int pass = 1; more; ++pass) {
+        Piece t;
+        more = next_piece(place, &t);
+        if (pass >= 2 && !__all_sync(kFullMask, tc::mbar_wait(&sh.tile_empty[pass & 1], ((pass >> 1) - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          sh.tile[pass & 1] = t;
+          tc::mbar_arrive(&sh.tile_full[pass & 1]);
+        }
+      }
+    } else if (warp == kTmaWarp) {
+      // ------------------------------------------------------------ copies
+      Piece t;
+      int g = 0, used = 0;  // key tiles, pieces with Q so far
+      int kc = 0, vc = 0;   // key tiles whose K, V were asked for
+      int ve = 0;           // edge tiles among the latter
+      const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0);
+      const uint32_t r_ve = tc2::in_cta(sh.v_edge, 0), r_q = tc2::in_cta(&sh.q_full, 0);
+      if (lane == 0) {
+        tc::prefetch_tmap(&tm_q);
+        if (!kFp8) {
+          tc::prefetch_tmap(&tm_k);
+          tc::prefetch_tmap(&tm_v);
+        }
+      }
+      // A lane below 16 looks after eight keys of a tile; the first one of those that lie
+      // side by side in a page copies them (up to 64: a box).
+      const int eight = 8 * (lane & 15), box = min(1 << shift, 64);
+      const bool lead = lane < 16 && (eight & (box - 1)) == 0;
+      const int none = max(1, p.cache.num_pages * p.cache.h_kv);  // past the pages: reads as zeros
+      for (int pass = 0; next_tile(pass, &t); ++pass) {
+        if (t.count == 0) continue;
+        if (used > 0) ok = __all_sync(kFullMask, tc::mbar_wait(&sh.q_empty, (used - 1) & 1)) != 0;
+        if (!ok) break;
+        if (lane == 0) {
+          if (rank == 0) tc::mbar_arrive_expect_tx(&sh.q_full, 2u * (uint32_t)(tok_cta * G) * D * 2);
+          for (int kb = 0; kb < D / 64; ++kb)
+            tc2::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G, t.q0 + t.tok0 + (int)rank * tok_cta, r_q);
+        }
+        __syncwarp();
+        ++used;
+        auto look = [&](int j) {
+          if (j >= t.count) return -1;
+          const Keys k = key_tile_of(t, j, window, sinks);
+          return entry_of(t, k.first + eight, eight < k.rows);
+        };
+        auto rows_of = [&](int j, int page) {
+          return j < t.count ? row_of(t, key_tile_of(t, j, window, sinks).first + eight, page) : ~0u;
+        };
+        uint32_t at[3] = {rows_of(0, look(0)), ~0u, ~0u};  // of key tiles j, j - 1, j - 2
+        int page = look(1);
+        for (int j = 0; j < t.count + C::kLag && ok; ++j) {
+          const uint32_t ahead = rows_of(j + 1, page);
+          page = look(j + 2);
+          if (j < t.count) {
+            const int h = g + j, s = h % C::kSlots;
+            const Keys k = key_tile_of(t, j, window, sinks);
+            if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.s_done, h - C::kSlots)) != 0)) break;
+            const bool wanted = eight < k.rows, missing = wanted && at[0] == ~0u;
+            const uint32_t gone = __ballot_sync(kFullMask, missing) & 0xffffu;
+            if (gone && rank == 0 && lane == 0) raise_error(p.err, kErrBadPage);
+            if (lane == 0) {
+              // (the softmax is through with tile h - kNoted: its P was used before the
+              // scores of h - kSlots were asked for)
+              sh.groups[h % kNoted] = 0xffffu & ~gone;
+              tc::mbar_arrive(&sh.noted[h % kNoted]);
+            }
+            if (!kFp8) {
+              const uint32_t bytes = __popc(__ballot_sync(kFullMask, lead && wanted)) * box * D * 2;
+              // the bytes of both CTAs count on the even CTA's barrier
+              if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh.k_full[s], bytes);
+              if (lead && wanted && (lane >> 3) == (int)rank) {
+                const int slot = missing ? 0 : at[0] & ((1 << shift) - 1), z = missing ? none : (int)(at[0] >> shift);
+#pragma unroll
+                for (int kb = 0; kb < D / 64; ++kb)
+                  tc2::tma_load_3d(smem + C::kK + s * C::kEntry + kb * 8192 + (lane & 7) * 1024, &tm_k, 64 * kb, slot, z,
+                                   r_k + s * 8);
+              }
+              __syncwarp();
+              kc = h + 1;
+            }
+          }
+          const int i = j - C::kLag;
+          if (!kFp8 && i >= 0) {
+            const int h = g + i, s = h % C::kSlots;
+            const Keys k = key_tile_of(t, i, window, sinks);
+            if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.o_done, h - C::kSlots)) != 0)) break;
+            const bool wanted = eight < k.rows, missing = at[C::kLag] == ~0u;
+            const uint32_t bytes = __popc(__ballot_sync(kFullMask, lead && wanted)) * box * D * 2;
+            // So do those of V, in an edge tile on a barrier of its own that the edge warp can
+            // count through; v_full keeps step.
+            const int e = ve % C::kSlots;
+            if (rank == 0 && lane == 0) {
+              tc::mbar_arrive_expect_tx(k.edge ? &sh.v_edge[e] : &sh.v_full[s], bytes);
+              if (k.edge) tc::mbar_arrive(&sh.v_full[s]);
+            }
+            if (lead && wanted) {
+              const int slot = missing ? 0 : at[C::kLag] & ((1 << shift) - 1);
+              const int z = missing ? none : (int)(at[C::kLag] >> shift);
+#pragma unroll
+              for (int kb = 0; kb < D / 128; ++kb)
+                tc2::tma_load_3d(smem + C::kV + s * C::kEntry + kb * 16384 + eight * 128, &tm_v,
+                                 (int)rank * (D / 2) + 64 * kb, slot, z, k.edge ? r_ve + e * 8 : r_v + s * 8);
+            }
+            __syncwarp();
+            vc = h + 1;
+            ve += k.edge;
+          }
+          at[2] = at[1];
+          at[1] = at[0];
+          at[0] = ahead;
+        }
+        g += t.count;
+        if (!ok) break;
+      }
+      // Copies still in flight land before the CTA ends: after an expired wait, the
+      // even CTA's barriers tell of both CTAs' copies.
+      if (lane == 0 && rank == 0) {
+        for (int h = max(0, kc - C::kSlots); h < kc; ++h) ok = of_tile(sh.k_full, h) && ok;
+        for (int h = max(0, vc - C::kSlots); h < vc; ++h) ok = of_tile(sh.v_full, h) && ok;
+        for (int e = max(0, ve - C::kSlots); e < ve; ++e) ok = of_tile(sh.v_edge, e) && ok;
+        if (used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ products
+      Piece t;
+      int used = 0;  // pieces with Q so far
+      // slots of K and V, score tiles to write and to read, and their barriers' phases
+      // (counted, not divided: the issue of a product waits for all of this)
+      uint32_t ks = 0, k_ph = 0, vs = 0, v_ph = 0, sw = 0, sr = 0, sr_ph = 0;
+      const uint32_t idesc_s = tc::idesc_bf16_f32(256, kKeys, false, false);
+      const uint32_t idesc_o = tc::idesc_bf16_f32(256, D, false, true);
+      const uint64_t dq = tc::smem_desc(sbase, 16, 1024, tc::kLayoutSw128);
+      const uint64_t dk = tc::smem_desc(sbase + C::kK, 16, 1024, tc::kLayoutSw128);
+      const uint64_t dv = tc::smem_desc(sbase + C::kV, 16384, 1024, tc::kLayoutSw128);
+      const bool leader = tc::elect_one();
+      // K or V is there: counted by the copies, or told by the warps that widen it in both CTAs
+      auto is_full = [&](uint64_t* bar, uint32_t parity) {
+        return kFp8 ? tc2::wait(bar, parity) : tc::mbar_wait(bar, parity);
+      };
+      auto step = [](uint32_t& i, uint32_t& ph, uint32_t n) {
+        if (++i == n) {
+          i = 0;
+          ph ^= 1;
+        }
+      };
+      int edges = 0;  // edge tiles so far
+      // the even CTA's warp issues for the pair
+      for (int pass = 0; rank == 0 && next_tile(pass, &t); ++pass) {
+        if (t.count == 0) continue;
+        const bool in = tc::mbar_wait(&sh.q_full, used & 1);
+        tc::fence_after_sync();
+        ok = __all_sync(kFullMask, in) != 0;
+        for (int j = 0; j < t.count + C::kLag && ok; ++j) {
+          if (j < t.count) {  // S = Q K^T of key tile j
+            const bool w = is_full(&sh.k_full[ks], k_ph);
+            tc::fence_after_sync();
+            if (!(ok = __all_sync(kFullMask, w) != 0)) break;
+            if (leader) {
+              const uint64_t kd = dk + ((ks * C::kEntry) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < C::kSteps; ++kk)
+                tc2::mma_ss(tmem + sw * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                            kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+              tc2::commit(&sh.s_done[ks]);
+              if (j == t.count - 1) tc2::commit(&sh.q_empty);
+            }
+            __syncwarp();
+            if (++sw == C::kS) sw = 0;
+            step(ks, k_ph, C::kSlots);
+          }
+          const int i = j - C::kLag;
+          if (i >= 0) {  // O += P V of key tile i
+            const Keys k = key_tile_of(t, i, window, sinks);
+            bool w = is_full(&sh.v_full[vs], v_ph);
+            if (k.edge) {  // V may have been edited in both CTAs (ordinary writes): acquire those
+              w = w && of_tile(sh.v_edge, edges) && tc2::wait(&sh.v_clean[edges % C::kSlots], (edges / C::kSlots) & 1);
+              ++edges;
+            }
+            w = w && tc::mbar_wait(&sh.p_ready[sr], sr_ph);
+            if (i == 0 && used > 0) w = w && tc::mbar_wait(&sh.o_free, (used - 1) & 1);
+            tc::fence_after_sync();
+            if (!(ok = __all_sync(kFullMask, w) != 0)) break;
+            if (leader) {
+              const uint64_t vd = dv + ((vs * C::kEntry) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                if (16 * kk < k.rows)  // no weight beyond
+                  tc2::mma_ts(tmem + C::kTmemO, tmem + sr * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), vd + ((kk * 2048) >> 4),
+                              idesc_o, (i > 0) || (kk > 0));
+              tc2::commit(&sh.o_done[vs]);
+            }
+            __syncwarp();
+            step(sr, sr_ph, C::kS);
+            step(vs, v_ph, C::kSlots);
+          }
+        }
+        if (!ok) break;
+        ++used;
+      }
+      // every product issued has completed before either CTA leaves the barrier at the end
+      if (rank == 0) {
+        if (leader) tc2::commit(&sh.drained);
+        __syncwarp();
+        if (!__all_sync(kFullMask, tc::mbar_wait(&sh.drained, 0))) ok = false;
+      }
+    } else if (warp == kEdgeWarp && rank == 0) {
+      // ------------------------------------------------------------ edge tiles
+      // V of both CTAs: a value that is not finite, in a row that some query of the pair does
+      // not see, becomes zero (the epilogue adds it where it is seen).
+      Piece t;
+      int g = 0, used = 0, edges = 0;
+      const uint32_t r_flags = tc2::in_cta(sh.flags_in, 1), r_poison = tc2::in_cta(sh.poison, 1);
+      const uint32_t v_even = tc2::in_cta(smem + C::kV, 0) + lane * 16, v_odd = tc2::in_cta(smem + C::kV, 1) + lane * 16;
+      for (int pass = 0; next_tile(pass, &t); ++pass) {
+        if (t.count == 0) continue;
+        bool told = false;  // a non-finite value that a row sees
+        for (int j = 0; j < t.count && ok; ++j) {
+          const Keys keys = key_tile_of(t, j, window, sinks);
+          if (!keys.edge) continue;
+          const int h = g + j, rows = keys.rows;  // rows of V that some query sees
+          const int row0 = edge_row(t, keys, window, sinks);
+          if (!(ok = __all_sync(kFullMask, tc2::wait(&sh.v_edge[edges % C::kSlots], (edges / C::kSlots) & 1)))) break;
+          const uint32_t slot = h % C::kSlots * C::kEntry;
+          // the largest of the magnitudes, as 16-bit integers (a non-finite one is 0x7f80 or
+          // more); in a short loop, as it runs once a tile of queries and not from a cache
+          uint32_t most = 0;
+#pragma unroll 1
+          for (int r = row0; r < rows; r += 16) {
+            // eight loads in flight: both halves' rows at D = 128, a half's at 256
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 8) {
+              uint4 y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int k = (c + i) % (D / 32);
+                const uint32_t at = slot + (k >> 2) * 16384 + r * 128 + (k & 3) * 512;
+                y[i] = c + i < D / 32 ? tc2::load_remote(v_odd + at)
+                                      : *reinterpret_cast<const uint4*>(smem + C::kV + at + lane * 16);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                most = __vimax3_u16x2(most, y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu);
+                most = __vimax3_u16x2(most, y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu);
+              }
+            }
+          }
+          bool seen = false;
+          const bool edited = __any_sync(kFullMask, (most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u);
+          if (edited) {
+#pragma unroll 1
+            for (int i = 0; i < 2 * (int)C::kEntry / 512; ++i) {  // four rows at a time
+              const int k = i % ((int)C::kEntry / 512), r = 4 * (k & 31);
+              if (r < row0) continue;
+              const uint32_t at = (i == k ? v_even : v_odd) + slot + k * 512;
+              auto finite = [](uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); };
+              const uint4 y = tc2::load_remote(at), z = make_uint4(finite(y.x), finite(y.y), finite(y.z), finite(y.w));
+              if (z.x != y.x || z.y != y.y || z.z != y.z || z.w != y.w) {
+                tc2::store_remote(at, z);
+                seen = seen || r + (lane >> 3) < rows;
+              }
+            }
+          }
+          if (__any_sync(kFullMask, seen)) told = true;
+          if (edited) tc2::fence_proxy_async();  // the edited V rows -> the tensor cores of both CTAs
+          __syncwarp();
+          if (lane == 0) {
+            if (edited) tc2::arrive_remote(tc2::in_cta(&sh.v_clean[edges % C::kSlots], 0));
+            else tc::mbar_arrive(&sh.v_clean[edges % C::kSlots]);
+          }
+          ++edges;
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          if (told) {
+            sh.poison[used & 3] = (uint32_t)used + 1;
+            tc2::store_remote(r_poison + (used & 3) * 4, (uint32_t)used + 1);
+          }
+          tc::mbar_arrive(&sh.flags_in[used & 3]);
+          if (told) tc2::arrive_remote(r_flags + (used & 3) * 8);
+          else tc2::arrive_remote_relaxed(r_flags + (used & 3) * 8);
+        }
+        g += t.count;
+        ++used;
+      }
+    }
+  }
+  if (!ok) raise_error(p.err, kErrDeviceTimeout);
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // neither CTA's memory is in use by the other any more
+  tc::fence_after_sync();
+  if (warp == 0) tc2::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// Tiles of queries whose keys several pairs went through: block (c, y) joins columns 32 y ..
+// of the tile that pair c started and others finished, if there is one.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_prefill_paged_join_kernel(const __grid_constant__ PagedPrefillArgs p) {
+  __shared__ Sums sums;
+  __shared__ int32_t slots[kPagedPrefillMaxPairs];  // of the parts, -1 for an empty one
+  __shared__ float top[2 * kRows], inv[2 * kRows];
+  tc::allow_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
+  const Work work(p);
+  Found found{0, 0, 0};
+  const bool any = p.num_seqs > 32 ? find_many<kJoinThreads>(p, work, c + 1, false, sums, &found)
+                                   : find_few(p, work, c + 1, false, lane, &found);
+  if (!any) return;
+  const int sharing = sharers(found.total, p.pairs);
+  const Shares shares(found.total, sharing);
+  const int64_t u = shares.start(c + 1);
+  Place at;
+  at.find(p, work, found, u, lane);
+  if (at.start == u || at.start < shares.start(c)) return;
+  const int64_t keys = work.keys(at.s, at.i), end = at.start + kTileCost + keys;
+  const Piece t = work.piece(at.s, at.n, at.kvh, at.i);
+  int parts = 0;
+  bool whole = false;
+  for (int k = tid; k < sharing - c; k += kJoinThreads) {
+    const int64_t from = max(shares.start(c + k), at.start), to = min(shares.start(c + k + 1), end);
+    int slot = -1;
+    if (from < to) {
+      const int v0 = work.visits(from - at.start, keys, t.count), v1 = work.visits(to - at.start, keys, t.count);
+      if (v0 < v1) slot = 2 * (c + k) + (k == 0 ? 1 : 0);
+      whole = v0 == 0 && v1 == t.count;
+    }
+    slots[k] = slot;
+  }
+  if (__syncthreads_or(whole)) return;  // (no keys at all, or all of them with one pair)
+  parts = shares.owner(end - 1) - c + 1;
+  const int G = p.h_q / p.cache.h_kv, tok_cta = kRows / G;
+  const int tokens = min(2 * tok_cta, t.a - t.tok0);
+  const int even = min(tok_cta, tokens) * G, all = tokens * G;  // rows, the even CTA's first
+  auto slot_of = [&](int k) { return p.partial + (int64_t)slots[k] * (2 * kRows * (D + 2)); };
+  tc::wait_prerequisites();  // the parts
+  for (int x = tid; x < all; x += kJoinThreads) {
+    const int at_row = x < even ? x : kRows + x - even;
+    float m = -INFINITY, l = 0.f;
+    for (int k = 0; k < parts; ++k)
+      if (slots[k] >= 0) m = fmaxf(m, slot_of(k)[2 * kRows * D + at_row]);
+    for (int k = 0; k < parts; ++k)
+      if (slots[k] >= 0) {
+        const float mk = slot_of(k)[2 * kRows * D + at_row];
+        if (mk != -INFINITY) l += ex2(mk - m) * slot_of(k)[2 * kRows * (D + 1) + at_row];
+      }
+    top[x] = m;
+    inv[x] = l == 0.f ? 0.f : 1.f / l;
+  }
+  __syncthreads();
+  for (int y = tid; y < 4 * all; y += kJoinThreads) {  // eight columns of a row
+    const int x = y % all, col = 32 * blockIdx.y + 8 * (y / all);
+    const int cta = x < even ? 0 : 1, row = x < even ? x : x - even;
+    const float m = top[x];
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      if (slots[k] < 0) continue;
+      const float* part = slot_of(k);
+      const float mk = part[2 * kRows * D + cta * kRows + row];
+      const float4 v = *reinterpret_cast<const float4*>(part + cta * kRows * D + col * kRows + row * 4);
+      const float4 w = *reinterpret_cast<const float4*>(part + cta * kRows * D + (col + 4) * kRows + row * 4);
+      if (mk == -INFINITY) continue;
+      const float f = ex2(mk - m);
+      a = make_float4(fmaf(f, v.x, a.x), fmaf(f, v.y, a.y), fmaf(f, v.z, a.z), fmaf(f, v.w, a.w));
+      b = make_float4(fmaf(f, w.x, b.x), fmaf(f, w.y, b.y), fmaf(f, w.z, b.z), fmaf(f, w.w, b.w));
+    }
+    const float s = inv[x];
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
+                         ((int64_t)(t.q0 + t.tok0 + cta * tok_cta + row / G) * p.h_q + (int64_t)t.kvh * G + row % G) * D + col;
+    *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16(a.x * s, a.y * s), pack_bf16(a.z * s, a.w * s),
+                                                pack_bf16(b.x * s, b.y * s), pack_bf16(b.z * s, b.w * s));
+  }
+}
+
+// A pool of pages as [pages x h_kv][page_size][D] bf16: boxes of 64 dimensions x `rows` rows
+bool encode_pages(CUtensorMap* map, const void* base, const PagedCache& c, int rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t row = (cuuint64_t)c.head_dim * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)1 << c.page_shift, (cuuint64_t)c.num_pages * c.h_kv};
+  const cuuint64_t strides[2] = {row, row << c.page_shift};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kFp8>
+cudaError_t launch(const PagedPrefillArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, kFp8>;
+  const int G = a.h_q / a.cache.h_kv, rows = a.cache.page_shift >= 6 ? 64 : 1 << a.cache.page_shift;
+  CUtensorMap mq, mk, mv;
+  if (!encode(&mq, a.q, D, a.h_q, a.total_q, a.q_stride, G, kRows / G)) return cudaErrorInvalidValue;
+  mk = mv = mq;  // (e4m3 rows are not copied)
+  if (!kFp8) {
+    PagedCache c = a.cache;
+    if (c.num_pages == 0) {  // no page is ever there: the kernel asks for what lies past this one
+      c.num_pages = c.h_kv = 1;
+      c.k_pages = c.v_pages = const_cast<void*>(a.q);
+    }
+    if (!encode_pages(&mk, c.k_pages, c, rows) || !encode_pages(&mv, c.v_pages, c, rows)) return cudaErrorInvalidValue;
+  }
+  const int smem = (int)(C::kShared + sizeof(Shared<D, kFp8>));
+  static_assert(C::kShared + sizeof(Shared<D, kFp8>) <= 227 * 1024, "shared memory");
+  static PerDeviceOnce attrs;
+  cudaError_t e = attrs.run([&] {
+    return cudaFuncSetAttribute(attn_prefill_paged_kernel<D, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3((unsigned)(2 * a.pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  e = cudaLaunchKernelEx(&cfg, attn_prefill_paged_kernel<D, kFp8>, mq, mk, mv, a);
+  if (e != cudaSuccess || a.pairs == 1) return e;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(a.pairs - 1), D / 32);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, attn_prefill_paged_join_kernel<D>, a);
+}
+
+}  // namespace
+
+size_t paged_prefill_workspace_bytes(int32_t head_dim) {
+  return (size_t)kPagedPrefillMaxPairs * 2 * 2 * kRows * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_attn_prefill_paged(const PagedPrefillArgs& in, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  PagedPrefillArgs a = in;
+  a.pairs = sms / 2 < kPagedPrefillMaxPairs ? sms / 2 : kPagedPrefillMaxPairs;
+  const bool fp8 = a.cache.dtype == kCacheE4M3;
+  if (a.cache.head_dim == 256) return fp8 ? launch<256, true>(a, stream) : launch<256, false>(a, stream);
+  return fp8 ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+}
+
+}  // namespace gdn

@@ -601,6 +601,45 @@ gdn_status gdn_attn_prefill(const void* q, const void* k, const void* v, void* o
                             int64_t v_stride, gdn_dtype dtype, float scale, gdn_stream_t stream);
 
 /*
+ * gdn_attn_prefill_paged — gdn_attn_prefill over the paged cache: packed new tokens of
+ * each sequence (a whole prompt, a piece of one, a few drafted tokens, a single one, in any
+ * mixture) attend to the sequence's cached rows, read as they are stored.  Sequence n has
+ * cache_len[n] cached positions, its new tokens' own among them, and its a =
+ * cu_seqlens_q[n+1] - cu_seqlens_q[n] queries are the last a of them.  A query at position p
+ * sees the keys 0 .. p, or with window > 0 the keys p - window + 1 .. p and the first
+ * `sinks` (those at or before p): softmax(scale q.k) V over them as in gdn_attn_prefill, 0
+ * for a query that sees none (a > cache_len[n]).  What a query does not see has no effect
+ * on it, whatever it holds; a position whose page is missing sets GDN_ERR_BAD_PAGE and takes
+ * no part.  Over e4m3 rows the result is that of the rows read back as bf16.
+ *
+ * q [total_q][h_q][head_dim] bf16 with q_stride elements between tokens (a multiple of 8);
+ * o dense; 1 to 8 query heads per KV head; the cache as for gdn_attn_decode_paged.
+ * cu_seqlens_q [num_seqs + 1] as for gdn_attn_prefill: a sequence whose range is bad is
+ * skipped and GDN_ERR_BAD_CU_SEQLENS recorded.  cache_len [num_seqs] int32 on the device, 0
+ * <= cache_len[n] <= max_pages x page_size (a value outside sets GDN_ERR_BAD_CACHE_LEN and
+ * gives o = 0).  window and sinks are not negative (sinks has no effect without a window).
+ *
+ * The keys of the whole batch are dealt evenly to the SMs whatever the lengths; tiles of
+ * queries that several share are joined through `workspace` (at least
+ * gdn_attn_prefill_paged_workspace_size(...) bytes, 16-byte aligned, any contents; not to be
+ * used by two calls that may run at the same time) in a fixed order: the result does not
+ * vary from run to run.
+ */
+gdn_status gdn_attn_prefill_paged(const void* q, int64_t q_stride, const void* k_pages,
+                                  const void* v_pages, const uint8_t* k_exp,
+                                  const uint8_t* v_exp, const int32_t* page_table,
+                                  const int32_t* cu_seqlens_q, const int32_t* cache_len, void* o,
+                                  int32_t num_seqs, int64_t total_q, int32_t h_q, int32_t h_kv,
+                                  int32_t head_dim, int32_t page_size, int32_t num_pages,
+                                  int32_t max_pages, gdn_cache_dtype cache_dtype, float scale,
+                                  int32_t window, int32_t sinks, void* workspace,
+                                  size_t workspace_bytes, gdn_stream_t stream);
+
+/* Workspace bytes for gdn_attn_prefill_paged with these heads (it does not depend on the
+ * batch or the cache); 0 for invalid arguments. */
+size_t gdn_attn_prefill_paged_workspace_size(int32_t h_q, int32_t h_kv, int32_t head_dim);
+
+/*
  * gdn_stream_status — synchronise `stream`, then report (and clear) the
  * current device's error word: GDN_OK, GDN_ERR_BAD_CU_SEQLENS,
  * GDN_ERR_BAD_CACHE_LEN, GDN_ERR_BAD_PAGE, GDN_ERR_DEVICE_TIMEOUT, or
