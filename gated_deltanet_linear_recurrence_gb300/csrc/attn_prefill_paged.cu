@@ -23,6 +23,7 @@ constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
 constexpr int kConverters = 8;       // warps of a pair that write an e4m3 tile's K or V
 constexpr int kNoted = 8;            // key tiles whose missing pages are noted
+constexpr int kAhead = 6;            // key tiles that e4m3 rows are brought into L2 ahead
 
 // Work, in keys: a tile of queries counts the keys that its rows see, and kTileCost for
 // taking it up (Q in, the first scores, O out).  A share is at least kMinShare.
@@ -306,6 +307,31 @@ struct Shared {  // beside the tiles
   float refs[2][128];     // and the references that they go by
 };
 
+// 16 bytes, or zeros; without a branch, behind which the value would be waited for
+__device__ __forceinline__ uint4 load_if(const void* src, bool valid) {
+  uint4 x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
+      : "l"(src), "r"((int)valid));
+  return x;
+}
+__device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other) {
+  int x;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+               : "=&r"(x)
+               : "l"(src), "r"((int)valid), "r"(other));
+  return x;
+}
+__device__ __forceinline__ uint32_t load_if(const uint8_t* src, bool valid, uint32_t other) {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.u8 %0, [%1];\n\t}"
+               : "=&r"(x)
+               : "l"(src), "r"((int)valid), "r"(other));
+  return x;
+}
 // Sixteen e4m3 codes of a row, times its unit, as bf16 (exact, and NaN for a NaN code).
 __device__ __forceinline__ void widen16(const uint4& x, uint32_t byte, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -440,11 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) tc::mbar_arrive(&sh.tile_empty[pass & 1]);
     return t->count >= 0;
   };
-  // The cached row of slot 0 of what holds key `key`, for the lane's eight keys from there: ~0
-  // without a page.
+  // The page table's entry for key `key` (-1 where there is none), and the key's cached row (~0
+  // without a page).
   const int shift = p.cache.page_shift;
   auto entry_of = [&](const Piece& t, int key, bool wanted) {
-    return wanted && (key >> shift) < p.cache.max_pages ? __ldg(p.cache.table + (int64_t)t.seq * p.cache.max_pages + (key >> shift)) : -1;
+    return load_if(p.cache.table + (int64_t)t.seq * p.cache.max_pages + (key >> shift),
+                   wanted && (key >> shift) < p.cache.max_pages, -1);
   };
   auto row_of = [&](const Piece& t, int key, int page) {
     return page >= 0 && page < p.cache.num_pages
@@ -782,11 +809,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int shf = it.v ? kVShift : kKShift;
         const uint32_t r = __shfl_sync(kFullMask, it.rows, (it.v ? 0 : 8 * (int)rank) + wq + 4 * (n >> shf));
         const uint8_t* src = (it.v ? v_codes : k_codes) + (int64_t)r * D + (n & ((1 << shf) - 1)) * 64;
-        return it.there && r != ~0u ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+        return load_if(src, it.there && r != ~0u);
       };
       auto units = [&](Item& it) {
         const uint32_t r = __shfl_sync(kFullMask, it.rows, (it.v ? 0 : 8 * (int)rank) + wq + 4 * ((lane >> 3) & (it.v ? 3 : 1)));
-        it.bytes = it.there && r != ~0u ? __ldg((it.v ? p.cache.v_exp : p.cache.k_exp) + r + (lane & 7)) : 127u;
+        it.bytes = load_if((it.v ? p.cache.v_exp : p.cache.k_exp) + r + (lane & 7), it.there && r != ~0u, 127u);
       };
       Piece late;  // whose epilogue is due
       int late_used = 0, late_h = 0, ve = 0;  // edge tiles so far
@@ -797,9 +824,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int count = more ? t.count : 0, steps = count > 0 ? count + C::kLag : 0;
         // the page of the lane's eight of key tile j, and their cached rows
         auto look = [&](int j) {
-          if (j >= count) return -1;
           const Keys k = key_tile_of(t, j, window, sinks);
-          return entry_of(t, k.first + 8 * (lane & 15), 8 * (lane & 15) < k.rows);
+          return entry_of(t, k.first + 8 * (lane & 15), j < count && 8 * (lane & 15) < k.rows);
         };
         auto rows_of = [&](int j, int page) {
           return j < count ? row_of(t, key_tile_of(t, j, window, sinks).first + 8 * (lane & 15), page) : ~0u;
@@ -850,6 +876,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (due && j == min(C::kLag, steps)) {
             epilogue(late, late_used, late_h);
             due = false;
+            // (again: kept over the epilogue, they would have to leave the registers, and every
+            // load would be waited for)
+#pragma unroll
+            for (int n = 0; n < C::kItem; ++n) x[n] = load(it, n);
           }
           if (j >= steps) break;
           at[2] = at[1];
@@ -903,6 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // side by side in a page copies them (up to 64: a box).
       const int eight = 8 * (lane & 15), box = min(1 << shift, 64);
       const bool lead = lane < 16 && (eight & (box - 1)) == 0;
+      const int run = min(1 << shift, kKeys);  // keys of a tile that lie side by side
       const int none = max(1, p.cache.num_pages * p.cache.h_kv);  // past the pages: reads as zeros
       for (int pass = 0; next_tile(pass, &t); ++pass) {
         if (t.count == 0) continue;
@@ -916,18 +947,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++used;
         auto look = [&](int j) {
-          if (j >= t.count) return -1;
           const Keys k = key_tile_of(t, j, window, sinks);
-          return entry_of(t, k.first + eight, eight < k.rows);
+          return entry_of(t, k.first + eight, j < t.count && eight < k.rows);
         };
         auto rows_of = [&](int j, int page) {
           return j < t.count ? row_of(t, key_tile_of(t, j, window, sinks).first + eight, page) : ~0u;
         };
         uint32_t at[3] = {rows_of(0, look(0)), ~0u, ~0u};  // of key tiles j, j - 1, j - 2
         int page = look(1);
+        // e4m3: the rows of key tiles to come are brought into L2, K's by the even CTA, V's by the other
+        auto bring = [&](int j, int page) {
+          const uint32_t r = rows_of(j, page);
+          if (lane < 16 && (eight & (run - 1)) == 0 && r != ~0u)
+            tc::prefetch_l2(static_cast<const uint8_t*>(rank == 0 ? p.cache.k_pages : p.cache.v_pages) + (int64_t)r * D, run * D);
+        };
+        int far = -1;
+        if (kFp8) {
+          for (int j = 1; j < kAhead; ++j) bring(j, look(j));
+          far = look(kAhead);
+        }
         for (int j = 0; j < t.count + C::kLag && ok; ++j) {
           const uint32_t ahead = rows_of(j + 1, page);
           page = look(j + 2);
+          if (kFp8) {
+            bring(j + kAhead, far);
+            far = look(j + kAhead + 1);
+          }
           if (j < t.count) {
             const int h = g + j, s = h % C::kSlots;
             const Keys k = key_tile_of(t, j, window, sinks);
