@@ -21,7 +21,7 @@ constexpr int kRows = 128;          // rows a CTA
 constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14, kEdgeWarp = 15;
 constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
-constexpr int kConverters = 8;       // warps of a pair that write an e4m3 tile's K or V
+constexpr int kConverters = 4;       // warps of a CTA that write an e4m3 tile's K or V
 constexpr int kNoted = 8;            // key tiles whose missing pages are noted
 constexpr int kAhead = 6;            // key tiles that e4m3 rows are brought into L2 ahead
 
@@ -310,8 +310,7 @@ struct Shared {  // beside the tiles
 // 16 bytes, or zeros; without a branch, behind which the value would be waited for
 __device__ __forceinline__ uint4 load_if(const void* src, bool valid) {
   uint4 x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
       "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
       "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
       : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
@@ -320,41 +319,48 @@ __device__ __forceinline__ uint4 load_if(const void* src, bool valid) {
 }
 __device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other) {
   int x;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
                : "=&r"(x)
                : "l"(src), "r"((int)valid), "r"(other));
   return x;
 }
 __device__ __forceinline__ uint32_t load_if(const uint8_t* src, bool valid, uint32_t other) {
   uint32_t x;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.u8 %0, [%1];\n\t}"
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.u8 %0, [%1];\n\t}"
                : "=&r"(x)
                : "l"(src), "r"((int)valid), "r"(other));
   return x;
+}
+// bytes 0 and 1 (kUpper: 2 and 3) of a word as two 16-bit integers, with their signs
+template <bool kUpper>
+__device__ __forceinline__ uint32_t signed_halves(uint32_t w) {
+  uint32_t y;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w), "n"(kUpper ? 0xb3a2 : 0x9180));
+  return y;
 }
 // Sixteen e4m3 codes of a row, times its unit, as bf16 (exact, and NaN for a NaN code).
 __device__ __forceinline__ void widen16(const uint4& x, uint32_t byte, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   const uint32_t unit = value_units(byte, byte);
-  uint32_t y[8], most = 0;
+  uint32_t y[8], nan = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t h = __byte_perm(w[i], 0, k == 0 ? 0x1404 : 0x3424);  // a code in each upper byte
-      const uint32_t m = (h >> 4) & kMagnitude;
-      most = __vmaxu2(most, m);
-      y[2 * i + k] = times(m | (h & kSigns), unit);
-    }
+  for (int i = 0; i < 4; ++i) {
+    nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;  // the top bit of a byte for a NaN code
+    // two codes with their signs above them, shifted into place
+    y[2 * i] = times((signed_halves<false>(w[i]) << 4) & (kMagnitude | kSigns), unit);
+    y[2 * i + 1] = times((signed_halves<true>(w[i]) << 4) & (kMagnitude | kSigns), unit);
+  }
   if (byte > kUnitTop) {  // the rest of a unit above 2^7
     const uint32_t rest = (byte - kUnitTop + 127) << 7;
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = times(y[i], rest | (rest << 16));
   }
-  if (nan_code(most)) {
+  if (nan & 0x80808080u) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      y[i] |= nan_where((__byte_perm(w[i / 2], 0, i & 1 ? 0x3424 : 0x1404) >> 4) & kMagnitude);
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] |= nan_where((signed_halves<false>(w[i]) << 4) & kMagnitude);
+      y[2 * i + 1] |= nan_where((signed_halves<true>(w[i]) << 4) & kMagnitude);
+    }
   }
   lo = make_uint4(y[0], y[1], y[2], y[3]);
   hi = make_uint4(y[4], y[5], y[6], y[7]);
@@ -378,8 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&sh.k_full[i], kFp8 ? kConverters : 1);
-      tc::mbar_init(&sh.v_full[i], kFp8 ? kConverters : 1);
+      // (e4m3: the even CTA's hear of the other one's warps from its products' warp)
+      const int full = kFp8 ? kConverters + (rank == 0 ? 1 : 0) : 1;
+      tc::mbar_init(&sh.k_full[i], full);
+      tc::mbar_init(&sh.v_full[i], full);
       tc::mbar_init(&sh.s_done[i], 1);
       tc::mbar_init(&sh.o_done[i], 1);
     }
@@ -390,8 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
       tc::mbar_init(&sh.sums_in[i], 8);
-      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products' and edge warps
-      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : 1));
+      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products' and edge
+      // warps (e4m3: the odd CTA's products' warp too)
+      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : kFp8 ? 2 : 1));
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sh.flags_in[i], 1);
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kNoted; ++i) tc::mbar_init(&sh.noted[i], 1);
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&sh.v_edge[i], kFp8 ? kConverters : 1);
+      tc::mbar_init(&sh.v_edge[i], kFp8 ? kConverters + (rank == 0 ? 1 : 0) : 1);
       tc::mbar_init(&sh.v_clean[i], 1);
     }
     tc::mbar_init(&sh.o_free, 2 * 4);
@@ -791,7 +800,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // dims at a time, which is a whole swizzle atom, in the order in which the products
       // take them, the next ones' codes on their way meanwhile.  The epilogue of a piece
       // follows the first V of the next one.
-      const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0), r_ve = tc2::in_cta(sh.v_edge, 0);
       // within an atom: row, and which 16 of its 64 codes, such that eight lanes' stores
       // fall into different banks
       const int r8 = ((lane >> 1) & 1) | ((lane >> 2) & 2) | (lane & 4), c4 = (lane & 1) | ((lane >> 3) & 2);
@@ -862,12 +870,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(atom + put2) = hi;
               x[n] = load(next, n);
             }
-            tc2::fence_proxy_async();  // the rows -> the tensor cores
+            tc::fence_proxy_async();  // the rows -> this CTA's tensor cores
             __syncwarp();
             const bool edge = v && key_tile_of(t, i, window, sinks).edge;
             if (lane == 0) {
-              if (edge) tc2::arrive_remote(r_ve + (ve % C::kSlots) * 8);
-              tc2::arrive_remote((v ? r_v : r_k) + s * 8);
+              if (edge) tc::mbar_arrive(&sh.v_edge[ve % C::kSlots]);
+              tc::mbar_arrive(v ? &sh.v_full[s] : &sh.k_full[s]);
             }
             ve += edge;
             it = next;
@@ -1118,6 +1126,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         ++used;
+      }
+      // The odd CTA's warp hands on that K and V have been widened there: a release for the
+      // cluster waits for everything that its thread has under way, which the warps that
+      // load and widen would do at every tile (800 of 4,300 cycles, when that was tried).
+      if (kFp8 && rank == 1) {
+        int g = 0;
+        const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0), r_ve = tc2::in_cta(sh.v_edge, 0);
+        for (int pass = 0; next_tile(pass, &t); ++pass) {
+          for (int j = 0; j < t.count + C::kLag && t.count > 0 && ok; ++j) {
+            if (j < t.count) {
+              if (!(ok = __all_sync(kFullMask, of_tile(sh.k_full, g + j)) != 0)) break;
+              if (leader) tc2::arrive_remote(r_k + (g + j) % C::kSlots * 8);
+            }
+            const int i = j - C::kLag;
+            if (i >= 0) {
+              if (!(ok = __all_sync(kFullMask, of_tile(sh.v_full, g + i)) != 0)) break;
+              const bool edge = key_tile_of(t, i, window, sinks).edge;
+              if (leader) {
+                if (edge) tc2::arrive_remote(r_ve + edges % C::kSlots * 8);
+                tc2::arrive_remote(r_v + (g + i) % C::kSlots * 8);
+              }
+              edges += edge;
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          g += max(0, t.count);
+        }
       }
       // every product issued has completed before either CTA leaves the barrier at the end
       if (rank == 0) {
