@@ -50,7 +50,6 @@ struct Cfg {
   static constexpr int kSteps = D / 16;
   static constexpr uint32_t kTmemO = kS * kKeys;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr int kItem = D / 32;  // 16-code loads of a thread for its half of K or V
   static_assert(kTmemO + D <= kTmemCols, "TMEM");
 };
 
@@ -305,6 +304,7 @@ struct Shared {  // beside the tiles
   float red[2][2][128];
   float sums[2][2][128];  // row sums of two pieces, in two parts
   float refs[2][128];     // and the references that they go by
+  alignas(16) uint8_t bytes[kConverters][2][32];  // e4m3: exponent bytes of a warp's four eights, two items
 };
 
 // 16 bytes, or zeros; without a branch, behind which the value would be waited for
@@ -324,19 +324,22 @@ __device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other
                : "l"(src), "r"((int)valid), "r"(other));
   return x;
 }
-__device__ __forceinline__ uint32_t load_if(const uint8_t* src, bool valid, uint32_t other) {
-  uint32_t x;
-  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.u8 %0, [%1];\n\t}"
-               : "=&r"(x)
-               : "l"(src), "r"((int)valid), "r"(other));
-  return x;
-}
 // bytes 0 and 1 (kUpper: 2 and 3) of a word as two 16-bit integers, with their signs
 template <bool kUpper>
 __device__ __forceinline__ uint32_t signed_halves(uint32_t w) {
   uint32_t y;
   asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w), "n"(kUpper ? 0xb3a2 : 0x9180));
   return y;
+}
+// 8 bytes from global to shared memory; zeros when !valid (nothing is read)
+__device__ __forceinline__ void copy8(const void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(valid ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // Sixteen e4m3 codes of a row, times its unit, as bf16 (exact, and NaN for a NaN code).
 __device__ __forceinline__ void widen16(const uint4& x, uint32_t byte, uint4& lo, uint4& hi) {
@@ -670,12 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t r_free = tc2::in_cta(&sh.o_free, 0);
     // 32 rows of 128 bytes for each warp, 16-byte pieces c of row r at c ^ (r & 7)
     uint8_t* stage = smem + C::kStage + wq * 4096;
-    int32_t to[8];  // which row of o rows 4 i + lane / 8 of the warp's are, from the first one
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = wq * 32 + 4 * i + (lane >> 3);
-      to[i] = r / G * p.h_q + r % G;
-    }
     // O of piece t, the used'th with keys, whose last key tile is h
     auto epilogue = [&](const Piece& t, int used, int h) {
       const int tok0 = t.tok0 + (int)rank * tok_cta;
@@ -685,6 +682,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int low = window ? max(0, lim - window) : 0;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
                            (((int64_t)t.q0 + tok0) * p.h_q + (int64_t)t.kvh * G) * D + (lane & 7) * 8;
+      int32_t to[8];  // which row of o rows 4 i + lane / 8 of the warp's are, from the first one
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = wq * 32 + 4 * i + (lane >> 3);
+        to[i] = r / G * p.h_q + r % G;
+      }
       float inv = 0.f, total = 0.f, ref = 0.f;
       bool dirty = false;
       if (t.count > 0) {
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // The warps of both CTAs widen K and V into shared memory: eights of keys x 64
+      // The warps of both CTAs widen K and V into shared memory: an eight of keys x 64
       // dims at a time, which is a whole swizzle atom, in the order in which the products
       // take them, the next ones' codes on their way meanwhile.  The epilogue of a piece
       // follows the first V of the next one.
@@ -804,27 +807,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       // fall into different banks
       const int r8 = ((lane >> 1) & 1) | ((lane >> 2) & 2) | (lane & 4), c4 = (lane & 1) | ((lane >> 3) & 2);
       const uint32_t put = r8 * 128 + (((2 * c4) ^ r8) << 4), put2 = r8 * 128 + (((2 * c4 + 1) ^ r8) << 4);
-      const uint8_t* k_codes = static_cast<const uint8_t*>(p.cache.k_pages) + r8 * D + 16 * c4;
+      // A warp's part of K or of V: four eights, D / 128 blocks of 64 dims.  Of K's 64 keys two
+      // warps share the eights and two the blocks; of V's 128 the four share the eights.
+      constexpr int kBlocks = D / 128;
+      const uint8_t* k_codes = static_cast<const uint8_t*>(p.cache.k_pages) + r8 * D + 16 * c4 + (wq >> 1) * (64 * kBlocks);
       const uint8_t* v_codes = static_cast<const uint8_t*>(p.cache.v_pages) + r8 * D + 16 * c4 + rank * (D / 2);
-      constexpr int kKShift = D == 256 ? 2 : 1, kVShift = kKShift - 1;  // blocks of 64 dims of a row, as powers
-      struct Item {  // half of K or of V of a key tile
+      const int k_eight = 8 * (int)rank + (wq & 1);  // and every second one; of V wq and every fourth
+      struct Item {      // a part of a key tile
         bool v, there;
         uint32_t rows;   // cached row of the lane's eight (lane & 15 of the tile)
-        uint32_t bytes;  // exponent byte of row lane % 8 of the warp's eight number lane / 8
       };
-      uint4 x[C::kItem];
-      auto load = [&](const Item& it, int n) {
-        const int shf = it.v ? kVShift : kKShift;
-        const uint32_t r = __shfl_sync(kFullMask, it.rows, (it.v ? 0 : 8 * (int)rank) + wq + 4 * (n >> shf));
-        const uint8_t* src = (it.v ? v_codes : k_codes) + (int64_t)r * D + (n & ((1 << shf) - 1)) * 64;
-        return load_if(src, it.there && r != ~0u);
+      uint4 x[4][kBlocks];
+      uint32_t row[4];  // cached rows of the eights being loaded
+      // The rows of an item, and its exponent bytes on their way into shared memory (in
+      // registers, which are handed from item to item, they would be waited for).
+      uint8_t(*bytes)[32] = sh.bytes[wq];
+      auto begin = [&](const Item& it, int parity) {
+        const uint32_t mine = __shfl_sync(kFullMask, it.rows, it.v ? wq + 4 * (lane & 3) : k_eight + 2 * (lane & 3));
+        if (lane < 4)
+          copy8(&bytes[parity][8 * lane], (it.v ? p.cache.v_exp : p.cache.k_exp) + (int64_t)mine, it.there && mine != ~0u);
+        copy_commit();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t r = __shfl_sync(kFullMask, mine, e);
+          row[e] = it.there ? r : ~0u;
+        }
       };
-      auto units = [&](Item& it) {
-        const uint32_t r = __shfl_sync(kFullMask, it.rows, (it.v ? 0 : 8 * (int)rank) + wq + 4 * ((lane >> 3) & (it.v ? 3 : 1)));
-        it.bytes = load_if((it.v ? p.cache.v_exp : p.cache.k_exp) + r + (lane & 7), it.there && r != ~0u, 127u);
-      };
+      auto load = [&](const uint8_t* codes, int e, int b) { return load_if(codes + (int64_t)row[e] * D + 64 * b, row[e] != ~0u); };
       Piece late;  // whose epilogue is due
-      int late_used = 0, late_h = 0, ve = 0;  // edge tiles so far
+      int late_used = 0, late_h = 0, parity = 0, ve = 0;  // (ve: edge tiles so far)
       bool due = false;
       for (int pass = 0; ok; ++pass) {
         const bool more = next_tile(pass, &t);
@@ -840,10 +851,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint32_t at[3] = {rows_of(0, look(0)), ~0u, ~0u};  // of key tiles j, j - 1, j - 2
         int page = look(1);
-        Item it{false, count > 0, at[0], 0};
-        units(it);
+        Item it{false, count > 0, at[0]};
+        begin(it, parity);
 #pragma unroll
-        for (int n = 0; n < C::kItem; ++n) x[n] = load(it, n);
+        for (int n = 0; n < 4 * kBlocks; ++n) x[n / kBlocks][n % kBlocks] = load(k_codes, n / kBlocks, n % kBlocks);
         for (int j = 0; ok; ++j) {
           const uint32_t ahead = rows_of(j + 1, page);
           page = look(j + 2);
@@ -851,25 +862,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int v = j < count ? 0 : 1; v < (j >= C::kLag && j < steps ? 2 : 1); ++v) {
             const int i = v ? j - C::kLag : j, h = g + i, s = h % C::kSlots;
             Item next;  // V of kLag tiles before, the next K, or the next V where there is no more K
-            if (!v && j >= C::kLag) next = Item{true, true, at[C::kLag], 0};
-            else if (j + 1 < count) next = Item{false, true, ahead, 0};
-            else if (!v) next = Item{true, true, j == 0 ? at[0] : at[1], 0};
-            else next = Item{true, i + 1 < count, at[C::kLag - 1], 0};
-            units(next);
+            if (!v && j >= C::kLag) next = Item{true, true, at[C::kLag]};
+            else if (j + 1 < count) next = Item{false, true, ahead};
+            else if (!v) next = Item{true, true, j == 0 ? at[0] : at[1]};
+            else next = Item{true, i + 1 < count, at[C::kLag - 1]};
+            begin(next, parity ^ 1);
+            const uint8_t* codes = next.v ? v_codes : k_codes;
             const bool w = h < C::kSlots || of_tile(v ? sh.o_done : sh.s_done, h - C::kSlots);
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
-            const int shf = v ? kVShift : kKShift;
-            uint8_t* to_slot = smem + (v ? C::kV : C::kK) + s * C::kEntry + wq * 1024;
+            copy_wait<1>();
+            __syncwarp();
+            uint8_t* to_slot = smem + s * C::kEntry + (v ? C::kV + wq * 1024 : C::kK + (wq & 1) * 1024 + (wq >> 1) * (8192 * kBlocks));
+            const int next_eight = v ? 4096 : 2048, next_block = v ? 16384 : 8192;
 #pragma unroll
-            for (int n = 0; n < C::kItem; ++n) {
-              const uint32_t byte = __shfl_sync(kFullMask, it.bytes, 8 * (n >> shf) + r8);
-              uint4 lo, hi;
-              widen16(x[n], byte, lo, hi);
-              uint8_t* atom = to_slot + (n & ((1 << shf) - 1)) * (v ? 16384 : 8192) + (n >> shf) * 4096;
-              *reinterpret_cast<uint4*>(atom + put) = lo;
-              *reinterpret_cast<uint4*>(atom + put2) = hi;
-              x[n] = load(next, n);
-            }
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int b = 0; b < kBlocks; ++b) {
+                uint4 lo, hi;
+                widen16(x[e][b], bytes[parity][8 * e + r8], lo, hi);
+                uint8_t* atom = to_slot + e * next_eight + b * next_block;
+                *reinterpret_cast<uint4*>(atom + put) = lo;
+                *reinterpret_cast<uint4*>(atom + put2) = hi;
+                x[e][b] = load(codes, e, b);
+              }
             tc::fence_proxy_async();  // the rows -> this CTA's tensor cores
             __syncwarp();
             const bool edge = v && key_tile_of(t, i, window, sinks).edge;
@@ -879,6 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ve += edge;
             it = next;
+            parity ^= 1;
           }
           if (!ok) break;
           if (due && j == min(C::kLag, steps)) {
@@ -886,8 +902,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             due = false;
             // (again: kept over the epilogue, they would have to leave the registers, and every
             // load would be waited for)
+            begin(it, parity);
 #pragma unroll
-            for (int n = 0; n < C::kItem; ++n) x[n] = load(it, n);
+            for (int n = 0; n < 4 * kBlocks; ++n)
+              x[n / kBlocks][n % kBlocks] = load(it.v ? v_codes : k_codes, n / kBlocks, n % kBlocks);
           }
           if (j >= steps) break;
           at[2] = at[1];
