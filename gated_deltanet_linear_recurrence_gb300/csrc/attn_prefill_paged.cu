@@ -38,9 +38,10 @@ struct Cfg {
   static constexpr int kS = D == 256 ? 2 : 3;
   static constexpr int kLag = kS - 1;  // key tiles that the scores are ahead of P V
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
-  static constexpr int kSoftmaxRegs = D == 256 ? 168 : 184, kEpilogueRegs = D == 256 ? 112 : 80;
-  static constexpr int kOut = D == 256 ? 64 : 32;  // columns of O that the epilogue holds
-  static_assert(2 * kSoftmaxRegs + kEpilogueRegs + 64 == 512, "registers");
+  static constexpr int kSoftmaxRegs = D == 256 ? 168 : kFp8 ? 176 : 184;
+  static constexpr int kEpilogueRegs = 512 - 64 - 2 * kSoftmaxRegs;
+  // columns of O that the epilogue holds (over e4m3 rows beside what widening them needs)
+  static constexpr int kOut = kFp8 ? 16 * (D / 128) : D == 256 ? 64 : 32;
   static constexpr uint32_t kQBytes = kRows * D * 2;
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
   static constexpr int kSlots = D == 256 ? 2 : 4;  // key tiles of K, and of V, in shared memory
@@ -295,9 +296,10 @@ struct Shared {  // beside the tiles
   uint64_t flags_in[4];
   uint32_t poison[4];
   uint64_t tile_full[2], tile_empty[2], drained;
-  Piece tile[2];
+  Piece tile[2], late[kConverters];
   uint32_t tmem;
   Sums work;
+  int begun;                // e4m3: key tiles whose K is being widened or has been
   uint32_t groups[kNoted];  // which eights of a key tile's keys have a page
   // halves: the row maxima of a key tile's halves, two key tiles; groups: the
   // references of two key tiles
@@ -414,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sh.v_edge[i], kFp8 ? kConverters + (rank == 0 ? 1 : 0) : 1);
       tc::mbar_init(&sh.v_clean[i], 1);
     }
+    sh.begun = 0;
     tc::mbar_init(&sh.o_free, 2 * 4);
     tc::mbar_init(&sh.drained, 1);
     tc::fence_mbar_init();
@@ -489,6 +492,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     return page >= 0 && page < p.cache.num_pages
                ? (((uint32_t)page * p.cache.h_kv + t.kvh) << shift) + (key & ((1 << shift) - 1))
                : ~0u;
+  };
+
+  // For the warp that brings K of key tile h: which eights of its keys have no page.  (It has
+  // waited for the scores of h - kSlots, before which the softmax was through with h - kNoted.)
+  auto note = [&](int h, bool missing) {
+    const uint32_t gone = __ballot_sync(kFullMask, missing) & 0xffffu;
+    if (lane == 0) {
+      if (gone && rank == 0) raise_error(p.err, kErrBadPage);
+      sh.groups[h % kNoted] = 0xffffu & ~gone;
+      tc::mbar_arrive(&sh.noted[h % kNoted]);
+    }
   };
 
   if (warp < kEpilogueWarp) {
@@ -674,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 32 rows of 128 bytes for each warp, 16-byte pieces c of row r at c ^ (r & 7)
     uint8_t* stage = smem + C::kStage + wq * 4096;
     // O of piece t, the used'th with keys, whose last key tile is h
-    auto epilogue = [&](const Piece& t, int used, int h) {
+    auto epilogue = [&](const Piece t, int used, int h) {
       const int tok0 = t.tok0 + (int)rank * tok_cta;
       const int rows = min(tok_cta, t.a - tok0) * G - wq * 32;  // that are there, of the warp's
       const bool real = lane < rows;
@@ -834,7 +848,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto load = [&](const uint8_t* codes, int e, int b) { return load_if(codes + (int64_t)row[e] * D + 64 * b, row[e] != ~0u); };
-      Piece late;  // whose epilogue is due
       int late_used = 0, late_h = 0, parity = 0, ve = 0;  // (ve: edge tiles so far)
       bool due = false;
       for (int pass = 0; ok; ++pass) {
@@ -870,6 +883,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* codes = next.v ? v_codes : k_codes;
             const bool w = h < C::kSlots || of_tile(v ? sh.o_done : sh.s_done, h - C::kSlots);
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
+            if (!v && wq == 0) {  // (for the first warp to say)
+              note(h, 8 * (lane & 15) < key_tile_of(t, j, window, sinks).rows && at[0] == ~0u);
+              if (lane == 0) *const_cast<volatile int*>(&sh.begun) = h + 1;
+            }
             copy_wait<1>();
             __syncwarp();
             uint8_t* to_slot = smem + s * C::kEntry + (v ? C::kV + wq * 1024 : C::kK + (wq & 1) * 1024 + (wq >> 1) * (8192 * kBlocks));
@@ -898,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           if (due && j == min(C::kLag, steps)) {
-            epilogue(late, late_used, late_h);
+            epilogue(sh.late[wq], late_used, late_h);
             due = false;
             // (again: kept over the epilogue, they would have to leave the registers, and every
             // load would be waited for)
@@ -913,7 +930,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           at[0] = ahead;
         }
         if (!ok || !more) break;
-        late = t;
+        if (lane == 0) sh.late[wq] = t;  // whose epilogue is due
+        __syncwarp();
         late_used = used;
         late_h = g + count - 1;
         due = true;
@@ -979,56 +997,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto rows_of = [&](int j, int page) {
           return j < t.count ? row_of(t, key_tile_of(t, j, window, sinks).first + eight, page) : ~0u;
         };
+        if (kFp8) {
+          // The rows of key tiles to come are brought into L2, K's by the even CTA, V's by the
+          // other, kAhead tiles before the warps that widen them.  (They say where they are in
+          // a number: this warp keeps nobody waiting, so that a barrier's phases might pass it by.)
+          int far = look(1);
+          for (int j = 1; j < t.count && ok; ++j) {
+            const uint32_t r = rows_of(j, far);
+            far = look(j + 1);
+            const uint64_t since = tc::globaltimer_ns();
+            while (*const_cast<volatile int*>(&sh.begun) < g + j - kAhead) {
+              __nanosleep(200);
+              if (tc::globaltimer_ns() - since > 1000000000ull) {
+                ok = false;
+                break;
+              }
+            }
+            if (lane < 16 && (eight & (run - 1)) == 0 && r != ~0u)
+              tc::prefetch_l2(static_cast<const uint8_t*>(rank == 0 ? p.cache.k_pages : p.cache.v_pages) + (int64_t)r * D, run * D);
+            ok = __all_sync(kFullMask, ok) != 0;
+          }
+          g += t.count;
+          if (!ok) break;
+          continue;
+        }
         uint32_t at[3] = {rows_of(0, look(0)), ~0u, ~0u};  // of key tiles j, j - 1, j - 2
         int page = look(1);
-        // e4m3: the rows of key tiles to come are brought into L2, K's by the even CTA, V's by the other
-        auto bring = [&](int j, int page) {
-          const uint32_t r = rows_of(j, page);
-          if (lane < 16 && (eight & (run - 1)) == 0 && r != ~0u)
-            tc::prefetch_l2(static_cast<const uint8_t*>(rank == 0 ? p.cache.k_pages : p.cache.v_pages) + (int64_t)r * D, run * D);
-        };
-        int far = -1;
-        if (kFp8) {
-          for (int j = 1; j < kAhead; ++j) bring(j, look(j));
-          far = look(kAhead);
-        }
         for (int j = 0; j < t.count + C::kLag && ok; ++j) {
           const uint32_t ahead = rows_of(j + 1, page);
           page = look(j + 2);
-          if (kFp8) {
-            bring(j + kAhead, far);
-            far = look(j + kAhead + 1);
-          }
           if (j < t.count) {
             const int h = g + j, s = h % C::kSlots;
             const Keys k = key_tile_of(t, j, window, sinks);
             if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.s_done, h - C::kSlots)) != 0)) break;
             const bool wanted = eight < k.rows, missing = wanted && at[0] == ~0u;
-            const uint32_t gone = __ballot_sync(kFullMask, missing) & 0xffffu;
-            if (gone && rank == 0 && lane == 0) raise_error(p.err, kErrBadPage);
-            if (lane == 0) {
-              // (the softmax is through with tile h - kNoted: its P was used before the
-              // scores of h - kSlots were asked for)
-              sh.groups[h % kNoted] = 0xffffu & ~gone;
-              tc::mbar_arrive(&sh.noted[h % kNoted]);
-            }
-            if (!kFp8) {
-              const uint32_t bytes = __popc(__ballot_sync(kFullMask, lead && wanted)) * box * D * 2;
-              // the bytes of both CTAs count on the even CTA's barrier
-              if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh.k_full[s], bytes);
-              if (lead && wanted && (lane >> 3) == (int)rank) {
-                const int slot = missing ? 0 : at[0] & ((1 << shift) - 1), z = missing ? none : (int)(at[0] >> shift);
+            note(h, missing);
+            const uint32_t bytes = __popc(__ballot_sync(kFullMask, lead && wanted)) * box * D * 2;
+            // the bytes of both CTAs count on the even CTA's barrier
+            if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh.k_full[s], bytes);
+            if (lead && wanted && (lane >> 3) == (int)rank) {
+              const int slot = missing ? 0 : at[0] & ((1 << shift) - 1), z = missing ? none : (int)(at[0] >> shift);
 #pragma unroll
-                for (int kb = 0; kb < D / 64; ++kb)
-                  tc2::tma_load_3d(smem + C::kK + s * C::kEntry + kb * 8192 + (lane & 7) * 1024, &tm_k, 64 * kb, slot, z,
-                                   r_k + s * 8);
-              }
-              __syncwarp();
-              kc = h + 1;
+              for (int kb = 0; kb < D / 64; ++kb)
+                tc2::tma_load_3d(smem + C::kK + s * C::kEntry + kb * 8192 + (lane & 7) * 1024, &tm_k, 64 * kb, slot, z,
+                                 r_k + s * 8);
             }
+            __syncwarp();
+            kc = h + 1;
           }
           const int i = j - C::kLag;
-          if (!kFp8 && i >= 0) {
+          if (i >= 0) {
             const int h = g + i, s = h % C::kSlots;
             const Keys k = key_tile_of(t, i, window, sinks);
             if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.o_done, h - C::kSlots)) != 0)) break;
