@@ -105,7 +105,7 @@ struct PagedPrefillArgs {
   const int32_t* cu_q;
   const int32_t* cache_len;
   void* o;         // [Tq][h_q][D], dense
-  float* partial;  // [pairs][2][256][D + 2]
+  float* partial;  // [pairs][2][256][D + 2], and what the joining pass has to know
   int32_t num_seqs;
   int64_t total_q;
   int32_t h_q;

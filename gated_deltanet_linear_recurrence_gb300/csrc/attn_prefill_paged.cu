@@ -142,6 +142,15 @@ struct Work {
     return (int)quotient((r - kTileCost) * count, keys);
   }
 };
+// What a pair leaves for the joining pass: which of its parts there are, and the tile of
+// queries that it has started and not finished (rows 0: none), whose keys pairs up to `last`
+// go through.
+struct Join {
+  int32_t there[2];
+  int32_t last, rows;
+  int32_t token, head;  // the tile's first row of q, and query head
+  int32_t unused[2];
+};
 // what the sequences come to, and where a share starts
 struct Found {
   int64_t total, base;  // all work, that before sequence seq
@@ -254,6 +263,10 @@ __device__ __noinline__ bool find_many(const PagedPrefillArgs& p, const Work& w,
   return true;
 }
 
+__device__ __forceinline__ Join* joins(const PagedPrefillArgs& p) {  // of the pairs, behind the parts
+  return reinterpret_cast<Join*>(p.partial + (int64_t)kPagedPrefillMaxPairs * 2 * (2 * kRows * (p.cache.head_dim + 2)));
+}
+
 // Key tile j of a piece: its first key, how many of its keys some row may see, and whether
 // some row does not see some of those (or the tile ends behind them).
 struct Keys {
@@ -333,6 +346,7 @@ __device__ __forceinline__ uint32_t signed_halves(uint32_t w) {
   asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w), "n"(kUpper ? 0xb3a2 : 0x9180));
   return y;
 }
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // 8 bytes from global to shared memory; zeros when !valid (nothing is read)
 __device__ __forceinline__ void copy8(const void* dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(valid ? 8 : 0)
@@ -434,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Shares shares(found.total, any ? sharers(found.total, p.pairs) : 1);
   int64_t u = any ? shares.start(me) : 0;
   const int64_t u_end = any ? shares.start(me + 1) : 0;
+  Join join{};
   auto next_piece = [&](Place& at, Piece* t) {
     while (u < u_end) {
       const int64_t keys = work.keys(at.s, at.i), end = at.start + kTileCost + keys;
@@ -441,10 +456,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       *t = work.piece(at.s, at.n, at.kvh, at.i);
       const int all = t->count, v0 = work.visits(r0, keys, all), v1 = work.visits(to - at.start, keys, all);
       u = to;
-      if (to == end) at.next(p, work, end);
       t->v0 = v0;
       t->count = v1 - v0;
       if (t->count < all) t->part = r0 > 0 ? 0 : 1;
+      if (t->part >= 0 && t->count > 0) join.there[t->part] = 1;
+      if (to < end && r0 == 0) {
+        join.last = shares.owner(end - 1);
+        join.rows = min(work.tokens.d, t->a - t->tok0) * G;
+        join.token = t->q0 + t->tok0;
+        join.head = t->kvh * G;
+      }
+      if (to == end) at.next(p, work, end);
       if (t->count > 0 || (all == 0 && r0 == 0)) return true;
     }
     t->count = -1;
@@ -889,6 +911,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             copy_wait<1>();
             __syncwarp();
+            uint32_t byte[4];  // (ahead of the stores, which they might be taken to depend on)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) byte[e] = bytes[parity][8 * e + r8];
             uint8_t* to_slot = smem + s * C::kEntry + (v ? C::kV + wq * 1024 : C::kK + (wq & 1) * 1024 + (wq >> 1) * (8192 * kBlocks));
             const int next_eight = v ? 4096 : 2048, next_block = v ? 16384 : 8192;
 #pragma unroll
@@ -896,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int b = 0; b < kBlocks; ++b) {
                 uint4 lo, hi;
-                widen16(x[e][b], bytes[parity][8 * e + r8], lo, hi);
+                widen16(x[e][b], byte[e], lo, hi);
                 uint8_t* atom = to_slot + e * next_eight + b * next_block;
                 *reinterpret_cast<uint4*>(atom + put) = lo;
                 *reinterpret_cast<uint4*>(atom + put2) = hi;
@@ -958,6 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mbar_arrive(&sh.tile_full[pass & 1]);
         }
       }
+      if (rank == 0 && lane == 0) joins(p)[me] = join;
     } else if (warp == kTmaWarp) {
       // ------------------------------------------------------------ copies
       Piece t;
@@ -1013,6 +1039,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
             }
+            // (the exponent bytes too: eight at a time, K's by lanes 0 to 15)
+            if (rank == 0 && r != ~0u) prefetch_line((lane < 16 ? p.cache.k_exp : p.cache.v_exp) + r);
             if (lane < 16 && (eight & (run - 1)) == 0 && r != ~0u)
               tc::prefetch_l2(static_cast<const uint8_t*>(rank == 0 ? p.cache.k_pages : p.cache.v_pages) + (int64_t)r * D, run * D);
             ok = __all_sync(kFullMask, ok) != 0;
@@ -1287,84 +1315,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tc2::tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Tiles of queries whose keys several pairs went through: block (c, y) joins columns 32 y ..
-// of the tile that pair c started and others finished, if there is one.
-constexpr int kJoinThreads = 256;
+// Tiles of queries whose keys several pairs went through: block (c, y, z) joins rows 32 y
+// and columns 64 z of the tile that pair c has started and others finished, if there is
+// one.  A lane has a row, the eight warps share the parts.
+constexpr int kJoinWarps = 8, kJoinColumns = 64;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_prefill_paged_join_kernel(const __grid_constant__ PagedPrefillArgs p) {
-  __shared__ Sums sums;
-  __shared__ int32_t slots[kPagedPrefillMaxPairs];  // of the parts, -1 for an empty one
-  __shared__ float top[2 * kRows], inv[2 * kRows];
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_paged_join_kernel(const __grid_constant__ PagedPrefillArgs p) {
+  constexpr int kEach = kPagedPrefillMaxPairs / kJoinWarps;  // parts of a warp, at most
+  static_assert(kEach * kJoinWarps == kPagedPrefillMaxPairs, "parts");
+  __shared__ float tops[kJoinWarps][32], sums[kJoinWarps][32];
+  __shared__ float4 columns[kJoinWarps][kJoinColumns / 8][32];
   tc::allow_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
-  const Work work(p);
-  Found found{0, 0, 0};
-  const bool any = p.num_seqs > 32 ? find_many<kJoinThreads>(p, work, c + 1, false, sums, &found)
-                                   : find_few(p, work, c + 1, false, lane, &found);
-  if (!any) return;
-  const int sharing = sharers(found.total, p.pairs);
-  const Shares shares(found.total, sharing);
-  const int64_t u = shares.start(c + 1);
-  Place at;
-  at.find(p, work, found, u, lane);
-  if (at.start == u || at.start < shares.start(c)) return;
-  const int64_t keys = work.keys(at.s, at.i), end = at.start + kTileCost + keys;
-  const Piece t = work.piece(at.s, at.n, at.kvh, at.i);
-  int parts = 0;
-  bool whole = false;
-  for (int k = tid; k < sharing - c; k += kJoinThreads) {
-    const int64_t from = max(shares.start(c + k), at.start), to = min(shares.start(c + k + 1), end);
-    int slot = -1;
-    if (from < to) {
-      const int v0 = work.visits(from - at.start, keys, t.count), v1 = work.visits(to - at.start, keys, t.count);
-      if (v0 < v1) slot = 2 * (c + k) + (k == 0 ? 1 : 0);
-      whole = v0 == 0 && v1 == t.count;
-    }
-    slots[k] = slot;
-  }
-  if (__syncthreads_or(whole)) return;  // (no keys at all, or all of them with one pair)
-  parts = shares.owner(end - 1) - c + 1;
-  const int G = p.h_q / p.cache.h_kv, tok_cta = kRows / G;
-  const int tokens = min(2 * tok_cta, t.a - t.tok0);
-  const int even = min(tok_cta, tokens) * G, all = tokens * G;  // rows, the even CTA's first
-  auto slot_of = [&](int k) { return p.partial + (int64_t)slots[k] * (2 * kRows * (D + 2)); };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   tc::wait_prerequisites();  // the parts
-  for (int x = tid; x < all; x += kJoinThreads) {
-    const int at_row = x < even ? x : kRows + x - even;
-    float m = -INFINITY, l = 0.f;
-    for (int k = 0; k < parts; ++k)
-      if (slots[k] >= 0) m = fmaxf(m, slot_of(k)[2 * kRows * D + at_row]);
-    for (int k = 0; k < parts; ++k)
-      if (slots[k] >= 0) {
-        const float mk = slot_of(k)[2 * kRows * D + at_row];
-        if (mk != -INFINITY) l += ex2(mk - m) * slot_of(k)[2 * kRows * (D + 1) + at_row];
-      }
-    top[x] = m;
-    inv[x] = l == 0.f ? 0.f : 1.f / l;
-  }
-  __syncthreads();
-  for (int y = tid; y < 4 * all; y += kJoinThreads) {  // eight columns of a row
-    const int x = y % all, col = 32 * blockIdx.y + 8 * (y / all);
-    const int cta = x < even ? 0 : 1, row = x < even ? x : x - even;
-    const float m = top[x];
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      if (slots[k] < 0) continue;
-      const float* part = slot_of(k);
-      const float mk = part[2 * kRows * D + cta * kRows + row];
-      const float4 v = *reinterpret_cast<const float4*>(part + cta * kRows * D + col * kRows + row * 4);
-      const float4 w = *reinterpret_cast<const float4*>(part + cta * kRows * D + (col + 4) * kRows + row * 4);
-      if (mk == -INFINITY) continue;
-      const float f = ex2(mk - m);
-      a = make_float4(fmaf(f, v.x, a.x), fmaf(f, v.y, a.y), fmaf(f, v.z, a.z), fmaf(f, v.w, a.w));
-      b = make_float4(fmaf(f, w.x, b.x), fmaf(f, w.y, b.y), fmaf(f, w.z, b.z), fmaf(f, w.w, b.w));
+  const Join* js = joins(p);
+  const int rows = __ldg(&js[c].rows), x = 32 * blockIdx.y + lane;
+  if (32 * (int)blockIdx.y >= rows) return;
+  const int last = __ldg(&js[c].last), token = __ldg(&js[c].token), head = __ldg(&js[c].head);
+  const int G = p.h_q / p.cache.h_kv, even = min(kRows / G * G, rows);  // rows of the even CTA
+  const bool real = x < rows;
+  const int cta = x >= even, row = real ? x - cta * even : 0;
+  // part k of the tile is in slot 1 of pair c, in slot 0 of the pairs after it
+  auto part_of = [&](int k) { return p.partial + (int64_t)(2 * (c + k) + (k == 0)) * (2 * kRows * (D + 2)); };
+  float m[kEach], top = -INFINITY;
+  bool some = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int k = warp + kJoinWarps * i;
+    m[i] = -INFINITY;
+    if (c + k <= last && __ldg(&js[c + k].there[k == 0])) {
+      m[i] = part_of(k)[2 * kRows * D + cta * kRows + row];
+      some = true;
     }
-    const float s = inv[x];
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
-                         ((int64_t)(t.q0 + t.tok0 + cta * tok_cta + row / G) * p.h_q + (int64_t)t.kvh * G + row % G) * D + col;
-    *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16(a.x * s, a.y * s), pack_bf16(a.z * s, a.w * s),
-                                                pack_bf16(b.x * s, b.y * s), pack_bf16(b.z * s, b.w * s));
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) top = fmaxf(top, m[i]);
+  tops[warp][lane] = top;
+  if (!__syncthreads_or(some)) return;  // all keys were one pair's, which has written o
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, tops[w][lane]);
+  float4 acc[kJoinColumns / 4];
+#pragma unroll
+  for (int i = 0; i < kJoinColumns / 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (m[i] == -INFINITY) continue;  // a part that is not there, or none of whose keys the row sees
+    const float f = ex2(m[i] - top);
+    const float* part = part_of(warp + kJoinWarps * i);
+    sum = fmaf(f, part[2 * kRows * (D + 1) + cta * kRows + row], sum);
+    const float4* o = reinterpret_cast<const float4*>(part + cta * kRows * D) + (kJoinColumns / 4) * blockIdx.z * kRows + row;
+#pragma unroll
+    for (int k = 0; k < kJoinColumns / 4; ++k) {
+      const float4 v = o[k * kRows];
+      acc[k] = make_float4(fmaf(f, v.x, acc[k].x), fmaf(f, v.y, acc[k].y), fmaf(f, v.z, acc[k].z), fmaf(f, v.w, acc[k].w));
+    }
+  }
+  sums[warp][lane] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) sum += sums[w][lane];
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
+                       ((int64_t)(token + x / G) * p.h_q + head + x % G) * D + kJoinColumns * blockIdx.z;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {  // of the columns: a warp adds up four of them over the warps
+    if (half) __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinColumns / 8; ++k) columns[warp][k][lane] = acc[half * (kJoinColumns / 8) + k];
+    __syncthreads();
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float4 v = columns[w][warp][lane];
+      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+    }
+    if (real)
+      *reinterpret_cast<uint2*>(out + half * (kJoinColumns / 2) + 4 * warp) =
+          make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
   }
 }
 
@@ -1420,8 +1449,9 @@ cudaError_t launch(const PagedPrefillArgs& a, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, attn_prefill_paged_kernel<D, kFp8>, mq, mk, mv, a);
   if (e != cudaSuccess || a.pairs == 1) return e;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)(a.pairs - 1), D / 32);
-  cfg.blockDim = dim3(kJoinThreads);
+  const int64_t most = min((int64_t)2 * (kRows / G), a.total_q) * G;  // rows of a tile
+  cfg.gridDim = dim3((unsigned)(a.pairs - 1), (unsigned)((most + 31) / 32), D / kJoinColumns);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_prefill_paged_join_kernel<D>, a);
 }
@@ -1429,7 +1459,7 @@ cudaError_t launch(const PagedPrefillArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t paged_prefill_workspace_bytes(int32_t head_dim) {
-  return (size_t)kPagedPrefillMaxPairs * 2 * 2 * kRows * (head_dim + 2) * sizeof(float);
+  return (size_t)kPagedPrefillMaxPairs * (2 * 2 * kRows * (head_dim + 2) * sizeof(float) + sizeof(Join));
 }
 
 cudaError_t launch_attn_prefill_paged(const PagedPrefillArgs& in, cudaStream_t stream) {
