@@ -162,6 +162,7 @@ struct Place {
   Seq s;
   int n, kvh, i;
   int64_t start;
+  int64_t u, u_end, total;  // of a share: where it is, where it ends; all work
   __device__ __forceinline__ void find(const PagedPrefillArgs& p, const Work& w, const Found& f, int64_t u, int lane) {
     n = f.seq;
     s = w.sequence(p, n, false);
@@ -312,6 +313,8 @@ struct Shared {  // beside the tiles
   Piece tile[2], late[kConverters];
   uint32_t tmem;
   Sums work;
+  Place place;
+  Join join;
   int begun;                // e4m3: key tiles whose K is being widened or has been
   uint32_t groups[kNoted];  // which eights of a key tile's keys have a page
   // halves: the row maxima of a key tile's halves, two key tiles; groups: the
@@ -445,38 +448,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool any = false;
   if (p.num_seqs > 32) any = find_many<kThreads>(p, work, me, blockIdx.x == 0, sh.work, &found);
   else if (warp == kScheduleWarp) any = find_few(p, work, me, blockIdx.x == 0, lane, &found);
-  const Shares shares(found.total, any ? sharers(found.total, p.pairs) : 1);
-  int64_t u = any ? shares.start(me) : 0;
-  const int64_t u_end = any ? shares.start(me + 1) : 0;
-  Join join{};
-  auto next_piece = [&](Place& at, Piece* t) {
-    while (u < u_end) {
+  // (the schedule warp keeps its place in shared memory: between two pieces it copies V)
+  auto next_piece = [&](Piece* t) {
+    Place at = sh.place;
+    __syncwarp();
+    bool found_one = false;
+    while (at.u < at.u_end && !found_one) {
       const int64_t keys = work.keys(at.s, at.i), end = at.start + kTileCost + keys;
-      const int64_t r0 = u - at.start, to = min(end, u_end);
+      const int64_t r0 = at.u - at.start, to = min(end, at.u_end);
       *t = work.piece(at.s, at.n, at.kvh, at.i);
       const int all = t->count, v0 = work.visits(r0, keys, all), v1 = work.visits(to - at.start, keys, all);
-      u = to;
+      at.u = to;
       t->v0 = v0;
       t->count = v1 - v0;
       if (t->count < all) t->part = r0 > 0 ? 0 : 1;
-      if (t->part >= 0 && t->count > 0) join.there[t->part] = 1;
-      if (to < end && r0 == 0) {
-        join.last = shares.owner(end - 1);
-        join.rows = min(work.tokens.d, t->a - t->tok0) * G;
-        join.token = t->q0 + t->tok0;
-        join.head = t->kvh * G;
+      if (lane == 0 && t->part >= 0 && t->count > 0) sh.join.there[t->part] = 1;
+      if (lane == 0 && to < end && r0 == 0) {
+        sh.join.last = Shares(at.total, sharers(at.total, p.pairs)).owner(end - 1);
+        sh.join.rows = min(work.tokens.d, t->a - t->tok0) * G;
+        sh.join.token = t->q0 + t->tok0;
+        sh.join.head = t->kvh * G;
       }
       if (to == end) at.next(p, work, end);
-      if (t->count > 0 || (all == 0 && r0 == 0)) return true;
+      found_one = t->count > 0 || (all == 0 && r0 == 0);
     }
-    t->count = -1;
-    return false;
+    if (!found_one) t->count = -1;
+    if (lane == 0) sh.place = at;
+    __syncwarp();
+    return found_one;
   };
-  Place place;
   if (warp == kScheduleWarp) {
+    Place at;
+    at.u = at.u_end = 0;
+    if (any) {
+      const Shares shares(found.total, sharers(found.total, p.pairs));
+      at.total = found.total;
+      at.u = shares.start(me);
+      at.u_end = shares.start(me + 1);
+      at.find(p, work, found, at.u, lane);
+    }
+    if (lane == 0) {
+      sh.place = at;
+      sh.join = Join{};
+    }
+    __syncwarp();
     Piece t;
-    if (any) place.find(p, work, found, u, lane);
-    next_piece(place, &t);
+    next_piece(&t);
     if (lane == 0) sh.tile[0] = t;
   }
   tc::fence_before_sync();
@@ -556,8 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = g + j, sb = h % C::kS;
         const Keys keys = key_tile_of(t, j, window, sinks);
         const int key0 = keys.first;
-        bool w = carried && of_tile(sh.s_done, h) && tc::mbar_wait(&sh.noted[h % kNoted], (h / kNoted) & 1);
+        // (there before the scores: what follows from the tile alone is done in their shadow)
+        bool w = carried && tc::mbar_wait(&sh.noted[h % kNoted], (h / kNoted) & 1);
         const uint32_t paged = sh.groups[h % kNoted];
+        const bool masked = (keys.edge || paged != 0xffffu) && !idle;
+        w = w && of_tile(sh.s_done, h);
         tc::fence_after_sync();
         w = __all_sync(kFullMask, w);
         const float none = down ? INFINITY : -INFINITY;
@@ -566,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // takes no more
         const bool upper = C::kCols > 64 && keys.rows > 64;
         const int cols = upper ? C::kCols : 64;
-        if ((keys.edge || paged != 0xffffu) && !idle) {
+        if (masked) {
           // The scores that a row does not see are overwritten, in one short loop before code
           // that all tiles share.
           const int left = lim - key0 - C::kCols * half;  // columns of this thread up to the row's last,
@@ -968,45 +988,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     tc2::fewer_registers<64>();
+    // For copies of K and V: a lane looks up the page of eight keys of a tile.  Keys that lie
+    // side by side in a page are copied together, up to 64 (a box); the first lane of a box asks
+    // for it, at 80 to 100 cycles a box and block of dims, which pages of few keys make many
+    // (so K and V have a warp each).
+    const int eight = 8 * (lane & 15), box = min(1 << shift, 64);
+    const bool lead = lane < 16 && (eight & (box - 1)) == 0;
+    const int none = max(1, p.cache.num_pages * p.cache.h_kv);  // past the pages: reads as zeros
+    auto look = [&](const Piece& t, int j) {
+      const Keys k = key_tile_of(t, j, window, sinks);
+      return entry_of(t, k.first + eight, j < t.count && eight < k.rows);
+    };
+    auto rows_of = [&](const Piece& t, int j, int page) {
+      return row_of(t, key_tile_of(t, j, window, sinks).first + eight, page);
+    };
     if (warp == kScheduleWarp) {
-      // ------------------------------------------------------------ schedule
-      bool more = sh.tile[0].count >= 0;
-      for (int pass = 1; more; ++pass) {
-        Piece t;
-        more = next_piece(place, &t);
+      // ------------------------------------------------------------ schedule, copies of V
+      Piece t = sh.tile[0];
+      int g = 0, vc = 0, ve = 0;  // key tiles; those whose V was asked for, edge tiles among them
+      const uint32_t r_v = tc2::in_cta(sh.v_full, 0), r_ve = tc2::in_cta(sh.v_edge, 0);
+      if (!kFp8 && lane == 0) tc::prefetch_tmap(&tm_v);
+      for (int pass = 1; t.count >= 0 && ok; ++pass) {
+        Piece next;
+        next_piece(&next);
         if (pass >= 2 && !__all_sync(kFullMask, tc::mbar_wait(&sh.tile_empty[pass & 1], ((pass >> 1) - 1) & 1))) {
           ok = false;
           break;
         }
         if (lane == 0) {
-          sh.tile[pass & 1] = t;
+          sh.tile[pass & 1] = next;
           tc::mbar_arrive(&sh.tile_full[pass & 1]);
         }
+        int page = kFp8 ? -1 : look(t, 0);
+        for (int j = 0; !kFp8 && j < t.count; ++j) {
+          const int h = g + j, s = h % C::kSlots, e = ve % C::kSlots;
+          const Keys k = key_tile_of(t, j, window, sinks);
+          const uint32_t r = rows_of(t, j, page);
+          page = look(t, j + 1);
+          const int slot = r == ~0u ? 0 : r & ((1 << shift) - 1), z = r == ~0u ? none : (int)(r >> shift);
+          const bool mine = lead && eight < k.rows;
+          uint8_t* to = smem + C::kV + s * C::kEntry + eight * 128;
+          const uint32_t bytes = ((k.rows + box - 1) & -box) * D * 2, bar = k.edge ? r_ve + e * 8 : r_v + s * 8;
+          if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.o_done, h - C::kSlots)) != 0)) break;
+          // The bytes of both CTAs count on the even CTA's barrier, in an edge tile on one of
+          // its own that the edge warp can count through; v_full keeps step.
+          if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(k.edge ? &sh.v_edge[e] : &sh.v_full[s], bytes);
+          if (mine) {
+#pragma unroll
+            for (int kb = 0; kb < D / 128; ++kb)
+              tc2::tma_load_3d(to + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, slot, z, bar);
+          }
+          __syncwarp();
+          if (k.edge && rank == 0 && lane == 0) tc::mbar_arrive(&sh.v_full[s]);
+          vc = h + 1;
+          ve += k.edge;
+        }
+        g += t.count;
+        t = next;
       }
-      if (rank == 0 && lane == 0) joins(p)[me] = join;
+      if (rank == 0 && lane == 0) joins(p)[me] = sh.join;
+      // Copies still in flight land before the CTA ends: after an expired wait, the
+      // even CTA's barriers tell of both CTAs' copies.
+      if (!kFp8 && lane == 0 && rank == 0) {
+        for (int h = max(0, vc - C::kSlots); h < vc; ++h) ok = of_tile(sh.v_full, h) && ok;
+        for (int e = max(0, ve - C::kSlots); e < ve; ++e) ok = of_tile(sh.v_edge, e) && ok;
+      }
     } else if (warp == kTmaWarp) {
-      // ------------------------------------------------------------ copies
+      // ------------------------------------------------------------ copies of Q and K
       Piece t;
       int g = 0, used = 0;  // key tiles, pieces with Q so far
-      int kc = 0, vc = 0;   // key tiles whose K, V were asked for
-      int ve = 0;           // edge tiles among the latter
-      const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0);
-      const uint32_t r_ve = tc2::in_cta(sh.v_edge, 0), r_q = tc2::in_cta(&sh.q_full, 0);
+      int kc = 0;           // key tiles whose K was asked for
+      const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_q = tc2::in_cta(&sh.q_full, 0);
       if (lane == 0) {
         tc::prefetch_tmap(&tm_q);
-        if (!kFp8) {
-          tc::prefetch_tmap(&tm_k);
-          tc::prefetch_tmap(&tm_v);
-        }
+        if (!kFp8) tc::prefetch_tmap(&tm_k);
       }
-      // A lane below 16 looks after eight keys of a tile; the first one of those that lie
-      // side by side in a page copies them (up to 64: a box).
-      const int eight = 8 * (lane & 15), box = min(1 << shift, 64);
-      const bool lead = lane < 16 && (eight & (box - 1)) == 0;
-      const int run = min(1 << shift, kKeys);  // keys of a tile that lie side by side
-      const int none = max(1, p.cache.num_pages * p.cache.h_kv);  // past the pages: reads as zeros
       for (int pass = 0; next_tile(pass, &t); ++pass) {
         if (t.count == 0) continue;
+        int page = look(t, 0);
         if (used > 0) ok = __all_sync(kFullMask, tc::mbar_wait(&sh.q_empty, (used - 1) & 1)) != 0;
         if (!ok) break;
         if (lane == 0) {
@@ -1016,102 +1075,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++used;
-        auto look = [&](int j) {
+        for (int j = 0; j < t.count && ok; ++j) {
+          const int h = g + j, s = h % C::kSlots;
           const Keys k = key_tile_of(t, j, window, sinks);
-          return entry_of(t, k.first + eight, j < t.count && eight < k.rows);
-        };
-        auto rows_of = [&](int j, int page) {
-          return j < t.count ? row_of(t, key_tile_of(t, j, window, sinks).first + eight, page) : ~0u;
-        };
-        if (kFp8) {
-          // The rows of key tiles to come are brought into L2, K's by the even CTA, V's by the
-          // other, kAhead tiles before the warps that widen them.  (They say where they are in
-          // a number: this warp keeps nobody waiting, so that a barrier's phases might pass it by.)
-          int far = look(1);
-          for (int j = 1; j < t.count && ok; ++j) {
-            const uint32_t r = rows_of(j, far);
-            far = look(j + 1);
+          const uint32_t r = rows_of(t, j, page);
+          page = look(t, j + 1);
+          if (kFp8) {
+            // The rows of key tiles to come are brought into L2, K's by the even CTA, V's by the
+            // other, kAhead tiles before the warps that widen them.  (They say where they are in
+            // a number: this warp keeps nobody waiting, so that a barrier's phases might pass it by.)
             const uint64_t since = tc::globaltimer_ns();
-            while (*const_cast<volatile int*>(&sh.begun) < g + j - kAhead) {
+            while (*const_cast<volatile int*>(&sh.begun) < h - kAhead) {
               __nanosleep(200);
               if (tc::globaltimer_ns() - since > 1000000000ull) {
                 ok = false;
                 break;
               }
             }
+            const int run = min(1 << shift, kKeys);  // keys of a tile that lie side by side
             // (the exponent bytes too: eight at a time, K's by lanes 0 to 15)
             if (rank == 0 && r != ~0u) prefetch_line((lane < 16 ? p.cache.k_exp : p.cache.v_exp) + r);
             if (lane < 16 && (eight & (run - 1)) == 0 && r != ~0u)
               tc::prefetch_l2(static_cast<const uint8_t*>(rank == 0 ? p.cache.k_pages : p.cache.v_pages) + (int64_t)r * D, run * D);
             ok = __all_sync(kFullMask, ok) != 0;
-          }
-          g += t.count;
-          if (!ok) break;
-          continue;
-        }
-        uint32_t at[3] = {rows_of(0, look(0)), ~0u, ~0u};  // of key tiles j, j - 1, j - 2
-        int page = look(1);
-        for (int j = 0; j < t.count + C::kLag && ok; ++j) {
-          const uint32_t ahead = rows_of(j + 1, page);
-          page = look(j + 2);
-          if (j < t.count) {
-            const int h = g + j, s = h % C::kSlots;
-            const Keys k = key_tile_of(t, j, window, sinks);
+          } else {
+            const int slot = r == ~0u ? 0 : r & ((1 << shift) - 1), z = r == ~0u ? none : (int)(r >> shift);
+            const bool mine = lead && eight < k.rows && (lane >> 3) == (int)rank;
+            uint8_t* to = smem + C::kK + s * C::kEntry + (lane & 7) * 1024;
+            const uint32_t bytes = ((k.rows + box - 1) & -box) * D * 2;
             if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.s_done, h - C::kSlots)) != 0)) break;
-            const bool wanted = eight < k.rows, missing = wanted && at[0] == ~0u;
-            note(h, missing);
-            const uint32_t bytes = __popc(__ballot_sync(kFullMask, lead && wanted)) * box * D * 2;
             // the bytes of both CTAs count on the even CTA's barrier
             if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh.k_full[s], bytes);
-            if (lead && wanted && (lane >> 3) == (int)rank) {
-              const int slot = missing ? 0 : at[0] & ((1 << shift) - 1), z = missing ? none : (int)(at[0] >> shift);
+            if (mine) {
 #pragma unroll
-              for (int kb = 0; kb < D / 64; ++kb)
-                tc2::tma_load_3d(smem + C::kK + s * C::kEntry + kb * 8192 + (lane & 7) * 1024, &tm_k, 64 * kb, slot, z,
-                                 r_k + s * 8);
+              for (int kb = 0; kb < D / 64; ++kb) tc2::tma_load_3d(to + kb * 8192, &tm_k, 64 * kb, slot, z, r_k + s * 8);
             }
             __syncwarp();
+            note(h, eight < k.rows && r == ~0u);
             kc = h + 1;
           }
-          const int i = j - C::kLag;
-          if (i >= 0) {
-            const int h = g + i, s = h % C::kSlots;
-            const Keys k = key_tile_of(t, i, window, sinks);
-            if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.o_done, h - C::kSlots)) != 0)) break;
-            const bool wanted = eight < k.rows, missing = at[C::kLag] == ~0u;
-            const uint32_t bytes = __popc(__ballot_sync(kFullMask, lead && wanted)) * box * D * 2;
-            // So do those of V, in an edge tile on a barrier of its own that the edge warp can
-            // count through; v_full keeps step.
-            const int e = ve % C::kSlots;
-            if (rank == 0 && lane == 0) {
-              tc::mbar_arrive_expect_tx(k.edge ? &sh.v_edge[e] : &sh.v_full[s], bytes);
-              if (k.edge) tc::mbar_arrive(&sh.v_full[s]);
-            }
-            if (lead && wanted) {
-              const int slot = missing ? 0 : at[C::kLag] & ((1 << shift) - 1);
-              const int z = missing ? none : (int)(at[C::kLag] >> shift);
-#pragma unroll
-              for (int kb = 0; kb < D / 128; ++kb)
-                tc2::tma_load_3d(smem + C::kV + s * C::kEntry + kb * 16384 + eight * 128, &tm_v,
-                                 (int)rank * (D / 2) + 64 * kb, slot, z, k.edge ? r_ve + e * 8 : r_v + s * 8);
-            }
-            __syncwarp();
-            vc = h + 1;
-            ve += k.edge;
-          }
-          at[2] = at[1];
-          at[1] = at[0];
-          at[0] = ahead;
         }
         g += t.count;
         if (!ok) break;
       }
-      // Copies still in flight land before the CTA ends: after an expired wait, the
-      // even CTA's barriers tell of both CTAs' copies.
-      if (lane == 0 && rank == 0) {
+      if (lane == 0 && rank == 0) {  // (as for V)
         for (int h = max(0, kc - C::kSlots); h < kc; ++h) ok = of_tile(sh.k_full, h) && ok;
-        for (int h = max(0, vc - C::kSlots); h < vc; ++h) ok = of_tile(sh.v_full, h) && ok;
-        for (int e = max(0, ve - C::kSlots); e < ve; ++e) ok = of_tile(sh.v_edge, e) && ok;
         if (used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
       }
     } else if (warp == kMmaWarp) {
