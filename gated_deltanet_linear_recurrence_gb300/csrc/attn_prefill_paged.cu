@@ -21,7 +21,7 @@ constexpr int kRows = 128;          // rows a CTA
 constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14, kEdgeWarp = 15;
 constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
-constexpr int kConverters = 4;       // warps of a CTA that write an e4m3 tile's K or V
+constexpr int kWideners = 2;         // warps of a CTA that write K of an e4m3 tile, or V
 constexpr int kNoted = 8;            // key tiles whose missing pages are noted
 constexpr int kAhead = 6;            // key tiles that e4m3 rows are brought into L2 ahead
 
@@ -38,10 +38,12 @@ struct Cfg {
   static constexpr int kS = D == 256 ? 2 : 3;
   static constexpr int kLag = kS - 1;  // key tiles that the scores are ahead of P V
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
-  static constexpr int kSoftmaxRegs = D == 256 ? 168 : kFp8 ? 176 : 184;
-  static constexpr int kEpilogueRegs = 512 - 64 - 2 * kSoftmaxRegs;
+  // Registers of a thread of the four warpgroups: softmax (two), epilogue, and the rest;
+  // together the 65,536 that the CTA starts with.
+  static constexpr int kSoftmaxRegs = kFp8 ? 160 : 168, kEpilogueRegs = kFp8 ? 112 : 88;
+  static constexpr int kOtherRegs = 512 - 2 * kSoftmaxRegs - kEpilogueRegs;
   // columns of O that the epilogue holds (over e4m3 rows beside what widening them needs)
-  static constexpr int kOut = kFp8 ? 16 * (D / 128) : D == 256 ? 64 : 32;
+  static constexpr int kOut = 32;
   static constexpr uint32_t kQBytes = kRows * D * 2;
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
   static constexpr int kSlots = D == 256 ? 2 : 4;  // key tiles of K, and of V, in shared memory
@@ -61,9 +63,9 @@ struct Seq {
 };
 // One piece of a pair's work: keys of a tile of queries; count < 0 ends the schedule
 struct Piece {
-  int32_t q0, a, off;
+  int32_t token, left;  // first row of q of the pair's; queries of the sequence from there
+  int32_t pos;          // its position (may be < 0)
   int32_t seq, kvh;
-  int32_t tok0;        // first token of the pair's rows
   int32_t sight;       // keys that the last row sees (its position + 1)
   int32_t firsts, w0;  // key tiles that hold the first keys; number of the window's first one
   int32_t v0, count;   // key tiles to go through, of both in this order
@@ -120,14 +122,14 @@ struct Work {
   }
   __device__ __forceinline__ Piece piece(const Seq& s, int seq, int kvh, int i) const {
     Piece t;
-    t.q0 = s.q0;
-    t.a = s.a;
-    t.off = s.off;
+    const int first = i * tokens.d;
+    t.token = s.q0 + first;
+    t.left = s.a - first;
+    t.pos = s.off + first;
     t.seq = seq;
     t.kvh = kvh;
-    t.tok0 = i * tokens.d;
-    t.sight = max(0, s.off + t.tok0 + min(s.a - t.tok0, tokens.d));
-    const int lo = window ? (int)max((int64_t)0, s.off + t.tok0 + 1 - window) : 0;
+    t.sight = max(0, t.pos + min(t.left, tokens.d));
+    const int lo = window ? (int)max((int64_t)0, t.pos + 1 - window) : 0;
     t.w0 = lo / kKeys;
     t.firsts = (int)min((int64_t)t.w0, ((int64_t)sinks + kKeys - 1) / kKeys);
     t.v0 = 0;
@@ -280,7 +282,7 @@ __device__ __forceinline__ Keys key_tile_of(const Piece& t, int j, int window, i
   const bool firsts = v < t.firsts;
   k.first = (firsts ? v : t.w0 + v - t.firsts) * kKeys;
   k.rows = min(kKeys, (firsts ? sinks : t.sight) - k.first);
-  const int whole = t.off + t.tok0 + 1;  // keys that every row sees, but for the window
+  const int whole = t.pos + 1;  // keys that every row sees, but for the window
   const int low = window ? max(0, t.sight - window) : 0;  // first key of the last row's window
   k.edge = k.first + kKeys > whole || max(k.first, sinks) < min(k.first + kKeys, low);
   return k;
@@ -289,7 +291,7 @@ __device__ __forceinline__ Keys key_tile_of(const Piece& t, int j, int window, i
 __device__ __forceinline__ int edge_row(const Piece& t, const Keys& k, int window, int sinks) {
   const int low = window ? max(0, t.sight - window) : 0;
   if (max(k.first, sinks) < min(k.first + kKeys, low)) return 0;
-  return max(0, t.off + t.tok0 + 1 - k.first) & ~15;
+  return max(0, t.pos + 1 - k.first) & ~15;
 }
 __device__ __forceinline__ uint32_t lowest(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 
@@ -310,7 +312,7 @@ struct Shared {  // beside the tiles
   uint64_t flags_in[4];
   uint32_t poison[4];
   uint64_t tile_full[2], tile_empty[2], drained;
-  Piece tile[2], late[kConverters];
+  Piece tile[2], late[4];
   uint32_t tmem;
   Sums work;
   Place place;
@@ -322,7 +324,7 @@ struct Shared {  // beside the tiles
   float red[2][2][128];
   float sums[2][2][128];  // row sums of two pieces, in two parts
   float refs[2][128];     // and the references that they go by
-  alignas(16) uint8_t bytes[kConverters][2][32];  // e4m3: exponent bytes of a warp's four eights, two items
+  alignas(16) uint8_t bytes[4][2][32];  // e4m3: exponent bytes of a warp's four eights, two items
 };
 
 // 16 bytes, or zeros; without a branch, behind which the value would be waited for
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       // (e4m3: the even CTA's hear of the other one's warps from its products' warp)
-      const int full = kFp8 ? kConverters + (rank == 0 ? 1 : 0) : 1;
+      const int full = kFp8 ? kWideners + (rank == 0 ? 1 : 0) : 1;
       tc::mbar_init(&sh.k_full[i], full);
       tc::mbar_init(&sh.v_full[i], full);
       tc::mbar_init(&sh.s_done[i], 1);
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kNoted; ++i) tc::mbar_init(&sh.noted[i], 1);
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&sh.v_edge[i], kFp8 ? kConverters + (rank == 0 ? 1 : 0) : 1);
+      tc::mbar_init(&sh.v_edge[i], kFp8 ? kWideners + (rank == 0 ? 1 : 0) : 1);
       tc::mbar_init(&sh.v_clean[i], 1);
     }
     sh.begun = 0;
@@ -465,8 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && t->part >= 0 && t->count > 0) sh.join.there[t->part] = 1;
       if (lane == 0 && to < end && r0 == 0) {
         sh.join.last = Shares(at.total, sharers(at.total, p.pairs)).owner(end - 1);
-        sh.join.rows = min(work.tokens.d, t->a - t->tok0) * G;
-        sh.join.token = t->q0 + t->tok0;
+        sh.join.rows = min(work.tokens.d, t->left) * G;
+        sh.join.token = t->token;
         sh.join.head = t->kvh * G;
       }
       if (to == end) at.next(p, work, end);
@@ -562,9 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // all softmax warps go on or none: they meet at barriers without a limit
       const bool more = next_tile(pass, &t);
       if (!(ok = tc::named_sync_and(kBarSoftmax, kSoftmaxThreads, ok && carried)) || !more) break;
-      const int tok = t.tok0 + (int)rank * tok_cta + row / G;
-      const bool real = row < tok_cta * G && tok < t.a;
-      const int lim = real ? max(0, t.off + tok + 1) : 0;   // keys this row sees,
+      const int tok = (int)rank * tok_cta + row / G;
+      const bool real = row < tok_cta * G && tok < t.left;
+      const int lim = real ? max(0, t.pos + tok + 1) : 0;   // keys this row sees,
       const int low = window ? max(0, lim - window) : 0;  // from this one, and the first ones
       const bool idle = !__any_sync(kFullMask, real);  // no queries: their P may be anything
       float m = -INFINITY, l = 0.f;
@@ -731,13 +733,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = smem + C::kStage + wq * 4096;
     // O of piece t, the used'th with keys, whose last key tile is h
     auto epilogue = [&](const Piece t, int used, int h) {
-      const int tok0 = t.tok0 + (int)rank * tok_cta;
-      const int rows = min(tok_cta, t.a - tok0) * G - wq * 32;  // that are there, of the warp's
+      const int tok0 = (int)rank * tok_cta;
+      const int rows = min(tok_cta, t.left - tok0) * G - wq * 32;  // that are there, of the warp's
       const bool real = lane < rows;
-      const int lim = real ? max(0, t.off + tok0 + row / G + 1) : 0;  // keys this row sees
+      const int lim = real ? max(0, t.pos + tok0 + row / G + 1) : 0;  // keys this row sees
       const int low = window ? max(0, lim - window) : 0;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
-                           (((int64_t)t.q0 + tok0) * p.h_q + (int64_t)t.kvh * G) * D + (lane & 7) * 8;
+                           (((int64_t)t.token + tok0) * p.h_q + (int64_t)t.kvh * G) * D + (lane & 7) * 8;
       int32_t to[8];  // which row of o rows 4 i + lane / 8 of the warp's are, from the first one
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -855,124 +857,116 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // The warps of both CTAs widen K and V into shared memory: an eight of keys x 64
-      // dims at a time, which is a whole swizzle atom, in the order in which the products
-      // take them, the next ones' codes on their way meanwhile.  The epilogue of a piece
-      // follows the first V of the next one.
+      // Two warps of each CTA widen its half of K, two that of V: an eight of keys x 64 dims
+      // at a time, which is a whole swizzle atom, the next ones' codes on their way meanwhile.
+      // The epilogue of a piece follows the first tiles of the next one.
+      const bool is_v = wq >= 2;
+      const int w2 = wq & 1;
+      const int eight = 8 * (lane & 15);
       // within an atom: row, and which 16 of its 64 codes, such that eight lanes' stores
       // fall into different banks
       const int r8 = ((lane >> 1) & 1) | ((lane >> 2) & 2) | (lane & 4), c4 = (lane & 1) | ((lane >> 3) & 2);
       const uint32_t put = r8 * 128 + (((2 * c4) ^ r8) << 4), put2 = r8 * 128 + (((2 * c4 + 1) ^ r8) << 4);
-      // A warp's part of K or of V: four eights, D / 128 blocks of 64 dims.  Of K's 64 keys two
-      // warps share the eights and two the blocks; of V's 128 the four share the eights.
+      // A warp's part of a key tile in two halves of four eights x D / 128 blocks of 64 dims:
+      // of K (64 keys, D dims) every second eight, half of the blocks; of V (128 keys, D / 2
+      // dims) half of every second eight, all blocks.
       constexpr int kBlocks = D / 128;
-      const uint8_t* k_codes = static_cast<const uint8_t*>(p.cache.k_pages) + r8 * D + 16 * c4 + (wq >> 1) * (64 * kBlocks);
-      const uint8_t* v_codes = static_cast<const uint8_t*>(p.cache.v_pages) + r8 * D + 16 * c4 + rank * (D / 2);
-      const int k_eight = 8 * (int)rank + (wq & 1);  // and every second one; of V wq and every fourth
-      struct Item {      // a part of a key tile
-        bool v, there;
-        uint32_t rows;   // cached row of the lane's eight (lane & 15 of the tile)
-      };
+      const uint8_t* codes = static_cast<const uint8_t*>(is_v ? p.cache.v_pages : p.cache.k_pages) + r8 * D + 16 * c4 +
+                             (is_v ? rank * (D / 2) : 0);
+      const uint8_t* exps = is_v ? p.cache.v_exp : p.cache.k_exp;
+      const int eight0 = (is_v ? 0 : 8 * (int)rank) + w2, eight_half = is_v ? 8 : 0, dims_half = is_v ? 0 : 64 * kBlocks;
+      uint8_t* const to_warp = smem + (is_v ? C::kV : C::kK) + w2 * 1024;
+      const int to_block = is_v ? 16384 : 8192, to_half = is_v ? 8192 : 8192 * kBlocks;
+      uint64_t* const free_bar = is_v ? sh.o_done : sh.s_done;
+      uint64_t* const full_bar = is_v ? sh.v_full : sh.k_full;
+      uint8_t(*bytes)[32] = sh.bytes[wq];  // exponent bytes of the half's four eights, two halves
       uint4 x[4][kBlocks];
       uint32_t row[4];  // cached rows of the eights being loaded
-      // The rows of an item, and its exponent bytes on their way into shared memory (in
-      // registers, which are handed from item to item, they would be waited for).
-      uint8_t(*bytes)[32] = sh.bytes[wq];
-      auto begin = [&](const Item& it, int parity) {
-        const uint32_t mine = __shfl_sync(kFullMask, it.rows, it.v ? wq + 4 * (lane & 3) : k_eight + 2 * (lane & 3));
-        if (lane < 4)
-          copy8(&bytes[parity][8 * lane], (it.v ? p.cache.v_exp : p.cache.k_exp) + (int64_t)mine, it.there && mine != ~0u);
+      // The rows of a half, and its exponent bytes on their way into shared memory (in
+      // registers, which are handed on, they would be waited for).
+      auto begin = [&](uint32_t rows, int half, int parity) {
+        const uint32_t mine = __shfl_sync(kFullMask, rows, eight0 + eight_half * half + 2 * (lane & 3));
+        if (lane < 4) copy8(&bytes[parity][8 * lane], exps + (int64_t)mine, mine != ~0u);
         copy_commit();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t r = __shfl_sync(kFullMask, mine, e);
-          row[e] = it.there ? r : ~0u;
-        }
+        for (int e = 0; e < 4; ++e) row[e] = __shfl_sync(kFullMask, mine, e);
       };
-      auto load = [&](const uint8_t* codes, int e, int b) { return load_if(codes + (int64_t)row[e] * D + 64 * b, row[e] != ~0u); };
+      auto load = [&](int half, int e, int b) { return load_if(codes + (int64_t)row[e] * D + 64 * b + half * dims_half, row[e] != ~0u); };
+      auto load_all = [&](int half) {
+#pragma unroll
+        for (int n = 0; n < 4 * kBlocks; ++n) x[n / kBlocks][n % kBlocks] = load(half, n / kBlocks, n % kBlocks);
+      };
       int late_used = 0, late_h = 0, parity = 0, ve = 0;  // (ve: edge tiles so far)
       bool due = false;
       for (int pass = 0; ok; ++pass) {
         const bool more = next_tile(pass, &t);
         if (!ok) break;
-        const int count = more ? t.count : 0, steps = count > 0 ? count + C::kLag : 0;
+        const int count = more ? t.count : 0;
         // the page of the lane's eight of key tile j, and their cached rows
         auto look = [&](int j) {
           const Keys k = key_tile_of(t, j, window, sinks);
-          return entry_of(t, k.first + 8 * (lane & 15), j < count && 8 * (lane & 15) < k.rows);
+          return entry_of(t, k.first + eight, j < count && eight < k.rows);
         };
-        auto rows_of = [&](int j, int page) {
-          return j < count ? row_of(t, key_tile_of(t, j, window, sinks).first + 8 * (lane & 15), page) : ~0u;
-        };
-        uint32_t at[3] = {rows_of(0, look(0)), ~0u, ~0u};  // of key tiles j, j - 1, j - 2
+        auto rows_of = [&](int j, int page) { return row_of(t, key_tile_of(t, j, window, sinks).first + eight, page); };
+        uint32_t rows = rows_of(0, look(0));
         int page = look(1);
-        Item it{false, count > 0, at[0]};
-        begin(it, parity);
-#pragma unroll
-        for (int n = 0; n < 4 * kBlocks; ++n) x[n / kBlocks][n % kBlocks] = load(k_codes, n / kBlocks, n % kBlocks);
+        copy_wait<0>();  // (the last bytes, of no row, into the same place)
+        begin(rows, 0, parity);
+        load_all(0);
         for (int j = 0; ok; ++j) {
-          const uint32_t ahead = rows_of(j + 1, page);
-          page = look(j + 2);
-#pragma unroll 1
-          for (int v = j < count ? 0 : 1; v < (j >= C::kLag && j < steps ? 2 : 1); ++v) {
-            const int i = v ? j - C::kLag : j, h = g + i, s = h % C::kSlots;
-            Item next;  // V of kLag tiles before, the next K, or the next V where there is no more K
-            if (!v && j >= C::kLag) next = Item{true, true, at[C::kLag]};
-            else if (j + 1 < count) next = Item{false, true, ahead};
-            else if (!v) next = Item{true, true, j == 0 ? at[0] : at[1]};
-            else next = Item{true, i + 1 < count, at[C::kLag - 1]};
-            begin(next, parity ^ 1);
-            const uint8_t* codes = next.v ? v_codes : k_codes;
-            const bool w = h < C::kSlots || of_tile(v ? sh.o_done : sh.s_done, h - C::kSlots);
-            if (!(ok = __all_sync(kFullMask, w) != 0)) break;
-            if (!v && wq == 0) {  // (for the first warp to say)
-              note(h, 8 * (lane & 15) < key_tile_of(t, j, window, sinks).rows && at[0] == ~0u);
+          const int h = g + j, s = h % C::kSlots;
+          if (j < count) {
+            const uint32_t ahead = rows_of(j + 1, page);
+            page = look(j + 2);
+            const Keys keys = key_tile_of(t, j, window, sinks);
+            if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(free_bar, h - C::kSlots)) != 0)) break;
+            if (wq == 0) {  // (for the first warp to say)
+              note(h, eight < keys.rows && rows == ~0u);
               if (lane == 0) *const_cast<volatile int*>(&sh.begun) = h + 1;
             }
-            copy_wait<1>();
-            __syncwarp();
-            uint32_t byte[4];  // (ahead of the stores, which they might be taken to depend on)
+            uint8_t* to = to_warp + s * C::kEntry;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              copy_wait<0>();
+              __syncwarp();
+              uint32_t byte[4];  // (ahead of the stores, which they might be taken to depend on)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) byte[e] = bytes[parity][8 * e + r8];
-            uint8_t* to_slot = smem + s * C::kEntry + (v ? C::kV + wq * 1024 : C::kK + (wq & 1) * 1024 + (wq >> 1) * (8192 * kBlocks));
-            const int next_eight = v ? 4096 : 2048, next_block = v ? 16384 : 8192;
+              for (int e = 0; e < 4; ++e) byte[e] = bytes[parity][8 * e + r8];
+              parity ^= 1;
+              begin(half ? ahead : rows, half ^ 1, parity);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+              for (int e = 0; e < 4; ++e)
 #pragma unroll
-              for (int b = 0; b < kBlocks; ++b) {
-                uint4 lo, hi;
-                widen16(x[e][b], byte[e], lo, hi);
-                uint8_t* atom = to_slot + e * next_eight + b * next_block;
-                *reinterpret_cast<uint4*>(atom + put) = lo;
-                *reinterpret_cast<uint4*>(atom + put2) = hi;
-                x[e][b] = load(codes, e, b);
-              }
+                for (int b = 0; b < kBlocks; ++b) {
+                  uint4 lo, hi;
+                  widen16(x[e][b], byte[e], lo, hi);
+                  uint8_t* atom = to + e * 2048 + b * to_block;
+                  *reinterpret_cast<uint4*>(atom + put) = lo;
+                  *reinterpret_cast<uint4*>(atom + put2) = hi;
+                  x[e][b] = load(half ^ 1, e, b);
+                }
+              to += to_half;
+            }
             tc::fence_proxy_async();  // the rows -> this CTA's tensor cores
             __syncwarp();
-            const bool edge = v && key_tile_of(t, i, window, sinks).edge;
+            const bool edge = is_v && keys.edge;
             if (lane == 0) {
               if (edge) tc::mbar_arrive(&sh.v_edge[ve % C::kSlots]);
-              tc::mbar_arrive(v ? &sh.v_full[s] : &sh.k_full[s]);
+              tc::mbar_arrive(&full_bar[s]);
             }
             ve += edge;
-            it = next;
-            parity ^= 1;
+            rows = ahead;
           }
-          if (!ok) break;
-          if (due && j == min(C::kLag, steps)) {
+          if (due && j == min(is_v ? 0 : C::kLag, max(0, count - 1))) {
             epilogue(sh.late[wq], late_used, late_h);
             due = false;
             // (again: kept over the epilogue, they would have to leave the registers, and every
             // load would be waited for)
-            begin(it, parity);
-#pragma unroll
-            for (int n = 0; n < 4 * kBlocks; ++n)
-              x[n / kBlocks][n % kBlocks] = load(it.v ? v_codes : k_codes, n / kBlocks, n % kBlocks);
+            copy_wait<0>();
+            begin(rows, 0, parity);
+            load_all(0);
           }
-          if (j >= steps) break;
-          at[2] = at[1];
-          at[1] = at[0];
-          at[0] = ahead;
+          if (j + 1 >= count) break;
         }
         if (!ok || !more) break;
         if (lane == 0) sh.late[wq] = t;  // whose epilogue is due
@@ -987,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    tc2::fewer_registers<64>();
+    tc2::fewer_registers<C::kOtherRegs>();
     // For copies of K and V: a lane looks up the page of eight keys of a tile.  Keys that lie
     // side by side in a page are copied together, up to 64 (a box); the first lane of a box asks
     // for it, at 80 to 100 cycles a box and block of dims, which pages of few keys make many
@@ -1071,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           if (rank == 0) tc::mbar_arrive_expect_tx(&sh.q_full, 2u * (uint32_t)(tok_cta * G) * D * 2);
           for (int kb = 0; kb < D / 64; ++kb)
-            tc2::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G, t.q0 + t.tok0 + (int)rank * tok_cta, r_q);
+            tc2::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G, t.token + (int)rank * tok_cta, r_q);
         }
         __syncwarp();
         ++used;
