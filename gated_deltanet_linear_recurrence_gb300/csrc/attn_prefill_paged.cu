@@ -344,13 +344,6 @@ __device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other
                : "l"(src), "r"((int)valid), "r"(other));
   return x;
 }
-// bytes 0 and 1 (kUpper: 2 and 3) of a word as two 16-bit integers, with their signs
-template <bool kUpper>
-__device__ __forceinline__ uint32_t signed_halves(uint32_t w) {
-  uint32_t y;
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w), "n"(kUpper ? 0xb3a2 : 0x9180));
-  return y;
-}
 __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // 8 bytes from global to shared memory; zeros when !valid (nothing is read)
 __device__ __forceinline__ void copy8(const void* dst, const void* src, bool valid) {
@@ -362,32 +355,36 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Sixteen e4m3 codes of a row, times its unit, as bf16 (exact, and NaN for a NaN code).
-__device__ __forceinline__ void widen16(const uint4& x, uint32_t byte, uint4& lo, uint4& hi) {
+// bytes 0 and 1 (kUpper: 2 and 3) of a word as two 16-bit integers, with their signs
+template <bool kUpper>
+__device__ __forceinline__ uint32_t signed_halves(uint32_t w) {
+  uint32_t y;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w), "n"(kUpper ? 0xb3a2 : 0x9180));
+  return y;
+}
+// Sixteen e4m3 codes of a row, times its unit (up to 2^7 of it), as bf16 (exact).  A NaN code
+// comes out as 480 units and raises the top bit of a byte of `odd`: see mend.
+__device__ __forceinline__ void widen16(const uint4& x, uint32_t unit, uint4& lo, uint4& hi, uint32_t& odd) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  const uint32_t unit = value_units(byte, byte);
-  uint32_t y[8], nan = 0;
+  uint32_t y[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;  // the top bit of a byte for a NaN code
+    odd |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
     // two codes with their signs above them, shifted into place
     y[2 * i] = times((signed_halves<false>(w[i]) << 4) & (kMagnitude | kSigns), unit);
     y[2 * i + 1] = times((signed_halves<true>(w[i]) << 4) & (kMagnitude | kSigns), unit);
   }
-  if (byte > kUnitTop) {  // the rest of a unit above 2^7
-    const uint32_t rest = (byte - kUnitTop + 127) << 7;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = times(y[i], rest | (rest << 16));
-  }
-  if (nan & 0x80808080u) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[2 * i] |= nan_where((signed_halves<false>(w[i]) << 4) & kMagnitude);
-      y[2 * i + 1] |= nan_where((signed_halves<true>(w[i]) << 4) & kMagnitude);
-    }
-  }
   lo = make_uint4(y[0], y[1], y[2], y[3]);
   hi = make_uint4(y[4], y[5], y[6], y[7]);
+}
+// Eight of those where a NaN code or a unit above 2^7 has been seen: NaN for 480 units, and
+// the rest of the unit.
+__device__ __forceinline__ uint4 mend(const uint4& x, uint32_t byte) {
+  const uint32_t nan = times(kMagnitude, value_units(byte, byte));
+  uint32_t rest = byte > kUnitTop ? (byte - kUnitTop + 127) << 7 : 127u << 7;
+  rest |= rest << 16;
+  auto two = [&](uint32_t y) { return times(y, rest) | (__vcmpeq2(y & ~kSigns, nan) & 0x7fc07fc0u); };
+  return make_uint4(two(x.x), two(x.y), two(x.z), two(x.w));
 }
 
 template <int D, bool kFp8>
@@ -934,17 +931,30 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 4; ++e) byte[e] = bytes[parity][8 * e + r8];
               parity ^= 1;
               begin(half ? ahead : rows, half ^ 1, parity);
+              uint32_t odd = 0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t unit = value_units(byte[e], byte[e]);
+                odd |= byte[e] > kUnitTop ? 0x80u : 0u;
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                   uint4 lo, hi;
-                  widen16(x[e][b], byte[e], lo, hi);
+                  widen16(x[e][b], unit, lo, hi, odd);
                   uint8_t* atom = to + e * 2048 + b * to_block;
                   *reinterpret_cast<uint4*>(atom + put) = lo;
                   *reinterpret_cast<uint4*>(atom + put2) = hi;
                   x[e][b] = load(half ^ 1, e, b);
                 }
+              }
+              if (odd & 0x80808080u) {  // in a loop of its own, as it hardly ever runs
+#pragma unroll 1
+                for (int n = 0; n < 4 * kBlocks; ++n) {
+                  uint8_t* atom = to + n / kBlocks * 2048 + n % kBlocks * to_block;
+                  const uint32_t b = bytes[parity ^ 1][8 * (n / kBlocks) + r8];
+                  *reinterpret_cast<uint4*>(atom + put) = mend(*reinterpret_cast<const uint4*>(atom + put), b);
+                  *reinterpret_cast<uint4*>(atom + put2) = mend(*reinterpret_cast<const uint4*>(atom + put2), b);
+                }
+              }
               to += to_half;
             }
             tc::fence_proxy_async();  // the rows -> this CTA's tensor cores
