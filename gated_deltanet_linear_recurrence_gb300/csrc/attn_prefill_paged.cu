@@ -324,19 +324,10 @@ struct Shared {  // beside the tiles
   float red[2][2][128];
   float sums[2][2][128];  // row sums of two pieces, in two parts
   float refs[2][128];     // and the references that they go by
-  alignas(16) uint8_t bytes[4][2][32];  // e4m3: exponent bytes of a warp's four eights, two items
+  alignas(16) uint8_t bytes[4][2][64];  // e4m3: exponent bytes of a warp's eights, two key tiles
 };
 
-// 16 bytes, or zeros; without a branch, behind which the value would be waited for
-__device__ __forceinline__ uint4 load_if(const void* src, bool valid) {
-  uint4 x;
-  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
-      : "l"(src), "r"((int)valid));
-  return x;
-}
+// a table's entry, or another value; without a branch, behind which it would be waited for
 __device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other) {
   int x;
   asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
@@ -348,6 +339,10 @@ __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("pre
 // 8 bytes from global to shared memory; zeros when !valid (nothing is read)
 __device__ __forceinline__ void copy8(const void* dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(valid ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(const void* dst, const void* src, bool valid) {  // the same of 16
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0)
                : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -864,34 +859,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       // fall into different banks
       const int r8 = ((lane >> 1) & 1) | ((lane >> 2) & 2) | (lane & 4), c4 = (lane & 1) | ((lane >> 3) & 2);
       const uint32_t put = r8 * 128 + (((2 * c4) ^ r8) << 4), put2 = r8 * 128 + (((2 * c4 + 1) ^ r8) << 4);
-      // A warp's part of a key tile in two halves of four eights x D / 128 blocks of 64 dims:
-      // of K (64 keys, D dims) every second eight, half of the blocks; of V (128 keys, D / 2
-      // dims) half of every second eight, all blocks.
-      constexpr int kBlocks = D / 128;
+      // A warp's part of a key tile is D / 64 groups of four atoms: of K (64 keys, D dims) every
+      // second eight, a block of 64 dims a group; of V (128 keys, D / 2 dims) every second eight
+      // too, four of those and a block a group.  A group's code is all there is to loop over:
+      // with eight atoms in it, and their codes in registers, instructions came from L2 (64 KB
+      // of code in the SM's way; 446 us for 2,000 tokens on 11,011).
+      constexpr int kGroupsOf = D / 64, kBlocks = D / 128;
       const uint8_t* codes = static_cast<const uint8_t*>(is_v ? p.cache.v_pages : p.cache.k_pages) + r8 * D + 16 * c4 +
                              (is_v ? rank * (D / 2) : 0);
       const uint8_t* exps = is_v ? p.cache.v_exp : p.cache.k_exp;
-      const int eight0 = (is_v ? 0 : 8 * (int)rank) + w2, eight_half = is_v ? 8 : 0, dims_half = is_v ? 0 : 64 * kBlocks;
+      const int eight0 = (is_v ? 0 : 8 * (int)rank) + w2;
       uint8_t* const to_warp = smem + (is_v ? C::kV : C::kK) + w2 * 1024;
-      const int to_block = is_v ? 16384 : 8192, to_half = is_v ? 8192 : 8192 * kBlocks;
       uint64_t* const free_bar = is_v ? sh.o_done : sh.s_done;
       uint64_t* const full_bar = is_v ? sh.v_full : sh.k_full;
-      uint8_t(*bytes)[32] = sh.bytes[wq];  // exponent bytes of the half's four eights, two halves
-      uint4 x[4][kBlocks];
-      uint32_t row[4];  // cached rows of the eights being loaded
-      // The rows of a half, and its exponent bytes on their way into shared memory (in
-      // registers, which are handed on, they would be waited for).
-      auto begin = [&](uint32_t rows, int half, int parity) {
-        const uint32_t mine = __shfl_sync(kFullMask, rows, eight0 + eight_half * half + 2 * (lane & 3));
-        if (lane < 4) copy8(&bytes[parity][8 * lane], exps + (int64_t)mine, mine != ~0u);
+      uint8_t(*bytes)[64] = sh.bytes[wq];  // exponent bytes of the warp's eights, two key tiles
+      uint8_t* const codes_in = stage + lane * 16;  // two groups' codes, which a lane brings for itself
+      // group q of a key tile: number of its first eight among the warp's, its block
+      auto eights_of = [&](int q) { return is_v ? 4 * (q / kBlocks) : 0; };
+      auto block_of = [&](int q) { return is_v ? q % kBlocks : q; };
+      auto bring = [&](uint32_t rows, int q) {  // (always a group of copies, whether there are any)
+        const uint8_t* src = codes + 64 * block_of(q);
+        const int first = eight0 + 2 * eights_of(q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t r = __shfl_sync(kFullMask, rows, first + 2 * e);
+          copy16(codes_in + ((q & 1) * 4 + e) * 512, src + (int64_t)r * D, r != ~0u);
+        }
         copy_commit();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) row[e] = __shfl_sync(kFullMask, mine, e);
       };
-      auto load = [&](int half, int e, int b) { return load_if(codes + (int64_t)row[e] * D + 64 * b + half * dims_half, row[e] != ~0u); };
-      auto load_all = [&](int half) {
-#pragma unroll
-        for (int n = 0; n < 4 * kBlocks; ++n) x[n / kBlocks][n % kBlocks] = load(half, n / kBlocks, n % kBlocks);
+      auto bring_bytes = [&](uint32_t rows, int parity) {  // (with the group that follows)
+        const uint32_t mine = __shfl_sync(kFullMask, rows, (eight0 + 2 * lane) & 15);
+        if (lane < (is_v ? 8 : 4)) copy8(&bytes[parity][8 * lane], exps + (int64_t)mine, mine != ~0u);
       };
       int late_used = 0, late_h = 0, parity = 0, ve = 0;  // (ve: edge tiles so far)
       bool due = false;
@@ -907,9 +905,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto rows_of = [&](int j, int page) { return row_of(t, key_tile_of(t, j, window, sinks).first + eight, page); };
         uint32_t rows = rows_of(0, look(0));
         int page = look(1);
-        copy_wait<0>();  // (the last bytes, of no row, into the same place)
-        begin(rows, 0, parity);
-        load_all(0);
+        copy_wait<0>();  // (the last ones, of no row, into the same places)
+        bring_bytes(rows, parity);
+        bring(rows, 0);
+        bring(rows, 1);
         for (int j = 0; ok; ++j) {
           const int h = g + j, s = h % C::kSlots;
           if (j < count) {
@@ -921,42 +920,41 @@ __global__ void __launch_bounds__(kThreads, 1)
               note(h, eight < keys.rows && rows == ~0u);
               if (lane == 0) *const_cast<volatile int*>(&sh.begun) = h + 1;
             }
-            uint8_t* to = to_warp + s * C::kEntry;
+            uint8_t* const to_tile = to_warp + s * C::kEntry;
+            bring_bytes(ahead, parity ^ 1);
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              copy_wait<0>();
-              __syncwarp();
-              uint32_t byte[4];  // (ahead of the stores, which they might be taken to depend on)
+            for (int q = 0; q < kGroupsOf; ++q) {
+              copy_wait<1>();
+              __syncwarp();  // (the bytes are other lanes')
+              const uint8_t* byte_of = &bytes[parity][8 * eights_of(q) + r8];
+              uint8_t* to = to_tile + eights_of(q) * 2048 + block_of(q) * (is_v ? 16384 : 8192);
+              uint4 x[4];
+              uint32_t byte[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) byte[e] = bytes[parity][8 * e + r8];
-              parity ^= 1;
-              begin(half ? ahead : rows, half ^ 1, parity);
+              for (int e = 0; e < 4; ++e) {
+                x[e] = *reinterpret_cast<const uint4*>(codes_in + ((q & 1) * 4 + e) * 512);
+                byte[e] = byte_of[8 * e];
+              }
               uint32_t odd = 0;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t unit = value_units(byte[e], byte[e]);
                 odd |= byte[e] > kUnitTop ? 0x80u : 0u;
-#pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                  uint4 lo, hi;
-                  widen16(x[e][b], unit, lo, hi, odd);
-                  uint8_t* atom = to + e * 2048 + b * to_block;
-                  *reinterpret_cast<uint4*>(atom + put) = lo;
-                  *reinterpret_cast<uint4*>(atom + put2) = hi;
-                  x[e][b] = load(half ^ 1, e, b);
-                }
+                uint4 lo, hi;
+                widen16(x[e], value_units(byte[e], byte[e]), lo, hi, odd);
+                *reinterpret_cast<uint4*>(to + e * 2048 + put) = lo;
+                *reinterpret_cast<uint4*>(to + e * 2048 + put2) = hi;
               }
               if (odd & 0x80808080u) {  // in a loop of its own, as it hardly ever runs
 #pragma unroll 1
-                for (int n = 0; n < 4 * kBlocks; ++n) {
-                  uint8_t* atom = to + n / kBlocks * 2048 + n % kBlocks * to_block;
-                  const uint32_t b = bytes[parity ^ 1][8 * (n / kBlocks) + r8];
-                  *reinterpret_cast<uint4*>(atom + put) = mend(*reinterpret_cast<const uint4*>(atom + put), b);
-                  *reinterpret_cast<uint4*>(atom + put2) = mend(*reinterpret_cast<const uint4*>(atom + put2), b);
+                for (int e = 0; e < 4; ++e) {
+                  uint8_t* atom = to + e * 2048;
+                  *reinterpret_cast<uint4*>(atom + put) = mend(*reinterpret_cast<const uint4*>(atom + put), byte_of[8 * e]);
+                  *reinterpret_cast<uint4*>(atom + put2) = mend(*reinterpret_cast<const uint4*>(atom + put2), byte_of[8 * e]);
                 }
               }
-              to += to_half;
+              bring(q + 2 < kGroupsOf ? rows : ahead, (q + 2) % kGroupsOf);
             }
+            parity ^= 1;
             tc::fence_proxy_async();  // the rows -> this CTA's tensor cores
             __syncwarp();
             const bool edge = is_v && keys.edge;
@@ -968,13 +966,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             rows = ahead;
           }
           if (due && j == min(is_v ? 0 : C::kLag, max(0, count - 1))) {
+            copy_wait<0>();
+            __syncwarp();
             epilogue(sh.late[wq], late_used, late_h);
             due = false;
-            // (again: kept over the epilogue, they would have to leave the registers, and every
-            // load would be waited for)
-            copy_wait<0>();
-            begin(rows, 0, parity);
-            load_all(0);
+            // (what was under way went where the epilogue keeps o)
+            bring_bytes(rows, parity);
+            bring(rows, 0);
+            bring(rows, 1);
           }
           if (j + 1 >= count) break;
         }
@@ -989,6 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++used;
         }
       }
+      copy_wait<0>();
     }
   } else {
     tc2::fewer_registers<C::kOtherRegs>();
@@ -1163,7 +1163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
             if (leader) {
               const uint64_t kd = dk + ((ks * C::kEntry) >> 4);
-#pragma unroll
+#pragma unroll 4
               for (int kk = 0; kk < C::kSteps; ++kk)
                 tc2::mma_ss(tmem + sw * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                             kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
@@ -1188,7 +1188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
             if (leader) {
               const uint64_t vd = dv + ((vs * C::kEntry) >> 4);
-#pragma unroll
+#pragma unroll 2
               for (int kk = 0; kk < kKeys / 16; ++kk)
                 if (16 * kk < k.rows)  // no weight beyond
                   tc2::mma_ts(tmem + C::kTmemO, tmem + sr * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), vd + ((kk * 2048) >> 4),
