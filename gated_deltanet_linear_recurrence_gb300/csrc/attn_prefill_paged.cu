@@ -21,7 +21,7 @@ constexpr int kRows = 128;          // rows a CTA
 constexpr int kSoftmaxThreads = 256, kEpilogueWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kScheduleWarp = 14, kEdgeWarp = 15;
 constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
-constexpr int kWideners = 2;         // warps of a CTA that write K of an e4m3 tile, or V
+constexpr int kWideners = 2;         // warps of a CTA that write its half of K of an e4m3 tile, or of V
 constexpr int kNoted = 8;            // key tiles whose missing pages are noted
 constexpr int kAhead = 6;            // key tiles that e4m3 rows are brought into L2 ahead
 
@@ -324,6 +324,7 @@ struct Shared {  // beside the tiles
   float red[2][2][128];
   float sums[2][2][128];  // row sums of two pieces, in two parts
   float refs[2][128];     // and the references that they go by
+  alignas(16) uint32_t said[4];        // e4m3: what the odd CTA copies to say that rows are there
   alignas(16) uint8_t bytes[4][2][64];  // e4m3: exponent bytes of a warp's eights, two key tiles
 };
 
@@ -336,6 +337,14 @@ __device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other
   return x;
 }
 __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// 16 bytes of this CTA's shared memory to the same place in the even CTA's, counted on a
+// barrier there
+__device__ __forceinline__ void tell(const void* what, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(
+                   tc2::in_cta(what, 0)),
+               "r"(tc::smem_u32(what)), "r"(tc2::in_cta(bar, 0))
+               : "memory");
+}
 // 8 bytes from global to shared memory; zeros when !valid (nothing is read)
 __device__ __forceinline__ void copy8(const void* dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(valid ? 8 : 0)
@@ -400,8 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      // (e4m3: the even CTA's hear of the other one's warps from its products' warp)
-      const int full = kFp8 ? kWideners + (rank == 0 ? 1 : 0) : 1;
+      const int full = kFp8 ? kWideners : 1;
       tc::mbar_init(&sh.k_full[i], full);
       tc::mbar_init(&sh.v_full[i], full);
       tc::mbar_init(&sh.s_done[i], 1);
@@ -414,9 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
       tc::mbar_init(&sh.sums_in[i], 8);
-      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products' and edge
-      // warps (e4m3: the odd CTA's products' warp too)
-      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : kFp8 ? 2 : 1));
+      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products' and edge warps
+      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : 1));
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sh.flags_in[i], 1);
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kNoted; ++i) tc::mbar_init(&sh.noted[i], 1);
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&sh.v_edge[i], kFp8 ? kWideners + (rank == 0 ? 1 : 0) : 1);
+      tc::mbar_init(&sh.v_edge[i], kFp8 ? kWideners : 1);
       tc::mbar_init(&sh.v_clean[i], 1);
     }
     sh.begun = 0;
@@ -957,10 +964,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             parity ^= 1;
             tc::fence_proxy_async();  // the rows -> this CTA's tensor cores
             __syncwarp();
+            // The even CTA's barriers hear of the odd one's rows by 16 bytes copied there: a
+            // copy, as the fence has ordered it behind the rows, and as its thread need not wait
+            // (an arrival there with a release waits for all that the thread has under way: 800 of
+            // 4,300 cycles a key tile, and from a warp of its own still 506 us where this takes 400).
             const bool edge = is_v && keys.edge;
             if (lane == 0) {
-              if (edge) tc::mbar_arrive(&sh.v_edge[ve % C::kSlots]);
-              tc::mbar_arrive(&full_bar[s]);
+              uint64_t* const edge_bar = &sh.v_edge[ve % C::kSlots];
+              if (rank == 1) {
+                if (edge) tell(sh.said, edge_bar);
+                tell(sh.said, &full_bar[s]);
+              } else if (w2 == 0) {
+                if (edge) tc::mbar_arrive_expect_tx(edge_bar, kWideners * 16);
+                tc::mbar_arrive_expect_tx(&full_bar[s], kWideners * 16);
+              } else {
+                if (edge) tc::mbar_arrive(edge_bar);
+                tc::mbar_arrive(&full_bar[s]);
+              }
             }
             ve += edge;
             rows = ahead;
@@ -1139,10 +1159,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dk = tc::smem_desc(sbase + C::kK, 16, 1024, tc::kLayoutSw128);
       const uint64_t dv = tc::smem_desc(sbase + C::kV, 16384, 1024, tc::kLayoutSw128);
       const bool leader = tc::elect_one();
-      // K or V is there: counted by the copies, or told by the warps that widen it in both CTAs
-      auto is_full = [&](uint64_t* bar, uint32_t parity) {
-        return kFp8 ? tc2::wait(bar, parity) : tc::mbar_wait(bar, parity);
-      };
       auto step = [](uint32_t& i, uint32_t& ph, uint32_t n) {
         if (++i == n) {
           i = 0;
@@ -1158,12 +1174,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(kFullMask, in) != 0;
         for (int j = 0; j < t.count + C::kLag && ok; ++j) {
           if (j < t.count) {  // S = Q K^T of key tile j
-            const bool w = is_full(&sh.k_full[ks], k_ph);
+            const bool w = tc::mbar_wait(&sh.k_full[ks], k_ph);
             tc::fence_after_sync();
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
             if (leader) {
               const uint64_t kd = dk + ((ks * C::kEntry) >> 4);
-#pragma unroll 4
+#pragma unroll
               for (int kk = 0; kk < C::kSteps; ++kk)
                 tc2::mma_ss(tmem + sw * kKeys, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                             kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
@@ -1177,7 +1193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int i = j - C::kLag;
           if (i >= 0) {  // O += P V of key tile i
             const Keys k = key_tile_of(t, i, window, sinks);
-            bool w = is_full(&sh.v_full[vs], v_ph);
+            bool w = tc::mbar_wait(&sh.v_full[vs], v_ph);
             if (k.edge) {  // V may have been edited in both CTAs (ordinary writes): acquire those
               w = w && of_tile(sh.v_edge, edges) && tc2::wait(&sh.v_clean[edges % C::kSlots], (edges / C::kSlots) & 1);
               ++edges;
@@ -1188,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = __all_sync(kFullMask, w) != 0)) break;
             if (leader) {
               const uint64_t vd = dv + ((vs * C::kEntry) >> 4);
-#pragma unroll 2
+#pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
                 if (16 * kk < k.rows)  // no weight beyond
                   tc2::mma_ts(tmem + C::kTmemO, tmem + sr * kKeys + 64 * (kk >> 2) + 8 * (kk & 3), vd + ((kk * 2048) >> 4),
@@ -1202,34 +1218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         ++used;
-      }
-      // The odd CTA's warp hands on that K and V have been widened there: a release for the
-      // cluster waits for everything that its thread has under way, which the warps that
-      // load and widen would do at every tile (800 of 4,300 cycles, when that was tried).
-      if (kFp8 && rank == 1) {
-        int g = 0;
-        const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_v = tc2::in_cta(sh.v_full, 0), r_ve = tc2::in_cta(sh.v_edge, 0);
-        for (int pass = 0; next_tile(pass, &t); ++pass) {
-          for (int j = 0; j < t.count + C::kLag && t.count > 0 && ok; ++j) {
-            if (j < t.count) {
-              if (!(ok = __all_sync(kFullMask, of_tile(sh.k_full, g + j)) != 0)) break;
-              if (leader) tc2::arrive_remote(r_k + (g + j) % C::kSlots * 8);
-            }
-            const int i = j - C::kLag;
-            if (i >= 0) {
-              if (!(ok = __all_sync(kFullMask, of_tile(sh.v_full, g + i)) != 0)) break;
-              const bool edge = key_tile_of(t, i, window, sinks).edge;
-              if (leader) {
-                if (edge) tc2::arrive_remote(r_ve + edges % C::kSlots * 8);
-                tc2::arrive_remote(r_v + (g + i) % C::kSlots * 8);
-              }
-              edges += edge;
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-          g += max(0, t.count);
-        }
       }
       // every product issued has completed before either CTA leaves the barrier at the end
       if (rank == 0) {
