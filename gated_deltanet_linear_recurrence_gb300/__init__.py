@@ -28,6 +28,7 @@ __all__ = ["gdn_prefill", "gdn_prefill_streamed", "gdn_prefill_streamed_workspac
 NOALLOC_SCRATCH_BYTES = 128 << 20  # GDN_NOALLOC_SCRATCH_BYTES in include/gdn.h
 
 _DTYPES = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
+_CACHE_DTYPES = {torch.bfloat16: _lib.GDN_CACHE_BF16, torch.float8_e4m3fn: _lib.GDN_CACHE_E4M3}
 
 
 def _ptr(t):
@@ -458,8 +459,10 @@ def gdn_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=Non
     return _lib.binding().attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, o, stream)
 
 
-def gdn_attn_prefill_paged_workspace_size(h_q, h_kv, head_dim):
-    return int(_lib.load().gdn_attn_prefill_paged_workspace_size(h_q, h_kv, head_dim))
+def gdn_attn_prefill_paged_workspace_size(h_q, h_kv, head_dim, cache_dtype=torch.bfloat16,
+                                          total_q=0):
+    return int(_lib.load().gdn_attn_prefill_paged_workspace_size(
+        h_q, h_kv, head_dim, _CACHE_DTYPES[cache_dtype], total_q))
 
 
 def gdn_attn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens_q, cache_len, k_exp=None,

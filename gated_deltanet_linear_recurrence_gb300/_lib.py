@@ -87,7 +87,7 @@ SIGNATURES = {
     "gdn_attn_prefill_paged": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                               _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
                                               ctypes.c_int, _f32, _i32, _i32, _vp, _sz, _vp]),
-    "gdn_attn_prefill_paged_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "gdn_attn_prefill_paged_workspace_size": (_sz, [_i32, _i32, _i32, ctypes.c_int, _i64]),
     "gdn_stream_status": (ctypes.c_int, [_vp]),
     "gdn_selftest_wait_timeout": (ctypes.c_int, [_i32, _vp]),
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -308,9 +308,12 @@ gdn_status gdn_attn_decode_paged(const void* q, int64_t q_stride, const void* k_
              : GDN_ERR_CUDA;
 }
 
-size_t gdn_attn_prefill_paged_workspace_size(int32_t h_q, int32_t h_kv, int32_t head_dim) {
-  if (check_heads(h_q, h_kv, head_dim) != GDN_OK) return 0;
-  return gdn::paged_prefill_workspace_bytes(head_dim);
+size_t gdn_attn_prefill_paged_workspace_size(int32_t h_q, int32_t h_kv, int32_t head_dim, gdn_cache_dtype cache_dtype,
+                                             int64_t total_q) {
+  if (check_heads(h_q, h_kv, head_dim) != GDN_OK || total_q < 0) return 0;
+  if (cache_dtype != GDN_CACHE_BF16 && cache_dtype != GDN_CACHE_E4M3) return 0;
+  return gdn::paged_prefill_workspace_bytes(head_dim) +
+         (gdn::paged_prefill_widens(total_q, h_q / h_kv, cache_dtype) ? gdn::kPagedPrefillWideBytes : 0);
 }
 
 gdn_status gdn_attn_prefill_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
@@ -338,7 +341,8 @@ gdn_status gdn_attn_prefill_paged(const void* q, int64_t q_stride, const void* k
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16) || !aligned(cu_seqlens_q, 4) ||
       !aligned(cache_len, 4))
     return GDN_ERR_MISALIGNED;
-  if (workspace_bytes < gdn::paged_prefill_workspace_bytes(head_dim)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  const size_t least = gdn::paged_prefill_workspace_bytes(head_dim);
+  if (workspace_bytes < least) return GDN_ERR_WORKSPACE_TOO_SMALL;
   gdn::PagedPrefillArgs a{};
   a.q = q;
   a.q_stride = q_stride;
@@ -354,6 +358,12 @@ gdn_status gdn_attn_prefill_paged(const void* q, int64_t q_stride, const void* k
   a.window = window < (int64_t)max_pages * page_size ? window : 0;
   a.sinks = a.window ? sinks : 0;
   a.scale = scale;
+  if (gdn::paged_prefill_widens(total_q, h_q / h_kv, cache_dtype)) {  // whole rows of K and V that the rest holds
+    const int64_t row = (int64_t)h_kv * head_dim * 2, rows = (int64_t)((workspace_bytes - least) / (2 * (size_t)row));
+    a.wide_rows = rows < INT32_MAX - 2047 ? rows : INT32_MAX - 2047;
+    a.wide_k = static_cast<uint8_t*>(workspace) + least;
+    a.wide_v = static_cast<uint8_t*>(a.wide_k) + a.wide_rows * row;
+  }
   if (!gdn::device_error_word(&a.err)) return GDN_ERR_CUDA;
   return gdn::launch_attn_prefill_paged(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK
                                                                                                  : GDN_ERR_CUDA;

@@ -355,7 +355,7 @@ PyObject* attn_prefill_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                           : s.given(rows(a[11], {T, h_q, c.D}, "o", true));
     at::Tensor ws;
     if (a[12] == Py_None) {
-      ws = s.scratch({(int64_t)p_prefill_paged_ws(as32(h_q), as32(c.h_kv), as32(c.D))}, c.options.dtype(at::kByte));
+      ws = s.scratch({(int64_t)p_prefill_paged_ws(as32(h_q), as32(c.h_kv), as32(c.D), c.dtype, T)}, c.options.dtype(at::kByte));
     } else {
       ws = tensor(a[12], "workspace");
       if (!(ws.is_cuda() && ws.is_contiguous())) value_error("workspace must be on the GPU, contiguous");

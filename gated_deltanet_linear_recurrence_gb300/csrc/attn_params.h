@@ -112,6 +112,10 @@ struct PagedPrefillArgs {
   int32_t window, sinks;  // keys a query sees of the last (0: all), and of the first
   int32_t pairs;          // of CTAs that share the work
   float scale;
+  // e4m3: room for rows that are widened once, [wide_rows][h_kv][D] bf16 of K and of V
+  void* wide_k;
+  void* wide_v;
+  int64_t wide_rows;
   int* err;
 };
 constexpr int32_t kPagedPrefillMaxPairs = 80;  // bounds the workspace
@@ -125,7 +129,9 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_append_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_decode_paged(const PagedAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const AttnPrefillArgs& a, cudaStream_t stream);
-size_t paged_prefill_workspace_bytes(int32_t head_dim);
+size_t paged_prefill_workspace_bytes(int32_t head_dim);  // without room for widened rows
+bool paged_prefill_widens(int64_t total_q, int32_t group, int dtype);
+constexpr size_t kPagedPrefillWideBytes = (size_t)128 << 20;  // that room, as asked for
 cudaError_t launch_attn_prefill_paged(const PagedPrefillArgs& a, cudaStream_t stream);
 
 // The current device's error word (gdn_api.cu); false when it cannot be located.

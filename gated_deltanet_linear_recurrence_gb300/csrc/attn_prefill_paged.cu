@@ -28,6 +28,9 @@ constexpr int kAhead = 6;            // key tiles that e4m3 rows are brought int
 // Work, in keys: a tile of queries counts the keys that its rows see, and kTileCost for
 // taking it up (Q in, the first scores, O out).  A share is at least kMinShare.
 constexpr int kTileCost = 256, kMinShare = 768;
+// e4m3 rows of a sequence with at least so many tiles of queries are widened once, into the
+// workspace, where there is room
+constexpr int kWideTiles = 3;
 
 template <int D, bool kFp8>
 struct Cfg {
@@ -38,6 +41,7 @@ struct Cfg {
   static constexpr int kS = D == 256 ? 2 : 3;
   static constexpr int kLag = kS - 1;  // key tiles that the scores are ahead of P V
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
+  static constexpr int kArrivals = kFp8 ? kWideners : 1;  // that make K or V of a key tile full, beside bytes
   // Registers of a thread of the four warpgroups: softmax (two), epilogue, and the rest;
   // together the 65,536 that the CTA starts with.
   static constexpr int kSoftmaxRegs = kFp8 ? 160 : 168, kEpilogueRegs = kFp8 ? 112 : 88;
@@ -70,6 +74,7 @@ struct Piece {
   int32_t firsts, w0;  // key tiles that hold the first keys; number of the window's first one
   int32_t v0, count;   // key tiles to go through, of both in this order
   int32_t part;        // where its partial result goes (0, 1), or -1: all of the tile's keys
+  int32_t wide;        // row of the widened copy that holds position 0, or -1
 };
 
 struct Work {
@@ -134,8 +139,12 @@ struct Work {
     t.firsts = (int)min((int64_t)t.w0, ((int64_t)sinks + kKeys - 1) / kKeys);
     t.v0 = 0;
     t.count = t.firsts + (t.sight + kKeys - 1) / kKeys - t.w0;
-    t.part = -1;
+    t.part = t.wide = -1;
     return t;
+  }
+  // rows of the widened copy that a sequence takes
+  __device__ __forceinline__ int64_t wide(const PagedPrefillArgs& p, const Seq& s) const {
+    return p.wide_rows > 0 && s.tiles >= kWideTiles ? (int64_t)s.off + s.a : 0;
   }
   // how many of a tile's `count` key tiles lie before work r of it
   __device__ __forceinline__ int visits(int64_t r, int64_t keys, int count) const {
@@ -156,6 +165,7 @@ struct Join {
 // what the sequences come to, and where a share starts
 struct Found {
   int64_t total, base;  // all work, that before sequence seq
+  int64_t wide;         // rows of the widened copy that the sequences before it take
   int seq;
 };
 
@@ -165,8 +175,10 @@ struct Place {
   int n, kvh, i;
   int64_t start;
   int64_t u, u_end, total;  // of a share: where it is, where it ends; all work
+  int64_t wide;             // rows of the widened copy before the sequence's
   __device__ __forceinline__ void find(const PagedPrefillArgs& p, const Work& w, const Found& f, int64_t u, int lane) {
     n = f.seq;
+    wide = f.wide;
     s = w.sequence(p, n, false);
     const int64_t head = w.before(s, s.tiles);
     kvh = (int)quotient(u - f.base, head);
@@ -189,6 +201,7 @@ struct Place {
     if (++kvh < p.cache.h_kv) return;
     kvh = 0;
     do {
+      wide += w.wide(p, s);
       if (++n >= p.num_seqs) return;
       s = w.sequence(p, n, false);
     } while (s.tiles == 0);
@@ -219,10 +232,12 @@ __device__ __forceinline__ bool find_few(const PagedPrefillArgs& p, const Work& 
   const int64_t u = Shares(f->total, n).start(c);
   f->seq = __ffs(__ballot_sync(kFullMask, incl > u)) - 1;
   f->base = __shfl_sync(kFullMask, incl - mine, f->seq);
+  const int64_t rows = w.wide(p, s);
+  f->wide = p.wide_rows > 0 ? __shfl_sync(kFullMask, scan_up(rows, lane) - rows, f->seq) : 0;
   return true;
 }
 struct Sums {  // the block's, for this
-  int64_t of[16];
+  int64_t of[16], rows[16];
   Found found;
 };
 template <int kT>
@@ -231,18 +246,25 @@ __device__ __noinline__ bool find_many(const PagedPrefillArgs& p, const Work& w,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.num_seqs - 1) / kT + 1;  // sequences a thread counts
   const int lo = (int)min((int64_t)p.num_seqs, (int64_t)tid * per), hi = (int)min((int64_t)p.num_seqs, (int64_t)lo + per);
-  int64_t mine = 0;
+  int64_t mine = 0, rows = 0;
   for (int n = lo; n < hi; ++n) {
     const Seq s = w.sequence(p, n, report);
     if (s.tiles > 0) mine += p.cache.h_kv * w.before(s, s.tiles);
+    rows += w.wide(p, s);
   }
-  const int64_t incl = scan_up(mine, lane);
-  if (lane == 31) sh.of[warp] = incl;
+  const int64_t incl = scan_up(mine, lane), rows_incl = scan_up(rows, lane);
+  if (lane == 31) {
+    sh.of[warp] = incl;
+    sh.rows[warp] = rows_incl;
+  }
   __syncthreads();
-  int64_t before = incl - mine, total = 0;
+  int64_t before = incl - mine, total = 0, wide = rows_incl - rows;
 #pragma unroll
   for (int k = 0; k < kT / 32; ++k) {
-    if (k < warp) before += sh.of[k];
+    if (k < warp) {
+      before += sh.of[k];
+      wide += sh.rows[k];
+    }
     total += sh.of[k];
   }
   const int sharing = sharers(total, p.pairs);
@@ -255,9 +277,11 @@ __device__ __noinline__ bool find_many(const PagedPrefillArgs& p, const Work& w,
       if (u < before + x) {
         sh.found.seq = n;
         sh.found.base = before;
+        sh.found.wide = wide;
         break;
       }
       before += x;
+      wide += w.wide(p, s);
     }
   }
   __syncthreads();
@@ -292,6 +316,12 @@ __device__ __forceinline__ int edge_row(const Piece& t, const Keys& k, int windo
   const int low = window ? max(0, t.sight - window) : 0;
   if (max(k.first, sinks) < min(k.first + kKeys, low)) return 0;
   return max(0, t.pos + 1 - k.first) & ~15;
+}
+// how many of a piece's key tiles are edge tiles, for a warp that does not go through them
+__device__ __forceinline__ int edges_of(const Piece& t, int window, int sinks, int lane) {
+  int n = 0;
+  for (int j = lane; j < t.count; j += 32) n += key_tile_of(t, j, window, sinks).edge;
+  return __reduce_add_sync(kFullMask, n);
 }
 __device__ __forceinline__ uint32_t lowest(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 
@@ -409,9 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      const int full = kFp8 ? kWideners : 1;
-      tc::mbar_init(&sh.k_full[i], full);
-      tc::mbar_init(&sh.v_full[i], full);
+      tc::mbar_init(&sh.k_full[i], C::kArrivals);
+      tc::mbar_init(&sh.v_full[i], C::kArrivals);
       tc::mbar_init(&sh.s_done[i], 1);
       tc::mbar_init(&sh.o_done[i], 1);
     }
@@ -431,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kNoted; ++i) tc::mbar_init(&sh.noted[i], 1);
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&sh.v_edge[i], kFp8 ? kWideners : 1);
+      tc::mbar_init(&sh.v_edge[i], C::kArrivals);
       tc::mbar_init(&sh.v_clean[i], 1);
     }
     sh.begun = 0;
@@ -445,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- this pair's share, and its pieces one after the other (for the schedule warp)
   const Work work(p);
   const int me = blockIdx.x / 2;
-  Found found{0, 0, 0};
+  Found found{0, 0, 0, 0};
   bool any = false;
   if (p.num_seqs > 32) any = find_many<kThreads>(p, work, me, blockIdx.x == 0, sh.work, &found);
   else if (warp == kScheduleWarp) any = find_few(p, work, me, blockIdx.x == 0, lane, &found);
@@ -458,6 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t keys = work.keys(at.s, at.i), end = at.start + kTileCost + keys;
       const int64_t r0 = at.u - at.start, to = min(end, at.u_end);
       *t = work.piece(at.s, at.n, at.kvh, at.i);
+      const int64_t rows = kFp8 ? work.wide(p, at.s) : 0;
+      t->wide = rows > 0 && at.wide + rows <= p.wide_rows ? (int32_t)at.wide : -1;
       const int all = t->count, v0 = work.visits(r0, keys, all), v1 = work.visits(to - at.start, keys, all);
       at.u = to;
       t->v0 = v0;
@@ -903,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int pass = 0; ok; ++pass) {
         const bool more = next_tile(pass, &t);
         if (!ok) break;
-        const int count = more ? t.count : 0;
+        const int tiles = more ? t.count : 0, count = tiles > 0 && t.wide < 0 ? tiles : 0;  // all, to widen
         // the page of the lane's eight of key tile j, and their cached rows
         auto look = [&](int j) {
           const Keys k = key_tile_of(t, j, window, sinks);
@@ -1001,10 +1032,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) sh.late[wq] = t;  // whose epilogue is due
         __syncwarp();
         late_used = used;
-        late_h = g + count - 1;
+        late_h = g + tiles - 1;
         due = true;
-        if (count > 0) {
-          g += count;
+        if (tiles > 0) {
+          if (is_v && count == 0) ve += edges_of(t, window, sinks, lane);
+          g += tiles;
           ++used;
         }
       }
@@ -1016,22 +1048,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     // side by side in a page are copied together, up to 64 (a box); the first lane of a box asks
     // for it, at 80 to 100 cycles a box and block of dims, which pages of few keys make many
     // (so K and V have a warp each).
-    const int eight = 8 * (lane & 15), box = min(1 << shift, 64);
+    // A widened copy's rows, [row][KV head][D], lie side by side.
+    const int eight = 8 * (lane & 15), box = kFp8 ? 64 : min(1 << shift, 64);
     const bool lead = lane < 16 && (eight & (box - 1)) == 0;
     const int none = max(1, p.cache.num_pages * p.cache.h_kv);  // past the pages: reads as zeros
     auto look = [&](const Piece& t, int j) {
       const Keys k = key_tile_of(t, j, window, sinks);
       return entry_of(t, k.first + eight, j < t.count && eight < k.rows);
     };
-    auto rows_of = [&](const Piece& t, int j, int page) {
-      return row_of(t, key_tile_of(t, j, window, sinks).first + eight, page);
+    struct Where {  // of the lane's eight keys of a tile
+      uint32_t row;  // in the cache (~0: no page)
+      int y, z;      // in the tensor maps
+    };
+    auto where = [&](const Piece& t, const Keys& k, int page) {
+      Where w;
+      w.row = row_of(t, k.first + eight, page);
+      w.y = w.row == ~0u ? 0 : w.row & ((1 << shift) - 1);
+      w.z = w.row == ~0u ? none : (int)(w.row >> shift);
+      if (kFp8) {
+        w.y = t.kvh;
+        w.z = t.wide + k.first + eight;
+      }
+      return w;
     };
     if (warp == kScheduleWarp) {
       // ------------------------------------------------------------ schedule, copies of V
       Piece t = sh.tile[0];
-      int g = 0, vc = 0, ve = 0;  // key tiles; those whose V was asked for, edge tiles among them
+      int g = 0, vc = 0, ve = 0;  // key tiles; up to which V was asked for; edge tiles
+      bool last_copied = false;
       const uint32_t r_v = tc2::in_cta(sh.v_full, 0), r_ve = tc2::in_cta(sh.v_edge, 0);
-      if (!kFp8 && lane == 0) tc::prefetch_tmap(&tm_v);
+      if (lane == 0) tc::prefetch_tmap(&tm_v);
       for (int pass = 1; t.count >= 0 && ok; ++pass) {
         Piece next;
         next_piece(&next);
@@ -1043,27 +1089,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh.tile[pass & 1] = next;
           tc::mbar_arrive(&sh.tile_full[pass & 1]);
         }
+        const bool copied = !kFp8 || t.wide >= 0;  // (not widened by warps of their own)
+        if (!copied) ve += edges_of(t, window, sinks, lane);
+        if (t.count > 0) last_copied = copied;
         int page = kFp8 ? -1 : look(t, 0);
-        for (int j = 0; !kFp8 && j < t.count; ++j) {
+        for (int j = 0; copied && j < t.count; ++j) {
           const int h = g + j, s = h % C::kSlots, e = ve % C::kSlots;
           const Keys k = key_tile_of(t, j, window, sinks);
-          const uint32_t r = rows_of(t, j, page);
-          page = look(t, j + 1);
-          const int slot = r == ~0u ? 0 : r & ((1 << shift) - 1), z = r == ~0u ? none : (int)(r >> shift);
+          const Where at = where(t, k, page);
+          if (!kFp8) page = look(t, j + 1);
           const bool mine = lead && eight < k.rows;
           uint8_t* to = smem + C::kV + s * C::kEntry + eight * 128;
           const uint32_t bytes = ((k.rows + box - 1) & -box) * D * 2, bar = k.edge ? r_ve + e * 8 : r_v + s * 8;
           if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.o_done, h - C::kSlots)) != 0)) break;
           // The bytes of both CTAs count on the even CTA's barrier, in an edge tile on one of
           // its own that the edge warp can count through; v_full keeps step.
-          if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(k.edge ? &sh.v_edge[e] : &sh.v_full[s], bytes);
+          if (rank == 0 && lane == 0) {
+            tc::mbar_arrive_expect_tx(k.edge ? &sh.v_edge[e] : &sh.v_full[s], bytes);
+            for (int i = 1; i < C::kArrivals; ++i) tc::mbar_arrive(k.edge ? &sh.v_edge[e] : &sh.v_full[s]);
+          }
           if (mine) {
 #pragma unroll
             for (int kb = 0; kb < D / 128; ++kb)
-              tc2::tma_load_3d(to + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, slot, z, bar);
+              tc2::tma_load_3d(to + kb * 16384, &tm_v, (int)rank * (D / 2) + 64 * kb, at.y, at.z, bar);
           }
           __syncwarp();
-          if (k.edge && rank == 0 && lane == 0) tc::mbar_arrive(&sh.v_full[s]);
+          if (k.edge && rank == 0 && lane == 0)
+            for (int i = 0; i < C::kArrivals; ++i) tc::mbar_arrive(&sh.v_full[s]);
           vc = h + 1;
           ve += k.edge;
         }
@@ -1073,7 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rank == 0 && lane == 0) joins(p)[me] = sh.join;
       // Copies still in flight land before the CTA ends: after an expired wait, the
       // even CTA's barriers tell of both CTAs' copies.
-      if (!kFp8 && lane == 0 && rank == 0) {
+      if (lane == 0 && rank == 0 && last_copied) {
         for (int h = max(0, vc - C::kSlots); h < vc; ++h) ok = of_tile(sh.v_full, h) && ok;
         for (int e = max(0, ve - C::kSlots); e < ve; ++e) ok = of_tile(sh.v_edge, e) && ok;
       }
@@ -1081,11 +1133,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ copies of Q and K
       Piece t;
       int g = 0, used = 0;  // key tiles, pieces with Q so far
-      int kc = 0;           // key tiles whose K was asked for
+      int kc = 0;           // key tiles up to which K was asked for
+      bool last_copied = false;
       const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_q = tc2::in_cta(&sh.q_full, 0);
       if (lane == 0) {
         tc::prefetch_tmap(&tm_q);
-        if (!kFp8) tc::prefetch_tmap(&tm_k);
+        tc::prefetch_tmap(&tm_k);
       }
       for (int pass = 0; next_tile(pass, &t); ++pass) {
         if (t.count == 0) continue;
@@ -1099,12 +1152,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++used;
+        last_copied = !kFp8 || t.wide >= 0;
         for (int j = 0; j < t.count && ok; ++j) {
           const int h = g + j, s = h % C::kSlots;
           const Keys k = key_tile_of(t, j, window, sinks);
-          const uint32_t r = rows_of(t, j, page);
+          const Where at = where(t, k, page);
+          const uint32_t r = at.row;
           page = look(t, j + 1);
-          if (kFp8) {
+          if (kFp8 && t.wide < 0) {
             // The rows of key tiles to come are brought into L2, K's by the even CTA, V's by the
             // other, kAhead tiles before the warps that widen them.  (They say where they are in
             // a number: this warp keeps nobody waiting, so that a barrier's phases might pass it by.)
@@ -1123,16 +1178,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::prefetch_l2(static_cast<const uint8_t*>(rank == 0 ? p.cache.k_pages : p.cache.v_pages) + (int64_t)r * D, run * D);
             ok = __all_sync(kFullMask, ok) != 0;
           } else {
-            const int slot = r == ~0u ? 0 : r & ((1 << shift) - 1), z = r == ~0u ? none : (int)(r >> shift);
             const bool mine = lead && eight < k.rows && (lane >> 3) == (int)rank;
             uint8_t* to = smem + C::kK + s * C::kEntry + (lane & 7) * 1024;
             const uint32_t bytes = ((k.rows + box - 1) & -box) * D * 2;
             if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.s_done, h - C::kSlots)) != 0)) break;
             // the bytes of both CTAs count on the even CTA's barrier
-            if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh.k_full[s], bytes);
+            if (rank == 0 && lane == 0) {
+              tc::mbar_arrive_expect_tx(&sh.k_full[s], bytes);
+              for (int i = 1; i < C::kArrivals; ++i) tc::mbar_arrive(&sh.k_full[s]);
+            }
             if (mine) {
 #pragma unroll
-              for (int kb = 0; kb < D / 64; ++kb) tc2::tma_load_3d(to + kb * 8192, &tm_k, 64 * kb, slot, z, r_k + s * 8);
+              for (int kb = 0; kb < D / 64; ++kb) tc2::tma_load_3d(to + kb * 8192, &tm_k, 64 * kb, at.y, at.z, r_k + s * 8);
             }
             __syncwarp();
             note(h, eight < k.rows && r == ~0u);
@@ -1143,7 +1200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (lane == 0 && rank == 0) {  // (as for V)
-        for (int h = max(0, kc - C::kSlots); h < kc; ++h) ok = of_tile(sh.k_full, h) && ok;
+        for (int h = max(0, kc - C::kSlots); last_copied && h < kc; ++h) ok = of_tile(sh.k_full, h) && ok;
         if (used > 0 && !tc::mbar_wait(&sh.q_full, (used - 1) & 1)) ok = false;
       }
     } else if (warp == kMmaWarp) {
@@ -1315,6 +1372,83 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tc2::tmem_dealloc(tmem, C::kTmemCols);
 }
 
+// The rows of e4m3 sequences with many tiles of queries, widened once: a warp a row of all
+// heads, for a block's 32 rows after the sequences have been counted as find_many does.
+constexpr int kWidenThreads = 256, kWidenRows = 32;
+template <int D>
+__global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const __grid_constant__ PagedPrefillArgs p) {
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+  __shared__ int64_t sums[kWidenThreads / 32];
+  __shared__ int64_t found_base;
+  __shared__ int found_seq;
+  tc::allow_dependents();
+  tc::wait_prerequisites();
+  const Work work(p);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.num_seqs - 1) / kWidenThreads + 1;  // sequences a thread counts
+  const int lo = (int)min((int64_t)p.num_seqs, (int64_t)tid * per), hi = (int)min((int64_t)p.num_seqs, (int64_t)lo + per);
+  int64_t mine = 0;
+  for (int n = lo; n < hi; ++n) mine += work.wide(p, work.sequence(p, n, false));
+  const int64_t incl = scan_up(mine, lane);
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+  for (int k = 0; k < kWidenThreads / 32; ++k) {
+    if (k < warp) before += sums[k];
+    total += sums[k];
+  }
+  total = min(total, p.wide_rows);  // (the rows of a sequence that ends beyond are not used)
+  for (int64_t first = (int64_t)blockIdx.x * kWidenRows; first < total; first += (int64_t)gridDim.x * kWidenRows) {
+    __syncthreads();
+    if (before <= first && first < before + mine) {
+      int64_t base = before;
+      for (int n = lo; n < hi; ++n) {
+        const int64_t rows = work.wide(p, work.sequence(p, n, false));
+        if (first < base + rows) {
+          found_seq = n;
+          found_base = base;
+          break;
+        }
+        base += rows;
+      }
+    }
+    __syncthreads();
+    int n = found_seq;
+    int64_t base = found_base, rows = work.wide(p, work.sequence(p, n, false));
+    for (int64_t row = first + warp; row < min(total, first + kWidenRows); row += kWidenThreads / 32) {
+      while (row >= base + rows) {  // (there is one: row < total)
+        base += rows;
+        rows = work.wide(p, work.sequence(p, ++n, false));
+      }
+      const int pos = (int)(row - base), entry = pos >> p.cache.page_shift;
+      const int page = entry < p.cache.max_pages ? __ldg(p.cache.table + (int64_t)n * p.cache.max_pages + entry) : -1;
+      const bool there = page >= 0 && page < p.cache.num_pages;
+      const int64_t at = (((int64_t)(there ? page : 0) * p.cache.h_kv) << p.cache.page_shift) + (pos & ((1 << p.cache.page_shift) - 1));
+#pragma unroll 2
+      for (int h = lane / kLanes; h < p.cache.h_kv; h += kHeads) {
+        const int64_t r = at + ((int64_t)h << p.cache.page_shift);
+        const int64_t to = (row * p.cache.h_kv + h) * D + 8 * (lane % kLanes);
+        uint2 kc = make_uint2(0, 0), vc = kc;
+        uint32_t kb = 127, vb = 127;
+        if (there) {
+          kc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache.k_pages) + r * D) + lane % kLanes);
+          vc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache.v_pages) + r * D) + lane % kLanes);
+          kb = __ldg(p.cache.k_exp + r);
+          vb = __ldg(p.cache.v_exp + r);
+        }
+        auto wide = [&](uint2 c, uint32_t byte) {
+          uint4 x, unused;
+          uint32_t odd = byte > kUnitTop ? 0x80u : 0u;
+          widen16(make_uint4(c.x, c.y, 0, 0), value_units(byte, byte), x, unused, odd);
+          return odd & 0x80808080u ? mend(x, byte) : x;
+        };
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.wide_k) + to) = wide(kc, kb);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.wide_v) + to) = wide(vc, vb);
+      }
+    }
+  }
+}
+
 // Tiles of queries whose keys several pairs went through: block (c, y, z) joins rows 32 y
 // and columns 64 z of the tile that pair c has started and others finished, if there is
 // one.  A lane has a row, the eight warps share the parts.
@@ -1416,7 +1550,6 @@ cudaError_t launch(const PagedPrefillArgs& a, cudaStream_t stream) {
   const int G = a.h_q / a.cache.h_kv, rows = a.cache.page_shift >= 6 ? 64 : 1 << a.cache.page_shift;
   CUtensorMap mq, mk, mv;
   if (!encode(&mq, a.q, D, a.h_q, a.total_q, a.q_stride, G, kRows / G)) return cudaErrorInvalidValue;
-  mk = mv = mq;  // (e4m3 rows are not copied)
   if (!kFp8) {
     PagedCache c = a.cache;
     if (c.num_pages == 0) {  // no page is ever there: the kernel asks for what lies past this one
@@ -1424,6 +1557,13 @@ cudaError_t launch(const PagedPrefillArgs& a, cudaStream_t stream) {
       c.k_pages = c.v_pages = const_cast<void*>(a.q);
     }
     if (!encode_pages(&mk, c.k_pages, c, rows) || !encode_pages(&mv, c.v_pages, c, rows)) return cudaErrorInvalidValue;
+  } else if (a.wide_rows > 0) {
+    const int64_t stride = (int64_t)a.cache.h_kv * D;
+    if (!encode(&mk, a.wide_k, D, a.cache.h_kv, a.wide_rows, stride, 1, 64) ||
+        !encode(&mv, a.wide_v, D, a.cache.h_kv, a.wide_rows, stride, 1, 64))
+      return cudaErrorInvalidValue;
+  } else {
+    mk = mv = mq;  // (not copied)
   }
   const int smem = (int)(C::kShared + sizeof(Shared<D, kFp8>));
   static_assert(C::kShared + sizeof(Shared<D, kFp8>) <= 227 * 1024, "shared memory");
@@ -1443,6 +1583,14 @@ cudaError_t launch(const PagedPrefillArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  if (a.wide_rows > 0) {
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)min((int64_t)16 * a.pairs, (a.wide_rows + kWidenRows - 1) / kWidenRows));
+    cfg.blockDim = dim3(kWidenThreads);
+    e = cudaLaunchKernelEx(&cfg, widen_rows_kernel<D>, a);
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 2;
+  }
   cfg.gridDim = dim3((unsigned)(2 * a.pairs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
@@ -1457,6 +1605,11 @@ cudaError_t launch(const PagedPrefillArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// A call whose queries may make kWideTiles tiles of a sequence, over e4m3 rows
+bool paged_prefill_widens(int64_t total_q, int32_t group, int dtype) {
+  return dtype == kCacheE4M3 && total_q > (int64_t)(kWideTiles - 1) * 2 * (kRows / group);
+}
 
 size_t paged_prefill_workspace_bytes(int32_t head_dim) {
   return (size_t)kPagedPrefillMaxPairs * (2 * 2 * kRows * (head_dim + 2) * sizeof(float) + sizeof(Join));

@@ -150,6 +150,40 @@ def test_keys_split_over_many_pairs(D, h_q, h_kv, new, lengths, fp8):
     b.check(window=3333, sinks=4)
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_widened_once_or_by_each_tile(D):
+    """Over e4m3 rows: sequences with many tiles of queries have their rows widened into the
+    workspace while there is room, with the same results; a mixture of both, with windows,
+    missing pages, NaN codes and units above 2^7."""
+    new, lengths = [300, 1, 140, 200, 3, 129], [500, 700, 140, 1001, 333, 129]
+    b = Batch(new, lengths, 8, 1, D, 16, True, 20)
+    least = gdn_attn_prefill_paged_workspace_size(8, 1, D)
+    full = gdn_attn_prefill_paged_workspace_size(8, 1, D, E4M3, sum(new))
+    assert full - least == 128 << 20 and least == gdn_attn_prefill_paged_workspace_size(8, 1, D, E4M3, 64)
+    assert least == gdn_attn_prefill_paged_workspace_size(8, 1, D, torch.bfloat16, 10 ** 6)
+    ws = torch.full((full,), 0xff, dtype=torch.uint8, device="cuda")
+    row = 4 * D
+    for kw in (dict(), dict(window=150, sinks=20)):
+        want = b.check(**kw, workspace=ws[:least])
+        # none fits, some do, the last one ends a row too late, all do
+        for rows in (0, 400, 500, 639, 640, 1640, 1641, 1769, 1770, 5000):
+            ws[least:] = 0xff
+            assert torch.equal(b.run(**kw, workspace=ws[:least + rows * row]), want), rows
+    b.table[3, 20] = 10 ** 6
+    gone = [np.arange(x) // 16 == (20 if i == 3 else -1) for i, x in enumerate(lengths)]
+    want = b.check(gone=gone, workspace=ws[:least])
+    assert torch.equal(b.check(gone=gone, workspace=ws), want)
+    b.table[3, 20] = 0  # (some page: its rows are other ones)
+    b.kp.view(torch.uint8)[int(b.table[0, 25]), 0, 5, 9] = 0xff
+    b.vp.view(torch.uint8)[int(b.table[2, 3]), 0, 7, D - 1] = 0x7f
+    b.ve[int(b.table[0, 2]), 0, 3] = 200
+    b.ke[int(b.table[5, 2]), 0, 3] = 140
+    want = b.run(workspace=ws[:least])
+    got = b.run(workspace=ws)
+    assert gdn_stream_status() == "GDN_OK" and torch.isnan(want).any() and torch.isfinite(want).any()
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("D", [128, 256])
 def test_many_sequences(D, fp8):
