@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "attn_params.h"
 #include "attn_tc.cuh"
@@ -27,7 +29,7 @@ constexpr int kAhead = 6;            // key tiles that e4m3 rows are brought int
 
 // Work, in keys: a tile of queries counts the keys that its rows see, and kTileCost for
 // taking it up (Q in, the first scores, O out).  A share is at least kMinShare.
-constexpr int kTileCost = 256, kMinShare = 768;
+constexpr int kTileCost = 384, kMinShare = 384;
 // e4m3 rows of a sequence with at least so many tiles of queries are widened once, into the
 // workspace, where there is room
 constexpr int kWideTiles = 3;
@@ -1449,16 +1451,16 @@ __global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const __grid_
   }
 }
 
-// Tiles of queries whose keys several pairs went through: block (c, y, z) joins rows 32 y
-// and columns 64 z of the tile that pair c has started and others finished, if there is
-// one.  A lane has a row, the eight warps share the parts.
+// Tiles of queries whose keys several pairs went through: block (c, y, z) joins rows 32 y ..
+// and columns 64 z .. of the tile that pair c has started and others finished, if there
+// is one.  A lane has a row, a warp eight columns of all parts: they are two at most with
+// many tiles and some tens with few, whose loads then go out eight and four at a time.
+// (Eight warps that shared the parts and met in shared memory took 30 us for two parts of
+// 75 tiles of 256 rows.)
 constexpr int kJoinWarps = 8, kJoinColumns = 64;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_paged_join_kernel(const __grid_constant__ PagedPrefillArgs p) {
-  constexpr int kEach = kPagedPrefillMaxPairs / kJoinWarps;  // parts of a warp, at most
-  static_assert(kEach * kJoinWarps == kPagedPrefillMaxPairs, "parts");
-  __shared__ float tops[kJoinWarps][32], sums[kJoinWarps][32];
-  __shared__ float4 columns[kJoinWarps][kJoinColumns / 8][32];
+  constexpr int kMasks = (kPagedPrefillMaxPairs + 31) / 32;
   tc::allow_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   tc::wait_prerequisites();  // the parts
@@ -1469,65 +1471,64 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_paged_join_kerne
   const int G = p.h_q / p.cache.h_kv, even = min(kRows / G * G, rows);  // rows of the even CTA
   const bool real = x < rows;
   const int cta = x >= even, row = real ? x - cta * even : 0;
-  // part k of the tile is in slot 1 of pair c, in slot 0 of the pairs after it
+  // which parts there are: k of the tile is in slot 1 of pair c, in slot 0 of the pairs after it
+  uint32_t there[kMasks], any = 0;
+#pragma unroll
+  for (int i = 0; i < kMasks; ++i) {
+    const int k = 32 * i + lane;
+    there[i] = __ballot_sync(kFullMask, c + k <= last && __ldg(&js[c + k].there[k == 0]));
+    any |= there[i];
+  }
+  if (any == 0) return;  // all keys were one pair's, which has written o
+  const int parts = last - c + 1;
+  auto is_there = [&](int k) {
+    uint32_t m = there[0];
+#pragma unroll
+    for (int i = 1; i < kMasks; ++i) m = k >= 32 * i ? there[i] : m;
+    return ((m >> (k & 31)) & 1) != 0;
+  };
   auto part_of = [&](int k) { return p.partial + (int64_t)(2 * (c + k) + (k == 0)) * (2 * kRows * (D + 2)); };
-  float m[kEach], top = -INFINITY;
-  bool some = false;
+  const int at_row = cta * kRows + row, column = kJoinColumns * blockIdx.z + 8 * warp;
+  float top = -INFINITY, sum = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  auto join = [&](auto batch) {
+    constexpr int N = decltype(batch)::value;  // parts whose loads go out together
+    for (int k0 = 0; k0 < parts; k0 += 2 * N) {
+      float m[2 * N];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int k = warp + kJoinWarps * i;
-    m[i] = -INFINITY;
-    if (c + k <= last && __ldg(&js[c + k].there[k == 0])) {
-      m[i] = part_of(k)[2 * kRows * D + cta * kRows + row];
-      some = true;
+      for (int i = 0; i < 2 * N; ++i) m[i] = part_of(min(k0 + i, parts - 1))[2 * kRows * D + at_row];
+#pragma unroll
+      for (int i = 0; i < 2 * N; ++i)
+        if (is_there(min(k0 + i, parts - 1))) top = fmaxf(top, m[i]);
     }
-  }
+    for (int k0 = 0; k0 < parts; k0 += N) {
+      float m[N], l[N];
+      float4 v[N], w[N];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) top = fmaxf(top, m[i]);
-  tops[warp][lane] = top;
-  if (!__syncthreads_or(some)) return;  // all keys were one pair's, which has written o
+      for (int i = 0; i < N; ++i) {
+        const float* part = part_of(min(k0 + i, parts - 1));
+        m[i] = part[2 * kRows * D + at_row];
+        l[i] = part[2 * kRows * (D + 1) + at_row];
+        v[i] = *reinterpret_cast<const float4*>(part + cta * kRows * D + column * kRows + row * 4);
+        w[i] = *reinterpret_cast<const float4*>(part + cta * kRows * D + (column + 4) * kRows + row * 4);
+      }
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, tops[w][lane]);
-  float4 acc[kJoinColumns / 4];
-#pragma unroll
-  for (int i = 0; i < kJoinColumns / 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    if (m[i] == -INFINITY) continue;  // a part that is not there, or none of whose keys the row sees
-    const float f = ex2(m[i] - top);
-    const float* part = part_of(warp + kJoinWarps * i);
-    sum = fmaf(f, part[2 * kRows * (D + 1) + cta * kRows + row], sum);
-    const float4* o = reinterpret_cast<const float4*>(part + cta * kRows * D) + (kJoinColumns / 4) * blockIdx.z * kRows + row;
-#pragma unroll
-    for (int k = 0; k < kJoinColumns / 4; ++k) {
-      const float4 v = o[k * kRows];
-      acc[k] = make_float4(fmaf(f, v.x, acc[k].x), fmaf(f, v.y, acc[k].y), fmaf(f, v.z, acc[k].z), fmaf(f, v.w, acc[k].w));
+      for (int i = 0; i < N; ++i) {
+        if (k0 + i >= parts || !is_there(k0 + i) || m[i] == -INFINITY) continue;  // not there, or the row sees none of its keys
+        const float f = ex2(m[i] - top);
+        sum = fmaf(f, l[i], sum);
+        a = make_float4(fmaf(f, v[i].x, a.x), fmaf(f, v[i].y, a.y), fmaf(f, v[i].z, a.z), fmaf(f, v[i].w, a.w));
+        b = make_float4(fmaf(f, w[i].x, b.x), fmaf(f, w[i].y, b.y), fmaf(f, w[i].z, b.z), fmaf(f, w[i].w, b.w));
+      }
     }
-  }
-  sums[warp][lane] = sum;
-  __syncthreads();
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) sum += sums[w][lane];
+  };
+  if (parts <= 2) join(std::integral_constant<int, 2>{});
+  else join(std::integral_constant<int, 4>{});
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
-                       ((int64_t)(token + x / G) * p.h_q + head + x % G) * D + kJoinColumns * blockIdx.z;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {  // of the columns: a warp adds up four of them over the warps
-    if (half) __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kJoinColumns / 8; ++k) columns[warp][k][lane] = acc[half * (kJoinColumns / 8) + k];
-    __syncthreads();
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const float4 v = columns[w][warp][lane];
-      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
-    }
-    if (real)
-      *reinterpret_cast<uint2*>(out + half * (kJoinColumns / 2) + 4 * warp) =
-          make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+  if (real) {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)(token + x / G) * p.h_q + head + x % G) * D + column;
+    *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv),
+                                                pack_bf16(b.x * inv, b.y * inv), pack_bf16(b.z * inv, b.w * inv));
   }
 }
 
