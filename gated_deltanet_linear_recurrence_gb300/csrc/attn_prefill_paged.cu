@@ -25,7 +25,6 @@ constexpr int kThreads = 512;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of the softmax warps
 constexpr int kWideners = 2;         // warps of a CTA that write its half of K of an e4m3 tile, or of V
 constexpr int kNoted = 8;            // key tiles whose missing pages are noted
-constexpr int kAhead = 6;            // key tiles that e4m3 rows are brought into L2 ahead
 
 // Work, in keys: a tile of queries counts the keys that its rows see, and kTileCost for
 // taking it up (Q in, the first scores, O out).  A share is at least kMinShare.
@@ -349,7 +348,6 @@ struct Shared {  // beside the tiles
   Sums work;
   Place place;
   Join join;
-  int begun;                // e4m3: key tiles whose K is being widened or has been
   uint32_t groups[kNoted];  // which eights of a key tile's keys have a page
   // halves: the row maxima of a key tile's halves, two key tiles; groups: the
   // references of two key tiles
@@ -368,7 +366,6 @@ __device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other
                : "l"(src), "r"((int)valid), "r"(other));
   return x;
 }
-__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // 16 bytes of this CTA's shared memory to the same place in the even CTA's, counted on a
 // barrier there
 __device__ __forceinline__ void tell(const void* what, uint64_t* bar) {
@@ -465,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sh.v_edge[i], C::kArrivals);
       tc::mbar_init(&sh.v_clean[i], 1);
     }
-    sh.begun = 0;
     tc::mbar_init(&sh.o_free, 2 * 4);
     tc::mbar_init(&sh.drained, 1);
     tc::fence_mbar_init();
@@ -956,10 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             page = look(j + 2);
             const Keys keys = key_tile_of(t, j, window, sinks);
             if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(free_bar, h - C::kSlots)) != 0)) break;
-            if (wq == 0) {  // (for the first warp to say)
-              note(h, eight < keys.rows && rows == ~0u);
-              if (lane == 0) *const_cast<volatile int*>(&sh.begun) = h + 1;
-            }
+            if (wq == 0) note(h, eight < keys.rows && rows == ~0u);  // (for the first warp to say)
             uint8_t* const to_tile = to_warp + s * C::kEntry;
             bring_bytes(ahead, parity ^ 1);
 #pragma unroll 1
@@ -1155,48 +1148,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++used;
         last_copied = !kFp8 || t.wide >= 0;
-        for (int j = 0; j < t.count && ok; ++j) {
+        for (int j = 0; last_copied && j < t.count && ok; ++j) {
           const int h = g + j, s = h % C::kSlots;
           const Keys k = key_tile_of(t, j, window, sinks);
           const Where at = where(t, k, page);
-          const uint32_t r = at.row;
           page = look(t, j + 1);
-          if (kFp8 && t.wide < 0) {
-            // The rows of key tiles to come are brought into L2, K's by the even CTA, V's by the
-            // other, kAhead tiles before the warps that widen them.  (They say where they are in
-            // a number: this warp keeps nobody waiting, so that a barrier's phases might pass it by.)
-            const uint64_t since = tc::globaltimer_ns();
-            while (*const_cast<volatile int*>(&sh.begun) < h - kAhead) {
-              __nanosleep(200);
-              if (tc::globaltimer_ns() - since > 1000000000ull) {
-                ok = false;
-                break;
-              }
-            }
-            const int run = min(1 << shift, kKeys);  // keys of a tile that lie side by side
-            // (the exponent bytes too: eight at a time, K's by lanes 0 to 15)
-            if (rank == 0 && r != ~0u) prefetch_line((lane < 16 ? p.cache.k_exp : p.cache.v_exp) + r);
-            if (lane < 16 && (eight & (run - 1)) == 0 && r != ~0u)
-              tc::prefetch_l2(static_cast<const uint8_t*>(rank == 0 ? p.cache.k_pages : p.cache.v_pages) + (int64_t)r * D, run * D);
-            ok = __all_sync(kFullMask, ok) != 0;
-          } else {
-            const bool mine = lead && eight < k.rows && (lane >> 3) == (int)rank;
-            uint8_t* to = smem + C::kK + s * C::kEntry + (lane & 7) * 1024;
-            const uint32_t bytes = ((k.rows + box - 1) & -box) * D * 2;
-            if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.s_done, h - C::kSlots)) != 0)) break;
-            // the bytes of both CTAs count on the even CTA's barrier
-            if (rank == 0 && lane == 0) {
-              tc::mbar_arrive_expect_tx(&sh.k_full[s], bytes);
-              for (int i = 1; i < C::kArrivals; ++i) tc::mbar_arrive(&sh.k_full[s]);
-            }
-            if (mine) {
-#pragma unroll
-              for (int kb = 0; kb < D / 64; ++kb) tc2::tma_load_3d(to + kb * 8192, &tm_k, 64 * kb, at.y, at.z, r_k + s * 8);
-            }
-            __syncwarp();
-            note(h, eight < k.rows && r == ~0u);
-            kc = h + 1;
+          const bool mine = lead && eight < k.rows && (lane >> 3) == (int)rank;
+          uint8_t* to = smem + C::kK + s * C::kEntry + (lane & 7) * 1024;
+          const uint32_t bytes = ((k.rows + box - 1) & -box) * D * 2;
+          if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(sh.s_done, h - C::kSlots)) != 0)) break;
+          // the bytes of both CTAs count on the even CTA's barrier
+          if (rank == 0 && lane == 0) {
+            tc::mbar_arrive_expect_tx(&sh.k_full[s], bytes);
+            for (int i = 1; i < C::kArrivals; ++i) tc::mbar_arrive(&sh.k_full[s]);
           }
+          if (mine) {
+#pragma unroll
+            for (int kb = 0; kb < D / 64; ++kb) tc2::tma_load_3d(to + kb * 8192, &tm_k, 64 * kb, at.y, at.z, r_k + s * 8);
+          }
+          __syncwarp();
+          note(h, eight < k.rows && at.row == ~0u);
+          kc = h + 1;
         }
         g += t.count;
         if (!ok) break;
