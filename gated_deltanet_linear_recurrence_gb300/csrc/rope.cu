@@ -30,7 +30,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kAhead = 4;  // rows (D = 256; pairs of rows at 128) whose loads a warp has under way
 
 enum class To { kDense, kBF16, kE4M3 };
@@ -92,7 +92,7 @@ __device__ __forceinline__ float norm_factor(float4& a, float4& b, float eps) {
 }
 
 template <int D, bool kPairs, To kTo>
-__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 8) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kLanes = D / 8;        // lanes per row
   constexpr int kHeads = 32 / kLanes;  // rows a warp holds at once
   tc::allow_dependents();
