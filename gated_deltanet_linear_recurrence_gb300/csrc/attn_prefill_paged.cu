@@ -1,6 +1,52 @@
 // attn_prefill_paged.cu — attention of packed new tokens over the paged cache, bf16 or
 // e4m3: prompts, pieces of them, a few drafted tokens and single ones in one call, over
 // all keys before them or a window and the first few.
+//
+// For query row r (token and query head) at position p, which sees the keys j <= p with
+// j > p - window or j < sinks (all j <= p without a window):
+//     s_rj = scale q_r.k_j,   o_r = sum_j 2^(t_rj - m_r) v_j / l_r,
+//     t_rj = s_rj log2(e),    l_r = sum_j 2^(t_rj - m_r)
+// over 128-key tiles with a running reference m_r, on CTA pairs with tcgen05, as the
+// attention of packed prompts does it (attn_prefill.cu explains the pair's tile, its TMEM
+// and shared memory, the softmax and the care for values that are not finite).  What is
+// different here:
+//
+// Work.  (m, l, O) of disjoint sets of keys join by rescaling to the larger m.  So a pair's
+// share is not tiles of queries but an equal part of all keys that tiles of queries go
+// through, in (sequence, KV head, tile) order: single tokens over long caches and long
+// prompts fill the GPU alike, and the last wave of tiles costs nothing (2,048 tokens on
+// 16,000 keys 254 to 264 us, where whole tiles take 260 to 272).  The counts before a tile
+// are sums of max(0, x + i n) over its number i, which has a closed form, so each pair finds
+// its share by itself.  A tile of queries that several pairs go through is joined by a
+// second kernel, from (m, l, O) in the workspace, in the order of the pairs.
+//
+// Keys.  With a window a piece of work goes through the key tiles of the first keys, then
+// those from the window's first one on.  Tiles of which some row does not see some key are
+// edge tiles (masks; V looked through).  A position without a page is masked like them: the
+// warp that brings K notes which eights of a tile's keys have no page.
+//
+// bf16 rows come by TMA, up to 64 keys of a page at a time.  Pages of 16 keys cost 1 to 3 %,
+// of 8 keys 20 %: the copies are asked for one by one, and K and V have a warp each for it
+// (with one warp for both 2,000 tokens on 11,011, heads of 128, pages of 16, took 324 us
+// for 229).
+//
+// e4m3 rows are widened to bf16 (exact: a row's unit is a power of two), once for all tiles
+// of queries of a sequence, by a kernel before this one, where the sequence has kWideTiles or
+// more and the workspace has room; else by two warps for K and two for V, from codes that
+// they copy for themselves into the swizzled tiles that the products read.  Bound by those
+// warps' instructions: 58 for 16 codes of a lane, and by where they come from (see there).
+//
+// Measured, calls back to back (both kernels; "floor" is the larger of bytes at a plain
+// copy's rate and flops at a plain product's burst rate).  bf16: 2,048 tokens on 16,000
+// keys, 16 heads of 256 on 2, 264 to 290 us by the board's power, floor 261; 4,000 on 20,000
+// in a window of 4,096 192 to 204 us, floor 140 (a tile's window spans 34 or 35 key tiles for
+// 32 of keys, three of them edge tiles); 512 on 6,000 beside 24 single tokens, 32 heads of
+// 128 on 8, 102 us, floor 53; 32 tokens on 131,072 72 us, floor 41; five on a million 316 us,
+// 6.5 TB/s; 28 tokens of eight sequences on up to 4,090 keys 22 us (latency: 12 us of this
+// kernel before its last key tile, 4 of the join).  e4m3: 2,000 on 11,011, 32 heads of
+// 128 on 8, 244 us, floor 171 (409 widened by each tile of queries); 8 on 131,072 and 60,001
+// 113 us, floor 29; 64 single tokens in a window of 2,048 96 us, floor 19 (over bf16 rows
+// 67 us): 2.6 us a key tile of 128 x 256, of which 1.0 is the product's.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -195,17 +241,25 @@ struct Place {
     i = lo;
     start = at + w.before(s, i);
   }
-  __device__ __forceinline__ void next(const PagedPrefillArgs& p, const Work& w, int64_t end) {
+  __device__ __forceinline__ void next(const PagedPrefillArgs& p, const Work& w, int64_t end, int lane) {
     start = end;
     if (++i < s.tiles) return;
     i = 0;
     if (++kvh < p.cache.h_kv) return;
     kvh = 0;
-    do {
-      wide += w.wide(p, s);
-      if (++n >= p.num_seqs) return;
-      s = w.sequence(p, n, false);
-    } while (s.tiles == 0);
+    wide += w.wide(p, s);
+    for (++n; n < p.num_seqs; n += 32) {  // the next one with queries, 32 at a time
+      const Seq mine = w.sequence(p, n + lane, false);
+      const unsigned some = __ballot_sync(kFullMask, mine.tiles > 0);
+      if (some == 0) continue;
+      const int src = __ffs(some) - 1;
+      n += src;
+      s.q0 = __shfl_sync(kFullMask, mine.q0, src);
+      s.a = __shfl_sync(kFullMask, mine.a, src);
+      s.off = __shfl_sync(kFullMask, mine.off, src);
+      s.tiles = __shfl_sync(kFullMask, mine.tiles, src);
+      return;
+    }
   }
 };
 
@@ -499,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.join.token = t->token;
         sh.join.head = t->kvh * G;
       }
-      if (to == end) at.next(p, work, end);
+      if (to == end) at.next(p, work, end, lane);
       found_one = t->count > 0 || (all == 0 && r0 == 0);
     }
     if (!found_one) t->count = -1;

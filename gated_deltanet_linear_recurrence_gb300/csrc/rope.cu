@@ -146,8 +146,11 @@ __global__ void __launch_bounds__(kWarps * 32, 8) rope_kernel(const __grid_const
   int64_t pos = 0, row0 = 0;
   bool placed = true;
   if (kTo != To::kDense) {
-    int n;
-    placed = token_position(a.rows, t, lane, n, pos);
+    int n = t;
+    // (one token of each sequence, as a decoding step has: no search, 8.9 us for 256 with it)
+    const bool step = t < a.rows.num_seqs && __ldg(a.rows.cu_seqlens + t) == t && __ldg(a.rows.cu_seqlens + t + 1) == t + 1;
+    if (step) pos = __ldg(a.rows.start + t);
+    else placed = token_position(a.rows, t, lane, n, pos);
     if (g0 == 0) check_packing(a.rows, t, lane);
     if (!placed) return;
     row0 = g1 > q_groups ? position_row(a.rows, n, pos, lane) : -1;
