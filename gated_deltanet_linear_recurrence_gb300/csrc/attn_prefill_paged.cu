@@ -885,10 +885,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t r = row_of(t, key, entry_of(t, key, true));
               if (key >= lim || (key < low && key >= sinks) || r == ~0u) continue;
               if (kFp8) {
-                const uint8_t* src = static_cast<const uint8_t*>(p.cache.v_pages) + (int64_t)r * D + i;
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.cache.v_pages) + (int64_t)r * D + i);
+                const uint32_t byte = __ldg(p.cache.v_exp + r);
 #pragma unroll
-                for (int k = 0; k < C::kOut; ++k)
-                  if ((__ldg(src + k) & 0x7f) == 0x7f) ov[k] = NAN;
+                for (int k = 0; k < C::kOut; k += 16) {
+                  uint4 y[2];
+                  uint32_t odd = 0;
+                  widen16(__ldg(src + k / 16), value_units(byte, byte), y[0], y[1], odd);
+#pragma unroll
+                  for (int n = 0; n < 2; ++n) {
+                    const uint4 z = mend(y[n], byte);
+                    const uint32_t two[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      ov[k + 8 * n + 2 * e] += poison_of(two[e] & 0xffffu);
+                      ov[k + 8 * n + 2 * e + 1] += poison_of(two[e] >> 16);
+                    }
+                  }
+                }
               } else {
                 const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.cache.v_pages) + (int64_t)r * D + i);
 #pragma unroll

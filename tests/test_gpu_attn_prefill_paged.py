@@ -251,6 +251,27 @@ def test_what_is_not_seen(D, fp8):
     assert gdn_stream_status() == "GDN_OK"
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_codes_whose_values_overflow(D):
+    """A unit of 2^120 and a code of 448 read back as infinite: seen or not seen like one."""
+    b = Batch([70], [300], 8, 1, D, 16, True, 19)
+    clean = b.run()
+    for pos in (295, 100):
+        page, slot = int(b.table[0, pos // 16]), pos % 16
+        b.vp.view(torch.uint8)[page, 0, slot] = 0
+        b.vp.view(torch.uint8)[page, 0, slot, 3] = 0x7e
+        b.ve[page, 0, slot] = 247
+        got = b.run()
+        see = torch.from_numpy(seen(70, 300, 0, 0)[:, pos]).cuda()
+        assert torch.isinf(got[see][..., 3]).all() and torch.isfinite(got[~see]).all()
+        rest = got.clone()
+        rest[..., 3] = 0
+        assert torch.isfinite(rest).all()
+        assert not (~see).any() or ((got[~see] - clean[~see]).abs().max() < 0.1 * clean.abs().max())
+        b.ve[page, 0, slot] = 127
+    assert gdn_stream_status() == "GDN_OK"
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("page", [8, 64, 256])
 def test_missing_pages(page, fp8):
