@@ -90,17 +90,26 @@ struct Cfg {
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
   static constexpr int kArrivals = kFp8 ? kWideners : 1;  // that make K or V of a key tile full, beside bytes
   // Registers of a thread of the four warpgroups: softmax (two), epilogue, and the rest;
-  // together the 65,536 that the CTA starts with.
-  static constexpr int kSoftmaxRegs = kFp8 ? 160 : 168, kEpilogueRegs = kFp8 ? 112 : 88;
+  // together the 65,536 that the CTA starts with, of which a thread has 128.  What widens e4m3
+  // rows spills with fewer than all of those (64 tokens on 9,000 positions each, 112 212 us, 128
+  // 204), the softmax with fewer than 152 at D = 128 (2,000 tokens on 11,011: 144 248 us, 152 242).
+  static constexpr int kSoftmaxRegs = !kFp8 ? 168 : D == 256 ? 144 : 152, kEpilogueRegs = kFp8 ? 128 : 88;
   static constexpr int kOtherRegs = 512 - 2 * kSoftmaxRegs - kEpilogueRegs;
-  // columns of O that the epilogue holds (over e4m3 rows beside what widening them needs)
-  static constexpr int kOut = 32;
+  static_assert(kSoftmaxRegs >= 128 && kEpilogueRegs <= 128 && kOtherRegs <= 128, "more, and fewer");
+  static constexpr int kOut = 32;  // columns of O that the epilogue holds
   static constexpr uint32_t kQBytes = kRows * D * 2;
   static constexpr uint32_t kEntry = 64 * D * 2;  // half of K (64 keys) or of V (D / 2 dims)
   static constexpr int kSlots = D == 256 ? 2 : 4;  // key tiles of K, and of V, in shared memory
   static constexpr uint32_t kK = kQBytes, kV = kK + kSlots * kEntry;
-  static constexpr uint32_t kStage = kV + kSlots * kEntry;  // 64 columns of o on their way out
-  static constexpr uint32_t kShared = kStage + kRows * 128;  // the barriers and the rest
+  // Groups of e4m3 codes (2 KB) that a warp which widens them has under way.  D = 256, 5 tokens
+  // on 131,072 positions: one 140 us, two 114, three (all that fits) 107; D = 128: two 165, four
+  // 169.
+  static constexpr int kDeep = D == 256 ? 3 : 2;
+  // a warp's: 64 columns of o on their way out, and those codes
+  static constexpr uint32_t kStageWarp = kFp8 ? kDeep * 2048 : 32 * 128;
+  static_assert(kStageWarp >= 32 * 128, "64 columns of o");
+  static constexpr uint32_t kStage = kV + kSlots * kEntry;
+  static constexpr uint32_t kShared = kStage + 4 * kStageWarp;  // the barriers and the rest
   static constexpr int kSteps = D / 16;
   static constexpr uint32_t kTmemO = kS * kKeys;
   static constexpr uint32_t kTmemCols = 512;
@@ -617,8 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                : ~0u;
   };
 
-  // For the warp that brings K of key tile h: which eights of its keys have no page.  (It has
-  // waited for the scores of h - kSlots, before which the softmax was through with h - kNoted.)
+  // For the warp that brings K of key tile h, or over e4m3 rows V (which has less to do): which
+  // eights of its keys have no page.  (It has waited for the scores of h - kSlots, or the product
+  // with V, before which the softmax was through with h - kNoted.)
   auto note = [&](int h, bool missing) {
     const uint32_t gone = __ballot_sync(kFullMask, missing) & 0xffffu;
     if (lane == 0) {
@@ -812,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t r_free = tc2::in_cta(&sh.o_free, 0);
     // 32 rows of 128 bytes for each warp, 16-byte pieces c of row r at c ^ (r & 7)
-    uint8_t* stage = smem + C::kStage + wq * 4096;
+    uint8_t* stage = smem + C::kStage + wq * C::kStageWarp;
     // O of piece t, the used'th with keys, whose last key tile is h
     auto epilogue = [&](const Piece t, int used, int h) {
       const int tok0 = (int)rank * tok_cta;
@@ -976,26 +986,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* const to_warp = smem + (is_v ? C::kV : C::kK) + w2 * 1024;
       uint64_t* const free_bar = is_v ? sh.o_done : sh.s_done;
       uint64_t* const full_bar = is_v ? sh.v_full : sh.k_full;
-      uint8_t(*bytes)[64] = sh.bytes[wq];  // exponent bytes of the warp's eights, two key tiles
-      uint8_t* const codes_in = stage + lane * 16;  // two groups' codes, which a lane brings for itself
+      uint8_t(*bytes)[64] = sh.bytes[wq];  // exponent bytes of the warp's eights
+      uint8_t* const codes_in = stage + lane * 16;  // groups' codes, which a lane brings for itself
+      int slot = 0;  // of those: the oldest group's
       // group q of a key tile: number of its first eight among the warp's, its block
       auto eights_of = [&](int q) { return is_v ? 4 * (q / kBlocks) : 0; };
       auto block_of = [&](int q) { return is_v ? q % kBlocks : q; };
+      // (groups of the same eights follow each other: their rows are kept, and their units)
+      auto first_of_eights = [&](int q) { return is_v ? q % kBlocks == 0 : q == 0; };
+      uint32_t from[4], unit[4], high = 0;
       auto bring = [&](uint32_t rows, int q) {  // (always a group of copies, whether there are any)
-        const uint8_t* src = codes + 64 * block_of(q);
-        const int first = eight0 + 2 * eights_of(q);
+        if (first_of_eights(q)) {
+          const int first = eight0 + 2 * eights_of(q);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t r = __shfl_sync(kFullMask, rows, first + 2 * e);
-          copy16(codes_in + ((q & 1) * 4 + e) * 512, src + (int64_t)r * D, r != ~0u);
+          for (int e = 0; e < 4; ++e) from[e] = __shfl_sync(kFullMask, rows, first + 2 * e);
         }
+        const uint8_t* src = codes + 64 * block_of(q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) copy16(codes_in + (slot * 4 + e) * 512, src + (int64_t)from[e] * D, from[e] != ~0u);
         copy_commit();
+        if (++slot == C::kDeep) slot = 0;
       };
-      auto bring_bytes = [&](uint32_t rows, int parity) {  // (with the group that follows)
+      auto bring_bytes = [&](uint32_t rows, int b) {  // (with the group that follows)
         const uint32_t mine = __shfl_sync(kFullMask, rows, (eight0 + 2 * lane) & 15);
-        if (lane < (is_v ? 8 : 4)) copy8(&bytes[parity][8 * lane], exps + (int64_t)mine, mine != ~0u);
+        if (lane < (is_v ? 8 : 4)) copy8(&bytes[b][8 * lane], exps + (int64_t)mine, mine != ~0u);
       };
       int late_used = 0, late_h = 0, parity = 0, ve = 0;  // (ve: edge tiles so far)
+      auto start = [&](uint32_t rows) {
+        bring_bytes(rows, parity);
+#pragma unroll
+        for (int q = 0; q < C::kDeep; ++q) bring(rows, q);
+      };
       bool due = false;
       for (int pass = 0; ok; ++pass) {
         const bool more = next_tile(pass, &t);
@@ -1010,9 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t rows = rows_of(0, look(0));
         int page = look(1);
         copy_wait<0>();  // (the last ones, of no row, into the same places)
-        bring_bytes(rows, parity);
-        bring(rows, 0);
-        bring(rows, 1);
+        start(rows);
         for (int j = 0; ok; ++j) {
           const int h = g + j, s = h % C::kSlots;
           if (j < count) {
@@ -1020,28 +1039,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             page = look(j + 2);
             const Keys keys = key_tile_of(t, j, window, sinks);
             if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(free_bar, h - C::kSlots)) != 0)) break;
-            if (wq == 0) note(h, eight < keys.rows && rows == ~0u);  // (for the first warp to say)
+            if (wq == 2) note(h, eight < keys.rows && rows == ~0u);
             uint8_t* const to_tile = to_warp + s * C::kEntry;
             bring_bytes(ahead, parity ^ 1);
 #pragma unroll 1
             for (int q = 0; q < kGroupsOf; ++q) {
-              copy_wait<1>();
-              __syncwarp();  // (the bytes are other lanes')
+              copy_wait<C::kDeep - 1>();
               const uint8_t* byte_of = &bytes[parity][8 * eights_of(q) + r8];
+              if (first_of_eights(q)) {
+                __syncwarp();  // (the bytes are other lanes')
+                high = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t byte = byte_of[8 * e];
+                  unit[e] = value_units(byte, byte);
+                  high |= byte > kUnitTop ? 0x80u : 0u;
+                }
+              }
               uint8_t* to = to_tile + eights_of(q) * 2048 + block_of(q) * (is_v ? 16384 : 8192);
               uint4 x[4];
-              uint32_t byte[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const uint4*>(codes_in + (slot * 4 + e) * 512);
+              // into the place of these codes, which have been read, before they are worked on
+              bring(q + C::kDeep < kGroupsOf ? rows : ahead, (q + C::kDeep) % kGroupsOf);
+              uint32_t odd = high;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                x[e] = *reinterpret_cast<const uint4*>(codes_in + ((q & 1) * 4 + e) * 512);
-                byte[e] = byte_of[8 * e];
-              }
-              uint32_t odd = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                odd |= byte[e] > kUnitTop ? 0x80u : 0u;
                 uint4 lo, hi;
-                widen16(x[e], value_units(byte[e], byte[e]), lo, hi, odd);
+                widen16(x[e], unit[e], lo, hi, odd);
                 *reinterpret_cast<uint4*>(to + e * 2048 + put) = lo;
                 *reinterpret_cast<uint4*>(to + e * 2048 + put2) = hi;
               }
@@ -1053,7 +1078,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                   *reinterpret_cast<uint4*>(atom + put2) = mend(*reinterpret_cast<const uint4*>(atom + put2), byte_of[8 * e]);
                 }
               }
-              bring(q + 2 < kGroupsOf ? rows : ahead, (q + 2) % kGroupsOf);
             }
             parity ^= 1;
             tc::fence_proxy_async();  // the rows -> this CTA's tensor cores
@@ -1079,15 +1103,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ve += edge;
             rows = ahead;
           }
-          if (due && j == min(is_v ? 0 : C::kLag, max(0, count - 1))) {
+          if (due && j == min(C::kLag, max(0, count - 1))) {
             copy_wait<0>();
             __syncwarp();
             epilogue(sh.late[wq], late_used, late_h);
             due = false;
             // (what was under way went where the epilogue keeps o)
-            bring_bytes(rows, parity);
-            bring(rows, 0);
-            bring(rows, 1);
+            start(rows);
           }
           if (j + 1 >= count) break;
         }
