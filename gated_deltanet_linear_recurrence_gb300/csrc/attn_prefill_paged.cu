@@ -117,6 +117,14 @@ struct Cfg {
 };
 
 // ------------------------------------------------------------------ work
+// a table's entry, or another value; without a branch, behind which it would be waited for
+__device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other) {
+  int x;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+               : "=&r"(x)
+               : "l"(src), "r"((int)valid), "r"(other));
+  return x;
+}
 // One sequence's queries and keys (bad ones have no queries; recorded once).
 struct Seq {
   int q0, a, off, tiles;  // first row of q, queries, keys before the first of them, tiles of queries
@@ -143,9 +151,9 @@ struct Work {
 
   __device__ __forceinline__ Seq sequence(const PagedPrefillArgs& p, int n, bool report) const {
     Seq s{0, 0, 0, 0};
-    if (n >= p.num_seqs) return s;
-    const int q0 = __ldg(p.cu_q + n), q1 = __ldg(p.cu_q + n + 1);
-    int len = __ldg(p.cache_len + n);
+    const bool valid = n < p.num_seqs;
+    const int q0 = load_if(p.cu_q + n, valid, 0), q1 = load_if(p.cu_q + n + 1, valid, 0);
+    int len = load_if(p.cache_len + n, valid, 0);
     const bool bad = q0 < 0 || q1 < q0 || q1 > p.total_q;
     const bool open = (n == 0 && q0 != 0) || (n == p.num_seqs - 1 && q1 != p.total_q);
     const bool beyond = len < 0 || (int64_t)len > ((int64_t)p.cache.max_pages << p.cache.page_shift);
@@ -229,9 +237,10 @@ struct Found {
 struct Place {
   Seq s;
   int n, kvh, i;
-  int64_t start;
-  int64_t u, u_end, total;  // of a share: where it is, where it ends; all work
-  int64_t wide;             // rows of the widened copy before the sequence's
+  int64_t start, end;           // (end: -1 before it is known)
+  int64_t u0, u, u_end, total;  // of a share: where it starts, is and ends; all work
+  int64_t wide;                 // rows of the widened copy before the sequence's
+  int there;                    // which of its two parts there are, as bits
   __device__ __forceinline__ void find(const PagedPrefillArgs& p, const Work& w, const Found& f, int64_t u, int lane) {
     n = f.seq;
     wide = f.wide;
@@ -250,7 +259,7 @@ struct Place {
     i = lo;
     start = at + w.before(s, i);
   }
-  __device__ __forceinline__ void next(const PagedPrefillArgs& p, const Work& w, int64_t end, int lane) {
+  __device__ __forceinline__ void next(const PagedPrefillArgs& p, const Work& w, int lane) {
     start = end;
     if (++i < s.tiles) return;
     i = 0;
@@ -272,8 +281,10 @@ struct Place {
   }
 };
 
-// The share of pair c: false when there is none.  With up to 32 sequences every warp that
-// asks counts them for itself; with more the whole block takes part.
+// The share of pair c: false when there is none.  Up to kFew sequences are counted by the
+// schedule's warp alone (64 of them: 2 us; by the block, which meets twice, 6.6), more by the
+// whole block.
+constexpr int kFew = 256;
 __device__ __forceinline__ int sharers(int64_t total, int pairs) {
   return (int)min((int64_t)pairs, max((int64_t)1, quotient(total, kMinShare)));
 }
@@ -287,17 +298,39 @@ __device__ __forceinline__ int64_t scan_up(int64_t x, int lane) {
 }
 // total, and the sequence that holds work u of share c (its first piece of work)
 __device__ __forceinline__ bool find_few(const PagedPrefillArgs& p, const Work& w, int c, bool report, int lane, Found* f) {
-  const Seq s = w.sequence(p, lane, report);
-  const int64_t mine = s.tiles > 0 ? p.cache.h_kv * w.before(s, s.tiles) : 0;
+  const int per = (p.num_seqs + 31) / 32;  // sequences a lane counts
+  int64_t mine = 0, rows = 0;
+  for (int i = 0; i < per; i += 2) {
+    Seq s[2];  // (loaded together)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) s[k] = w.sequence(p, i + k < per ? lane * per + i + k : p.num_seqs, report);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      mine += s[k].tiles > 0 ? p.cache.h_kv * w.before(s[k], s[k].tiles) : 0;
+      rows += w.wide(p, s[k]);
+    }
+  }
   const int64_t incl = scan_up(mine, lane);
   f->total = __shfl_sync(kFullMask, incl, 31);
-  const int n = sharers(f->total, p.pairs);
-  if (f->total == 0 || c >= n) return false;
-  const int64_t u = Shares(f->total, n).start(c);
-  f->seq = __ffs(__ballot_sync(kFullMask, incl > u)) - 1;
-  f->base = __shfl_sync(kFullMask, incl - mine, f->seq);
-  const int64_t rows = w.wide(p, s);
-  f->wide = p.wide_rows > 0 ? __shfl_sync(kFullMask, scan_up(rows, lane) - rows, f->seq) : 0;
+  const int sharing = sharers(f->total, p.pairs);
+  if (f->total == 0 || c >= sharing) return false;
+  const int64_t u = Shares(f->total, sharing).start(c);
+  int n = lane * per;
+  int64_t base = incl - mine, wide = p.wide_rows > 0 ? scan_up(rows, lane) - rows : 0;
+  const int src = __ffs(__ballot_sync(kFullMask, incl > u)) - 1;
+  if (lane == src) {
+    for (int left = per - 1; left > 0; --left) {  // (in the last one, if in none before)
+      const Seq s = w.sequence(p, n, false);
+      const int64_t x = s.tiles > 0 ? p.cache.h_kv * w.before(s, s.tiles) : 0;
+      if (u < base + x) break;
+      base += x;
+      wide += w.wide(p, s);
+      ++n;
+    }
+  }
+  f->seq = __shfl_sync(kFullMask, n, src);
+  f->base = __shfl_sync(kFullMask, base, src);
+  f->wide = __shfl_sync(kFullMask, wide, src);
   return true;
 }
 struct Sums {  // the block's, for this
@@ -410,7 +443,6 @@ struct Shared {  // beside the tiles
   uint32_t tmem;
   Sums work;
   Place place;
-  Join join;
   uint32_t groups[kNoted];  // which eights of a key tile's keys have a page
   // halves: the row maxima of a key tile's halves, two key tiles; groups: the
   // references of two key tiles
@@ -421,14 +453,6 @@ struct Shared {  // beside the tiles
   alignas(16) uint8_t bytes[4][2][64];  // e4m3: exponent bytes of a warp's eights, two key tiles
 };
 
-// a table's entry, or another value; without a branch, behind which it would be waited for
-__device__ __forceinline__ int load_if(const int32_t* src, bool valid, int other) {
-  int x;
-  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
-               : "=&r"(x)
-               : "l"(src), "r"((int)valid), "r"(other));
-  return x;
-}
 // 16 bytes of this CTA's shared memory to the same place in the even CTA's, counted on a
 // barrier there
 __device__ __forceinline__ void tell(const void* what, uint64_t* bar) {
@@ -537,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int me = blockIdx.x / 2;
   Found found{0, 0, 0, 0};
   bool any = false;
-  if (p.num_seqs > 32) any = find_many<kThreads>(p, work, me, blockIdx.x == 0, sh.work, &found);
+  if (p.num_seqs > kFew) any = find_many<kThreads>(p, work, me, blockIdx.x == 0, sh.work, &found);
   else if (warp == kScheduleWarp) any = find_few(p, work, me, blockIdx.x == 0, lane, &found);
   // (the schedule warp keeps its place in shared memory: between two pieces it copies V)
   auto next_piece = [&](Piece* t) {
@@ -545,24 +569,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     bool found_one = false;
     while (at.u < at.u_end && !found_one) {
-      const int64_t keys = work.keys(at.s, at.i), end = at.start + kTileCost + keys;
-      const int64_t r0 = at.u - at.start, to = min(end, at.u_end);
+      if (at.u == at.end) at.next(p, work, lane);
+      const int64_t keys = work.keys(at.s, at.i), r0 = at.u - at.start;
+      at.end = at.start + kTileCost + keys;
+      at.u = min(at.end, at.u_end);
       *t = work.piece(at.s, at.n, at.kvh, at.i);
       const int64_t rows = kFp8 ? work.wide(p, at.s) : 0;
       t->wide = rows > 0 && at.wide + rows <= p.wide_rows ? (int32_t)at.wide : -1;
-      const int all = t->count, v0 = work.visits(r0, keys, all), v1 = work.visits(to - at.start, keys, all);
-      at.u = to;
+      const int all = t->count, v0 = work.visits(r0, keys, all), v1 = work.visits(at.u - at.start, keys, all);
       t->v0 = v0;
       t->count = v1 - v0;
       if (t->count < all) t->part = r0 > 0 ? 0 : 1;
-      if (lane == 0 && t->part >= 0 && t->count > 0) sh.join.there[t->part] = 1;
-      if (lane == 0 && to < end && r0 == 0) {
-        sh.join.last = Shares(at.total, sharers(at.total, p.pairs)).owner(end - 1);
-        sh.join.rows = min(work.tokens.d, t->left) * G;
-        sh.join.token = t->token;
-        sh.join.head = t->kvh * G;
-      }
-      if (to == end) at.next(p, work, end, lane);
+      if (t->part >= 0 && t->count > 0) at.there |= 1 << t->part;
       found_one = t->count > 0 || (all == 0 && r0 == 0);
     }
     if (!found_one) t->count = -1;
@@ -573,17 +591,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kScheduleWarp) {
     Place at;
     at.u = at.u_end = 0;
+    at.end = -1;
+    at.there = 0;
     if (any) {
       const Shares shares(found.total, sharers(found.total, p.pairs));
       at.total = found.total;
-      at.u = shares.start(me);
+      at.u0 = at.u = shares.start(me);
       at.u_end = shares.start(me + 1);
       at.find(p, work, found, at.u, lane);
     }
-    if (lane == 0) {
-      sh.place = at;
-      sh.join = Join{};
-    }
+    if (lane == 0) sh.place = at;
     __syncwarp();
     Piece t;
     next_piece(&t);
@@ -1207,7 +1224,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         g += t.count;
         t = next;
       }
-      if (rank == 0 && lane == 0) joins(p)[me] = sh.join;
+      if (rank == 0 && lane == 0) {
+        const Place& at = sh.place;
+        Join join{};
+        join.there[0] = at.there & 1;
+        join.there[1] = at.there >> 1;
+        if (at.u < at.end && at.start >= at.u0) {  // its last tile, which it has started
+          const int first = at.i * work.tokens.d;
+          join.last = Shares(at.total, sharers(at.total, p.pairs)).owner(at.end - 1);
+          join.rows = min(work.tokens.d, at.s.a - first) * G;
+          join.token = at.s.q0 + first;
+          join.head = at.kvh * G;
+        }
+        joins(p)[me] = join;
+      }
       // Copies still in flight land before the CTA ends: after an expired wait, the
       // even CTA's barriers tell of both CTAs' copies.
       if (lane == 0 && rank == 0 && last_copied) {

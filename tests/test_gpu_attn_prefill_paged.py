@@ -195,6 +195,22 @@ def test_many_sequences(D, fp8):
         Batch(new, lengths, 4, 2, D, 16, fp8, n).check()
 
 
+@pytest.mark.parametrize("n", [31, 32, 63, 64, 65, 255, 256, 257])
+def test_sequences_counted_by_a_warp_or_the_block(n):
+    """Up to 256 are counted by one warp, some a lane: empty ones in between and at both ends,
+    long ones (whose e4m3 rows are widened once) at places that end a lane's."""
+    new, lengths = [1] * n, [(7 * i) % 50 for i in range(n)]
+    for i in range(0, n, 5):
+        new[i] = 0
+    for i in (1, n // 2, n - 2):
+        new[i], lengths[i] = 150, 300 + i
+    new[-1] = 0
+    for fp8 in (False, True):
+        b = Batch(new, lengths, 8, 1, 128, 16, fp8, n)
+        b.check()
+        b.check(window=40, sinks=3)
+
+
 def test_weight_on_one_row():
     """Each query puts all its weight on one cached row, which its output has to be."""
     for fp8 in (False, True):
