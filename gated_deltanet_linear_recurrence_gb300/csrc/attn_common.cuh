@@ -79,9 +79,9 @@ struct Divisor {
   int d;
   uint32_t inv;
   __device__ __forceinline__ explicit Divisor(int by) : d(by), inv(0xffffffffu / (uint32_t)by + 1u) {}
-  __device__ __forceinline__ int divide(int x) const {
-    const int q = (int)__umulhi((uint32_t)x, inv);
-    return (int64_t)q * d > x ? q - 1 : q;
+  __device__ __forceinline__ uint32_t divide(uint32_t x) const {
+    const uint32_t q = __umulhi(x, inv);
+    return (uint64_t)q * (uint32_t)d > x ? q - 1 : q;
   }
 };
 

@@ -171,7 +171,7 @@ struct Work {
   __device__ __forceinline__ int64_t ramp(int64_t x, int m) const {
     if (m <= 0 || x + (int64_t)(m - 1) * tokens.d <= 0) return 0;
     // (-x < m tokens, which a sequence's queries bound)
-    const int k = x >= 0 ? 0 : (int)((uint32_t)(-x + tokens.d - 1) / (uint32_t)tokens.d);
+    const int k = x >= 0 ? 0 : (int)tokens.divide((uint32_t)(-x + tokens.d - 1));
     const int64_t n = m - k;
     return n * (x + (int64_t)k * tokens.d) + tokens.d * (n * (n - 1) / 2);
   }
@@ -220,7 +220,7 @@ struct Work {
 // What a pair leaves for the joining pass: which of its parts there are, and the tile of
 // queries that it has started and not finished (rows 0: none), whose keys pairs up to `last`
 // go through.
-struct Join {
+struct alignas(16) Join {
   int32_t there[2];
   int32_t last, rows;
   int32_t token, head;  // the tile's first row of q, and query head
@@ -553,6 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&sh.drained, 1);
     tc::fence_mbar_init();
   }
+  if (lane == 0 && warp == kTmaWarp) {
+    tc::prefetch_tmap(&tm_q);
+    tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_v);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t sbase = tc::smem_u32(smem);
+  bool ok = true;
   tc::wait_prerequisites();  // q, the cache, its table, the offsets and lengths come from earlier kernels
   tc::allow_dependents();
 
@@ -604,23 +616,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     Piece t;
     next_piece(&t);
-    if (lane == 0) sh.tile[0] = t;
+    if (lane == 0) {
+      sh.tile[0] = t;
+      tc::mbar_arrive(&sh.tile_full[0]);
+    }
+    __syncwarp();
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::cluster_sync();
-  tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem;
-  const uint32_t sbase = tc::smem_u32(smem);
-  bool ok = true;
 
   // wait for what a barrier by key tile says of key tile h
   auto of_tile = [&](uint64_t* bars, int h) { return tc::mbar_wait(&bars[h % C::kSlots], (h / C::kSlots) & 1); };
 
   // The warp's next piece (pass counts them); false at the end or when a wait expired.
   auto next_tile = [&](int pass, Piece* t) {
-    // (the first is there from the start; of tile_full's phases it takes none)
-    const bool w = pass == 0 || __all_sync(kFullMask, tc::mbar_wait(&sh.tile_full[pass & 1], ((pass - 1) >> 1) & 1));
+    const bool w = __all_sync(kFullMask, tc::mbar_wait(&sh.tile_full[pass & 1], (pass >> 1) & 1));
     if (!w) {
       ok = false;
       return false;
@@ -1179,7 +1187,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       int g = 0, vc = 0, ve = 0;  // key tiles; up to which V was asked for; edge tiles
       bool last_copied = false;
       const uint32_t r_v = tc2::in_cta(sh.v_full, 0), r_ve = tc2::in_cta(sh.v_edge, 0);
-      if (lane == 0) tc::prefetch_tmap(&tm_v);
       for (int pass = 1; t.count >= 0 && ok; ++pass) {
         Piece next;
         next_piece(&next);
@@ -1251,10 +1258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kc = 0;           // key tiles up to which K was asked for
       bool last_copied = false;
       const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_q = tc2::in_cta(&sh.q_full, 0);
-      if (lane == 0) {
-        tc::prefetch_tmap(&tm_q);
-        tc::prefetch_tmap(&tm_k);
-      }
       for (int pass = 0; next_tile(pass, &t); ++pass) {
         if (t.count == 0) continue;
         int page = look(t, 0);
@@ -1556,10 +1559,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_paged_join_kerne
   tc::allow_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   tc::wait_prerequisites();  // the parts
+  // (what there is to know is read at once, of the pairs that may have parts: kMasks times 32)
   const Join* js = joins(p);
-  const int rows = __ldg(&js[c].rows), x = 32 * blockIdx.y + lane;
+  const int4 facts = __ldg(reinterpret_cast<const int4*>(&js[c]));  // there, last, rows
+  const int2 place = __ldg(reinterpret_cast<const int2*>(&js[c].token));
+  int other[kMasks];
+#pragma unroll
+  for (int i = 0; i < kMasks; ++i) {
+    const int k = 32 * i + lane;
+    other[i] = __ldg(&js[min(c + k, p.pairs - 1)].there[k == 0]);
+  }
+  const int last = facts.z, rows = facts.w, token = place.x, head = place.y, x = 32 * blockIdx.y + lane;
   if (32 * (int)blockIdx.y >= rows) return;
-  const int last = __ldg(&js[c].last), token = __ldg(&js[c].token), head = __ldg(&js[c].head);
   const int G = p.h_q / p.cache.h_kv, even = min(kRows / G * G, rows);  // rows of the even CTA
   const bool real = x < rows;
   const int cta = x >= even, row = real ? x - cta * even : 0;
@@ -1567,8 +1578,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_paged_join_kerne
   uint32_t there[kMasks], any = 0;
 #pragma unroll
   for (int i = 0; i < kMasks; ++i) {
-    const int k = 32 * i + lane;
-    there[i] = __ballot_sync(kFullMask, c + k <= last && __ldg(&js[c + k].there[k == 0]));
+    there[i] = __ballot_sync(kFullMask, c + 32 * i + lane <= last && other[i]);
     any |= there[i];
   }
   if (any == 0) return;  // all keys were one pair's, which has written o
@@ -1579,26 +1589,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_paged_join_kerne
     for (int i = 1; i < kMasks; ++i) m = k >= 32 * i ? there[i] : m;
     return ((m >> (k & 31)) & 1) != 0;
   };
-  auto part_of = [&](int k) { return p.partial + (int64_t)(2 * (c + k) + (k == 0)) * (2 * kRows * (D + 2)); };
   const int at_row = cta * kRows + row, column = kJoinColumns * blockIdx.z + 8 * warp;
   float top = -INFINITY, sum = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  auto scale = [](float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); };
   auto join = [&](auto batch) {
     constexpr int N = decltype(batch)::value;  // parts whose loads go out together
-    for (int k0 = 0; k0 < parts; k0 += 2 * N) {
-      float m[2 * N];
-#pragma unroll
-      for (int i = 0; i < 2 * N; ++i) m[i] = part_of(min(k0 + i, parts - 1))[2 * kRows * D + at_row];
-#pragma unroll
-      for (int i = 0; i < 2 * N; ++i)
-        if (is_there(min(k0 + i, parts - 1))) top = fmaxf(top, m[i]);
-    }
     for (int k0 = 0; k0 < parts; k0 += N) {
-      float m[N], l[N];
+      float m[N], l[N], most = top;
       float4 v[N], w[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float* part = part_of(min(k0 + i, parts - 1));
+        const int k = min(k0 + i, parts - 1);
+        const float* part = p.partial + (int64_t)(2 * (c + k) + (k == 0)) * (2 * kRows * (D + 2));
         m[i] = part[2 * kRows * D + at_row];
         l[i] = part[2 * kRows * (D + 1) + at_row];
         v[i] = *reinterpret_cast<const float4*>(part + cta * kRows * D + column * kRows + row * 4);
@@ -1606,7 +1609,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_paged_join_kerne
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (k0 + i >= parts || !is_there(k0 + i) || m[i] == -INFINITY) continue;  // not there, or the row sees none of its keys
+        // not there, or the row sees none of its keys
+        if (k0 + i >= parts || !is_there(k0 + i)) m[i] = -INFINITY;
+        most = fmaxf(most, m[i]);
+      }
+      if (top != most && top != -INFINITY) {
+        const float f = ex2(top - most);
+        sum *= f;
+        a = scale(a, f);
+        b = scale(b, f);
+      }
+      top = most;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (m[i] == -INFINITY) continue;
         const float f = ex2(m[i] - top);
         sum = fmaf(f, l[i], sum);
         a = make_float4(fmaf(f, v[i].x, a.x), fmaf(f, v[i].y, a.y), fmaf(f, v[i].z, a.z), fmaf(f, v[i].w, a.w));
