@@ -79,6 +79,7 @@ struct Divisor {
   int d;
   uint32_t inv;
   __device__ __forceinline__ explicit Divisor(int by) : d(by), inv(0xffffffffu / (uint32_t)by + 1u) {}
+  __device__ __forceinline__ Divisor(int by, uint32_t inverse) : d(by), inv(inverse) {}  // (as above)
   __device__ __forceinline__ uint32_t divide(uint32_t x) const {
     const uint32_t q = __umulhi(x, inv);
     return (uint64_t)q * (uint32_t)d > x ? q - 1 : q;

@@ -111,6 +111,8 @@ struct PagedPrefillArgs {
   int32_t h_q;
   int32_t window, sinks;  // keys a query sees of the last (0: all), and of the first
   int32_t pairs;          // of CTAs that share the work
+  int32_t group, tile;    // query heads a KV head, tokens of a pair (the launch fills these in)
+  uint32_t tile_inv;      // floor((2^32 - 1) / tile) + 1
   float scale;
   // e4m3: room for rows that are widened once, [wide_rows][h_kv][D] bf16 of K and of V
   void* wide_k;

@@ -147,7 +147,7 @@ struct Work {
   Divisor tokens;  // of a pair
   __device__ __forceinline__ explicit Work(const PagedPrefillArgs& p)
       : window(p.window), reach((int64_t)p.window + p.sinks), sinks(p.window ? p.sinks : 0),
-        tokens(2 * (kRows / (p.h_q / p.cache.h_kv))) {}
+        tokens(p.tile, p.tile_inv) {}
 
   __device__ __forceinline__ Seq sequence(const PagedPrefillArgs& p, int n, bool report) const {
     Seq s{0, 0, 0, 0};
@@ -230,7 +230,9 @@ struct alignas(16) Join {
 struct Found {
   int64_t total, base;  // all work, that before sequence seq
   int64_t wide;         // rows of the widened copy that the sequences before it take
+  int64_t work;         // of it, all heads
   int seq;
+  Seq s;
 };
 
 // A place in the work: tile i of KV head kvh of sequence n, which starts at `start`.
@@ -244,8 +246,8 @@ struct Place {
   __device__ __forceinline__ void find(const PagedPrefillArgs& p, const Work& w, const Found& f, int64_t u, int lane) {
     n = f.seq;
     wide = f.wide;
-    s = w.sequence(p, n, false);
-    const int64_t head = w.before(s, s.tiles);
+    s = f.s;
+    const int64_t head = quotient(f.work, p.cache.h_kv);
     kvh = (int)quotient(u - f.base, head);
     const int64_t at = f.base + kvh * head;
     // the last tile that starts at u or before: 32 probes a step
@@ -257,7 +259,7 @@ struct Place {
       hi = min(hi, lo + step);
     }
     i = lo;
-    start = at + w.before(s, i);
+    start = at + (i > 0 ? w.before(s, i) : 0);
   }
   __device__ __forceinline__ void next(const PagedPrefillArgs& p, const Work& w, int lane) {
     start = end;
@@ -299,38 +301,39 @@ __device__ __forceinline__ int64_t scan_up(int64_t x, int lane) {
 // total, and the sequence that holds work u of share c (its first piece of work)
 __device__ __forceinline__ bool find_few(const PagedPrefillArgs& p, const Work& w, int c, bool report, int lane, Found* f) {
   const int per = (p.num_seqs + 31) / 32;  // sequences a lane counts
-  int64_t mine = 0, rows = 0;
-  for (int i = 0; i < per; i += 2) {
-    Seq s[2];  // (loaded together)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) s[k] = w.sequence(p, i + k < per ? lane * per + i + k : p.num_seqs, report);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      mine += s[k].tiles > 0 ? p.cache.h_kv * w.before(s[k], s[k].tiles) : 0;
-      rows += w.wide(p, s[k]);
-    }
+  int n = lane * per;
+  auto work_of = [&](const Seq& s) { return s.tiles > 0 ? p.cache.h_kv * w.before(s, s.tiles) : 0; };
+  Seq s = w.sequence(p, n, report);  // of the lane's, the first
+  int64_t x = work_of(s);
+  int64_t mine = x, rows = w.wide(p, s);
+  for (int i = 1; i < per; ++i) {
+    const Seq more = w.sequence(p, n + i, report);
+    mine += work_of(more);
+    rows += w.wide(p, more);
   }
   const int64_t incl = scan_up(mine, lane);
   f->total = __shfl_sync(kFullMask, incl, 31);
   const int sharing = sharers(f->total, p.pairs);
   if (f->total == 0 || c >= sharing) return false;
   const int64_t u = Shares(f->total, sharing).start(c);
-  int n = lane * per;
   int64_t base = incl - mine, wide = p.wide_rows > 0 ? scan_up(rows, lane) - rows : 0;
   const int src = __ffs(__ballot_sync(kFullMask, incl > u)) - 1;
   if (lane == src) {
-    for (int left = per - 1; left > 0; --left) {  // (in the last one, if in none before)
-      const Seq s = w.sequence(p, n, false);
-      const int64_t x = s.tiles > 0 ? p.cache.h_kv * w.before(s, s.tiles) : 0;
-      if (u < base + x) break;
+    while (u >= base + x) {  // (it is one of the lane's)
       base += x;
       wide += w.wide(p, s);
-      ++n;
+      s = w.sequence(p, ++n, false);
+      x = work_of(s);
     }
   }
   f->seq = __shfl_sync(kFullMask, n, src);
   f->base = __shfl_sync(kFullMask, base, src);
   f->wide = __shfl_sync(kFullMask, wide, src);
+  f->work = __shfl_sync(kFullMask, x, src);
+  f->s.q0 = __shfl_sync(kFullMask, s.q0, src);
+  f->s.a = __shfl_sync(kFullMask, s.a, src);
+  f->s.off = __shfl_sync(kFullMask, s.off, src);
+  f->s.tiles = __shfl_sync(kFullMask, s.tiles, src);
   return true;
 }
 struct Sums {  // the block's, for this
@@ -375,6 +378,8 @@ __device__ __noinline__ bool find_many(const PagedPrefillArgs& p, const Work& w,
         sh.found.seq = n;
         sh.found.base = before;
         sh.found.wide = wide;
+        sh.found.work = x;
+        sh.found.s = s;
         break;
       }
       before += x;
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Shared<D, kFp8>& sh = *reinterpret_cast<Shared<D, kFp8>*>(smem + C::kShared);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = tc::cluster_rank();
-  const int G = p.h_q / p.cache.h_kv;
+  const int G = p.group;
   const int tok_cta = kRows / G;  // tokens a CTA
   const int window = p.window, sinks = window ? p.sinks : 0;
   if (warp == 0) {
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- this pair's share, and its pieces one after the other (for the schedule warp)
   const Work work(p);
   const int me = blockIdx.x / 2;
-  Found found{0, 0, 0, 0};
+  Found found{};
   bool any = false;
   if (p.num_seqs > kFew) any = find_many<kThreads>(p, work, me, blockIdx.x == 0, sh.work, &found);
   else if (warp == kScheduleWarp) any = find_few(p, work, me, blockIdx.x == 0, lane, &found);
@@ -1571,7 +1576,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_paged_join_kerne
   }
   const int last = facts.z, rows = facts.w, token = place.x, head = place.y, x = 32 * blockIdx.y + lane;
   if (32 * (int)blockIdx.y >= rows) return;
-  const int G = p.h_q / p.cache.h_kv, even = min(kRows / G * G, rows);  // rows of the even CTA
+  const int G = p.group, even = min(kRows / G * G, rows);  // rows of the even CTA
   const bool real = x < rows;
   const int cta = x >= even, row = real ? x - cta * even : 0;
   // which parts there are: k of the tile is in slot 1 of pair c, in slot 0 of the pairs after it
@@ -1730,6 +1735,9 @@ cudaError_t launch_attn_prefill_paged(const PagedPrefillArgs& in, cudaStream_t s
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   PagedPrefillArgs a = in;
+  a.group = a.h_q / a.cache.h_kv;
+  a.tile = 2 * (kRows / a.group);
+  a.tile_inv = 0xffffffffu / (uint32_t)a.tile + 1u;
   a.pairs = sms / 2 < kPagedPrefillMaxPairs ? sms / 2 : kPagedPrefillMaxPairs;
   const bool fp8 = a.cache.dtype == kCacheE4M3;
   if (a.cache.head_dim == 256) return fp8 ? launch<256, true>(a, stream) : launch<256, false>(a, stream);
