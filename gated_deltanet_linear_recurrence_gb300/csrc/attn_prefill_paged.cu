@@ -15,7 +15,8 @@
 // share is not tiles of queries but an equal part of all keys that tiles of queries go
 // through, in (sequence, KV head, tile) order: single tokens over long caches and long
 // prompts fill the GPU alike, and the last wave of tiles costs nothing (2,048 tokens on
-// 16,000 keys 254 to 264 us, where whole tiles take 260 to 272).  The counts before a tile
+// 16,000 keys 254 to 264 us, where whole tiles take 260 to 272; 2 tokens on 16,000 keys 22
+// us for 139).  The counts before a tile
 // are sums of max(0, x + i n) over its number i, which has a closed form, so each pair finds
 // its share by itself.  A tile of queries that several pairs go through is joined by a
 // second kernel, from (m, l, O) in the workspace, in the order of the pairs.
@@ -25,7 +26,7 @@
 // edge tiles (masks; V looked through).  A position without a page is masked like them: the
 // warp that brings K notes which eights of a tile's keys have no page.
 //
-// bf16 rows come by TMA, up to 64 keys of a page at a time.  Pages of 16 keys cost 1 to 3 %,
+// bf16 rows come by TMA, up to 64 keys of a page at a time.  Pages of 16 keys cost 1 to 2 %,
 // of 8 keys 20 %: the copies are asked for one by one, and K and V have a warp each for it
 // (with one warp for both 2,000 tokens on 11,011, heads of 128, pages of 16, took 324 us
 // for 229).
@@ -34,19 +35,21 @@
 // of queries of a sequence, by a kernel before this one, where the sequence has kWideTiles or
 // more and the workspace has room; else by two warps for K and two for V, from codes that
 // they copy for themselves into the swizzled tiles that the products read.  Bound by those
-// warps' instructions: 58 for 16 codes of a lane, and by where they come from (see there).
+// warps: 58 instructions for 16 codes of a lane at one warp a scheduler, and by where they come
+// from (see there): a key tile takes 1.3 us at D = 128 and 2.1 at 256, its products 0.7 and 1.4.
 //
 // Measured, calls back to back (both kernels; "floor" is the larger of bytes at a plain
 // copy's rate and flops at a plain product's burst rate).  bf16: 2,048 tokens on 16,000
-// keys, 16 heads of 256 on 2, 264 to 290 us by the board's power, floor 261; 4,000 on 20,000
-// in a window of 4,096 192 to 204 us, floor 140 (a tile's window spans 34 or 35 key tiles for
-// 32 of keys, three of them edge tiles); 512 on 6,000 beside 24 single tokens, 32 heads of
-// 128 on 8, 102 us, floor 53; 32 tokens on 131,072 72 us, floor 41; five on a million 316 us,
-// 6.5 TB/s; 28 tokens of eight sequences on up to 4,090 keys 22 us (latency: 12 us of this
-// kernel before its last key tile, 4 of the join).  e4m3: 2,000 on 11,011, 32 heads of
-// 128 on 8, 244 us, floor 171 (409 widened by each tile of queries); 8 on 131,072 and 60,001
-// 113 us, floor 29; 64 single tokens in a window of 2,048 96 us, floor 19 (over bf16 rows
-// 67 us): 2.6 us a key tile of 128 x 256, of which 1.0 is the product's.
+// keys, 16 heads of 256 on 2, 254 to 290 us by the board's power, floor 261; 4,000 on 20,000
+// in a window of 4,096 188 to 200 us, floor 140 (a tile's window spans 34 or 35 key tiles for
+// 32 of keys, three of them edge tiles, and a tile of queries costs 12 us beside its key tiles);
+// 512 on 6,000 beside 24 single tokens, 32 heads of 128 on 8, 101 us, floor 53 (products of
+// 256 rows for the single tokens' four, as long as their rows take to come, and neither under
+// the other); 32 tokens on 131,072 69 us, floor 41; five on a million 315 us, 6.5 TB/s; 28
+// tokens of eight sequences on up to 4,090 keys 19 us (latency: 7 us from the start to
+// the first scores, 4 of the join).  e4m3: 2,000 on 11,011, 32 heads of 128 on 8, 243 us,
+// floor 171 (409 widened by each tile of queries); 8 on 131,072 and 60,001 98 us, floor 29; 64
+// single tokens in a window of 2,048 81 us, floor 19 (over bf16 rows 61 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -73,10 +76,14 @@ constexpr int kWideners = 2;         // warps of a CTA that write its half of K 
 constexpr int kNoted = 8;            // key tiles whose missing pages are noted
 
 // Work, in keys: a tile of queries counts the keys that its rows see, and kTileCost for
-// taking it up (Q in, the first scores, O out).  A share is at least kMinShare.
+// taking it up (Q in, the first scores, O out): 512 tokens on 6,000 beside 24 single ones took
+// 128 us with 128, 116 with 256, 106 with 384, 107 with 640.  A share is at least kMinShare: 28
+// tokens on up to 4,090 keys took 22.8 us with 384, 24.1 with 768, 29.3 with 1,536.
 constexpr int kTileCost = 384, kMinShare = 384;
 // e4m3 rows of a sequence with at least so many tiles of queries are widened once, into the
-// workspace, where there is room
+// workspace, where there is room: that writes and reads back four bytes a code, some 20 us for
+// 11,011 rows of 8 heads of 128, where each tile of queries that widens for itself takes 12 us
+// more (32 of them 409 us for 243)
 constexpr int kWideTiles = 3;
 
 template <int D, bool kFp8>
@@ -413,11 +420,17 @@ __device__ __forceinline__ Keys key_tile_of(const Piece& t, int j, int window, i
   k.edge = k.first + kKeys > whole || max(k.first, sinks) < min(k.first + kKeys, low);
   return k;
 }
-// the first row of an edge tile's V that may need care (those before, every row sees)
-__device__ __forceinline__ int edge_row(const Piece& t, const Keys& k, int window, int sinks) {
+// Which rows of an edge tile's V may need care (the others, every row of queries sees): those
+// before the window of the last one, and those after the position of the first, in sixteens.
+struct Care {
+  int before, from;
+};
+__device__ __forceinline__ Care care_of(const Piece& t, const Keys& k, int window, int sinks) {
   const int low = window ? max(0, t.sight - window) : 0;
-  if (max(k.first, sinks) < min(k.first + kKeys, low)) return 0;
-  return max(0, t.pos + 1 - k.first) & ~15;
+  Care c;
+  c.before = max(k.first, sinks) < min(k.first + kKeys, low) ? low - k.first : 0;
+  c.from = max(0, t.pos + 1 - k.first) & ~15;
+  return c;
 }
 // how many of a piece's key tiles are edge tiles, for a warp that does not go through them
 __device__ __forceinline__ int edges_of(const Piece& t, int window, int sinks, int lane) {
@@ -919,8 +932,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < t.count; ++j) {
             const Keys keys = key_tile_of(t, j, window, sinks);
             if (!keys.edge) continue;
+            const Care care = care_of(t, keys, window, sinks);
 #pragma unroll 1
-            for (int x = edge_row(t, keys, window, sinks); x < keys.rows; ++x) {
+            for (int x = care.before > 0 ? 0 : care.from; x < keys.rows; ++x) {
               const int key = keys.first + x;
               const uint32_t r = row_of(t, key, entry_of(t, key, true));
               if (key >= lim || (key < low && key >= sinks) || r == ~0u) continue;
@@ -1399,7 +1413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Keys keys = key_tile_of(t, j, window, sinks);
           if (!keys.edge) continue;
           const int h = g + j, rows = keys.rows;  // rows of V that some query sees
-          const int row0 = edge_row(t, keys, window, sinks);
+          const Care care = care_of(t, keys, window, sinks);
+          const int row0 = care.before > 0 ? 0 : care.from;
           if (!(ok = __all_sync(kFullMask, tc2::wait(&sh.v_edge[edges % C::kSlots], (edges / C::kSlots) & 1)))) break;
           const uint32_t slot = h % C::kSlots * C::kEntry;
           // the largest of the magnitudes, as 16-bit integers (a non-finite one is 0x7f80 or
@@ -1407,6 +1422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t most = 0;
 #pragma unroll 1
           for (int r = row0; r < rows; r += 16) {
+            if (r >= care.before && r < care.from) {
+              r = care.from - 16;
+              continue;
+            }
             // eight loads in flight: both halves' rows at D = 128, a half's at 256
 #pragma unroll
             for (int c = 0; c < D / 16; c += 8) {
