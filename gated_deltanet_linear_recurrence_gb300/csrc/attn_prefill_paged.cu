@@ -81,10 +81,11 @@ constexpr int kNoted = 8;            // key tiles whose missing pages are noted
 // tokens on up to 4,090 keys took 22.8 us with 384, 24.1 with 768, 29.3 with 1,536.
 constexpr int kTileCost = 384, kMinShare = 384;
 // e4m3 rows of a sequence with at least so many tiles of queries are widened once, into the
-// workspace, where there is room: that writes and reads back four bytes a code, some 20 us for
-// 11,011 rows of 8 heads of 128, where each tile of queries that widens for itself takes 12 us
-// more (32 of them 409 us for 243)
-constexpr int kWideTiles = 3;
+// workspace, where there is room (it writes and reads back four bytes a code, and is a kernel
+// more).  Once, or by each tile: tiles of 64 tokens on 11,011 rows of 8 heads of
+// 128: three 52, 57 us, four 60, 70, thirty-two 242, 410; of 32 tokens on 16,000 rows of 2 heads of
+// 256: three 47, 43, four 47, 48, five 51, 54; three on 1,500 rows of 8 heads of 128 28, 23.
+constexpr int kWideTiles = 4;
 
 template <int D, bool kFp8>
 struct Cfg {
@@ -1494,8 +1495,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The rows of e4m3 sequences with many tiles of queries, widened once: a warp a row of all
-// heads, for a block's 32 rows after the sequences have been counted as find_many does.
-constexpr int kWidenThreads = 256, kWidenRows = 32;
+// heads, for a block's rows (some 16 KB of codes) after the sequences have been counted as find_many does.
+// (At 8 heads of 128 16 rows a block took 104 us with 600 tokens' attention on 11,011 rows, 32
+// 109; at 2 of 256 for 96 on 16,000 16 rows 47.3, 32 46.1.)
+constexpr int kWidenThreads = 256;
+inline __host__ __device__ int widen_rows_of_block(int h_kv, int D) {
+  const int rows = 16384 / (h_kv * D);
+  return rows < 8 ? 8 : rows > 32 ? 32 : rows;
+}
 template <int D>
 __global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const __grid_constant__ PagedPrefillArgs p) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
@@ -1505,7 +1512,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const __grid_
   tc::allow_dependents();
   tc::wait_prerequisites();
   const Work work(p);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, block_rows = widen_rows_of_block(p.cache.h_kv, D);
   const int per = (p.num_seqs - 1) / kWidenThreads + 1;  // sequences a thread counts
   const int lo = (int)min((int64_t)p.num_seqs, (int64_t)tid * per), hi = (int)min((int64_t)p.num_seqs, (int64_t)lo + per);
   int64_t mine = 0;
@@ -1519,7 +1526,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const __grid_
     total += sums[k];
   }
   total = min(total, p.wide_rows);  // (the rows of a sequence that ends beyond are not used)
-  for (int64_t first = (int64_t)blockIdx.x * kWidenRows; first < total; first += (int64_t)gridDim.x * kWidenRows) {
+  for (int64_t first = (int64_t)blockIdx.x * block_rows; first < total; first += (int64_t)gridDim.x * block_rows) {
     __syncthreads();
     if (before <= first && first < before + mine) {
       int64_t base = before;
@@ -1536,7 +1543,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const __grid_
     __syncthreads();
     int n = found_seq;
     int64_t base = found_base, rows = work.wide(p, work.sequence(p, n, false));
-    for (int64_t row = first + warp; row < min(total, first + kWidenRows); row += kWidenThreads / 32) {
+    for (int64_t row = first + warp; row < min(total, first + block_rows); row += kWidenThreads / 32) {
       while (row >= base + rows) {  // (there is one: row < total)
         base += rows;
         rows = work.wide(p, work.sequence(p, ++n, false));
@@ -1718,7 +1725,8 @@ cudaError_t launch(const PagedPrefillArgs& a, cudaStream_t stream) {
   cfg.numAttrs = 2;
   if (a.wide_rows > 0) {
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)min((int64_t)16 * a.pairs, (a.wide_rows + kWidenRows - 1) / kWidenRows));
+    const int rows_of_block = widen_rows_of_block(a.cache.h_kv, D);
+    cfg.gridDim = dim3((unsigned)min((int64_t)16 * a.pairs, (a.wide_rows + rows_of_block - 1) / rows_of_block));
     cfg.blockDim = dim3(kWidenThreads);
     e = cudaLaunchKernelEx(&cfg, widen_rows_kernel<D>, a);
     if (e != cudaSuccess) return e;
