@@ -346,3 +346,22 @@ def test_binding_refuses():
                            axes=[0] * 32)
     torch.cuda.synchronize()
     assert gdn_stream_status() == "GDN_OK"
+
+
+def test_outputs_share_an_allocation_and_nothing_else():
+    q, k = torch.randn(5, 3, 128).bfloat16().cuda(), torch.randn(5, 2, 128).bfloat16().cuda()
+    pos, f = torch.zeros(5, dtype=torch.int32).cuda(), torch.ones(8).cuda()
+    a, b = gdn_qk_norm_rope(q, k, pos, f)  # (position 0: as they were)
+    assert a.shape == q.shape and b.shape == k.shape and a.is_contiguous() and b.is_contiguous()
+    a.zero_()
+    assert torch.equal(b, k) and a._version == 1 and b._version == 0
+    b.fill_(2)
+    assert not a.any()
+    del a
+    torch.full((5, 3, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert (b == 2).all()
+    with torch.inference_mode():
+        a, b = gdn_qk_norm_rope(q, k, pos, f)
+        assert torch.equal(a, q) and torch.equal(b, k) and b.is_inference()
+    a, b = gdn_qk_norm_rope(q[:0], k[:0], pos[:0], f)
+    assert a.shape == (0, 3, 128) and b.shape == (0, 2, 128)
