@@ -458,8 +458,9 @@ struct Shared {  // beside the tiles
   uint64_t flags_in[4];
   uint32_t poison[4];
   uint64_t tile_full[2], tile_empty[2], drained;
+  uint64_t copy_v[2];  // e4m3: V of a piece (by number & 1) may be copied
   Piece tile[2], late[4];
-  uint32_t tmem;
+  uint32_t tmem, failed;
   Sums work;
   Place place;
   uint32_t groups[kNoted];  // which eights of a key tile's keys have a page
@@ -555,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.m_ready[i][k], 1);
       tc::mbar_init(&sh.tile_full[i], 1);
+      tc::mbar_init(&sh.copy_v[i], 1);
       tc::mbar_init(&sh.sums_in[i], 8);
       // readers: the softmax, epilogue and TMA warps, and in the even CTA the products' and edge warps
       tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : 1));
@@ -570,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::mbar_init(&sh.o_free, 2 * 4);
     tc::mbar_init(&sh.drained, 1);
+    sh.failed = 0;
     tc::fence_mbar_init();
   }
   if (lane == 0 && warp == kTmaWarp) {
@@ -1062,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < C::kDeep; ++q) bring(rows, q);
       };
-      bool due = false;
+      bool due = false, late_wide = false;
       for (int pass = 0; ok; ++pass) {
         const bool more = next_tile(pass, &t);
         if (!ok) break;
@@ -1077,9 +1080,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int page = look(1);
         copy_wait<0>();  // (the last ones, of no row, into the same places)
         start(rows);
-        for (int j = 0; ok; ++j) {
+        // After a piece that was copied, whose key tiles these warps have not waited for one by
+        // one, its epilogue comes first: by then all its products are done, and the waits for
+        // free slots are for the barriers' present phases.
+        const int when = late_wide ? -1 : min(C::kLag, max(0, count - 1));
+        for (int j = min(when, 0); ok; ++j) {
           const int h = g + j, s = h % C::kSlots;
-          if (j < count) {
+          if (j >= 0 && j < count) {
             const uint32_t ahead = rows_of(j + 1, page);
             page = look(j + 2);
             const Keys keys = key_tile_of(t, j, window, sinks);
@@ -1148,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ve += edge;
             rows = ahead;
           }
-          if (due && j == min(C::kLag, max(0, count - 1))) {
+          if (due && j == when) {
             copy_wait<0>();
             __syncwarp();
             epilogue(sh.late[wq], late_used, late_h);
@@ -1163,6 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         late_used = used;
         late_h = g + tiles - 1;
+        late_wide = count < tiles;
         due = true;
         if (tiles > 0) {
           if (is_v && count == 0) ve += edges_of(t, window, sinks, lane);
@@ -1218,6 +1226,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh.tile[pass & 1] = next;
           tc::mbar_arrive(&sh.tile_full[pass & 1]);
         }
+        // Before a copied piece there may be ones that were widened, whose key tiles this warp has
+        // not waited for one by one: it goes on when their scores are done (and so all products
+        // with V up to kSlots key tiles before this piece's first), which the other copying warp
+        // tells for each piece in turn; of those, it is never two ahead, as this warp hands the
+        // pieces out.
+        if (kFp8 && !(ok = __all_sync(kFullMask, tc::mbar_wait(&sh.copy_v[(pass - 1) & 1], ((pass - 1) >> 1) & 1)) != 0)) break;
         const bool copied = !kFp8 || t.wide >= 0;  // (not widened by warps of their own)
         if (!copied) ve += edges_of(t, window, sinks, lane);
         if (t.count > 0) last_copied = copied;
@@ -1279,11 +1293,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool last_copied = false;
       const uint32_t r_k = tc2::in_cta(sh.k_full, 0), r_q = tc2::in_cta(&sh.q_full, 0);
       for (int pass = 0; next_tile(pass, &t); ++pass) {
-        if (t.count == 0) continue;
+        if (t.count == 0) {
+          if (kFp8 && lane == 0) tc::mbar_arrive(&sh.copy_v[pass & 1]);
+          continue;
+        }
         int page = look(t, 0);
         if (used > 0) ok = __all_sync(kFullMask, tc::mbar_wait(&sh.q_empty, (used - 1) & 1)) != 0;
         if (!ok) break;
         if (lane == 0) {
+          if (kFp8) tc::mbar_arrive(&sh.copy_v[pass & 1]);
           if (rank == 0) tc::mbar_arrive_expect_tx(&sh.q_full, 2u * (uint32_t)(tok_cta * G) * D * 2);
           for (int kb = 0; kb < D / 64; ++kb)
             tc2::tma_load_3d(smem + kb * 16384, &tm_q, 64 * kb, t.kvh * G, t.token + (int)rank * tok_cta, r_q);
@@ -1485,11 +1503,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (!ok) raise_error(p.err, kErrDeviceTimeout);
+  if (!ok) {
+    raise_error(p.err, kErrDeviceTimeout);
+    if (kFp8) sh.failed = 1;
+  }
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();  // neither CTA's memory is in use by the other any more
+  // (but for what the odd CTA has told and the even one, which gave up, not waited for: 16 bytes
+  // on their way, some 1 us)
+  if (kFp8 && rank == 0 && sh.failed) __nanosleep(100000);
   tc::fence_after_sync();
   if (warp == 0) tc2::tmem_dealloc(tmem, C::kTmemCols);
 }

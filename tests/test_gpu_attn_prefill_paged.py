@@ -184,6 +184,22 @@ def test_widened_once_or_by_each_tile(D):
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("D,h_kv", [(128, 1), (256, 1), (128, 4)])
+def test_pieces_widened_and_copied_in_turn(D, h_kv):
+    """Over e4m3 rows a pair goes from a piece whose rows are copied (widened once) to one that it
+    widens for itself and back, with more key tiles in each than there are slots for."""
+    new, lengths = [], []
+    for i in range(5):
+        new += [5, 300, 1, 2, 0, 160]
+        lengths += [5000 - 700 * i, 3000 + 111 * i, 1500, 2900 + i, 40, 2500]
+    b = Batch(new, lengths, 8 * h_kv, h_kv, D, 32, True, D + h_kv)
+    got = b.check()
+    for _ in range(5):
+        assert torch.equal(b.run(), got)
+    b.check(window=1100, sinks=200)
+    assert gdn_stream_status() == "GDN_OK"
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("D", [128, 256])
 def test_many_sequences(D, fp8):
