@@ -80,6 +80,10 @@ constexpr int kNoted = 8;            // key tiles whose missing pages are noted
 // 128 us with 128, 116 with 256, 106 with 384, 107 with 640.  A share is at least kMinShare: 28
 // tokens on up to 4,090 keys took 22.8 us with 384, 24.1 with 768, 29.3 with 1,536.
 constexpr int kTileCost = 384, kMinShare = 384;
+// Over e4m3 rows a key counts more in tiles of queries that widen it for themselves (at times
+// the time: 1.3 us a key tile of 128 at D = 128, 2.1 at 256) than in those that find it widened
+// (0.8, 1.2): 512 tokens on 6,000 beside 24 single ones 156 us, all alike 177.
+constexpr int kNarrowWeight = 7, kWideWeight = 4;
 // e4m3 rows of a sequence with at least so many tiles of queries are widened once, into the
 // workspace, where there is room (it writes and reads back four bytes a code, and is a kernel
 // more).  Once, or by each tile: tiles of 64 tokens on 11,011 rows of 8 heads of
@@ -149,6 +153,7 @@ struct Piece {
   int32_t wide;        // row of the widened copy that holds position 0, or -1
 };
 
+template <bool kFp8>
 struct Work {
   int64_t window, reach;  // reach = window + sinks
   int sinks;
@@ -175,6 +180,12 @@ struct Work {
     s.tiles = s.a > 0 ? tokens.divide(s.a - 1) + 1 : 0;
     return s;
   }
+  // of a sequence's keys (whether there is room to widen them or not, so that the same shares
+  // and results come out), and of kMinShare's
+  __device__ __forceinline__ int weight(const Seq& s) const {
+    return !kFp8 ? 1 : s.tiles >= kWideTiles ? kWideWeight : kNarrowWeight;
+  }
+  __device__ __forceinline__ int unit() const { return kFp8 ? kNarrowWeight : 1; }
   // sum over i < m of max(0, x + i tokens)
   __device__ __forceinline__ int64_t ramp(int64_t x, int m) const {
     if (m <= 0 || x + (int64_t)(m - 1) * tokens.d <= 0) return 0;
@@ -189,7 +200,7 @@ struct Work {
     if (m > 0 && m == s.tiles)
       x -= max((int64_t)0, s.off + (int64_t)m * tokens.d) - max((int64_t)0, (int64_t)s.off + s.a);
     if (window) x -= ramp((int64_t)s.off + 1 - reach, m);
-    return x + (int64_t)m * kTileCost;
+    return weight(s) * (x + (int64_t)m * kTileCost);
   }
   // keys that tile i counts
   __device__ __forceinline__ int64_t keys(const Seq& s, int i) const {
@@ -218,11 +229,11 @@ struct Work {
   __device__ __forceinline__ int64_t wide(const PagedPrefillArgs& p, const Seq& s) const {
     return p.wide_rows > 0 && s.tiles >= kWideTiles ? (int64_t)s.off + s.a : 0;
   }
-  // how many of a tile's `count` key tiles lie before work r of it
-  __device__ __forceinline__ int visits(int64_t r, int64_t keys, int count) const {
-    if (r <= kTileCost) return 0;
-    if (r >= kTileCost + keys) return count;
-    return (int)quotient((r - kTileCost) * count, keys);
+  // how many of a tile's `count` key tiles lie before work r of it, at `weight` a key
+  __device__ __forceinline__ int visits(int64_t r, int64_t keys, int weight, int count) const {
+    r -= weight * kTileCost;
+    keys *= weight;
+    return r <= 0 ? 0 : r >= keys ? count : (int)quotient(r * count, keys);
   }
 };
 // What a pair leaves for the joining pass: which of its parts there are, and the tile of
@@ -251,7 +262,8 @@ struct Place {
   int64_t u0, u, u_end, total;  // of a share: where it starts, is and ends; all work
   int64_t wide;                 // rows of the widened copy before the sequence's
   int there;                    // which of its two parts there are, as bits
-  __device__ __forceinline__ void find(const PagedPrefillArgs& p, const Work& w, const Found& f, int64_t u, int lane) {
+  template <class W>
+  __device__ __forceinline__ void find(const PagedPrefillArgs& p, const W& w, const Found& f, int64_t u, int lane) {
     n = f.seq;
     wide = f.wide;
     s = f.s;
@@ -269,7 +281,8 @@ struct Place {
     i = lo;
     start = at + (i > 0 ? w.before(s, i) : 0);
   }
-  __device__ __forceinline__ void next(const PagedPrefillArgs& p, const Work& w, int lane) {
+  template <class W>
+  __device__ __forceinline__ void next(const PagedPrefillArgs& p, const W& w, int lane) {
     start = end;
     if (++i < s.tiles) return;
     i = 0;
@@ -295,8 +308,9 @@ struct Place {
 // schedule's warp alone (64 of them: 2 us; by the block, which meets twice, 6.6), more by the
 // whole block.
 constexpr int kFew = 256;
-__device__ __forceinline__ int sharers(int64_t total, int pairs) {
-  return (int)min((int64_t)pairs, max((int64_t)1, quotient(total, kMinShare)));
+template <class W>
+__device__ __forceinline__ int sharers(const W& w, int64_t total, int pairs) {
+  return (int)min((int64_t)pairs, max((int64_t)1, quotient(total, w.unit() * kMinShare)));
 }
 __device__ __forceinline__ int64_t scan_up(int64_t x, int lane) {
 #pragma unroll
@@ -307,7 +321,8 @@ __device__ __forceinline__ int64_t scan_up(int64_t x, int lane) {
   return x;
 }
 // total, and the sequence that holds work u of share c (its first piece of work)
-__device__ __forceinline__ bool find_few(const PagedPrefillArgs& p, const Work& w, int c, bool report, int lane, Found* f) {
+template <class W>
+__device__ __forceinline__ bool find_few(const PagedPrefillArgs& p, const W& w, int c, bool report, int lane, Found* f) {
   const int per = (p.num_seqs + 31) / 32;  // sequences a lane counts
   int n = lane * per;
   auto work_of = [&](const Seq& s) { return s.tiles > 0 ? p.cache.h_kv * w.before(s, s.tiles) : 0; };
@@ -321,7 +336,7 @@ __device__ __forceinline__ bool find_few(const PagedPrefillArgs& p, const Work& 
   }
   const int64_t incl = scan_up(mine, lane);
   f->total = __shfl_sync(kFullMask, incl, 31);
-  const int sharing = sharers(f->total, p.pairs);
+  const int sharing = sharers(w, f->total, p.pairs);
   if (f->total == 0 || c >= sharing) return false;
   const int64_t u = Shares(f->total, sharing).start(c);
   int64_t base = incl - mine, wide = p.wide_rows > 0 ? scan_up(rows, lane) - rows : 0;
@@ -348,8 +363,8 @@ struct Sums {  // the block's, for this
   int64_t of[16], rows[16];
   Found found;
 };
-template <int kT>
-__device__ __noinline__ bool find_many(const PagedPrefillArgs& p, const Work& w, int c, bool report, Sums& sh, Found* f) {
+template <int kT, class W>
+__device__ __noinline__ bool find_many(const PagedPrefillArgs& p, const W& w, int c, bool report, Sums& sh, Found* f) {
   static_assert(kT <= 512, "sums");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.num_seqs - 1) / kT + 1;  // sequences a thread counts
@@ -375,7 +390,7 @@ __device__ __noinline__ bool find_many(const PagedPrefillArgs& p, const Work& w,
     }
     total += sh.of[k];
   }
-  const int sharing = sharers(total, p.pairs);
+  const int sharing = sharers(w, total, p.pairs);
   if (total == 0 || c >= sharing) return false;  // (for all threads alike)
   const int64_t u = Shares(total, sharing).start(c);
   if (before <= u && u < before + mine) {
@@ -591,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::allow_dependents();
 
   // ---- this pair's share, and its pieces one after the other (for the schedule warp)
-  const Work work(p);
+  const Work<kFp8> work(p);
   const int me = blockIdx.x / 2;
   Found found{};
   bool any = false;
@@ -605,12 +620,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (at.u < at.u_end && !found_one) {
       if (at.u == at.end) at.next(p, work, lane);
       const int64_t keys = work.keys(at.s, at.i), r0 = at.u - at.start;
-      at.end = at.start + kTileCost + keys;
+      const int weight = work.weight(at.s);
+      at.end = at.start + weight * (kTileCost + keys);
       at.u = min(at.end, at.u_end);
       *t = work.piece(at.s, at.n, at.kvh, at.i);
       const int64_t rows = kFp8 ? work.wide(p, at.s) : 0;
       t->wide = rows > 0 && at.wide + rows <= p.wide_rows ? (int32_t)at.wide : -1;
-      const int all = t->count, v0 = work.visits(r0, keys, all), v1 = work.visits(at.u - at.start, keys, all);
+      const int all = t->count, v0 = work.visits(r0, keys, weight, all), v1 = work.visits(at.u - at.start, keys, weight, all);
       t->v0 = v0;
       t->count = v1 - v0;
       if (t->count < all) t->part = r0 > 0 ? 0 : 1;
@@ -628,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     at.end = -1;
     at.there = 0;
     if (any) {
-      const Shares shares(found.total, sharers(found.total, p.pairs));
+      const Shares shares(found.total, sharers(work, found.total, p.pairs));
       at.total = found.total;
       at.u0 = at.u = shares.start(me);
       at.u_end = shares.start(me + 1);
@@ -1272,7 +1288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         join.there[1] = at.there >> 1;
         if (at.u < at.end && at.start >= at.u0) {  // its last tile, which it has started
           const int first = at.i * work.tokens.d;
-          join.last = Shares(at.total, sharers(at.total, p.pairs)).owner(at.end - 1);
+          join.last = Shares(at.total, sharers(work, at.total, p.pairs)).owner(at.end - 1);
           join.rows = min(work.tokens.d, at.s.a - first) * G;
           join.token = at.s.q0 + first;
           join.head = at.kvh * G;
@@ -1535,7 +1551,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const __grid_
   __shared__ int found_seq;
   tc::allow_dependents();
   tc::wait_prerequisites();
-  const Work work(p);
+  const Work<true> work(p);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, block_rows = widen_rows_of_block(p.cache.h_kv, D);
   const int per = (p.num_seqs - 1) / kWidenThreads + 1;  // sequences a thread counts
   const int lo = (int)min((int64_t)p.num_seqs, (int64_t)tid * per), hi = (int)min((int64_t)p.num_seqs, (int64_t)lo + per);
