@@ -59,10 +59,10 @@ def test_workspace(lib):
         least = size(16, 2, d)
         assert least > 0 and least % 16 == 0
         assert call(lib, d=d, bytes=least - 1) == SMALL and call(lib, d=d, bytes=0) == SMALL
-        # eight heads on a KV head: 32 tokens a tile of queries; room for widened rows from a third tile on
-        assert size(16, 2, d, e4m3, 64) == least and size(16, 2, d, e4m3, 65) == least + (128 << 20)
+        # eight heads on a KV head: 32 tokens a tile of queries; room for widened rows from a fourth tile on
+        assert size(16, 2, d, e4m3, 96) == least and size(16, 2, d, e4m3, 97) == least + (128 << 20)
         assert size(16, 2, d, torch.bfloat16, 10 ** 9) == least
-    assert size(3, 3, 128, e4m3, 512) == size(3, 3, 128) and size(3, 3, 128, e4m3, 513) > size(3, 3, 128)
+    assert size(3, 3, 128, e4m3, 768) == size(3, 3, 128) and size(3, 3, 128, e4m3, 769) > size(3, 3, 128)
     for bad in ((16, 2, 64), (18, 2, 256), (0, 1, 128), (16, 2, 256, e4m3, -1)):
         assert size(*bad) == 0
     assert lib.gdn_attn_prefill_paged_workspace_size(16, 2, 256, 7, 0) == 0
