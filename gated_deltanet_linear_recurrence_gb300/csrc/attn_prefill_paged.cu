@@ -23,8 +23,8 @@
 //
 // Keys.  With a window a piece of work goes through the key tiles of the first keys, then
 // those from the window's first one on.  Tiles of which some row does not see some key are
-// edge tiles (masks; V looked through).  A position without a page is masked like them: the
-// warp that brings K notes which eights of a tile's keys have no page.
+// edge tiles (masks; V looked through).  A position without a page is masked like them: a
+// warp that brings K or V notes which eights of a tile's keys have no page.
 //
 // bf16 rows come by TMA, up to 64 keys of a page at a time.  Pages of 16 keys cost 1 to 2 %,
 // of 8 keys 20 %: the copies are asked for one by one, and K and V have a warp each for it

@@ -638,7 +638,7 @@ gdn_status gdn_attn_prefill_paged(const void* q, int64_t q_stride, const void* k
 /* Workspace bytes for gdn_attn_prefill_paged with these heads, a cache of that type and up to
  * total_q queries (it does not depend on the sequences or the cache's size); 0 for invalid
  * arguments.  What is needed is the value for total_q = 0; with an e4m3 cache and more
- * queries than two tiles hold, it has room besides (128 MB) in which the rows of sequences
+ * queries than three tiles hold, it has room besides (128 MB) in which the rows of sequences
  * with many queries are widened to bf16 once instead of by every tile of queries: those
  * that fit, in order, so any size from the former on is taken, and the results are the same. */
 size_t gdn_attn_prefill_paged_workspace_size(int32_t h_q, int32_t h_kv, int32_t head_dim,
