@@ -901,12 +901,23 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
     // stage the state.  Every hand-off is an mbarrier with a bounded wait.
     const int rl = 32 * (warp & 1) + lane;  // accumulator row of this thread within its half
     // Output of chunk cp (the warps on lanes 64-127): O = Gamma Q S^T + P U, in
-    // two parts.  take_gates(cp) waits for P U, reads the rows' output factors
-    // and releases the chunk's tail stage early, so that the next tail copy has
-    // time to land; write_output(cp) forms and stores the rows after the next
-    // state has been staged, so that its global stores neither compete with the
-    // U warps' shared-memory stores nor delay the state (D and P U are
-    // triple-buffered in TMEM for that).
+    // two parts.  take_gates(cp) waits for P U and reads the rows' output factors,
+    // after which the chunk's tail stage is released; write_output(cp) forms and
+    // stores the rows after the next state has been staged, so that its global
+    // stores neither compete with the U warps' shared-memory stores nor delay the
+    // state (D and P U are triple-buffered in TMEM for that).
+    //
+    // The stage is rewritten by bulk copies, through the async proxy, which an
+    // arrival alone does not order behind ordinary reads: a factor that was still
+    // on its way when its thread arrived came out as that of chunk cp + NSTG, in
+    // one of 10^7 to 10^8 chunks (of 28,000 passes over 131,072 tokens 78, in
+    // pieces of 8,192 637).  So a fence.proxy.async stands between the read and
+    // the arrival.  The two-kernel form has one of its own, so that the tail copy
+    // has time to land (32,768 tokens 724 us; 719 without the fence, 794 with the
+    // arrival behind the state's staging); the cooperative form arrives behind the
+    // fence of that staging (16,384 tokens 306 us; with a fence of its own 326,
+    // without one 315).
+    const bool late_release = item_flags != nullptr;
     auto take_gates = [&](int cp) {
       const int stp = cp % NSTG;
       // P U of chunk cp + 3 is issued only after these warps stage chunk cp + 3's
@@ -915,8 +926,11 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
       tc::fence_after_sync();
       const float gr =
           reinterpret_cast<const float*>(smem + CF::CC_GATE + stp * kGateBytes)[rl];
-      tc::fence_before_sync();
-      tc::mbar_arrive(&tempty[stp]);
+      if (!late_release) {
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        tc::mbar_arrive(&tempty[stp]);
+      }
       return gr;
     };
     auto write_output = [&](int cp, float Gam_r) {
@@ -1057,6 +1071,7 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
             p.state_out[(srow0 + 32 * b0 + i) * DKP + jrow] = sc[i];
       } else {
         stage_state(sc, c + 1);
+        if (late_release && (warp & 3) >= 2 && c > 0) tc::mbar_arrive(&tempty[(c - 1) % NSTG]);
       }
       if ((warp & 3) >= 2 && c > 0) write_output(c - 1, gam_prev);  // after the staging
     }
