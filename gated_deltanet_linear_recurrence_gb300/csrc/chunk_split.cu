@@ -638,10 +638,12 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                                              ~static_cast<uintptr_t>(1023));
   const int pt = threadIdx.x;
   const int64_t item = blockIdx.x;
-  // The chain kernel may launch once every CTA of this grid has started; its
-  // CTAs need an SM with room, so they start as this grid drains.
-  allow_dependents();
+  // The chain kernel may launch once every CTA of this grid is past its wait (it
+  // reads the offsets, which an earlier kernel may have written, before its own
+  // wait for this grid); its CTAs need an SM with room, so they start as this grid
+  // drains.
   wait_prerequisites();  // the chunk table of the plan kernel
+  allow_dependents();
   int n, c;
   if (!item_chunk(p, item, n, c)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PP_MISC);

@@ -1,8 +1,8 @@
 """The chunked evaluations give the same bits over and over: a hand-off between their warps
 that holds nearly always shows after some thousands of passes only.  Output factors that were
 read too late came out wrong in one of 10^7 to 10^8 chunks: in 250 of 37,000 passes over
-32,768 tokens in pieces of 8,192, and in some ten of 4,000 over 8,192 at once; the packed and
-the cooperative form share that code."""
+32,768 tokens in pieces of 8,192, in some ten of 4,000 over 8,192 at once and in some five of as
+many in the cooperative form."""
 import pytest
 import torch
 
@@ -56,3 +56,28 @@ def test_whole_calls_repeat_themselves(lengths, algo, passes):
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     same(lambda: gdn_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], x["cu_seqlens"],
                              state_in=x["state_in"], algo=algo, workspace=ws), passes)
+
+
+@pytest.mark.parametrize("algo", ["chunked_split", "chunked_coop"])
+def test_offsets_that_the_kernel_before_has_written(algo):
+    """One tensor of offsets for prompts of two lengths in turn, filled by the kernel right
+    before each call: no warp of a call may see those of the call before."""
+    long, short = data([640]), data([64])
+    cu = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ends = torch.tensor([[0, 640], [0, 64]], dtype=torch.int32, device="cuda")
+    ws = torch.empty(gdn_prefill_workspace_size(1, 640, 16, 32, 128, 128, torch.bfloat16, algo),
+                     dtype=torch.uint8, device="cuda")
+
+    def call(i):
+        x = (long, short)[i]
+        cu.copy_(ends[i])
+        return gdn_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, state_in=x["state_in"],
+                           algo=algo, workspace=ws)
+
+    refs = [call(0), call(1)]
+    for n in range(1000):
+        for i in (0, 1):
+            o, s = call(i)
+            assert torch.equal(o, refs[i][0]), report("o", n, o, refs[i][0])
+            assert torch.equal(s, refs[i][1]), report("state", n, s, refs[i][1])
+    assert gdn_stream_status() == "GDN_OK"
