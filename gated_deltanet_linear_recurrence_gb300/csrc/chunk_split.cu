@@ -812,6 +812,9 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
     if (lane == 0) {
       tc::prefetch_tmap(tm_q);
       tc::prefetch_tmap(tm_k);
+      // the packages' gates and decayed K were stored by ordinary stores, and the
+      // copies below read them through the async proxy
+      if (!item_flags) asm volatile("fence.proxy.async.global;" ::: "memory");
       for (int c = 0; c < nchunks && ok; ++c) {
         const int st = c % NSTG;
         const int64_t item = first_item + (int64_t)c * p.h_v;
