@@ -24,7 +24,9 @@
 // Keys.  With a window a piece of work goes through the key tiles of the first keys, then
 // those from the window's first one on.  Tiles of which some row does not see some key are
 // edge tiles (masks; V looked through).  A position without a page is masked like them: a
-// warp that brings K or V notes which eights of a tile's keys have no page.
+// warp that brings K or V notes which eights of a tile's keys have no page.  Pages of which no
+// query sees a key (before the window's first one, a tile starts at a multiple of 128) are not
+// looked up: they may be gone.
 //
 // bf16 rows come by TMA, up to 64 keys of a page at a time.  Pages of 16 keys cost 1 to 2 %,
 // of 8 keys 20 %: the copies are asked for one by one, and K and V have a warp each for it
@@ -676,9 +678,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) tc::mbar_arrive(&sh.tile_empty[pass & 1]);
     return t->count >= 0;
   };
+  // Whether key `key` of a tile that starts before the window of the first row, or of the first
+  // keys, is in a page of which some row sees a key: a page that nobody sees need not be there.
+  const int shift = p.cache.page_shift;
+  auto seen_page = [&](const Piece& t, int key) {
+    const int low = window && t.pos >= window ? t.pos + 1 - window : 0;  // first key of the window
+    return (key | ((1 << shift) - 1)) >= low || key >> shift << shift < sinks;
+  };
+  // Whether the warp's lanes look key `first` + `eight` of key tile k up.
+  auto wanted = [&](const Piece& t, const Keys& k, int eight) {
+    return eight < k.rows && seen_page(t, k.first + eight);
+  };
   // The page table's entry for key `key` (-1 where there is none), and the key's cached row (~0
   // without a page).
-  const int shift = p.cache.page_shift;
   auto entry_of = [&](const Piece& t, int key, bool wanted) {
     return load_if(p.cache.table + (int64_t)t.seq * p.cache.max_pages + (key >> shift),
                    wanted && (key >> shift) < p.cache.max_pages, -1);
@@ -1089,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the page of the lane's eight of key tile j, and their cached rows
         auto look = [&](int j) {
           const Keys k = key_tile_of(t, j, window, sinks);
-          return entry_of(t, k.first + eight, j < count && eight < k.rows);
+          return entry_of(t, k.first + eight, j < count && wanted(t, k, eight));
         };
         auto rows_of = [&](int j, int page) { return row_of(t, key_tile_of(t, j, window, sinks).first + eight, page); };
         uint32_t rows = rows_of(0, look(0));
@@ -1107,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             page = look(j + 2);
             const Keys keys = key_tile_of(t, j, window, sinks);
             if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(free_bar, h - C::kSlots)) != 0)) break;
-            if (wq == 2) note(h, eight < keys.rows && rows == ~0u);
+            if (wq == 2) note(h, wanted(t, keys, eight) && rows == ~0u);
             uint8_t* const to_tile = to_warp + s * C::kEntry;
             bring_bytes(ahead, parity ^ 1);
 #pragma unroll 1
@@ -1208,7 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int none = max(1, p.cache.num_pages * p.cache.h_kv);  // past the pages: reads as zeros
     auto look = [&](const Piece& t, int j) {
       const Keys k = key_tile_of(t, j, window, sinks);
-      return entry_of(t, k.first + eight, j < t.count && eight < k.rows);
+      return entry_of(t, k.first + eight, j < t.count && wanted(t, k, eight));
     };
     struct Where {  // of the lane's eight keys of a tile
       uint32_t row;  // in the cache (~0: no page)
@@ -1344,7 +1356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kb = 0; kb < D / 64; ++kb) tc2::tma_load_3d(to + kb * 8192, &tm_k, 64 * kb, at.y, at.z, r_k + s * 8);
           }
           __syncwarp();
-          note(h, eight < k.rows && at.row == ~0u);
+          note(h, wanted(t, k, eight) && at.row == ~0u);
           kc = h + 1;
         }
         g += t.count;

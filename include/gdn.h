@@ -609,8 +609,10 @@ gdn_status gdn_attn_prefill(const void* q, const void* k, const void* v, void* o
  * sees the keys 0 .. p, or with window > 0 the keys p - window + 1 .. p and the first
  * `sinks` (those at or before p): softmax(scale q.k) V over them as in gdn_attn_prefill, 0
  * for a query that sees none (a > cache_len[n]).  What a query does not see has no effect
- * on it, whatever it holds; a position whose page is missing sets GDN_ERR_BAD_PAGE and takes
- * no part.  Over e4m3 rows the result is that of the rows read back as bf16.
+ * on it, whatever it holds; a position that some query sees and whose page is missing sets
+ * GDN_ERR_BAD_PAGE and takes no part.  A page of which no query sees a key (behind every
+ * window) may be missing: it is not an error.  Over e4m3 rows the result is that of the rows
+ * read back as bf16.
  *
  * q [total_q][h_q][head_dim] bf16 with q_stride elements between tokens (a multiple of 8);
  * o dense; 1 to 8 query heads per KV head; the cache as for gdn_attn_decode_paged.
