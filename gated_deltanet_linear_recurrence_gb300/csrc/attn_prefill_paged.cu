@@ -103,6 +103,8 @@ struct Cfg {
   static constexpr int kLag = kS - 1;  // key tiles that the scores are ahead of P V
   static constexpr int kPWarps = 4 * kHalves;  // warps that write P of a key tile
   static constexpr int kArrivals = kFp8 ? kWideners : 1;  // that make K or V of a key tile full, beside bytes
+  // and V of an edge tile, in the even CTA: for the odd CTA's warps its edge warp arrives
+  static constexpr int kEdgeArrivals = kFp8 ? kWideners + 1 : 1;
   // Registers of a thread of the four warpgroups: softmax (two), epilogue, and the rest;
   // together the 65,536 that the CTA starts with, of which a thread has 128.  What widens e4m3
   // rows spills with fewer than all of those (64 tokens on 9,000 positions each, 112 212 us, 128
@@ -575,8 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sh.tile_full[i], 1);
       tc::mbar_init(&sh.copy_v[i], 1);
       tc::mbar_init(&sh.sums_in[i], 8);
-      // readers: the softmax, epilogue and TMA warps, and in the even CTA the products' and edge warps
-      tc::mbar_init(&sh.tile_empty[i], 12 + (rank == 0 ? 3 : 1));
+      // readers: the softmax, epilogue and TMA warps, in the even CTA the products' and the edge
+      // warp, in the odd one the edge warp over e4m3 rows
+      tc::mbar_init(&sh.tile_empty[i], 13 + (rank == 0 ? 2 : kFp8 ? 1 : 0));
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sh.flags_in[i], 1);
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kNoted; ++i) tc::mbar_init(&sh.noted[i], 1);
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&sh.v_edge[i], C::kArrivals);
+      tc::mbar_init(&sh.v_edge[i], rank == 0 ? C::kEdgeArrivals : kWideners);
       tc::mbar_init(&sh.v_clean[i], 1);
     }
     tc::mbar_init(&sh.o_free, 2 * 4);
@@ -1087,7 +1090,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t mine = __shfl_sync(kFullMask, rows, (eight0 + 2 * lane) & 15);
         if (lane < (is_v ? 8 : 4)) copy8(&bytes[b][8 * lane], exps + (int64_t)mine, mine != ~0u);
       };
-      int late_used = 0, late_h = 0, parity = 0, ve = 0;  // (ve: edge tiles so far)
+      int late_used = 0, late_h = 0, parity = 0;
+      int ve = 0;  // edge tiles so far; in the odd CTA without those of copied pieces
       auto start = [&](uint32_t rows) {
         bring_bytes(rows, parity);
 #pragma unroll
@@ -1162,23 +1166,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             parity ^= 1;
             tc::fence_proxy_async();  // the rows -> this CTA's tensor cores
             __syncwarp();
-            // The even CTA's barriers hear of the odd one's rows by 16 bytes copied there: a
-            // copy, as the fence has ordered it behind the rows, and as its thread need not wait
-            // (an arrival there with a release waits for all that the thread has under way: 800 of
-            // 4,300 cycles a key tile, and from a warp of its own still 506 us where this takes 400).
+            // The even CTA's tensor cores hear of the odd one's rows by 16 bytes copied there: the
+            // fence has ordered the copy behind the rows, it is in the tensor cores' proxy, and
+            // its arrival on the barrier is a release in the cluster; its thread need not wait
+            // (an arrival there with a release of its own waits for all that the thread has under
+            // way: 800 of 4,300 cycles a key tile, and from a warp of its own still 506 us where
+            // this takes 400).  The edge warp reads the rows with ordinary loads, for which a copy
+            // says nothing of other threads' ordinary stores: V of an edge tile, of which there
+            // are few, is handed on by the odd CTA's edge warp (by such arrivals from here 8 tokens
+            // on 131,072 positions took 85 us, by its edge warp 75).
             const bool edge = is_v && keys.edge;
             if (lane == 0) {
-              uint64_t* const edge_bar = &sh.v_edge[ve % C::kSlots];
-              if (rank == 1) {
-                if (edge) tell(sh.said, edge_bar);
-                tell(sh.said, &full_bar[s]);
-              } else if (w2 == 0) {
-                if (edge) tc::mbar_arrive_expect_tx(edge_bar, kWideners * 16);
-                tc::mbar_arrive_expect_tx(&full_bar[s], kWideners * 16);
-              } else {
-                if (edge) tc::mbar_arrive(edge_bar);
-                tc::mbar_arrive(&full_bar[s]);
-              }
+              if (edge) tc::mbar_arrive(&sh.v_edge[ve % C::kSlots]);
+              if (rank == 1) tell(sh.said, &full_bar[s]);
+              else if (w2 == 0) tc::mbar_arrive_expect_tx(&full_bar[s], kWideners * 16);
+              else tc::mbar_arrive(&full_bar[s]);
             }
             ve += edge;
             rows = ahead;
@@ -1201,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         late_wide = count < tiles;
         due = true;
         if (tiles > 0) {
-          if (is_v && count == 0) ve += edges_of(t, window, sinks, lane);
+          if (is_v && rank == 0 && count == 0) ve += edges_of(t, window, sinks, lane);
           g += tiles;
           ++used;
         }
@@ -1277,7 +1279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // its own that the edge warp can count through; v_full keeps step.
           if (rank == 0 && lane == 0) {
             tc::mbar_arrive_expect_tx(k.edge ? &sh.v_edge[e] : &sh.v_full[s], bytes);
-            for (int i = 1; i < C::kArrivals; ++i) tc::mbar_arrive(k.edge ? &sh.v_edge[e] : &sh.v_full[s]);
+            for (int i = 1; i < (k.edge ? C::kEdgeArrivals : C::kArrivals); ++i)
+              tc::mbar_arrive(k.edge ? &sh.v_edge[e] : &sh.v_full[s]);
           }
           if (mine) {
 #pragma unroll
@@ -1528,6 +1531,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         g += t.count;
         ++used;
+      }
+    } else if (kFp8 && warp == kEdgeWarp) {
+      // ------------------------------------------------------------ edge tiles of the odd CTA
+      // V that this CTA's warps have widened, handed to the even CTA's edge warp.
+      Piece t;
+      int edges = 0, own = 0;  // edge tiles, as that warp counts them; of those, the ones widened here
+      const uint32_t r_edge = tc2::in_cta(sh.v_edge, 0);
+      for (int pass = 0; ok && next_tile(pass, &t); ++pass) {
+        const int n = edges_of(t, window, sinks, lane);
+        for (int i = 0; i < n && t.wide < 0; ++i) {
+          if (!(ok = __all_sync(kFullMask, of_tile(sh.v_edge, own)) != 0)) break;
+          if (lane == 0) tc2::arrive_remote(r_edge + (edges + i) % C::kSlots * 8);
+          ++own;
+        }
+        edges += n;
       }
     }
   }
