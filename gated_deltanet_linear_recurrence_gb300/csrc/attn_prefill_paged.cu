@@ -488,7 +488,10 @@ struct Shared {  // beside the tiles
   float red[2][2][128];
   float sums[2][2][128];  // row sums of two pieces, in two parts
   float refs[2][128];     // and the references that they go by
-  alignas(16) uint32_t said[4];        // e4m3: what the odd CTA copies to say that rows are there
+  // e4m3: what a warp of the odd CTA copies to say that its rows of a key tile are there (by
+  // slots: the tile's number + 1), and in the even CTA what it has copied last
+  alignas(16) uint32_t said[4][C::kSlots][4];
+  uint32_t said_last[4][C::kSlots];
   alignas(16) uint8_t bytes[4][2][64];  // e4m3: exponent bytes of a warp's eights, two key tiles
 };
 
@@ -594,6 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&sh.drained, 1);
     sh.failed = 0;
     tc::fence_mbar_init();
+  }
+  if (kFp8 && tid < 4 * C::kSlots) {
+    sh.said[tid / C::kSlots][tid % C::kSlots][0] = 0;
+    sh.said_last[tid / C::kSlots][tid % C::kSlots] = 0;
   }
   if (lane == 0 && warp == kTmaWarp) {
     tc::prefetch_tmap(&tm_q);
@@ -1124,6 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Keys keys = key_tile_of(t, j, window, sinks);
             if (h >= C::kSlots && !(ok = __all_sync(kFullMask, of_tile(free_bar, h - C::kSlots)) != 0)) break;
             if (wq == 2) note(h, wanted(t, keys, eight) && rows == ~0u);
+            if (rank == 1) sh.said[wq][s][0] = (uint32_t)h + 1;  // (long before the fence, which waits for it)
             uint8_t* const to_tile = to_warp + s * C::kEntry;
             bring_bytes(ahead, parity ^ 1);
 #pragma unroll 1
@@ -1178,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool edge = is_v && keys.edge;
             if (lane == 0) {
               if (edge) tc::mbar_arrive(&sh.v_edge[ve % C::kSlots]);
-              if (rank == 1) tell(sh.said, &full_bar[s]);
+              if (rank == 1) tell(sh.said[wq][s], &full_bar[s]);
               else if (w2 == 0) tc::mbar_arrive_expect_tx(&full_bar[s], kWideners * 16);
               else tc::mbar_arrive(&full_bar[s]);
             }
@@ -1209,6 +1217,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       copy_wait<0>();
+      __syncwarp();
+      if (rank == 1 && lane < C::kSlots) tc2::store_remote(tc2::in_cta(&sh.said_last[wq][lane], 0), sh.said[wq][lane][0]);
     }
   } else {
     tc2::fewer_registers<C::kOtherRegs>();
@@ -1557,9 +1567,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();  // neither CTA's memory is in use by the other any more
-  // (but for what the odd CTA has told and the even one, which gave up, not waited for: 16 bytes
-  // on their way, some 1 us)
-  if (kFp8 && rank == 0 && sh.failed) __nanosleep(100000);
+  // (but for what the odd CTA has told and the even one, which gave up, has not waited for: 16
+  // bytes a copy, of which it knows what they will be)
+  if (kFp8 && rank == 0 && sh.failed && tid < 4 * C::kSlots) {
+    const volatile uint32_t* there = sh.said[tid / C::kSlots][tid % C::kSlots];
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (*there != sh.said_last[tid / C::kSlots][tid % C::kSlots] && tc::globaltimer_ns() - t0 < 1000000000ull)
+      __nanosleep(100);
+  }
   tc::fence_after_sync();
   if (warp == 0) tc2::tmem_dealloc(tmem, C::kTmemCols);
 }
