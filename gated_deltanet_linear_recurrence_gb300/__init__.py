@@ -418,8 +418,7 @@ def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, no
     first, with weights [D] fp32 (ones when None); no norm when None.  ``axes``: with
     positions [A, T], the axis that each frequency goes by (bytes, or a list of
     rotary_dim / 2 numbers below A).  q, k and the outputs may be slices of a fused
-    projection, an output also its input itself.  Returns (q_out, k_out), in one
-    allocation where neither is given."""
+    projection, an output also its input itself.  Returns (q_out, k_out)."""
     return _lib.binding().qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, norm_eps, axes,
                                        interleaved, q_out, k_out, stream)
 

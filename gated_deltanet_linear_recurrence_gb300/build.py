@@ -48,7 +48,8 @@ def _binding_command(out):
             "-isystem", os.path.join(base, "include"),
             "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
             "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", out,
-            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+            "-lc10_cuda"]
 
 
 def _binding_made_with():
