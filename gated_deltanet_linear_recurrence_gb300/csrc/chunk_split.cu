@@ -766,7 +766,7 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
   const int64_t srow0 = ((int64_t)n * p.h_v + h) * p.d_v + s * DVS;
 
   // mbarriers.  full/tfull: TMA and bulk copies landed; empty: the stage's MMAs
-  // are done (tcgen05.commit); tempty: the output warps took the chunk's gates.
+  // are done (tcgen05.commit); tempty: the output warps saw P U of the chunk done.
   // bar_d, bar_s, bar_o: D, the state update, P U complete (tcgen05.commit;
   // bar_o one per chunk modulo 3); bar_u: the U warps staged U; bar_ss: every
   // epilogue warp staged the state.
@@ -901,42 +901,33 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
     // Epilogue warps.  Those on TMEM lanes 0-63 form U (staged once: the update
     // takes the package's decayed K, so no per-row scaling is left on this
     // critical step) and preload the next chunk's U~; those on lanes 64-127
-    // take the previous chunk's gates, clear rows 64-127 of the next D buffer
+    // wait for the previous chunk's P U, clear rows 64-127 of the next D buffer
     // and, once the state is staged, store the previous chunk's output; all
     // stage the state.  Every hand-off is an mbarrier with a bounded wait.
     const int rl = 32 * (warp & 1) + lane;  // accumulator row of this thread within its half
-    // Output of chunk cp (the warps on lanes 64-127): O = Gamma Q S^T + P U, in
-    // two parts.  take_gates(cp) waits for P U and reads the rows' output factors,
-    // after which the chunk's tail stage is released; write_output(cp) forms and
-    // stores the rows after the next state has been staged, so that its global
-    // stores neither compete with the U warps' shared-memory stores nor delay the
-    // state (D and P U are triple-buffered in TMEM for that).
+    // Output of chunk cp (the warps on lanes 64-127): O = Gamma Q S^T + P U.  Its rows'
+    // factors are read when the chunk's state is staged (gates below); product_done(cp)
+    // waits for P U and releases the chunk's tail stage; write_output(cp) forms and
+    // stores the rows after the next state has been staged, so that its global stores
+    // neither compete with the U warps' shared-memory stores nor delay the state (D and
+    // P U are triple-buffered in TMEM for that).
     //
-    // The stage is rewritten by bulk copies, through the async proxy, which an
-    // arrival alone does not order behind ordinary reads: a factor that was still
-    // on its way when its thread arrived came out as that of chunk cp + NSTG, in
-    // one of 10^7 to 10^8 chunks (of 28,000 passes over 131,072 tokens 78, in
-    // pieces of 8,192 637).  So a fence.proxy.async stands between the read and
-    // the arrival.  The two-kernel form has one of its own, so that the tail copy
-    // has time to land (32,768 tokens 724 us; 719 without the fence, 794 with the
-    // arrival behind the state's staging); the cooperative form arrives behind the
-    // fence of that staging (16,384 tokens 306 us; with a fence of its own 326,
-    // without one 315).
+    // The stage is rewritten by bulk copies, through the async proxy, which an arrival
+    // alone does not order behind ordinary reads: factors read right before it, and still
+    // on their way when their thread arrived, came out as those of chunk cp + NSTG, in
+    // one of 10^7 to 10^8 chunks (of 28,000 passes over 131,072 tokens 78, in pieces of
+    // 8,192 637).  The fence.proxy.async of the staging orders them (a fence of its own
+    // here instead costs 1 to 3 %).  The two-kernel form releases the stage at once, so
+    // that the tail copy has time to land (32,768 tokens 714 us, behind the next
+    // staging 794); the cooperative form behind the next staging, off the way to it
+    // (131,072 tokens 2,293 us, at once 2,324).
     const bool late_release = item_flags != nullptr;
-    auto take_gates = [&](int cp) {
-      const int stp = cp % NSTG;
+    auto product_done = [&](int cp) {
       // P U of chunk cp + 3 is issued only after these warps stage chunk cp + 3's
       // state, later than this wait, so the phase parity is unambiguous
       ok = tc::mbar_wait(&bar_o[cp % 3], (cp / 3) & 1) && ok;
       tc::fence_after_sync();
-      const float gr =
-          reinterpret_cast<const float*>(smem + CF::CC_GATE + stp * kGateBytes)[rl];
-      if (!late_release) {
-        tc::fence_proxy_async();
-        tc::fence_before_sync();
-        tc::mbar_arrive(&tempty[stp]);
-      }
-      return gr;
+      if (!late_release) tc::mbar_arrive(&tempty[cp % NSTG]);
     };
     auto write_output = [&](int cp, float Gam_r) {
       const int64_t t0p = t_beg + (int64_t)cp * kC;
@@ -965,7 +956,8 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
     };
     // S (fp32, thread j holds column j of the slice) -> bf16 operand copy for
     // chunk cn's D, then Gamma_n of chunk cn applied in TMEM (the update MMA
-    // accumulates onto it); then tell the MMA warp.
+    // accumulates onto it); then tell the MMA warp.  Returns the output factor of the
+    // thread's row of that chunk.
     auto stage_state = [&](float (&sc)[32 * BPW], int cn) {
 #pragma unroll
       for (int b = 0; b < BPW; ++b)
@@ -974,8 +966,8 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
           st_chunk<2>(smem + CF::CC_SS + (b0 + b) * 8192, jrow * 64 + c4 * 16, sc + 32 * b + 8 * c4);
       const int stn = cn % NSTG;
       ok = tc::mbar_wait(&tfull[stn], (cn / NSTG) & 1) && ok;
-      const float Gam_n =
-          reinterpret_cast<const float*>(smem + CF::CC_GATE + stn * kGateBytes)[128];
+      const float* gates = reinterpret_cast<const float*>(smem + CF::CC_GATE + stn * kGateBytes);
+      const float Gam_n = gates[128], Gam_r = gates[rl];
 #pragma unroll
       for (int i = 0; i < 32 * BPW; ++i) sc[i] *= Gam_n;
 #pragma unroll
@@ -985,6 +977,7 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
       tc::fence_proxy_async();
       tc::fence_before_sync();
       tc::mbar_arrive(bar_ss);
+      return Gam_r;
     };
     // D of chunk cn accumulates onto its TMEM buffer, preloaded with U~ in rows
     // 0-63 (by the warps on those lanes) and zeros in rows 64-127 (the output
@@ -1019,6 +1012,7 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
         for (int b = b0; b < b0 + BPW; ++b) tc::tmem_st32(td + 32 * b, u);
       }
     };
+    float gam_prev = 0.f, gam = 0.f;  // output factors of the previous chunk's rows and of this one's
     {  // initial state: rows 32 b0 .. of the slice, column jrow
       float sc[32 * BPW];
 #pragma unroll
@@ -1032,10 +1026,9 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
             p.state_out[(srow0 + 32 * b0 + i) * DKP + jrow] = sc[i];
       } else {
         preload(0);
-        stage_state(sc, 0);
+        gam = stage_state(sc, 0);
       }
     }
-    float gam_prev = 0.f;  // output factor of the previous chunk's rows (output warps)
     for (int c = 0; c < nchunks && ok; ++c) {
       if ((warp & 3) < 2) {  // U = U~ - W S^T for rows r = lanes 0-63
         // D(c) completes after P U(c - 2), the last reader of the U buffer about
@@ -1058,7 +1051,7 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
         tc::mbar_arrive(bar_u);
         if (c + 1 < nchunks) preload(c + 1);  // while the state update runs
       } else {
-        if (c > 0) gam_prev = take_gates(c - 1);
+        if (c > 0) product_done(c - 1);
         if (c + 1 < nchunks) preload(c + 1);  // the buffer's rows were read by output c - 2
         ok = tc::mbar_wait(bar_d, c & 1) && ok;  // D has read the staged state rewritten below
       }
@@ -1069,19 +1062,24 @@ __device__ __forceinline__ void chain_run(const SplitParams& p, const CUtensorMa
       for (int b = 0; b < BPW; ++b)
         tc::tmem_ld32(tmem + lane_base + CF::TC_S + 32 * (b0 + b),
                       *reinterpret_cast<float(*)[32]>(sc + 32 * b));
+      float gam_next = 0.f;
       if (c == nchunks - 1) {
         if (jrow < DKP)
 #pragma unroll
           for (int i = 0; i < 32 * BPW; ++i)
             p.state_out[(srow0 + 32 * b0 + i) * DKP + jrow] = sc[i];
       } else {
-        stage_state(sc, c + 1);
+        gam_next = stage_state(sc, c + 1);
         if (late_release && (warp & 3) >= 2 && c > 0) tc::mbar_arrive(&tempty[(c - 1) % NSTG]);
       }
       if ((warp & 3) >= 2 && c > 0) write_output(c - 1, gam_prev);  // after the staging
+      gam_prev = gam;
+      gam = gam_next;
     }
-    if (ok && nchunks > 0 && (warp & 3) >= 2)  // the last output
-      write_output(nchunks - 1, take_gates(nchunks - 1));
+    if (ok && nchunks > 0 && (warp & 3) >= 2) {  // the last output
+      product_done(nchunks - 1);
+      write_output(nchunks - 1, gam_prev);
+    }
   }
   if (!ok) raise_error(p.err, kErrDeviceTimeout);
   tc::fence_before_sync();
