@@ -40,20 +40,20 @@ FP32_LANES_PER_SM = 128
 # stripped) hash to the recorded value.
 NCU_TRAFFIC = {
     "chunk_split": {"files": ["chunk_split.cu", "chunk_common.cuh", "tc.cuh", "rows.cuh"],
-                    "sha256_16": "4dbd7899e795fe3c",
-                    "bytes": (68_258_048 + 62_212_608) + (135_572_224 + 13_334_784),
+                    "sha256_16": "c38a217bd8d6a4cf",
+                    "bytes": (68_255_232 + 62_033_408) + (135_567_616 + 13_236_736),
                     "profile": "profiles/chunk_split_t4096.md"},
     "chunk_coop": {"files": ["chunk_split.cu", "chunk_common.cuh", "tc.cuh", "rows.cuh"],
-                   "sha256_16": "4dbd7899e795fe3c", "bytes": 69_837_312 + 99_008_000,
+                   "sha256_16": "c38a217bd8d6a4cf", "bytes": 69_414_144 + 98_602_496,
                    "profile": "profiles/chunk_coop_t4096.md"},
     "chunk_coop@prefill_t131072": {
         "files": ["chunk_split.cu", "chunk_common.cuh", "tc.cuh", "rows.cuh"],
-        "sha256_16": "4dbd7899e795fe3c", "bytes": 4_049_355_008 + 4_838_642_176,
+        "sha256_16": "c38a217bd8d6a4cf", "bytes": 2_201_586_944 + 4_815_151_616,
         "profile": "profiles/chunk_coop_t131072.md"},
     "chunk_split@prefill_varlen10": {
         "files": ["chunk_split.cu", "chunk_common.cuh", "tc.cuh", "rows.cuh"],
-        "sha256_16": "4dbd7899e795fe3c",
-        "bytes": 12_544 + (4_362_177_024 + 7_522_012_928) + (8_666_622_720 + 2_143_017_984),
+        "sha256_16": "c38a217bd8d6a4cf",
+        "bytes": 12_800 + (4_362_328_832 + 7_521_726_720) + (8_666_467_072 + 2_143_092_992),
         "profile": "profiles/chunk_split_varlen10.md"},
     "chunk_prefill": {"files": ["chunk_prefill.cu", "chunk_common.cuh", "tc.cuh", "rows.cuh"],
                       "sha256_16": "f95c4a11744de65c", "bytes": 68_218_112 + 5_280_768,

@@ -8,7 +8,9 @@
 //     t_rj = s_rj log2(e),    l_r = sum_j 2^(t_rj - m_r)
 // over 128-key tiles with a running reference m_r, on CTA pairs with tcgen05, as the
 // attention of packed prompts does it (attn_prefill.cu explains the pair's tile, its TMEM
-// and shared memory, the softmax and the care for values that are not finite).  What is
+// and shared memory, the softmax and the care for values that are not finite).  Weights are
+// rounded to bf16 for the product with V, as there (2^-8 of sum w |v| at most; their sum l and O
+// stay in fp32): pairs would double that product, half of a piece's time.  What is
 // different here:
 //
 // Work.  (m, l, O) of disjoint sets of keys join by rescaling to the larger m.  So a pair's
@@ -50,8 +52,8 @@
 // the other); 32 tokens on 131,072 69 us, floor 41; five on a million 315 us, 6.5 TB/s; 28
 // tokens of eight sequences on up to 4,090 keys 19 us (latency: 7 us from the start to
 // the first scores, 4 of the join).  e4m3: 2,000 on 11,011, 32 heads of 128 on 8, 243 us,
-// floor 171 (409 widened by each tile of queries); 8 on 131,072 and 60,001 98 us, floor 29; 64
-// single tokens in a window of 2,048 81 us, floor 19 (over bf16 rows 61 us).
+// floor 171 (409 widened by each tile of queries); 8 on 131,072 and 60,001 99 us, floor 29; 64
+// single tokens in a window of 2,048 83 us, floor 19 (over bf16 rows 61 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
